@@ -1,0 +1,326 @@
+// few_tokens.cu -- the whole expert layer for up to 64 tokens in two kernels:
+//   inner[t, e] = weight[t, e] * silu(Wg[e] x[t]) * (Wu[e] x[t])        few_inner_kernel
+//   out[t]      = sum over e of W2[e] inner[t, e] (+ shared rows)       few_out_kernel
+// Every expert that a token chose is read once, whole, and nothing else of the weights:
+// the floor is those bytes.  Both kernels find the chosen experts and their tokens from
+// topk_idx by themselves (a bit mask of tokens for each expert in shared memory), so
+// there is no layout, dispatch or combine pass and no row moves.
+//
+// The inner rows are float32 results that the second product needs as bf16.  One
+// rounding there would cost as much as the output's own; they are kept as a bf16 value
+// and a bf16 remainder (16 significant bits) instead, and the second kernel multiplies
+// by both: the tensor cores have time to spare while the weights arrive.
+//
+// Sums run in a fixed order (warps take fixed pieces, their partial sums are added in
+// warp order): results do not vary from run to run.
+#include "expert_ops.cuh"
+#include "skinny.cuh"
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxEntries = kFewMaxTokens * kMaxTopk;
+
+// What a CTA knows of the routing: the experts with a token, in ascending order, and the
+// rows of their tokens (ascending; rows of one expert are neighbours in `inner`).
+struct Routing {
+    unsigned long long mask[kMaxExperts];
+    int16_t expert[kMaxExperts];
+    int16_t base[kMaxExperts + 1];
+    uint8_t token[kMaxEntries];
+    int32_t warp_sum[kWarps];
+    int32_t count;   // experts with a token
+};
+
+__device__ __forceinline__ void build_routing(Routing& r, const FewArgs& a) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int e = tid; e < a.E; e += kThreads) r.mask[e] = 0;
+    __syncthreads();
+    for (int i = tid; i < a.T * a.K; i += kThreads) {
+        const int64_t e = a.topk[i];
+        if (e >= 0 && e < a.E) atomicOr(&r.mask[e], 1ull << (i / a.K));
+        else if (e != -1 && a.status) ep_set_status(a.status, EP_ERR_BAD_EXPERT_ID);
+    }
+    __syncthreads();
+    // thread t holds experts 2t and 2t + 1; experts in the high half of the sums, rows in the low
+    const int e0 = 2 * tid;
+    const unsigned long long m0 = e0 < a.E ? r.mask[e0] : 0, m1 = e0 + 1 < a.E ? r.mask[e0 + 1] : 0;
+    const int v0 = m0 ? (1 << 16) + __popcll(m0) : 0, v1 = m1 ? (1 << 16) + __popcll(m1) : 0;
+    int s = v0 + v1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += n;
+    }
+    if (lane == 31) r.warp_sum[warp] = s;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) s += r.warp_sum[w];
+    int at = s - v0 - v1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const unsigned long long m = h ? m1 : m0;
+        if (m) {
+            const int pos = at >> 16;
+            int row = at & 0xffff;
+            r.expert[pos] = (int16_t)(e0 + h);
+            r.base[pos] = (int16_t)row;
+            for (unsigned long long left = m; left; left &= left - 1) r.token[row++] = (uint8_t)(__ffsll(left) - 1);
+        }
+        at += h ? v1 : v0;
+    }
+    if (tid == kThreads - 1) {
+        r.count = s >> 16;
+        r.base[s >> 16] = (int16_t)(s & 0xffff);
+    }
+    __syncthreads();
+}
+
+static_assert(kMaxExperts <= 2 * kThreads, "a thread holds two experts");
+static_assert(kFewMaxTokens <= 64, "a token mask is 64 bits");
+
+// Router weight of (token, expert): its entries' weights in slot order (one, unless a
+// token names an expert twice).
+__device__ __forceinline__ float routing_weight(const FewArgs& a, int token, int expert) {
+    float w = 0.0f;
+    for (int k = 0; k < a.K; ++k)
+        if (a.topk[token * a.K + k] == expert) w += a.topk_w[token * a.K + k];
+    return w;
+}
+
+// An item is eight inner channels of one expert: their gate rows are rows 0-7 of the
+// 16-row tile and their up rows 8-15, so a lane ends with both of a channel.  The warps
+// share the item's k and add their parts in shared memory.
+template <bool W8, int NT>
+__device__ __forceinline__ void inner_item(const FewArgs& a, const Routing& r, int pos, int tile, float* red) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+    const int e = r.expert[pos], row0 = r.base[pos], m = r.base[pos + 1] - row0;
+    const int k_bytes = a.H * (W8 ? 1 : 2);
+    const uint8_t* r0 = a.w13 + ((int64_t)e * 2 * a.I + tile * 8 + g) * k_bytes;
+    const uint8_t* r1 = r0 + (int64_t)a.I * k_bytes;
+    const uint8_t* tok[NT];
+    float acc[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int col = min(j * 8 + g, m - 1);   // columns past the last token repeat it and are not stored
+        tok[j] = reinterpret_cast<const uint8_t*>(a.x) + (int64_t)r.token[row0 + col] * a.H * 2;
+        acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+    }
+    mma_pieces<W8, false, NT, 1>(acc, r0, r1, tok, 0, warp, (k_bytes + 127) / 128, kWarps, q * 16, k_bytes);
+    // red[warp][column][16 rows]
+    float* mine = red + warp * NT * 8 * 16;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        mine[(j * 8 + 2 * q) * 16 + g] = acc[j][0];
+        mine[(j * 8 + 2 * q + 1) * 16 + g] = acc[j][1];
+        mine[(j * 8 + 2 * q) * 16 + g + 8] = acc[j][2];
+        mine[(j * 8 + 2 * q + 1) * 16 + g + 8] = acc[j][3];
+    }
+    __syncthreads();
+    for (int i = tid; i < m * 8; i += kThreads) {
+        const int col = i >> 3, c = i & 7, channel = tile * 8 + c;
+        float gate = 0.0f, up = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            gate += red[(w * NT * 8 + col) * 16 + c];
+            up += red[(w * NT * 8 + col) * 16 + c + 8];
+        }
+        if constexpr (W8) {
+            const float* sc = a.w13_scales + (int64_t)e * 2 * a.I + channel;
+            gate *= sc[0];
+            up *= sc[a.I];
+        }
+        const float h = gate / (1.0f + expf(-gate)) * up * routing_weight(a, r.token[row0 + col], e);
+        const uint32_t hi = pack_bf16x2_rn(h, 0.0f) & 0xffffu;
+        uint16_t* dst = a.inner + (int64_t)(row0 + col) * 2 * a.I + channel;
+        dst[0] = (uint16_t)hi;
+        dst[a.I] = (uint16_t)pack_bf16x2_rn(h - bf16_bits_to_float(hi), 0.0f);
+    }
+    __syncthreads();
+}
+
+template <bool W8, int MAXNT>
+__global__ void __launch_bounds__(kThreads) few_inner_kernel(const FewArgs a) {
+    __shared__ Routing r;
+    __shared__ float red[kWarps * MAXNT * 8 * 16];
+    build_routing(r, a);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tiles = a.I / 8;
+    const int items = r.count * tiles;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int pos = item / tiles, tile = item % tiles;
+        const int m = r.base[pos + 1] - r.base[pos];
+        if (MAXNT == 1 || m <= 8) inner_item<W8, 1>(a, r, pos, tile, red);
+        else if (MAXNT == 2 || m <= 16) inner_item<W8, (MAXNT < 2 ? MAXNT : 2)>(a, r, pos, tile, red);
+        else if (m <= 32) inner_item<W8, (MAXNT < 4 ? MAXNT : 4)>(a, r, pos, tile, red);
+        else inner_item<W8, MAXNT>(a, r, pos, tile, red);
+    }
+}
+
+// The part of one expert in a warp's range of pieces, added to the warp's own sums
+// [token][16 rows].
+template <bool W8, int NT>
+__device__ __forceinline__ void out_part(const FewArgs& a, const Routing& r, int pos, int h0, int first, int end,
+                                         float* sums) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int e = r.expert[pos], row0 = r.base[pos], m = r.base[pos + 1] - row0;
+    const int k_bytes = a.I * (W8 ? 1 : 2);
+    const int ra = min(h0 + g, a.H - 1), rb = min(h0 + g + 8, a.H - 1);   // rows past H are not stored
+    const uint8_t* w = a.w2 + (int64_t)e * a.H * k_bytes;
+    const uint8_t* tok[NT];
+    float acc[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        tok[j] = reinterpret_cast<const uint8_t*>(a.inner) + (int64_t)(row0 + min(j * 8 + g, m - 1)) * a.I * 4;
+        acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+    }
+    mma_pieces<W8, false, NT, 2>(acc, w + (int64_t)ra * k_bytes, w + (int64_t)rb * k_bytes, tok, (int64_t)a.I * 2,
+                                 first, end, 1, q * 16, k_bytes);
+    float sa = 1.0f, sb = 1.0f;
+    if constexpr (W8) {
+        sa = a.w2_scales[(int64_t)e * a.H + ra];
+        sb = a.w2_scales[(int64_t)e * a.H + rb];
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int col = j * 8 + 2 * q + c;
+            if (col < m) {
+                float* s = sums + r.token[row0 + col] * 16 + g;
+                s[0] += sa * acc[j][c];
+                s[8] += sb * acc[j][c + 2];
+            }
+        }
+    }
+    __syncwarp();
+}
+
+// A CTA owns 16 columns of the output for every token.  The pieces of all experts form
+// one line, of which each warp takes an equal stretch.
+template <bool W8, int MAXNT>
+__global__ void __launch_bounds__(kThreads) few_out_kernel(const FewArgs a) {
+    __shared__ Routing r;
+    extern __shared__ float sums[];   // [warp][token][16]
+    const int tid = threadIdx.x, warp = tid >> 5;
+    for (int i = tid; i < kWarps * a.T * 16; i += kThreads) sums[i] = 0.0f;
+    build_routing(r, a);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int h0 = blockIdx.x * 16;
+    const int pieces = (a.I * (W8 ? 1 : 2) + 127) / 128;
+    const int total = r.count * pieces;
+    const int begin = (int)((int64_t)total * warp / kWarps), end = (int)((int64_t)total * (warp + 1) / kWarps);
+    float* mine = sums + warp * a.T * 16;
+    for (int at = begin; at < end;) {
+        const int pos = at / pieces, first = at % pieces, last = min(pieces, first + end - at);
+        const int m = r.base[pos + 1] - r.base[pos];
+        if (MAXNT == 1 || m <= 8) out_part<W8, 1>(a, r, pos, h0, first, last, mine);
+        else if (MAXNT == 2 || m <= 16) out_part<W8, (MAXNT < 2 ? MAXNT : 2)>(a, r, pos, h0, first, last, mine);
+        else if (m <= 32) out_part<W8, (MAXNT < 4 ? MAXNT : 4)>(a, r, pos, h0, first, last, mine);
+        else out_part<W8, MAXNT>(a, r, pos, h0, first, last, mine);
+        at += last - first;
+    }
+    __syncthreads();
+    for (int i = tid; i < a.T * 16; i += kThreads) {
+        const int t = i >> 4, h = h0 + (i & 15);
+        if (h >= a.H) continue;
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) s += sums[w * a.T * 16 + i];
+        for (int k = 0; k < a.S; ++k) s += bf16_bits_to_float(a.shared[((int64_t)k * a.T + t) * a.H + h]);
+        a.out[(int64_t)t * a.H + h] = (uint16_t)pack_bf16x2_rn(s, 0.0f);
+    }
+}
+
+template <bool W8, int MAXNT>
+cudaError_t launch(const FewArgs& a, int sms, cudaStream_t st) {
+    const int64_t entries = (int64_t)a.T * a.K;
+    const int64_t items = (entries < a.E ? entries : a.E) * (a.I / 8);
+    const int64_t most = (int64_t)sms * 4;
+    few_inner_kernel<W8, MAXNT><<<(unsigned)(items < most ? items : most), kThreads, 0, st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // The second kernel may start while the first drains: it reads the routing, then waits.
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)((a.H + 15) / 16));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(float) * kWarps * (size_t)a.T * 16;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, few_out_kernel<W8, MAXNT>, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+bool aligned(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
+
+size_t workspace_bytes(int64_t T, int64_t K, int64_t I) { return (size_t)(T * K * I * 4); }
+
+ep_status check_sizes(int32_t T, int32_t H, int32_t E, int32_t K, int32_t I) {
+    if (T < 0 || H < 8 || H > 8192 || E < 1 || E > kMaxExperts || K < 1 || K > kMaxTopk || K > E)
+        return EP_ERR_INVALID_ARG;
+    if (I < 8 || I > 65536 || H % 8 != 0 || I % 8 != 0) return EP_ERR_INVALID_ARG;
+    return T > kFewMaxTokens ? EP_ERR_UNSUPPORTED : EP_OK;
+}
+
+}  // namespace
+
+// The number of tile columns is a template bound: with at most 8 or 16 tokens the
+// accumulators of wider tiles would only cost registers, and so loads in flight.
+cudaError_t launch_few_tokens(const FewArgs& a, bool w8, int sms, cudaStream_t st) {
+    if (a.T <= 8) return w8 ? launch<true, 1>(a, sms, st) : launch<false, 1>(a, sms, st);
+    if (a.T <= 16) return w8 ? launch<true, 2>(a, sms, st) : launch<false, 2>(a, sms, st);
+    return w8 ? launch<true, 8>(a, sms, st) : launch<false, 8>(a, sms, st);
+}
+
+extern "C" ep_status ep_moe_few_tokens_workspace_size(int32_t num_tokens, int32_t hidden, int32_t num_experts,
+                                                      int32_t topk, int32_t inner, size_t* bytes) {
+    const ep_status s = check_sizes(num_tokens, hidden, num_experts, topk, inner);
+    if (s != EP_OK) return s;
+    if (!bytes) return EP_ERR_INVALID_ARG;
+    *bytes = workspace_bytes(num_tokens, topk, inner);
+    return EP_OK;
+}
+
+extern "C" ep_status ep_moe_few_tokens(const void* x, const int64_t* topk_idx, const float* topk_weights,
+                                       int32_t num_tokens, int32_t hidden, int32_t num_experts, int32_t topk,
+                                       int32_t inner, const void* w13, const float* w13_scales, const void* w2,
+                                       const float* w2_scales, const void* shared, int32_t num_shared, void* out,
+                                       void* workspace, size_t workspace_size, int32_t* status,
+                                       ep_stream_t stream) {
+    const ep_status s = check_sizes(num_tokens, hidden, num_experts, topk, inner);
+    if (s != EP_OK) return s;
+    if (!w13 || !w2 || !aligned(w13, 16) || !aligned(w2, 16)) return EP_ERR_INVALID_ARG;
+    if ((w13_scales == nullptr) != (w2_scales == nullptr)) return EP_ERR_INVALID_ARG;
+    const bool w8 = w13_scales != nullptr;
+    if (w8 && (hidden % 16 != 0 || inner % 16 != 0 || !aligned(w13_scales, 4) || !aligned(w2_scales, 4)))
+        return EP_ERR_INVALID_ARG;
+    if (num_shared < 0 || num_shared > kMaxShared || (num_shared > 0 && (!shared || !aligned(shared, 2))))
+        return EP_ERR_INVALID_ARG;
+    if (status && !aligned(status, 4)) return EP_ERR_INVALID_ARG;
+    if (num_tokens == 0) return EP_OK;
+    if (!x || !aligned(x, 16) || !topk_idx || !aligned(topk_idx, 8) || !topk_weights || !aligned(topk_weights, 4) ||
+        !out || !aligned(out, 2))
+        return EP_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) || workspace_size < workspace_bytes(num_tokens, topk, inner))
+        return EP_ERR_INVALID_ARG;
+    FewArgs a;
+    a.x = (const uint16_t*)x;
+    a.topk = topk_idx;
+    a.topk_w = topk_weights;
+    a.w13 = (const uint8_t*)w13;
+    a.w13_scales = w13_scales;
+    a.w2 = (const uint8_t*)w2;
+    a.w2_scales = w2_scales;
+    a.shared = (const uint16_t*)shared;
+    a.out = (uint16_t*)out;
+    a.inner = (uint16_t*)workspace;
+    a.status = status;
+    a.T = num_tokens; a.K = topk; a.E = num_experts; a.H = hidden; a.I = inner; a.S = num_shared;
+    const int sms = ep_current_sms();
+    if (sms <= 0) return EP_ERR_CUDA;
+    return launch_few_tokens(a, w8, sms, (cudaStream_t)stream) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+}

@@ -1,0 +1,393 @@
+// rows.cu -- rows of 8-bit codes with scales from bf16 rows: after a residual add
+// and RMSNorm (rms_norm_quant_kernel), or as they are (quant_rows_kernel).  Either
+// leaves rows that ep_dispatch_ex moves unchanged (EP_DISPATCH_PRE_ENCODED), so a
+// token is encoded once however many experts it goes to.
+//
+// The mathematics of the normalised form, for one row:
+//   h = bf16(x + residual),  t = h * gamma,  r = 1 / sqrt(mean(h^2) + eps),  y = t * r
+//   per token / per 128 columns:  m = max|t|,  code = nearest(t * top / m),  scale = m * r / top
+//   MX blocks of 32 columns:      2^s, s = floor(log2(max|t| * r)) - emax,  code = nearest(y * 2^-s)
+// The root cancels in the codes of the first kind, so the maximum does not wait for
+// it: one pass over the row, one barrier.  t is exact in float32 (8 x 8 significant
+// bits), and so is t * top (top has three or seven); the quotient is corrected once
+// with an FMA remainder, which makes every tie between two codes an exact value and
+// leaves no non-tie on one: the codes are the formula's, not a float32 neighbour's.
+// (Distance of a non-tie from a tie: at least 2^-24 of it, from the widths 23 and 16
+// bits of numerator and divisor; the corrected quotient is closer than that.)
+// h is rounded to bf16 before the norm: that rounded row is what the residual stream
+// stores, and normalising exactly it makes the result the same whether the addition
+// was fused or not.
+#include "expert_ops.cuh"
+#include "quant.cuh"
+
+namespace {
+
+// Sum of float32 values with its rounding error carried along: about 48 bits.
+struct Sum2 { float hi, lo; };
+
+__device__ __forceinline__ void sum2_add(Sum2& s, float hi, float lo) {
+    const float t = __fadd_rn(s.hi, hi);
+    const float b = __fsub_rn(t, s.hi);
+    const float e = __fadd_rn(__fsub_rn(s.hi, __fsub_rn(t, b)), __fsub_rn(hi, b));
+    s.hi = t;
+    s.lo = __fadd_rn(s.lo, __fadd_rn(e, lo));
+}
+
+__device__ __forceinline__ uint4 ld_stream_v4(const void* p) {   // not .nc: h_out may be one of the inputs
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
+// Codes of 8 values t with largest magnitude m (finite, > 0) at TOP: the divisor is
+// brought near 1 by a power of two (exact), so that t * top cannot overflow.
+template <int Q>
+__device__ __forceinline__ uint2 encode_ratio(const float t[8], float m) {
+    constexpr float top = QTraits<Q>::dmax;
+    const int e = max((int)(__float_as_uint(m) >> 23) - 127, -110);
+    // 2^-e: e = 127 gives the subnormal 2^-127
+    const float p = e < 127 ? __uint_as_float((uint32_t)(127 - e) << 23) : 5.877471754111438e-39f;
+    const float a = __fmul_rn(top, p), b = __fmul_rn(m, p), inv = __fdiv_rn(1.0f, b);
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float n = __fmul_rn(t[i], a);
+        const float q0 = __fmul_rn(n, inv);
+        q[i] = __fmaf_rn(__fmaf_rn(-q0, b, n), inv, q0);
+    }
+    if constexpr (Q == M_INT8) {
+        // adding 1.5 * 2^23 rounds to nearest even and leaves the code in the low byte
+        int c[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = __float_as_int(__fadd_rn(q[i], 12582912.0f));
+        return make_uint2(pack4_low_bytes(c[0], c[1], c[2], c[3]), pack4_low_bytes(c[4], c[5], c[6], c[7]));
+    } else {
+        constexpr int C = QTraits<Q>::fp8;
+        return make_uint2(cvt_fp8x2<C>(q[0], q[1]) | (cvt_fp8x2<C>(q[2], q[3]) << 16),
+                          cvt_fp8x2<C>(q[4], q[5]) | (cvt_fp8x2<C>(q[6], q[7]) << 16));
+    }
+}
+
+__device__ __forceinline__ bool finite_bits(uint32_t magnitude) { return magnitude < 0x7f800000u; }
+
+// One CTA per row; thread t holds the 16-byte vectors u * blockDim + t of the row in
+// registers between the single barrier and the stores.
+template <int Q, int VPT>
+__global__ void __launch_bounds__(1024) rms_norm_quant_kernel(const RowQuantArgs a) {
+    using TR = QTraits<Q>;
+    __shared__ float2 s_sum[32];
+    __shared__ uint32_t s_max[32];
+    const int nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, nwarps = nt >> 5;
+    const int64_t row = blockIdx.x;
+    const uint16_t* x = a.x + row * a.x_stride;
+    const uint16_t* res = a.residual ? a.residual + row * a.residual_stride : nullptr;
+
+    uint4 v[VPT], g[VPT];
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+        const int vi = u * nt + tid;
+        v[u] = vi < a.nvec ? ld_stream_v4(x + 8 * vi) : make_uint4(0, 0, 0, 0);
+    }
+    if (res) {
+        uint4 w[VPT];
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            const int vi = u * nt + tid;
+            w[u] = vi < a.nvec ? ld_stream_v4(res + 8 * vi) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            float f[8], r[8];
+            unpack8(v[u], f);
+            unpack8(w[u], r);
+            v[u].x = pack_bf16x2_rn(__fadd_rn(f[0], r[0]), __fadd_rn(f[1], r[1]));
+            v[u].y = pack_bf16x2_rn(__fadd_rn(f[2], r[2]), __fadd_rn(f[3], r[3]));
+            v[u].z = pack_bf16x2_rn(__fadd_rn(f[4], r[4]), __fadd_rn(f[5], r[5]));
+            v[u].w = pack_bf16x2_rn(__fadd_rn(f[6], r[6]), __fadd_rn(f[7], r[7]));
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+        const int vi = u * nt + tid;
+        g[u] = vi < a.nvec ? __ldg(reinterpret_cast<const uint4*>(a.gamma) + vi) : make_uint4(0, 0, 0, 0);
+    }
+    if (a.h_out) {
+        uint16_t* h = a.h_out + row * a.h_stride;
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            const int vi = u * nt + tid;
+            if (vi < a.nvec) st_v4(h + 8 * vi, v[u]);
+        }
+    }
+
+    // the sum of squares, and max|t| as magnitude bits: an integer maximum, under which
+    // a NaN lies above every number and so marks its row or block
+    float t[VPT][8];
+    Sum2 s = {0.0f, 0.0f};
+    uint32_t m = 0, gm[VPT];
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+        float f[8], c[8];
+        unpack8(v[u], f);
+        unpack8(g[u], c);
+        gm[u] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (TR::mx) sum2_add(s, __fmul_rn(f[i], f[i]), 0.0f);
+            else s.hi = __fmaf_rn(f[i], f[i], s.hi);
+            t[u][i] = __fmul_rn(f[i], c[i]);
+            gm[u] = max(gm[u], __float_as_uint(t[u][i]) & 0x7fffffffu);
+        }
+        m = max(m, gm[u]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float hi = __shfl_xor_sync(kFull, s.hi, o);
+        if constexpr (TR::mx) sum2_add(s, hi, __shfl_xor_sync(kFull, s.lo, o));
+        else s.hi = __fadd_rn(s.hi, hi);
+    }
+    if constexpr (TR::token) m = __reduce_max_sync(kFull, m);
+    if ((tid & 31) == 0) {
+        s_sum[warp] = make_float2(s.hi, s.lo);
+        if constexpr (TR::token) s_max[warp] = m;
+    }
+    __syncthreads();
+    s = Sum2{0.0f, 0.0f};
+    for (int w = 0; w < nwarps; ++w) {
+        if constexpr (TR::mx) sum2_add(s, s_sum[w].x, s_sum[w].y);
+        else s.hi = __fadd_rn(s.hi, s_sum[w].x);
+        if constexpr (TR::token) m = max(m, s_max[w]);
+    }
+    const float n = (float)a.H;
+    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(__fadd_rn(s.hi, s.lo), n), a.eps)));
+    const bool row_ok = finite_bits(__float_as_uint(s.hi) & 0x7fffffffu);
+    const float nan = __uint_as_float(0x7fc00000u);
+    uint8_t* data = a.data + row * a.H;
+
+    if constexpr (TR::token) {
+        const float mf = __uint_as_float(m);
+        const bool ok = row_ok && finite_bits(m);
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            const int vi = u * nt + tid;
+            if (vi < a.nvec) st_v2(data + 8 * vi, ok && m ? encode_ratio<Q>(t[u], mf) : make_uint2(0, 0));
+        }
+        if (tid == 0)
+            reinterpret_cast<float*>(a.scales)[row] =
+                !ok ? nan : m ? __fdiv_rn(__fmul_rn(mf, rstd), TR::dmax) : 0.0f;
+    } else if constexpr (TR::group) {
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            const int vi = u * nt + tid;
+            uint32_t gmax = gm[u];   // 16 consecutive lanes hold a group
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) gmax = max(gmax, __shfl_xor_sync(kFull, gmax, o));
+            const float mf = __uint_as_float(gmax);
+            const bool ok = row_ok && finite_bits(gmax);
+            if (vi < a.nvec) {
+                st_v2(data + 8 * vi, ok && gmax ? encode_ratio<Q>(t[u], mf) : make_uint2(0, 0));
+                if ((vi & 15) == 0)
+                    reinterpret_cast<float*>(a.scales + row * a.scale_bytes)[vi >> 4] =
+                        !ok ? nan : gmax ? __fdiv_rn(__fmul_rn(mf, rstd), TR::dmax) : 0.0f;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            const int vi = u * nt + tid;
+            uint32_t bm = gm[u];   // 4 consecutive lanes hold a block
+            bm = max(bm, __shfl_xor_sync(kFull, bm, 1));
+            bm = max(bm, __shfl_xor_sync(kFull, bm, 2));
+            const float mf = __uint_as_float(bm);
+            const bool ok = row_ok && finite_bits(bm);
+            const uint32_t p = __float_as_uint(__fmul_rn(mf, rstd));
+            int ex = (int)(p >> 23) - 127;
+            const uint32_t frac = p & 0x7fffffu;
+            // Within 2^-17 of a power of two the float32 product may lie on the wrong side of
+            // it; m * r >= 2^k is then decided as m^2 H >= 4^k (sum + H eps) in 64 bits (rare).
+            if (ok && bm && (frac < 64u || frac > 0x7fffffu - 64u) && ex > -120 && ex < 128) {
+                const int k = frac < 64u ? ex : ex + 1;
+                const double lhs = (double)mf * (double)mf * (double)n;
+                const double rhs = ldexp((double)s.hi + (double)s.lo + (double)n * (double)a.eps, 2 * k);
+                ex = lhs >= rhs ? k : k - 1;
+            }
+            int se = (p >> 23) == 0 ? -127 : max(ex - TR::emax, -127);
+            se = min(se, 127);
+            const float mul = __uint_as_float((uint32_t)(127 - se) << 23);   // 2^-se; se = 127 only for values
+                                                                             // that no finite row reaches
+            uint2 c = make_uint2(0, 0);
+            if (ok && bm) {
+                float q[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(__fmul_rn(t[u][i], rstd), mul);
+                c.x = cvt_fp8x2<Q>(q[0], q[1]) | (cvt_fp8x2<Q>(q[2], q[3]) << 16);
+                c.y = cvt_fp8x2<Q>(q[4], q[5]) | (cvt_fp8x2<Q>(q[6], q[7]) << 16);
+            }
+            if (vi < a.nvec) {
+                st_v2(data + 8 * vi, c);
+                if ((vi & 3) == 0)
+                    a.scales[row * a.scale_bytes + (vi >> 2)] = (uint8_t)(!ok ? 255 : bm ? se + 127 : 0);
+            }
+        }
+    }
+}
+
+// The rows as they are, with the dispatch kernels' arithmetic (quant.cuh), so that the
+// codes and scales are those of a fused dispatch bit for bit.
+template <int Q, int VPT>
+__global__ void __launch_bounds__(1024) quant_rows_kernel(const RowQuantArgs a) {
+    using TR = QTraits<Q>;
+    __shared__ uint32_t s_max[32];
+    const int nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, nwarps = nt >> 5;
+    const int64_t row = blockIdx.x;
+    const uint16_t* x = a.x + row * a.x_stride;
+    uint4 v[VPT];
+    uint32_t m = 0;
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+        const int vi = u * nt + tid;
+        v[u] = vi < a.nvec ? ld_nc_v4(x + 8 * vi) : make_uint4(0, 0, 0, 0);
+    }
+    float s = 0.0f;
+    if constexpr (TR::token) {
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) m = max(m, vec_absmax_bits(v[u]));
+        m = __reduce_max_sync(kFull, m);
+        if ((tid & 31) == 0) s_max[warp] = m;
+        __syncthreads();
+        for (int w = 0; w < nwarps; ++w) m = max(m, s_max[w]);
+        s = __fdiv_rn(TR::dmax, bf16_bits_to_float(m));
+        if (tid == 0) reinterpret_cast<float*>(a.scales)[row] = __fdiv_rn(1.0f, s);
+    }
+    uint8_t* data = a.data + row * a.H;
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+        const int vi = u * nt + tid;
+        float f[8], ginv = 0.0f;
+        uint32_t c[2], sbyte = 0;
+        unpack8(v[u], f);
+        encode_vec<Q>(v[u], f, s, m != 0, c, sbyte, ginv);
+        if (vi < a.nvec) {
+            st_v2(data + 8 * vi, make_uint2(c[0], c[1]));
+            if constexpr (TR::group) {
+                if ((vi & 15) == 0) reinterpret_cast<float*>(a.scales + row * a.scale_bytes)[vi >> 4] = ginv;
+            }
+            if constexpr (TR::mx) {
+                if ((vi & 3) == 0) a.scales[row * a.scale_bytes + (vi >> 2)] = (uint8_t)sbyte;
+            }
+        }
+    }
+}
+
+// With fewer rows than SMs a row gets a thread for every vector (the shortest
+// dependent chain); otherwise about 256 threads a row, so that several rows share an SM.
+template <int Q, template <int, int> class K>
+cudaError_t launch_rows(const RowQuantArgs& a, int sms, cudaStream_t st) {
+    const int vpt = a.rows <= sms || a.nvec <= 256 ? 1 : a.nvec <= 512 ? 2 : 4;
+    const int nt = ((a.nvec + vpt - 1) / vpt + 31) / 32 * 32;
+    const dim3 grid((unsigned)a.rows);
+    if (vpt == 1) K<Q, 1>::run(a, grid, nt, st);
+    else if (vpt == 2) K<Q, 2>::run(a, grid, nt, st);
+    else K<Q, 4>::run(a, grid, nt, st);
+    return cudaGetLastError();
+}
+
+template <int Q, int VPT>
+struct NormKernel {
+    static void run(const RowQuantArgs& a, dim3 grid, int nt, cudaStream_t st) {
+        rms_norm_quant_kernel<Q, VPT><<<grid, nt, 0, st>>>(a);
+    }
+};
+
+template <int Q, int VPT>
+struct QuantKernel {
+    static void run(const RowQuantArgs& a, dim3 grid, int nt, cudaStream_t st) {
+        quant_rows_kernel<Q, VPT><<<grid, nt, 0, st>>>(a);
+    }
+};
+
+template <template <int, int> class K>
+cudaError_t launch_mode(const RowQuantArgs& a, int quant, int sms, cudaStream_t st) {
+    switch (quant) {
+        case EP_QUANT_INT8_PER_TOKEN: return launch_rows<M_INT8, K>(a, sms, st);
+        case EP_QUANT_MXFP8_E4M3: return launch_rows<M_E4M3, K>(a, sms, st);
+        case EP_QUANT_MXFP8_E5M2: return launch_rows<M_E5M2, K>(a, sms, st);
+        case EP_QUANT_FP8_E4M3_PER_TOKEN: return launch_rows<M_FP8T_E4M3, K>(a, sms, st);
+        case EP_QUANT_FP8_E5M2_PER_TOKEN: return launch_rows<M_FP8T_E5M2, K>(a, sms, st);
+        case EP_QUANT_FP8_E4M3_PER_GROUP: return launch_rows<M_FP8G_E4M3, K>(a, sms, st);
+        case EP_QUANT_FP8_E5M2_PER_GROUP: return launch_rows<M_FP8G_E5M2, K>(a, sms, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+bool aligned(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
+
+// Checks shared by both entry points; fills the sizes of `a`.
+ep_status check_rows(const void* x, int64_t x_stride, int64_t rows, int32_t hidden, ep_quant_mode q,
+                     const void* data, const void* scales, RowQuantArgs* a) {
+    if (q == EP_QUANT_NONE || q == EP_QUANT_INT8_STATIC || q == EP_QUANT_MXFP4_E2M1) return EP_ERR_UNSUPPORTED;
+    int64_t db = 0, sb = 0;
+    const ep_status s = ep_recv_row_bytes(hidden, q, &db, &sb);
+    if (s != EP_OK) return s;
+    if (hidden > 8192 || rows < 0 || rows > INT32_MAX) return EP_ERR_INVALID_ARG;
+    if (x_stride < hidden || x_stride % 8 != 0) return EP_ERR_INVALID_ARG;
+    if (rows > 0) {
+        if (!x || !data || !scales) return EP_ERR_INVALID_ARG;
+        if (!aligned(x, 16) || !aligned(data, 16) || !aligned(scales, 4)) return EP_ERR_INVALID_ARG;
+    }
+    a->x = (const uint16_t*)x;
+    a->x_stride = x_stride;
+    a->data = (uint8_t*)const_cast<void*>(data);
+    a->scales = (uint8_t*)const_cast<void*>(scales);
+    a->rows = rows;
+    a->H = hidden;
+    a->nvec = hidden / 8;
+    a->scale_bytes = (int32_t)sb;
+    return EP_OK;
+}
+
+}  // namespace
+
+cudaError_t launch_rms_norm_quant(const RowQuantArgs& a, int quant, int sms, cudaStream_t st) {
+    return launch_mode<NormKernel>(a, quant, sms, st);
+}
+
+cudaError_t launch_quant_rows(const RowQuantArgs& a, int quant, int sms, cudaStream_t st) {
+    return launch_mode<QuantKernel>(a, quant, sms, st);
+}
+
+extern "C" ep_status ep_rms_norm_quant(const void* x, int64_t x_stride, const void* residual,
+                                       int64_t residual_stride, const void* gamma, float eps, int64_t rows,
+                                       int32_t hidden, ep_quant_mode quant, void* h_out, int64_t h_stride,
+                                       void* data, void* scales, ep_stream_t stream) {
+    RowQuantArgs a{};
+    const ep_status s = check_rows(x, x_stride, rows, hidden, quant, data, scales, &a);
+    if (s != EP_OK) return s;
+    if (!(eps >= 0.0f) || eps > 3.0e38f) return EP_ERR_INVALID_ARG;
+    if (!gamma || !aligned(gamma, 16)) return EP_ERR_INVALID_ARG;
+    if (residual && (!aligned(residual, 16) || residual_stride < hidden || residual_stride % 8 != 0))
+        return EP_ERR_INVALID_ARG;
+    if (h_out && (!aligned(h_out, 16) || h_stride < hidden || h_stride % 8 != 0)) return EP_ERR_INVALID_ARG;
+    if (rows == 0) return EP_OK;
+    a.residual = (const uint16_t*)residual;
+    a.residual_stride = residual_stride;
+    a.gamma = (const uint16_t*)gamma;
+    a.h_out = (uint16_t*)h_out;
+    a.h_stride = h_stride;
+    a.eps = eps;
+    const int sms = ep_current_sms();
+    if (sms <= 0) return EP_ERR_CUDA;
+    return launch_rms_norm_quant(a, quant, sms, (cudaStream_t)stream) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+}
+
+extern "C" ep_status ep_quant_rows(const void* x, int64_t x_stride, int64_t rows, int32_t hidden,
+                                   ep_quant_mode quant, void* data, void* scales, ep_stream_t stream) {
+    RowQuantArgs a{};
+    const ep_status s = check_rows(x, x_stride, rows, hidden, quant, data, scales, &a);
+    if (s != EP_OK) return s;
+    if (rows == 0) return EP_OK;
+    const int sms = ep_current_sms();
+    if (sms <= 0) return EP_ERR_CUDA;
+    return launch_quant_rows(a, quant, sms, (cudaStream_t)stream) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+}

@@ -112,6 +112,11 @@ def _load():
         "ep_dispatch_wait": ([vp, st, vp, vp, i64, ctypes.c_uint32, vp, vp, i64, vp], st),
         "ep_combine_async": ([vp, vp, i64, vp, i64, vp], st),
         "ep_combine_wait": ([vp, vp, i64, vp, vp, i32, vp, vp], st),
+        "ep_rms_norm_quant": ([vp, i64, vp, i64, vp, ctypes.c_float, i64, i32, st, vp, i64, vp, vp, vp], st),
+        "ep_quant_rows": ([vp, i64, i64, i32, st, vp, vp, vp], st),
+        "ep_moe_few_tokens_workspace_size": ([i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)], st),
+        "ep_moe_few_tokens": ([vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp,
+                               ctypes.c_size_t, vp, vp], st),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -338,6 +343,104 @@ def ep_expert_identity_tokens(h: int, quant: int, recv_data, recv_scales, recv_t
                                           _ptr(recv_topk_idx), _ptr(recv_topk_weights),
                                           int(rows_capacity), int(mark_mod), _ptr(y), _stream(stream)),
            "ep_expert_identity_tokens")
+
+
+# ---------------------------------------------------------------- expert-layer operators
+
+def _require(ok: bool, what: str):
+    if not ok:
+        raise EPError(EP_ERR_INVALID_ARG, what)
+
+
+def _row_stride(t: torch.Tensor, rows: int, hidden: int, what: str) -> int:
+    """Elements between the rows of a bf16 [rows, hidden] tensor whose columns lie together."""
+    _require(t.dtype == torch.bfloat16 and t.dim() == 2 and t.shape[0] == rows and t.shape[1] == hidden
+             and (hidden == 1 or t.stride(1) == 1), what)
+    return t.stride(0) if rows > 1 else hidden
+
+
+def ep_rms_norm_quant(x: torch.Tensor, residual, gamma: torch.Tensor, eps: float, quant: int, h_out,
+                      data: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+    """8-bit rows of RMSNorm(x + residual) * gamma.  x, residual (or None) and h_out (or None: the
+    sum is not kept) are bf16 [rows, H], rows any stride apart; data and scales as of alloc_recv,
+    contiguous, of any type of the same bytes."""
+    _require(x.dim() == 2, "x: [rows, hidden]")
+    rows, hidden = x.shape
+    xs = _row_stride(x, rows, hidden, "x: bf16 [rows, hidden]")
+    rs = 0 if residual is None else _row_stride(residual, rows, hidden, "residual: as x")
+    hs = 0 if h_out is None else _row_stride(h_out, rows, hidden, "h_out: as x")
+    _require(gamma.dtype == torch.bfloat16 and gamma.numel() == hidden and gamma.is_contiguous(),
+             "gamma: bf16 [hidden]")
+    _check_rows_out(quant, rows, hidden, data, scales)
+    _check(_lib.ep_rms_norm_quant(x.data_ptr(), xs, _ptr(residual), rs, gamma.data_ptr(), eps, rows, hidden, quant,
+                                  _ptr(h_out), hs, data.data_ptr(), scales.data_ptr(), _stream(stream)),
+           "ep_rms_norm_quant")
+
+
+# bytes of a row's scales by mode, of one hidden column (0: four bytes a row)
+_SCALE_DIVISOR = {EP_QUANT_INT8_PER_TOKEN: 0, EP_QUANT_FP8_E4M3_PER_TOKEN: 0, EP_QUANT_FP8_E5M2_PER_TOKEN: 0,
+                  EP_QUANT_MXFP8_E4M3: 32, EP_QUANT_MXFP8_E5M2: 32,
+                  EP_QUANT_FP8_E4M3_PER_GROUP: 32, EP_QUANT_FP8_E5M2_PER_GROUP: 32}
+
+
+def _check_rows_out(quant: int, rows: int, hidden: int, data: torch.Tensor, scales: torch.Tensor):
+    per = _SCALE_DIVISOR.get(quant)
+    if per is None:
+        raise EPError(EP_ERR_UNSUPPORTED, "8-bit rows with scales: quant mode")
+    _require(data.is_contiguous() and data.nbytes >= rows * hidden, "data: [rows, hidden] bytes")
+    _require(scales.is_contiguous() and scales.nbytes >= rows * (hidden // per if per else 4),
+             "scales: as of ep_recv_row_bytes")
+
+
+def ep_quant_rows(x: torch.Tensor, quant: int, data: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+    """8-bit rows of bf16 [rows, H] as ep_dispatch encodes them."""
+    _require(x.dim() == 2, "x: [rows, hidden]")
+    rows, hidden = x.shape
+    xs = _row_stride(x, rows, hidden, "x: bf16 [rows, hidden]")
+    _check_rows_out(quant, rows, hidden, data, scales)
+    _check(_lib.ep_quant_rows(x.data_ptr(), xs, rows, hidden, quant, data.data_ptr(), scales.data_ptr(),
+                              _stream(stream)), "ep_quant_rows")
+
+
+def ep_moe_few_tokens_workspace_size(T: int, H: int, E: int, K: int, I: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.ep_moe_few_tokens_workspace_size(T, H, E, K, I, ctypes.byref(n)),
+           "ep_moe_few_tokens_workspace_size")
+    return int(n.value)
+
+
+def ep_moe_few_tokens(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor, w13: torch.Tensor,
+                      w2: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, w13_scales=None,
+                      w2_scales=None, shared=None, status=None, stream=None) -> None:
+    """The expert layer of up to 64 tokens: x [T, H] bf16, topk_idx [T, K] int64, topk_weights [T, K]
+    float32, w13 [E, 2I, H] and w2 [E, H, I] in bf16, or in int8 with float32 row scales w13_scales
+    [E, 2I] and w2_scales [E, H]; shared [S, T, H] bf16 or None; out [T, H] bf16; workspace uint8."""
+    T, H = x.shape
+    E, I = w13.shape[0], w13.shape[1] // 2
+    K = topk_idx.shape[1]
+    wt = torch.bfloat16 if w13_scales is None else torch.int8
+    _require(x.dtype == torch.bfloat16 and x.is_contiguous(), "x: bf16 [T, H]")
+    _require(topk_idx.dtype == torch.int64 and topk_idx.is_contiguous() and topk_idx.shape[0] == T,
+             "topk_idx: int64 [T, K]")
+    _require(topk_weights.dtype == torch.float32 and topk_weights.is_contiguous()
+             and topk_weights.shape == topk_idx.shape, "topk_weights: float32 [T, K]")
+    _require(w13.dtype == wt and w13.is_contiguous() and w13.shape == (E, 2 * I, H), "w13: [E, 2I, H]")
+    _require(w2.dtype == wt and w2.is_contiguous() and w2.shape == (E, H, I), "w2: [E, H, I]")
+    _require((w13_scales is None) == (w2_scales is None), "w13_scales, w2_scales: both or neither")
+    if w13_scales is not None:
+        _require(w13_scales.dtype == torch.float32 and w13_scales.is_contiguous()
+                 and w13_scales.numel() == E * 2 * I, "w13_scales: float32 [E, 2I]")
+        _require(w2_scales.dtype == torch.float32 and w2_scales.is_contiguous()
+                 and w2_scales.numel() == E * H, "w2_scales: float32 [E, H]")
+    S = 0 if shared is None else shared.shape[0]
+    if shared is not None:
+        _require(shared.dtype == torch.bfloat16 and shared.is_contiguous() and shared.shape == (S, T, H),
+                 "shared: bf16 [S, T, H]")
+    _require(out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == (T, H), "out: bf16 [T, H]")
+    _check(_lib.ep_moe_few_tokens(x.data_ptr(), topk_idx.data_ptr(), topk_weights.data_ptr(), T, H, E, K, I,
+                                  w13.data_ptr(), _ptr(w13_scales), w2.data_ptr(), _ptr(w2_scales), _ptr(shared), S,
+                                  out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _ptr(status),
+                                  _stream(stream)), "ep_moe_few_tokens")
 
 
 # ---------------------------------------------------------------- convenience wrapper

@@ -497,6 +497,64 @@ ep_status ep_step_host(ep_handle* handle, ep_quant_mode quant, const int64_t* to
                        int32_t num_shared, void* out_host, const ep_step_buffers* dev,
                        ep_stream_t stream);
 
+/* ---- Expert-layer operators ------------------------------------------------
+ *
+ * What stands before dispatch (a normalised row in 8 bits), between dispatch and
+ * combine (the experts' products), and in place of the whole chain when there are
+ * only a few tokens.  They need no handle; `status`, where given, is a caller-owned
+ * device word that receives the first device-side error (the caller clears it). */
+
+/* Device.  For each of `rows` rows of `hidden` bf16 columns:
+ *   h = bf16(x + residual), or x without a residual;
+ *   y = h * gamma / sqrt(mean(h^2) + eps), in float32;
+ *   data, scales = the codes and scales of y in the receive-row format of `quant`
+ *   (row-major, ep_recv_row_bytes), which ep_dispatch_ex moves unchanged.
+ * quant: EP_QUANT_INT8_PER_TOKEN, the FP8 per-token and per-group modes, or MXFP8
+ * (EP_ERR_UNSUPPORTED otherwise).  Codes are nearest to y / scale, ties to even, with
+ * scale = max|y| / top (top 127, 448 or 57344), or the power of two
+ * 2^(floor(log2 max|y|) - emax) of 32 columns.  The norm is taken of the rounded h, the
+ * row that h_out stores: the result is that of a separate addition.
+ * An all-zero row (or group, or block) has zero codes and scale 0 (MX: byte 0).  A row
+ * with a NaN or an infinity, or whose sum of squares passes the float32 range, and a
+ * group or block whose gamma holds one, gets NaN scales (MX: byte 255) and zero codes.
+ * x, residual (may be NULL) and h_out (may be NULL) have their own strides between
+ * rows, in elements, multiples of 8 and at least `hidden`; x, residual, gamma, h_out and
+ * data are 16-byte aligned, scales 4-byte aligned.  h_out may be x or residual itself
+ * (with its stride).  hidden as for ep_params; eps >= 0. */
+ep_status ep_rms_norm_quant(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                            const void* gamma, float eps, int64_t rows, int32_t hidden, ep_quant_mode quant,
+                            void* h_out, int64_t h_stride, void* data, void* scales, ep_stream_t stream);
+
+/* Device.  The rows of x (bf16, x_stride elements apart) in the receive-row format of
+ * `quant` (the modes of ep_rms_norm_quant), with the arithmetic of ep_dispatch: the same
+ * codes and scales that a fused dispatch of these rows writes. */
+ep_status ep_quant_rows(const void* x, int64_t x_stride, int64_t rows, int32_t hidden, ep_quant_mode quant,
+                        void* data, void* scales, ep_stream_t stream);
+
+/* Host only: bytes of the workspace of ep_moe_few_tokens. */
+ep_status ep_moe_few_tokens_workspace_size(int32_t num_tokens, int32_t hidden, int32_t num_experts, int32_t topk,
+                                           int32_t inner, size_t* bytes);
+
+/* Device.  The whole expert layer for num_tokens <= 64 tokens (more:
+ * EP_ERR_UNSUPPORTED; they take the layout, dispatch and combine path):
+ *   out[t] = sum over k of topk_weights[t,k] * W2[e] (silu(Wg[e] x[t]) * (Wu[e] x[t]))
+ *            + sum over s of shared[s,t],       e = topk_idx[t,k],
+ * products and sums in float32, one rounding to bf16 at the end.  Entries of -1 add
+ * nothing (their weight is not read into the sum); other ids outside [0, E) count as -1
+ * and set EP_ERR_BAD_EXPERT_ID in *status (may be NULL).
+ * x [T, H] bf16; topk_idx [T, K] int64; topk_weights [T, K] float32; w13 [E, 2I, H], the I
+ * rows of Wg and then those of Wu; w2 [E, H, I]; shared [num_shared, T, H] bf16
+ * (num_shared <= 16); out [T, H] bf16.  The weights are bf16, or int8 with a float32 scale
+ * for each row: w13_scales [E, 2I] and w2_scales [E, H] (both or neither).  hidden H in
+ * [8, 8192], inner I in [8, 65536], both multiples of 8 (int8: of 16); E <= 512, K <= 16.
+ * x, w13, w2 and workspace are 16-byte aligned.  The workspace is scratch: calls that may
+ * overlap need their own. */
+ep_status ep_moe_few_tokens(const void* x, const int64_t* topk_idx, const float* topk_weights, int32_t num_tokens,
+                            int32_t hidden, int32_t num_experts, int32_t topk, int32_t inner, const void* w13,
+                            const float* w13_scales, const void* w2, const float* w2_scales, const void* shared,
+                            int32_t num_shared, void* out, void* workspace, size_t workspace_size, int32_t* status,
+                            ep_stream_t stream);
+
 /* ---- Test hook ------------------------------------------------------------ */
 
 /* Device.  For tests of the bounded waits only, never part of the path: runs
