@@ -48,3 +48,80 @@ struct FewArgs {
 };
 
 cudaError_t launch_few_tokens(const FewArgs& a, bool int8_weights, int sms, cudaStream_t st);
+
+struct MatmulArgs {
+    const uint8_t* a;          // [rows][K] int8 token rows
+    const float* a_scales;     // [rows]
+    const uint8_t* w;          // [E][N][K] int8
+    const float* w_scales;     // [E][N]
+    const int32_t* expert_base;  // [E + 1] first row of each expert, or null: all rows belong to one matrix
+    uint16_t* out;             // [rows][N] bf16, or [rows][N / 2] with swiglu
+    int32_t* status;           // or null
+    int64_t rows;              // rows of a and out
+    int32_t K, N, E;
+    int32_t swiglu;
+};
+
+cudaError_t launch_matmul_skinny(const MatmulArgs& a, int sms, cudaStream_t st);
+
+// The segments of a grouped product in shared memory: first row and first token tile of each
+// expert.  Device data is not trusted with addresses: rows are clamped to the buffers'.
+struct Segments {
+    int32_t base[kMaxExperts];
+    int32_t rows[kMaxExperts];
+    int32_t tile[kMaxExperts + 1];   // first token tile of each expert; [E]: all tiles
+    int32_t warp_sum[32];
+};
+
+// All threads of a CTA of NT threads, kMaxExperts <= 2 NT.  False: the segments need more rows than
+// there are (EP_ERR_CAPACITY is set), and nothing may be written.
+template <int NT>
+__device__ __forceinline__ bool load_segments(Segments& s, const MatmulArgs& a, int tile_rows) {
+    static_assert(kMaxExperts <= 2 * NT, "a thread holds two experts");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int tiles[2] = {0, 0};
+    bool fits = true;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int e = 2 * tid + h;
+        if (e >= a.E) continue;
+        int64_t b = 0, end = a.rows;
+        if (a.expert_base) {
+            b = a.expert_base[e];
+            end = a.expert_base[e + 1];
+            fits = fits && end <= a.rows;
+            b = b < 0 ? 0 : b > a.rows ? a.rows : b;
+            end = end < b ? b : end > a.rows ? a.rows : end;
+        }
+        s.base[e] = (int32_t)b;
+        s.rows[e] = (int32_t)(end - b);
+        tiles[h] = (int)((end - b + tile_rows - 1) / tile_rows);
+    }
+    int sum = tiles[0] + tiles[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += n;
+    }
+    if (lane == 31) s.warp_sum[warp] = sum;
+    fits = __syncthreads_and(fits);
+    for (int w = 0; w < warp; ++w) sum += s.warp_sum[w];
+    const int at = sum - tiles[0] - tiles[1];
+    if (2 * tid < a.E) s.tile[2 * tid] = at;
+    if (2 * tid + 1 < a.E) s.tile[2 * tid + 1] = at + tiles[0];
+    if (tid == NT - 1) s.tile[a.E] = sum;
+    if (!fits && tid == 0 && a.status) ep_set_status(a.status, EP_ERR_CAPACITY);
+    __syncthreads();
+    return fits;
+}
+
+// The expert that token tile t belongs to (tiles of empty experts do not exist).
+__device__ __forceinline__ int expert_of_tile(const Segments& s, int E, int t) {
+    int lo = 0, hi = E;   // last e with tile[e] <= t
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s.tile[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}

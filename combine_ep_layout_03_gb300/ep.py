@@ -114,6 +114,7 @@ def _load():
         "ep_combine_wait": ([vp, vp, i64, vp, vp, i32, vp, vp], st),
         "ep_rms_norm_quant": ([vp, i64, vp, i64, vp, ctypes.c_float, i64, i32, st, vp, i64, vp, vp, vp], st),
         "ep_quant_rows": ([vp, i64, i64, i32, st, vp, vp, vp], st),
+        "ep_expert_matmul": ([vp, vp, i64, i32, vp, vp, i32, i32, vp, i32, vp, vp, vp], st),
         "ep_moe_few_tokens_workspace_size": ([i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)], st),
         "ep_moe_few_tokens": ([vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp,
                                ctypes.c_size_t, vp, vp], st),
@@ -402,6 +403,28 @@ def ep_quant_rows(x: torch.Tensor, quant: int, data: torch.Tensor, scales: torch
                               _stream(stream)), "ep_quant_rows")
 
 
+def ep_expert_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, expert_base,
+                     out: torch.Tensor, swiglu: bool = False, status=None, stream=None) -> None:
+    """int8 rows times int8 expert matrices: a [rows, K] with float32 a_scales [rows], w [E, N, K] with
+    w_scales [E, N], expert_base int32 [E + 1] on the device (None: one matrix), out bf16 [rows, N],
+    or [rows, N / 2] = silu(gates) * ups with swiglu.  a and a_scales may be the receive buffers of an
+    int8 dispatch (uint8 of the same bytes)."""
+    _require(a.dim() == 2 and a.element_size() == 1 and a.is_contiguous(), "a: int8 [rows, K]")
+    rows, K = a.shape
+    _require(w.dim() == 3 and w.dtype == torch.int8 and w.is_contiguous() and w.shape[2] == K, "w: int8 [E, N, K]")
+    E, N = w.shape[0], w.shape[1]
+    _require(a_scales.is_contiguous() and a_scales.nbytes == 4 * rows, "a_scales: float32 [rows]")
+    _require(w_scales.dtype == torch.float32 and w_scales.is_contiguous() and w_scales.numel() == E * N,
+             "w_scales: float32 [E, N]")
+    _require((expert_base is None and E == 1) or (expert_base is not None and expert_base.dtype == torch.int32
+             and expert_base.is_contiguous() and expert_base.numel() == E + 1), "expert_base: int32 [E + 1]")
+    _require(out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == (rows, N // 2 if swiglu else N),
+             "out: bf16 [rows, N], or [rows, N / 2] with swiglu")
+    _check(_lib.ep_expert_matmul(a.data_ptr(), a_scales.data_ptr(), rows, K, w.data_ptr(), w_scales.data_ptr(), N, E,
+                                 _ptr(expert_base), 1 if swiglu else 0, out.data_ptr(), _ptr(status),
+                                 _stream(stream)), "ep_expert_matmul")
+
+
 def ep_moe_few_tokens_workspace_size(T: int, H: int, E: int, K: int, I: int) -> int:
     n = ctypes.c_size_t(0)
     _check(_lib.ep_moe_few_tokens_workspace_size(T, H, E, K, I, ctypes.byref(n)),
@@ -485,6 +508,7 @@ class EPLayout:
         v = ep_handle_views(self.h)
         self.recv_src_capacity = v.recv_src_capacity
         self.tok_capacity = v.tok_capacity
+        self._expert_base = None
 
     def __del__(self):
         h = getattr(self, "h", None)
@@ -573,6 +597,17 @@ class EPLayout:
                  (EP_DISPATCH_PRE_ENCODED if pre_encoded else 0))
         ep_dispatch_ex(self.h, x, x_scales, quant, scales, scale_kind, flags, recv_data, recv_scales,
                        recv_data.numel() // db, stream)
+
+    def expert_matmul(self, data: torch.Tensor, scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                      out: torch.Tensor, swiglu: bool = False, stream=None) -> torch.Tensor:
+        """ep_expert_matmul over the segments of this layout; too few rows show in status()."""
+        if self._expert_base is None:
+            v = ep_handle_views(self.h)
+            off = v.expert_base - self.ws.data_ptr()
+            self._expert_base = self.ws[off:off + 4 * (self.E + 1)].view(torch.int32)
+            self._status = self.ws[:4].view(torch.int32)
+        ep_expert_matmul(data, scales, w, w_scales, self._expert_base, out, swiglu, self._status, stream)
+        return out
 
     def combine(self, y: torch.Tensor, topk_weights: torch.Tensor, out: torch.Tensor,
                 shared: torch.Tensor | None = None, stream=None) -> torch.Tensor:

@@ -531,6 +531,22 @@ ep_status ep_rms_norm_quant(const void* x, int64_t x_stride, const void* residua
 ep_status ep_quant_rows(const void* x, int64_t x_stride, int64_t rows, int32_t hidden, ep_quant_mode quant,
                         void* data, void* scales, ep_stream_t stream);
 
+/* Device.  The 8-bit integer product of expert rows: for every row r of expert e's segment
+ * [expert_base[e], expert_base[e+1])
+ *   c[r,n] = a_scales[r] * w_scales[e,n] * sum_k a[r,k] * w[e,n,k],
+ * sums in float32 (exact while they stay within 2^24), rounded once to bf16:
+ *   out [rows, n] = c,  or with swiglu = 1 (n even)  out [rows, n/2] = silu(c[:, :n/2]) * c[:, n/2:].
+ * a [rows, k] int8 with a_scales [rows] are receive rows of EP_QUANT_INT8_PER_TOKEN (padding
+ * rows have scale 0 and give zeros); w [E, n, k] int8 with w_scales [E, n]; expert_base [E+1]
+ * int32 in device memory is the layout's (ep_handle_views), ascending.  `rows` is the capacity
+ * of a and out: rows past expert_base[E] are neither read nor written, and if expert_base asks
+ * for more than `rows`, nothing is written and *status (may be NULL) gets EP_ERR_CAPACITY.
+ * num_experts = 1 with expert_base NULL is a plain matrix product of all rows.
+ * k in [16, 65536], a multiple of 16; n in [1, 65536]; E <= 512; a and w 16-byte aligned. */
+ep_status ep_expert_matmul(const void* a, const float* a_scales, int64_t rows, int32_t k, const void* w,
+                           const float* w_scales, int32_t n, int32_t num_experts, const int32_t* expert_base,
+                           int32_t swiglu, void* out, int32_t* status, ep_stream_t stream);
+
 /* Host only: bytes of the workspace of ep_moe_few_tokens. */
 ep_status ep_moe_few_tokens_workspace_size(int32_t num_tokens, int32_t hidden, int32_t num_experts, int32_t topk,
                                            int32_t inner, size_t* bytes);

@@ -72,6 +72,23 @@ def test_few_tokens_limits():
     assert ep.lib.ep_moe_few_tokens_workspace_size(4, 250, 8, 2, 64, ctypes.byref(n)) == ep.EP_ERR_INVALID_ARG
 
 
+def matmul(a=A, sa=A, rows=100, k=256, w=B, sw=B, n=64, E=8, base=C, swiglu=0, out=D, status=None):
+    return ep.lib.ep_expert_matmul(a, sa, rows, k, w, sw, n, E, base, swiglu, out, status, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(a=None), dict(a=A + 8), dict(sa=None), dict(sa=A + 2), dict(rows=-1), dict(rows=(1 << 31) - 1), dict(k=0),
+    dict(k=8), dict(k=264), dict(k=65552), dict(w=None), dict(w=B + 8), dict(sw=None), dict(sw=B + 1), dict(n=0),
+    dict(n=65537), dict(n=63, swiglu=1), dict(swiglu=2), dict(E=0), dict(E=513), dict(base=None), dict(base=C + 2),
+    dict(out=None), dict(out=D + 1), dict(status=C + 2)])
+def test_matmul_refuses(kw):
+    assert matmul(**kw) == ep.EP_ERR_INVALID_ARG
+
+
+def test_matmul_of_no_rows():
+    assert matmul(rows=0, a=None, sa=None, out=None) == ep.EP_OK
+
+
 def test_binding_refuses_wrong_tensors():
     """Types, shapes and layouts that a pointer does not show."""
     bf, q = torch.bfloat16, ep.EP_QUANT_INT8_PER_TOKEN
@@ -97,4 +114,13 @@ def test_binding_refuses_wrong_tensors():
                     w2_scales=f(3, 64))):
         with pytest.raises(ep.EPError) as e:
             ep.ep_moe_few_tokens(**{**good, **kw}, stream=0)
+        assert e.value.status == ep.EP_ERR_INVALID_ARG
+    mm = dict(a=f(4, 64, dtype=torch.int8), a_scales=f(4), w=f(3, 32, 64, dtype=torch.int8), w_scales=f(3, 32),
+              expert_base=f(4, dtype=torch.int32), out=f(4, 32, dtype=bf))
+    for kw in (dict(a=f(4, 64)), dict(a=f(64, 4, dtype=torch.int8).t()), dict(a_scales=f(3)), dict(w=f(3, 32, 64)),
+               dict(w=f(3, 32, 48, dtype=torch.int8)), dict(w_scales=f(32)), dict(expert_base=None),
+               dict(expert_base=f(3, dtype=torch.int32)), dict(expert_base=f(4, dtype=torch.int64)),
+               dict(out=f(4, 32)), dict(out=f(4, 16, dtype=bf)), dict(swiglu=True)):
+        with pytest.raises(ep.EPError) as e:
+            ep.ep_expert_matmul(**{**mm, **kw}, stream=0)
         assert e.value.status == ep.EP_ERR_INVALID_ARG
