@@ -125,3 +125,6 @@ __device__ __forceinline__ int expert_of_tile(const Segments& s, int E, int t) {
     }
     return lo;
 }
+
+// The tensor-core form for experts with many rows (matmul_tiles.cu).
+cudaError_t launch_matmul_tiles(const MatmulArgs& a, int sms, cudaStream_t st);

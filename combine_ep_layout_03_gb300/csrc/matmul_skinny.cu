@@ -82,6 +82,10 @@ __global__ void __launch_bounds__(kThreads) matmul_skinny_kernel(const MatmulArg
     }
 }
 
+#ifndef EP_MATMUL_TILE_ROWS
+#define EP_MATMUL_TILE_ROWS 64
+#endif
+
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
 
 }  // namespace
@@ -123,5 +127,8 @@ extern "C" ep_status ep_expert_matmul(const void* a, const float* a_scales, int6
     m.swiglu = swiglu;
     const int sms = ep_current_sms();
     if (sms <= 0) return EP_ERR_CUDA;
-    return launch_matmul_skinny(m, sms, (cudaStream_t)stream) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+    const bool tiles = rows > (int64_t)num_experts * EP_MATMUL_TILE_ROWS;
+    const cudaError_t e = tiles ? launch_matmul_tiles(m, sms, (cudaStream_t)stream)
+                                : launch_matmul_skinny(m, sms, (cudaStream_t)stream);
+    return e == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }

@@ -1,0 +1,354 @@
+// matmul_tiles.cu -- the 8-bit integer product of expert rows on the tensor cores:
+//   c[r, n] = a_scales[r] * w_scales[e, n] * sum_k a[r, k] * w[e, n, k]
+//
+// sm_103a has no fast integer tensor path, but every int8 code is a float16 number, a
+// product of two is exact in float32, and sums stay exact up to 2^24.  So the codes are
+// read from memory as the 8 bits they are and become float16 inside the SM, on the way to
+// tcgen05.mma kind::f16.
+//
+// What bounds such a kernel is shared-memory traffic: a code is written by TMA, read, and
+// written and read again in 16 bits, against 128 bytes a clock.  Hence
+//  - pairs of CTAs (cta_group::2): 256 weight rows x up to 192 token rows a tile, each CTA
+//    converting its own 128 weight rows and only half of the token rows;
+//  - weights as the M operand, converted into tensor memory: written once, and neither that
+//    write nor the MMA's read of it touches shared memory;
+//  - tokens as the N operand, whose size an instruction can choose: a segment of few rows
+//    pays for few.
+// For 64 k a CTA moves 52 KB through shared memory (406 clocks) under 384 clocks of MMA
+// with 192 tokens.  Two accumulators of 192 columns and four 64-k stages of weights (32
+// columns each) fill the 512 columns of tensor memory, so a tile's epilogue runs under the
+// next tile's products.
+//
+// Warps: 0 TMA, 1 MMA (of the pair's first CTA), 2 tensor memory, 4-7 epilogue, 8-11 weights
+// to float16, 12-15 tokens to float16.  Every wait is bounded (EP_ERR_TIMEOUT).
+#include <atomic>
+
+#include "expert_ops.cuh"
+#include "tcgen05.cuh"
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kTileTokens = 192;       // token rows of a tile, both CTAs
+constexpr int kHalf = kTileTokens / 2; // token rows that one CTA converts
+constexpr int kRows = 128;             // weight rows of a CTA
+constexpr int kRawK = 128;             // k of a TMA stage (bytes of a row)
+constexpr int kRawStages = 5;
+constexpr int kCvtStages = 4;          // 64-k stages of float16 operands
+constexpr int kRawA = kRows * kRawK, kRawB = kHalf * kRawK, kRaw = kRawA + kRawB;
+constexpr int kCvtB = kHalf * 128;     // bytes: 64 float16 a row
+constexpr uint32_t kColumns = 512, kColA = 2 * kTileTokens;
+constexpr int kSmem = 1024 + kRawStages * kRaw + kCvtStages * kCvtB;
+constexpr int kBoxTokens = 32;         // rows of a token box
+
+static_assert(kColA + kCvtStages * 32 <= kColumns, "tensor memory");
+
+struct Shared {
+    Segments seg;
+    uint64_t raw_full[kRawStages], raw_empty[kRawStages];
+    uint64_t cvt_full[kCvtStages], cvt_empty[kCvtStages];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t drained;
+    uint32_t tmem;
+};
+
+struct Tile { int64_t row0; int expert, m, n, channel; };   // n: MMA columns, channel: tile of output channels
+
+// Tiles of one expert are neighbours, its token tiles fastest: concurrent pairs share weights and tokens in L2.
+__device__ __forceinline__ Tile tile_of(const Segments& s, const MatmulArgs& a, int ctiles, int64_t item) {
+    const int e = expert_of_tile(s, a.E, (int)(item / ctiles));
+    const int tiles = s.tile[e + 1] - s.tile[e];
+    const int local = (int)(item - (int64_t)s.tile[e] * ctiles);
+    const int per = ((s.rows[e] + tiles - 1) / tiles + 31) / 32 * 32;   // equal tiles, not full ones and a rest
+    const int first = local % tiles * per;
+    Tile t;
+    t.expert = e;
+    t.row0 = (int64_t)s.base[e] + first;
+    t.m = min(per, s.rows[e] - first);
+    t.n = (t.m + 31) / 32 * 32;
+    t.channel = local / tiles;
+    return t;
+}
+
+// Two of the bytes of w (each a code + 128) as float16: 0x64xx is 1024 + xx.
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t bytes_to_f16x2(uint32_t w) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(__byte_perm(w, 0x64646464u, SEL)), "r"(0x64806480u));
+    return r;
+}
+
+__device__ __forceinline__ void codes_to_f16(const uint4& v, uint32_t r[8]) {
+    const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r[2 * i] = bytes_to_f16x2<0x4140>(w[i]);
+        r[2 * i + 1] = bytes_to_f16x2<0x4342>(w[i]);
+    }
+}
+
+__device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// A ring position: stage and parity of use i.
+template <int STAGES>
+struct Ring {
+    int stage = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++stage == STAGES) { stage = 0; parity ^= 1; }
+    }
+    __device__ __forceinline__ void back() {
+        if (stage-- == 0) { stage = STAGES - 1; parity ^= 1; }
+    }
+};
+
+// The same answer in all lanes of a warp.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, kMaxPolls));
+}
+
+template <bool GLU>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_w,
+                    const __grid_constant__ CUtensorMap map_a) {
+    extern __shared__ uint8_t dynamic[];
+    __shared__ Shared sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (!load_segments<kThreads>(sh.seg, a, kTileTokens)) return;   // the same answer in both CTAs
+    const uint32_t cta = cluster_rank();
+    uint8_t* raw = dynamic + ((1024 - (smem_addr(dynamic) & 1023)) & 1023);
+    uint8_t* cvt = raw + kRawStages * kRaw;
+    if (tid == 0) {
+        for (int i = 0; i < kRawStages; ++i) { mbar_init(&sh.raw_full[i], 1); mbar_init(&sh.raw_empty[i], 8); }
+        for (int i = 0; i < kCvtStages; ++i) { mbar_init(&sh.cvt_full[i], 16); mbar_init(&sh.cvt_empty[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&sh.acc_full[i], 1); mbar_init(&sh.acc_empty[i], 8); }
+        mbar_init(&sh.drained, 1);
+        mbar_fence_init();
+    }
+    if (warp == 2) tmem_alloc_pair(&sh.tmem, kColumns);
+    tmem_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tmem_fence_after();
+    const uint32_t tmem = sh.tmem;
+
+    const int outs = GLU ? a.N / 2 : a.N;
+    const int per_pair = GLU ? kRows : 2 * kRows;   // output channels of a tile
+    const int ctiles = (outs + per_pair - 1) / per_pair;
+    const int64_t items = (int64_t)sh.seg.tile[a.E] * ctiles;
+    const int64_t first_item = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int steps = (a.K + 63) / 64, raws = (a.K + kRawK - 1) / kRawK;
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            Ring<kRawStages> r;
+            int used = 0;   // stages armed so far, at most kRawStages
+            for (int64_t item = first_item; ok && item < items; item += step) {
+                const Tile t = tile_of(sh.seg, a, ctiles, item);
+                const int half = t.n / 2, boxes = (half + kBoxTokens - 1) / kBoxTokens;
+                const int wrow = t.expert * a.N + t.channel * per_pair + (int)cta * (GLU ? kRows / 2 : kRows);
+                const int trow = (int)t.row0 + (int)cta * half;
+                for (int k = 0; ok && k < raws; ++k, r.next()) {
+                    if (!mbar_wait(&sh.raw_empty[r.stage], r.parity ^ 1, kMaxPolls)) { ok = false; break; }
+                    uint8_t* dst = raw + r.stage * kRaw;
+                    uint64_t* bar = &sh.raw_full[r.stage];
+                    mbar_arrive_expect_tx(bar, kRawA + boxes * kBoxTokens * kRawK);
+                    if (GLU) {
+                        // 16 gates and their 16 ups in each 32 lanes
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            tma_load_2d(dst + (2 * w) * 16 * kRawK, &map_w, k * kRawK, wrow + 16 * w, bar);
+                            tma_load_2d(dst + (2 * w + 1) * 16 * kRawK, &map_w, k * kRawK, wrow + outs + 16 * w, bar);
+                        }
+                    } else {
+                        tma_load_2d(dst, &map_w, k * kRawK, wrow, bar);
+                    }
+                    for (int b = 0; b < boxes; ++b)
+                        tma_load_2d(dst + kRawA + b * kBoxTokens * kRawK, &map_a, k * kRawK, trow + b * kBoxTokens, bar);
+                    used = min(used + 1, kRawStages);
+                }
+            }
+            // copies in flight end before the CTA does, also when a wait gave up
+            for (int i = 0; i < used; ++i) {
+                r.back();
+                ok = mbar_wait(&sh.raw_full[r.stage], r.parity, kMaxPolls) && ok;
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && cta == 0) {
+            Ring<kCvtStages> c;
+            Ring<2> acc;
+            for (int64_t item = first_item; ok && item < items; item += step, acc.next()) {
+                const Tile t = tile_of(sh.seg, a, ctiles, item);
+                const uint32_t idesc = mma_desc_f16(2 * kRows, t.n);
+                if (!mbar_wait_cluster(&sh.acc_empty[acc.stage], acc.parity ^ 1, kMaxPolls)) { ok = false; break; }
+                tmem_fence_after();
+                const uint32_t d = tmem + acc.stage * kTileTokens;
+                for (int k = 0; k < steps; ++k, c.next()) {
+                    if (!mbar_wait_cluster(&sh.cvt_full[c.stage], c.parity, kMaxPolls)) { ok = false; break; }
+                    tmem_fence_after();
+                    const uint32_t at = tmem + kColA + c.stage * 32;
+                    const uint64_t b = smem_desc_k128(smem_addr(cvt + c.stage * kCvtB));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma_pair_f16(d, at + 8 * j, b + 2 * j, idesc, k > 0 || j > 0);
+                    commit_pair(&sh.cvt_empty[c.stage]);
+                }
+                if (ok) commit_pair(&sh.acc_full[acc.stage]);
+            }
+            commit_leader(&sh.drained);   // no MMA is left when the CTAs part, also when a wait gave up
+            ok = mbar_wait(&sh.drained, 0, kMaxPolls) && ok;
+        }
+    } else if (warp >= 8) {
+        const bool weights = warp < 12;
+        const int w = warp & 3;
+        const uint32_t cvt_full0 = cluster_addr(smem_addr(&sh.cvt_full[0]), 0);
+        Ring<kRawStages> r;
+        Ring<kCvtStages> c;
+        int used = 0;   // stages handed over, at most kCvtStages
+        for (int64_t item = first_item; ok && item < items; item += step) {
+            const int groups = weights ? 0 : tile_of(sh.seg, a, ctiles, item).n / 16;   // of eight token rows
+            for (int k = 0; ok && k < raws; ++k, r.next()) {
+                if (!warp_wait(&sh.raw_full[r.stage], r.parity)) { ok = false; break; }
+                const uint8_t* src = raw + r.stage * kRaw;
+                for (int h = 0; h < 2 && 2 * k + h < steps; ++h, c.next()) {
+                    if (weights) {
+                        // a thread per weight row (tensor-memory lane): 64 codes, 32 columns
+                        const uint8_t* row = src + (w * 32 + lane) * kRawK;
+                        uint32_t v[32];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            codes_to_f16(lds_v4(row + (((4 * h + q) ^ (lane & 7)) * 16)), v + 8 * q);
+                        if (!warp_wait(&sh.cvt_empty[c.stage], c.parity ^ 1)) { ok = false; break; }
+                        tmem_fence_after();
+                        tmem_store32(tmem + ((uint32_t)(w * 32) << 16) + kColA + c.stage * 32, v);
+                        tmem_wait_stores();
+                        tmem_fence_before();
+                    } else {
+                        // a lane per 16 codes: eight rows and four chunks a warp, free of bank conflicts
+                        if (!warp_wait(&sh.cvt_empty[c.stage], c.parity ^ 1)) { ok = false; break; }
+                        const uint32_t dst = smem_addr(cvt + c.stage * kCvtB);
+                        const int rr = lane & 7, q = lane >> 3;
+                        for (int g = w; g < groups; g += 4) {
+                            uint32_t v[8];
+                            codes_to_f16(lds_v4(src + kRawA + (g * 8 + rr) * kRawK + (((4 * h + q) ^ rr) * 16)), v);
+                            const uint32_t row = dst + (g * 8 + rr) * 128;
+                            sts_v4(row + (((2 * q) ^ rr) * 16), v[0], v[1], v[2], v[3]);
+                            sts_v4(row + (((2 * q + 1) ^ rr) * 16), v[4], v[5], v[6], v[7]);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(cvt_full0 + c.stage * 8);
+                    used = min(used + 1, kCvtStages);
+                }
+                if (!ok) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.raw_empty[r.stage]);
+            }
+        }
+        // the commits that free the last stages reach this CTA before it ends
+        for (int i = 0; ok && i < used; ++i) {
+            c.back();
+            ok = warp_wait(&sh.cvt_empty[c.stage], c.parity);
+        }
+    } else if (warp >= 4) {
+        const int w = warp & 3;
+        const uint32_t acc_empty0 = cluster_addr(smem_addr(&sh.acc_empty[0]), 0);
+        Ring<2> acc;
+        for (int64_t item = first_item; item < items; item += step, acc.next()) {
+            const Tile t = tile_of(sh.seg, a, ctiles, item);
+            // lane: an output channel; with gates and ups, lanes 0-15 hold the gates of lanes 16-31's ups
+            const int ch = t.channel * per_pair + (int)cta * (GLU ? kRows / 2 : kRows) + w * (GLU ? 16 : 32) +
+                           (GLU ? lane & 15 : lane);
+            const bool in = ch < outs;
+            const float* sw = a.w_scales + (int64_t)t.expert * a.N + (in ? ch : 0);
+            const float s0 = sw[0], s1 = GLU ? sw[outs] : 0.0f;
+            if (!warp_wait(&sh.acc_full[acc.stage], acc.parity)) { ok = false; break; }
+            tmem_fence_after();
+            const uint32_t d = tmem + ((uint32_t)(w * 32) << 16) + acc.stage * kTileTokens;
+            for (int c0 = 0; c0 < t.m; c0 += 32) {
+                uint32_t v[32];
+                tmem_load32(d + c0, v);
+                const float sa = c0 + lane < t.m ? a.a_scales[t.row0 + c0 + lane] : 0.0f;
+                uint16_t* out = a.out + (t.row0 + c0) * outs + ch;
+                if (GLU) {
+                    const int odd = lane >> 4;   // lanes 0-15 finish the even tokens, lanes 16-31 the odd ones
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(odd ? v[i] : v[i + 1]), 16);
+                        const float s = __shfl_sync(0xffffffffu, sa, i + odd);
+                        const float gate = (odd ? other : __uint_as_float(v[i])) * s * s0;
+                        const float up = (odd ? __uint_as_float(v[i + 1]) : other) * s * s1;
+                        const float y = gate / (1.0f + expf(-gate)) * up;
+                        if (in && c0 + i + odd < t.m)
+                            out[(int64_t)(i + odd) * outs] = (uint16_t)pack_bf16x2_rn(y, 0.0f);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float y = __uint_as_float(v[i]) * __shfl_sync(0xffffffffu, sa, i) * s0;
+                        if (in && c0 + i < t.m) out[(int64_t)i * outs] = (uint16_t)pack_bf16x2_rn(y, 0.0f);
+                    }
+                }
+            }
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acc_empty0 + acc.stage * 8);
+        }
+    }
+    if (!ok && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    cluster_sync();   // neither CTA's shared or tensor memory goes while the pair's MMAs may read it
+    if (warp == 2) tmem_free_pair(tmem, kColumns);
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static std::atomic<void*> entry{nullptr};
+    void* p = entry.load(std::memory_order_relaxed);
+    if (!p) {
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess || found != cudaDriverEntryPointSuccess)
+            return nullptr;
+        entry.store(p, std::memory_order_relaxed);
+    }
+    return (EncodeTiled)p;
+}
+
+// Rows of `bytes` codes as boxes of 128 bytes x box_rows, 128-byte swizzle; zeros outside.
+bool make_map(EncodeTiled enc, CUtensorMap* map, const void* p, int64_t rows, int64_t bytes, int box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)bytes};
+    const cuuint32_t box[2] = {kRawK, (cuuint32_t)box_rows}, unit[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, box, unit,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t launch_matmul_tiles(const MatmulArgs& a, int sms, cudaStream_t st) {
+    EncodeTiled enc = encode_tiled();
+    if (!enc) return cudaErrorNotSupported;
+    CUtensorMap map_w, map_a;
+    if (!make_map(enc, &map_w, a.w, (int64_t)a.E * a.N, a.K, a.swiglu ? 16 : kRows) ||
+        !make_map(enc, &map_a, a.a, a.rows, a.K, kBoxTokens))
+        return cudaErrorInvalidValue;
+    const int64_t per_pair = a.swiglu ? kRows : 2 * kRows, outs = a.swiglu ? a.N / 2 : a.N;
+    const int64_t most = ((a.rows + kTileTokens - 1) / kTileTokens + (a.E > 1 ? a.E : 0)) * ((outs + per_pair - 1) / per_pair);
+    const int64_t pairs = most < sms / 2 ? most : sms / 2;
+    auto kernel = a.swiglu ? matmul_tiles_kernel<true> : matmul_tiles_kernel<false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)(2 * pairs), kThreads, kSmem, st>>>(a, map_w, map_a);
+    return cudaGetLastError();
+}
