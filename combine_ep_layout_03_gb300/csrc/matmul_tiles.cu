@@ -19,8 +19,9 @@
 // columns each) fill the 512 columns of tensor memory, so a tile's epilogue runs under the
 // next tile's products.
 //
-// Warps: 0 TMA, 1 MMA (of the pair's first CTA), 2 tensor memory, 4-7 epilogue, 8-11 weights
-// to float16, 12-15 tokens to float16.  Every wait is bounded (EP_ERR_TIMEOUT).
+// Warps: 0 TMA, 1 MMA (of the pair's first CTA), 2 tensor memory, 4-7 epilogue, 8-15 weights
+// to float16 (8-11 the first 64 k of a TMA stage, 12-15 the second), 16-23 tokens likewise: one
+// step of a warp, from its wait to its arrival, takes longer than the MMAs of 64 k.  Every wait is bounded (EP_ERR_TIMEOUT).
 #include <atomic>
 
 #include "expert_ops.cuh"
@@ -28,7 +29,7 @@
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 768;
 constexpr int kTileTokens = 192;       // token rows of a tile, both CTAs
 constexpr int kHalf = kTileTokens / 2; // token rows that one CTA converts
 constexpr int kRows = 128;             // weight rows of a CTA
@@ -121,7 +122,7 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
     uint8_t* raw = dynamic + ((1024 - (smem_addr(dynamic) & 1023)) & 1023);
     uint8_t* cvt = raw + kRawStages * kRaw;
     if (tid == 0) {
-        for (int i = 0; i < kRawStages; ++i) { mbar_init(&sh.raw_full[i], 1); mbar_init(&sh.raw_empty[i], 8); }
+        for (int i = 0; i < kRawStages; ++i) { mbar_init(&sh.raw_full[i], 1); mbar_init(&sh.raw_empty[i], 16); }
         for (int i = 0; i < kCvtStages; ++i) { mbar_init(&sh.cvt_full[i], 16); mbar_init(&sh.cvt_empty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&sh.acc_full[i], 1); mbar_init(&sh.acc_empty[i], 8); }
         mbar_init(&sh.drained, 1);
@@ -178,32 +179,46 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && cta == 0) {
+        // The whole warp walks the loop and one elected lane issues, so that descriptors stay in
+        // uniform registers.  Whether the next stage is full is asked before the MMAs of this
+        // one are issued: the answer takes longer than they do.
+        if (cta == 0) {
             Ring<kCvtStages> c;
             Ring<2> acc;
+            const uint32_t cvt0 = smem_addr(cvt);
+            bool ready = false;
             for (int64_t item = first_item; ok && item < items; item += step, acc.next()) {
                 const Tile t = tile_of(sh.seg, a, ctiles, item);
                 const uint32_t idesc = mma_desc_f16(2 * kRows, t.n);
-                if (!mbar_wait_cluster(&sh.acc_empty[acc.stage], acc.parity ^ 1, kMaxPolls)) { ok = false; break; }
+                if (!warp_wait(&sh.acc_empty[acc.stage], acc.parity ^ 1)) { ok = false; break; }
                 tmem_fence_after();
                 const uint32_t d = tmem + acc.stage * kTileTokens;
-                for (int k = 0; k < steps; ++k, c.next()) {
-                    if (!mbar_wait_cluster(&sh.cvt_full[c.stage], c.parity, kMaxPolls)) { ok = false; break; }
+                for (int k = 0; k < steps; ++k) {
+                    if (!ready && !warp_wait(&sh.cvt_full[c.stage], c.parity)) { ok = false; break; }
                     tmem_fence_after();
                     const uint32_t at = tmem + kColA + c.stage * 32;
-                    const uint64_t b = smem_desc_k128(smem_addr(cvt + c.stage * kCvtB));
+                    const uint64_t b = smem_desc_k128(cvt0 + c.stage * kCvtB);
+                    uint64_t* const empty = &sh.cvt_empty[c.stage];
+                    c.next();
+                    ready = __all_sync(0xffffffffu, mbar_try_wait(&sh.cvt_full[c.stage], c.parity));
+                    if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) mma_pair_f16(d, at + 8 * j, b + 2 * j, idesc, k > 0 || j > 0);
-                    commit_pair(&sh.cvt_empty[c.stage]);
+                        for (int j = 0; j < 4; ++j) mma_pair_f16(d, at + 8 * j, b + 2 * j, idesc, k > 0 || j > 0);
+                        commit_pair(empty);
+                    }
+                    __syncwarp();
                 }
-                if (ok) commit_pair(&sh.acc_full[acc.stage]);
+                if (ok && elect_one()) commit_pair(&sh.acc_full[acc.stage]);
+                __syncwarp();
             }
-            commit_leader(&sh.drained);   // no MMA is left when the CTAs part, also when a wait gave up
-            ok = mbar_wait(&sh.drained, 0, kMaxPolls) && ok;
+            // no MMA is left when the CTAs part, also when a wait gave up
+            if (elect_one()) commit_leader(&sh.drained);
+            __syncwarp();
+            ok = warp_wait(&sh.drained, 0) && ok;
         }
     } else if (warp >= 8) {
-        const bool weights = warp < 12;
-        const int w = warp & 3;
+        const bool weights = warp < 16;
+        const int w = warp & 3, mine = (warp >> 2) & 1;
         const uint32_t cvt_full0 = cluster_addr(smem_addr(&sh.cvt_full[0]), 0);
         Ring<kRawStages> r;
         Ring<kCvtStages> c;
@@ -214,6 +229,8 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
                 if (!warp_wait(&sh.raw_full[r.stage], r.parity)) { ok = false; break; }
                 const uint8_t* src = raw + r.stage * kRaw;
                 for (int h = 0; h < 2 && 2 * k + h < steps; ++h, c.next()) {
+                    used = min(used + 1, kCvtStages);
+                    if (h != mine) continue;
                     if (weights) {
                         // a thread per weight row (tensor-memory lane): 64 codes, 32 columns
                         const uint8_t* row = src + (w * 32 + lane) * kRawK;
@@ -242,7 +259,6 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(cvt_full0 + c.stage * 8);
-                    used = min(used + 1, kCvtStages);
                 }
                 if (!ok) break;
                 __syncwarp();
