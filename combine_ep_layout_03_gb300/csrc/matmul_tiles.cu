@@ -107,7 +107,7 @@ struct Ring {
 
 // The same answer in all lanes of a warp.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, kMaxPolls));
+    return __all_sync(0xffffffffu, mbar_wait_parked(bar, parity));
 }
 
 template <bool GLU>
@@ -153,7 +153,7 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
                 const int wrow = t.expert * a.N + t.channel * per_pair + (int)cta * (GLU ? kRows / 2 : kRows);
                 const int trow = (int)t.row0 + (int)cta * half;
                 for (int k = 0; ok && k < raws; ++k, r.next()) {
-                    if (!mbar_wait(&sh.raw_empty[r.stage], r.parity ^ 1, kMaxPolls)) { ok = false; break; }
+                    if (!mbar_wait_parked(&sh.raw_empty[r.stage], r.parity ^ 1)) { ok = false; break; }
                     uint8_t* dst = raw + r.stage * kRaw;
                     uint64_t* bar = &sh.raw_full[r.stage];
                     mbar_arrive_expect_tx(bar, kRawA + boxes * kBoxTokens * kRawK);
@@ -175,7 +175,7 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
             // copies in flight end before the CTA does, also when a wait gave up
             for (int i = 0; i < used; ++i) {
                 r.back();
-                ok = mbar_wait(&sh.raw_full[r.stage], r.parity, kMaxPolls) && ok;
+                ok = mbar_wait_parked(&sh.raw_full[r.stage], r.parity) && ok;
             }
         }
     } else if (warp == 1) {
@@ -224,7 +224,7 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
         Ring<kCvtStages> c;
         int used = 0;   // stages handed over, at most kCvtStages
         for (int64_t item = first_item; ok && item < items; item += step) {
-            const int groups = weights ? 0 : tile_of(sh.seg, a, ctiles, item).n / 16;   // of eight token rows
+            const int half = weights ? 0 : tile_of(sh.seg, a, ctiles, item).n / 2;
             for (int k = 0; ok && k < raws; ++k, r.next()) {
                 if (!warp_wait(&sh.raw_full[r.stage], r.parity)) { ok = false; break; }
                 const uint8_t* src = raw + r.stage * kRaw;
@@ -245,15 +245,23 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
                         tmem_fence_before();
                     } else {
                         // a lane per 16 codes: eight rows and four chunks a warp, free of bank conflicts
-                        if (!warp_wait(&sh.cvt_empty[c.stage], c.parity ^ 1)) { ok = false; break; }
                         const uint32_t dst = smem_addr(cvt + c.stage * kCvtB);
                         const int rr = lane & 7, q = lane >> 3;
-                        for (int g = w; g < groups; g += 4) {
+                        uint4 in[kHalf / 32];
+                        const uint8_t* from = src + kRawA + (w * 8 + rr) * kRawK + (((4 * h + q) ^ rr) * 16);
+#pragma unroll
+                        for (int g = 0; g < kHalf / 32; ++g)   // rows past the tile's hold anything, and nothing reads them
+                            in[g] = lds_v4(from + g * 32 * kRawK);
+                        if (!warp_wait(&sh.cvt_empty[c.stage], c.parity ^ 1)) { ok = false; break; }
+                        const uint32_t row = dst + (w * 8 + rr) * 128;
+                        const uint32_t c0 = row + (((2 * q) ^ rr) * 16), c1 = row + (((2 * q + 1) ^ rr) * 16);
+#pragma unroll
+                        for (int g = 0; g < kHalf / 32; ++g) {
+                            if (g * 32 + w * 8 >= half) break;
                             uint32_t v[8];
-                            codes_to_f16(lds_v4(src + kRawA + (g * 8 + rr) * kRawK + (((4 * h + q) ^ rr) * 16)), v);
-                            const uint32_t row = dst + (g * 8 + rr) * 128;
-                            sts_v4(row + (((2 * q) ^ rr) * 16), v[0], v[1], v[2], v[3]);
-                            sts_v4(row + (((2 * q + 1) ^ rr) * 16), v[4], v[5], v[6], v[7]);
+                            codes_to_f16(in[g], v);
+                            sts_v4(c0 + g * 32 * 128, v[0], v[1], v[2], v[3]);
+                            sts_v4(c1 + g * 32 * 128, v[4], v[5], v[6], v[7]);
                         }
                         fence_proxy_async_smem();
                     }

@@ -33,6 +33,28 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
 }
 
+// Bounded wait of a kernel whose warps share an SM's issue slots with the ones they wait for:
+// each poll may park the thread for up to 20 us, since short polls of a dozen warps took a third
+// of the slots.  Gives up after about four seconds.
+__device__ __forceinline__ bool mbar_wait_parked(uint64_t* bar, uint32_t parity) {
+    uint64_t start = 0;
+    for (uint32_t i = 0; i < kMaxPolls; ++i) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity), "r"(20000u) : "memory");
+        if (ok) return true;
+        if ((i & 63u) == 63u) {
+            uint64_t now;
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+            if (start == 0) start = now;
+            else if (now - start > 4000000000ull) return false;
+        }
+    }
+    return false;
+}
+
 // One lane of a converged warp, the same one each time.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
