@@ -88,7 +88,14 @@ __device__ __forceinline__ void codes_to_f16(const uint4& v, uint32_t r[8]) {
     }
 }
 
-__device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+__device__ __forceinline__ uint4 lds_at(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ void sts_at(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
@@ -105,9 +112,232 @@ struct Ring {
     }
 };
 
-// The same answer in all lanes of a warp.
+// A warp's wait, the same answer in all lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_parked(bar, parity));
+}
+
+// What every role of a CTA knows.
+struct Work {
+    const MatmulArgs& a;
+    Shared& sh;
+    uint8_t* raw;    // TMA stages: 128 weight rows, then up to 96 token rows, of 128 codes
+    uint8_t* cvt;    // float16 token rows of 64 k
+    uint32_t tmem, cta;
+    int outs, per_pair, ctiles, raws;
+    int64_t first, items, step;
+};
+
+template <bool GLU>
+__device__ __forceinline__ bool load_tiles(const Work& w, const CUtensorMap* map_w, const CUtensorMap* map_a) {
+    Ring<kRawStages> r;
+    int used = 0;   // stages armed so far, at most kRawStages
+    bool ok = true;
+    for (int64_t item = w.first; ok && item < w.items; item += w.step) {
+        const Tile t = tile_of(w.sh.seg, w.a, w.ctiles, item);
+        const int half = t.n / 2, boxes = (half + kBoxTokens - 1) / kBoxTokens;
+        const int wrow = t.expert * w.a.N + t.channel * w.per_pair + (int)w.cta * (GLU ? kRows / 2 : kRows);
+        const int trow = (int)t.row0 + (int)w.cta * half;
+        for (int k = 0; k < w.raws; ++k, r.next()) {
+            if (!mbar_wait_parked(&w.sh.raw_empty[r.stage], r.parity ^ 1)) { ok = false; break; }
+            uint8_t* dst = w.raw + r.stage * kRaw;
+            uint64_t* bar = &w.sh.raw_full[r.stage];
+            mbar_arrive_expect_tx(bar, kRawA + boxes * kBoxTokens * kRawK);
+            if (GLU) {
+                // 16 gates and their 16 ups in each 32 lanes
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    tma_load_2d(dst + (2 * i) * 16 * kRawK, map_w, k * kRawK, wrow + 16 * i, bar);
+                    tma_load_2d(dst + (2 * i + 1) * 16 * kRawK, map_w, k * kRawK, wrow + w.outs + 16 * i, bar);
+                }
+            } else {
+                tma_load_2d(dst, map_w, k * kRawK, wrow, bar);
+            }
+            for (int b = 0; b < boxes; ++b)
+                tma_load_2d(dst + kRawA + b * kBoxTokens * kRawK, map_a, k * kRawK, trow + b * kBoxTokens, bar);
+            used = min(used + 1, kRawStages);
+        }
+    }
+    // copies in flight end before the CTA does, also when a wait gave up
+    for (int i = 0; i < used; ++i) {
+        r.back();
+        ok = mbar_wait_parked(&w.sh.raw_full[r.stage], r.parity) && ok;
+    }
+    return ok;
+}
+
+// The whole warp walks the loop and one elected lane issues, so that descriptors stay in uniform
+// registers.  Whether the next stage is full is asked before the MMAs of this one are issued:
+// the answer takes longer than they do.
+__device__ __forceinline__ bool issue_mma(const Work& w) {
+    Ring<kCvtStages> c;
+    Ring<2> acc;
+    const uint32_t cvt0 = smem_addr(w.cvt);
+    bool ready = false, ok = true;
+    for (int64_t item = w.first; ok && item < w.items; item += w.step, acc.next()) {
+        const Tile t = tile_of(w.sh.seg, w.a, w.ctiles, item);
+        const uint32_t idesc = mma_desc_f16(2 * kRows, t.n);
+        if (!warp_wait(&w.sh.acc_empty[acc.stage], acc.parity ^ 1)) { ok = false; break; }
+        tmem_fence_after();
+        const uint32_t d = w.tmem + acc.stage * kTileTokens;
+        for (int k = 0; k < 2 * w.raws; ++k) {
+            if (!ready && !warp_wait(&w.sh.cvt_full[c.stage], c.parity)) { ok = false; break; }
+            tmem_fence_after();
+            const uint32_t at = w.tmem + kColA + c.stage * 32;
+            const uint64_t b = smem_desc_k128(cvt0 + c.stage * kCvtB);
+            uint64_t* const empty = &w.sh.cvt_empty[c.stage];
+            c.next();
+            ready = __all_sync(0xffffffffu, mbar_try_wait(&w.sh.cvt_full[c.stage], c.parity));
+            if (elect_one()) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mma_pair_f16(d, at + 8 * j, b + 2 * j, idesc, k > 0 || j > 0);
+                commit_pair(empty);
+            }
+            __syncwarp();
+        }
+        if (ok && elect_one()) commit_pair(&w.sh.acc_full[acc.stage]);
+        __syncwarp();
+    }
+    // no MMA is left when the CTAs part, also when a wait gave up
+    if (elect_one()) commit_leader(&w.sh.drained);
+    __syncwarp();
+    return warp_wait(&w.sh.drained, 0) && ok;
+}
+
+// Four warps turn the weights (WEIGHTS) or the tokens of half a TMA stage (64 k) into float16;
+// `half` 0 or 1.  A stage has two converted stages, so half h uses stages h and h + 2 in turn.
+template <bool WEIGHTS>
+__device__ __forceinline__ bool convert(const Work& w, int warp, int half) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t full0 = cluster_addr(smem_addr(&w.sh.cvt_full[half]), 0);
+    const uint32_t raw0 = smem_addr(w.raw);
+    const int rr = lane & 7, q = lane >> 3;
+    // weights: a thread per row (tensor-memory lane), its four chunks of 16 codes where the swizzle put them;
+    // tokens: a lane per chunk, eight rows and four chunks a warp, free of bank conflicts
+    uint32_t from[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        from[i] = WEIGHTS ? raw0 + (warp * 32 + lane) * kRawK + (((4 * half + i) ^ rr) * 16)
+                          : raw0 + kRawA + (warp * 8 + rr) * kRawK + (((4 * half + q) ^ rr) * 16) + i * 32 * kRawK;
+    const uint32_t to0 = smem_addr(w.cvt) + half * kCvtB + (warp * 8 + rr) * 128 + (((2 * q) ^ rr) * 16);
+    const uint32_t to1 = smem_addr(w.cvt) + half * kCvtB + (warp * 8 + rr) * 128 + (((2 * q + 1) ^ rr) * 16);
+    const uint32_t col = w.tmem + ((uint32_t)(warp * 32) << 16) + kColA + half * 32;
+    Ring<kRawStages> r;
+    Ring<2> c;   // converted stage half + 2 * c.stage
+    static_assert(kCvtStages == 4, "two halves, two stages each");
+    int64_t uses = 0;
+    bool ok = true;
+    for (int64_t item = w.first; ok && item < w.items; item += w.step) {
+        const int rows = WEIGHTS ? 0 : tile_of(w.sh.seg, w.a, w.ctiles, item).n / 2 - warp * 8;
+        uses += w.raws;
+        for (int k = 0; k < w.raws; ++k, r.next(), c.next()) {
+            if (!warp_wait(&w.sh.raw_full[r.stage], r.parity)) { ok = false; break; }
+            const uint32_t at = r.stage * kRaw;
+            uint64_t* const empty = &w.sh.cvt_empty[half + 2 * c.stage];
+            if (WEIGHTS) {
+                uint32_t v[32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) codes_to_f16(lds_at(from[i] + at), v + 8 * i);
+                if (!warp_wait(empty, c.parity ^ 1)) { ok = false; break; }
+                tmem_fence_after();
+                tmem_store32(col + c.stage * 64, v);
+                tmem_wait_stores();
+                tmem_fence_before();
+            } else {
+                uint4 in[kHalf / 32];
+#pragma unroll
+                for (int g = 0; g < kHalf / 32; ++g) in[g] = lds_at(from[g] + at);   // rows past the tile's are not used
+                if (!warp_wait(empty, c.parity ^ 1)) { ok = false; break; }
+                const uint32_t to = c.stage * 2 * kCvtB;
+#pragma unroll
+                for (int g = 0; g < kHalf / 32; ++g) {
+                    if (g * 32 >= rows) break;
+                    uint32_t v[8];
+                    codes_to_f16(in[g], v);
+                    sts_at(to0 + to + g * 32 * 128, v[0], v[1], v[2], v[3]);
+                    sts_at(to1 + to + g * 32 * 128, v[4], v[5], v[6], v[7]);
+                }
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive_cluster(full0 + c.stage * 16);
+                mbar_arrive(&w.sh.raw_empty[r.stage]);
+            }
+        }
+    }
+    // the commits that free the last stages reach this CTA before it ends
+    for (int i = 0; ok && i < 2 && i < uses; ++i) {
+        c.back();
+        ok = warp_wait(&w.sh.cvt_empty[half + 2 * c.stage], c.parity);
+    }
+    return ok;
+}
+
+// Lane: an output channel; with gates and ups, lanes 0-15 hold the gates of lanes 16-31's ups.
+template <bool GLU>
+__device__ __forceinline__ bool epilogue(const Work& w, int warp, float* scales) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t acc_empty0 = cluster_addr(smem_addr(&w.sh.acc_empty[0]), 0);
+    const int64_t outs = w.outs;
+    // two channels a store where rows keep them on four bytes
+    const bool wide = (outs & 1) == 0 && ((uintptr_t)w.a.out & 3) == 0;
+    Ring<2> acc;
+    for (int64_t item = w.first; item < w.items; item += w.step, acc.next()) {
+        const Tile t = tile_of(w.sh.seg, w.a, w.ctiles, item);
+        const int ch = t.channel * w.per_pair + (int)w.cta * (GLU ? kRows / 2 : kRows) + warp * (GLU ? 16 : 32) +
+                       (GLU ? lane & 15 : lane);
+        const bool in = ch < outs;
+        const float* sw = w.a.w_scales + (int64_t)t.expert * w.a.N + (in ? ch : 0);
+        const float s0 = sw[0], s1 = GLU ? sw[outs] : 0.0f;
+        for (int c = lane; c < t.n; c += 32) scales[c] = c < t.m ? w.a.a_scales[t.row0 + c] : 0.0f;
+        __syncwarp();
+        if (!warp_wait(&w.sh.acc_full[acc.stage], acc.parity)) return false;
+        tmem_fence_after();
+        const uint32_t d = w.tmem + ((uint32_t)(warp * 32) << 16) + acc.stage * kTileTokens;
+        for (int c0 = 0; c0 < t.m; c0 += 32) {
+            uint32_t v[32];
+            tmem_load32(d + c0, v);
+            const int left = t.m - c0;
+            if (GLU) {
+                // lanes 0-15 finish the even tokens, lanes 16-31 the odd ones
+                const int odd = lane >> 4;
+                uint16_t* out = w.a.out + (t.row0 + c0 + odd) * outs + ch;
+#pragma unroll
+                for (int i = 0; i < 32; i += 2, out += 2 * outs) {
+                    const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(odd ? v[i] : v[i + 1]), 16);
+                    const float s = scales[c0 + i + odd];
+                    const float gate = (odd ? other : __uint_as_float(v[i])) * s * s0;
+                    const float up = (odd ? __uint_as_float(v[i + 1]) : other) * s * s1;
+                    const float y = __fdividef(gate, 1.0f + __expf(-gate)) * up;
+                    if (in && i + odd < left) *out = (uint16_t)pack_bf16x2_rn(y, 0.0f);
+                }
+            } else if (wide) {
+                // neighbours trade halves: an even lane stores both channels of the even token
+                const int odd = lane & 1;
+                const uint32_t sel = odd ? 0x3276u : 0x5410u;
+                uint16_t* out = w.a.out + (t.row0 + c0 + odd) * outs + (ch - odd);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2, out += 2 * outs) {
+                    const float2 s = *reinterpret_cast<const float2*>(&scales[c0 + i]);
+                    const uint32_t y = pack_bf16x2_rn(__uint_as_float(v[i]) * s.x * s0, __uint_as_float(v[i + 1]) * s.y * s0);
+                    const uint32_t both = __byte_perm(y, __shfl_xor_sync(0xffffffffu, y, 1), sel);
+                    if (in && i + odd < left) *reinterpret_cast<uint32_t*>(out) = both;
+                }
+            } else {
+                uint16_t* out = w.a.out + (t.row0 + c0) * outs + ch;
+#pragma unroll
+                for (int i = 0; i < 32; ++i, out += outs) {
+                    const float y = __uint_as_float(v[i]) * scales[c0 + i] * s0;
+                    if (in && i < left) *out = (uint16_t)pack_bf16x2_rn(y, 0.0f);
+                }
+            }
+        }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty0 + acc.stage * 8);
+    }
+    return true;
 }
 
 template <bool GLU>
@@ -116,11 +346,11 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
                     const __grid_constant__ CUtensorMap map_a) {
     extern __shared__ uint8_t dynamic[];
     __shared__ Shared sh;
+    __shared__ __align__(16) float scales[4][kTileTokens];   // of the epilogue warps
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (!load_segments<kThreads>(sh.seg, a, kTileTokens)) return;   // the same answer in both CTAs
     const uint32_t cta = cluster_rank();
     uint8_t* raw = dynamic + ((1024 - (smem_addr(dynamic) & 1023)) & 1023);
-    uint8_t* cvt = raw + kRawStages * kRaw;
     if (tid == 0) {
         for (int i = 0; i < kRawStages; ++i) { mbar_init(&sh.raw_full[i], 1); mbar_init(&sh.raw_empty[i], 16); }
         for (int i = 0; i < kCvtStages; ++i) { mbar_init(&sh.cvt_full[i], 16); mbar_init(&sh.cvt_empty[i], 1); }
@@ -133,202 +363,30 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
     __syncthreads();
     cluster_sync();
     tmem_fence_after();
-    const uint32_t tmem = sh.tmem;
 
     const int outs = GLU ? a.N / 2 : a.N;
     const int per_pair = GLU ? kRows : 2 * kRows;   // output channels of a tile
     const int ctiles = (outs + per_pair - 1) / per_pair;
-    const int64_t items = (int64_t)sh.seg.tile[a.E] * ctiles;
-    const int64_t first_item = blockIdx.x >> 1, step = gridDim.x >> 1;
-    const int steps = (a.K + 63) / 64, raws = (a.K + kRawK - 1) / kRawK;
+    const Work w = {a, sh, raw, raw + kRawStages * kRaw, sh.tmem, cta, outs, per_pair, ctiles,
+                    (a.K + kRawK - 1) / kRawK, blockIdx.x >> 1, (int64_t)sh.seg.tile[a.E] * ctiles, gridDim.x >> 1};
     bool ok = true;
-
     if (warp == 0) {
-        if (lane == 0) {
-            Ring<kRawStages> r;
-            int used = 0;   // stages armed so far, at most kRawStages
-            for (int64_t item = first_item; ok && item < items; item += step) {
-                const Tile t = tile_of(sh.seg, a, ctiles, item);
-                const int half = t.n / 2, boxes = (half + kBoxTokens - 1) / kBoxTokens;
-                const int wrow = t.expert * a.N + t.channel * per_pair + (int)cta * (GLU ? kRows / 2 : kRows);
-                const int trow = (int)t.row0 + (int)cta * half;
-                for (int k = 0; ok && k < raws; ++k, r.next()) {
-                    if (!mbar_wait_parked(&sh.raw_empty[r.stage], r.parity ^ 1)) { ok = false; break; }
-                    uint8_t* dst = raw + r.stage * kRaw;
-                    uint64_t* bar = &sh.raw_full[r.stage];
-                    mbar_arrive_expect_tx(bar, kRawA + boxes * kBoxTokens * kRawK);
-                    if (GLU) {
-                        // 16 gates and their 16 ups in each 32 lanes
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            tma_load_2d(dst + (2 * w) * 16 * kRawK, &map_w, k * kRawK, wrow + 16 * w, bar);
-                            tma_load_2d(dst + (2 * w + 1) * 16 * kRawK, &map_w, k * kRawK, wrow + outs + 16 * w, bar);
-                        }
-                    } else {
-                        tma_load_2d(dst, &map_w, k * kRawK, wrow, bar);
-                    }
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(dst + kRawA + b * kBoxTokens * kRawK, &map_a, k * kRawK, trow + b * kBoxTokens, bar);
-                    used = min(used + 1, kRawStages);
-                }
-            }
-            // copies in flight end before the CTA does, also when a wait gave up
-            for (int i = 0; i < used; ++i) {
-                r.back();
-                ok = mbar_wait_parked(&sh.raw_full[r.stage], r.parity) && ok;
-            }
-        }
+        if (lane == 0) ok = load_tiles<GLU>(w, &map_w, &map_a);
     } else if (warp == 1) {
-        // The whole warp walks the loop and one elected lane issues, so that descriptors stay in
-        // uniform registers.  Whether the next stage is full is asked before the MMAs of this
-        // one are issued: the answer takes longer than they do.
-        if (cta == 0) {
-            Ring<kCvtStages> c;
-            Ring<2> acc;
-            const uint32_t cvt0 = smem_addr(cvt);
-            bool ready = false;
-            for (int64_t item = first_item; ok && item < items; item += step, acc.next()) {
-                const Tile t = tile_of(sh.seg, a, ctiles, item);
-                const uint32_t idesc = mma_desc_f16(2 * kRows, t.n);
-                if (!warp_wait(&sh.acc_empty[acc.stage], acc.parity ^ 1)) { ok = false; break; }
-                tmem_fence_after();
-                const uint32_t d = tmem + acc.stage * kTileTokens;
-                for (int k = 0; k < steps; ++k) {
-                    if (!ready && !warp_wait(&sh.cvt_full[c.stage], c.parity)) { ok = false; break; }
-                    tmem_fence_after();
-                    const uint32_t at = tmem + kColA + c.stage * 32;
-                    const uint64_t b = smem_desc_k128(cvt0 + c.stage * kCvtB);
-                    uint64_t* const empty = &sh.cvt_empty[c.stage];
-                    c.next();
-                    ready = __all_sync(0xffffffffu, mbar_try_wait(&sh.cvt_full[c.stage], c.parity));
-                    if (elect_one()) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) mma_pair_f16(d, at + 8 * j, b + 2 * j, idesc, k > 0 || j > 0);
-                        commit_pair(empty);
-                    }
-                    __syncwarp();
-                }
-                if (ok && elect_one()) commit_pair(&sh.acc_full[acc.stage]);
-                __syncwarp();
-            }
-            // no MMA is left when the CTAs part, also when a wait gave up
-            if (elect_one()) commit_leader(&sh.drained);
-            __syncwarp();
-            ok = warp_wait(&sh.drained, 0) && ok;
-        }
+        if (cta == 0) ok = issue_mma(w);
+    } else if (warp >= 16) {
+        ok = convert<false>(w, warp & 3, (warp >> 2) & 1);
     } else if (warp >= 8) {
-        const bool weights = warp < 16;
-        const int w = warp & 3, mine = (warp >> 2) & 1;
-        const uint32_t cvt_full0 = cluster_addr(smem_addr(&sh.cvt_full[0]), 0);
-        Ring<kRawStages> r;
-        Ring<kCvtStages> c;
-        int used = 0;   // stages handed over, at most kCvtStages
-        for (int64_t item = first_item; ok && item < items; item += step) {
-            const int half = weights ? 0 : tile_of(sh.seg, a, ctiles, item).n / 2;
-            for (int k = 0; ok && k < raws; ++k, r.next()) {
-                if (!warp_wait(&sh.raw_full[r.stage], r.parity)) { ok = false; break; }
-                const uint8_t* src = raw + r.stage * kRaw;
-                for (int h = 0; h < 2 && 2 * k + h < steps; ++h, c.next()) {
-                    used = min(used + 1, kCvtStages);
-                    if (h != mine) continue;
-                    if (weights) {
-                        // a thread per weight row (tensor-memory lane): 64 codes, 32 columns
-                        const uint8_t* row = src + (w * 32 + lane) * kRawK;
-                        uint32_t v[32];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            codes_to_f16(lds_v4(row + (((4 * h + q) ^ (lane & 7)) * 16)), v + 8 * q);
-                        if (!warp_wait(&sh.cvt_empty[c.stage], c.parity ^ 1)) { ok = false; break; }
-                        tmem_fence_after();
-                        tmem_store32(tmem + ((uint32_t)(w * 32) << 16) + kColA + c.stage * 32, v);
-                        tmem_wait_stores();
-                        tmem_fence_before();
-                    } else {
-                        // a lane per 16 codes: eight rows and four chunks a warp, free of bank conflicts
-                        const uint32_t dst = smem_addr(cvt + c.stage * kCvtB);
-                        const int rr = lane & 7, q = lane >> 3;
-                        uint4 in[kHalf / 32];
-                        const uint8_t* from = src + kRawA + (w * 8 + rr) * kRawK + (((4 * h + q) ^ rr) * 16);
-#pragma unroll
-                        for (int g = 0; g < kHalf / 32; ++g)   // rows past the tile's hold anything, and nothing reads them
-                            in[g] = lds_v4(from + g * 32 * kRawK);
-                        if (!warp_wait(&sh.cvt_empty[c.stage], c.parity ^ 1)) { ok = false; break; }
-                        const uint32_t row = dst + (w * 8 + rr) * 128;
-                        const uint32_t c0 = row + (((2 * q) ^ rr) * 16), c1 = row + (((2 * q + 1) ^ rr) * 16);
-#pragma unroll
-                        for (int g = 0; g < kHalf / 32; ++g) {
-                            if (g * 32 + w * 8 >= half) break;
-                            uint32_t v[8];
-                            codes_to_f16(in[g], v);
-                            sts_v4(c0 + g * 32 * 128, v[0], v[1], v[2], v[3]);
-                            sts_v4(c1 + g * 32 * 128, v[4], v[5], v[6], v[7]);
-                        }
-                        fence_proxy_async_smem();
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(cvt_full0 + c.stage * 8);
-                }
-                if (!ok) break;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.raw_empty[r.stage]);
-            }
-        }
-        // the commits that free the last stages reach this CTA before it ends
-        for (int i = 0; ok && i < used; ++i) {
-            c.back();
-            ok = warp_wait(&sh.cvt_empty[c.stage], c.parity);
-        }
+        ok = convert<true>(w, warp & 3, (warp >> 2) & 1);
     } else if (warp >= 4) {
-        const int w = warp & 3;
-        const uint32_t acc_empty0 = cluster_addr(smem_addr(&sh.acc_empty[0]), 0);
-        Ring<2> acc;
-        for (int64_t item = first_item; item < items; item += step, acc.next()) {
-            const Tile t = tile_of(sh.seg, a, ctiles, item);
-            // lane: an output channel; with gates and ups, lanes 0-15 hold the gates of lanes 16-31's ups
-            const int ch = t.channel * per_pair + (int)cta * (GLU ? kRows / 2 : kRows) + w * (GLU ? 16 : 32) +
-                           (GLU ? lane & 15 : lane);
-            const bool in = ch < outs;
-            const float* sw = a.w_scales + (int64_t)t.expert * a.N + (in ? ch : 0);
-            const float s0 = sw[0], s1 = GLU ? sw[outs] : 0.0f;
-            if (!warp_wait(&sh.acc_full[acc.stage], acc.parity)) { ok = false; break; }
-            tmem_fence_after();
-            const uint32_t d = tmem + ((uint32_t)(w * 32) << 16) + acc.stage * kTileTokens;
-            for (int c0 = 0; c0 < t.m; c0 += 32) {
-                uint32_t v[32];
-                tmem_load32(d + c0, v);
-                const float sa = c0 + lane < t.m ? a.a_scales[t.row0 + c0 + lane] : 0.0f;
-                uint16_t* out = a.out + (t.row0 + c0) * outs + ch;
-                if (GLU) {
-                    const int odd = lane >> 4;   // lanes 0-15 finish the even tokens, lanes 16-31 the odd ones
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(odd ? v[i] : v[i + 1]), 16);
-                        const float s = __shfl_sync(0xffffffffu, sa, i + odd);
-                        const float gate = (odd ? other : __uint_as_float(v[i])) * s * s0;
-                        const float up = (odd ? __uint_as_float(v[i + 1]) : other) * s * s1;
-                        const float y = gate / (1.0f + expf(-gate)) * up;
-                        if (in && c0 + i + odd < t.m)
-                            out[(int64_t)(i + odd) * outs] = (uint16_t)pack_bf16x2_rn(y, 0.0f);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float y = __uint_as_float(v[i]) * __shfl_sync(0xffffffffu, sa, i) * s0;
-                        if (in && c0 + i < t.m) out[(int64_t)i * outs] = (uint16_t)pack_bf16x2_rn(y, 0.0f);
-                    }
-                }
-            }
-            tmem_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(acc_empty0 + acc.stage * 8);
-        }
+        ok = epilogue<GLU>(w, warp & 3, scales[warp & 3]);
     }
     if (!ok && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
     cluster_sync();   // neither CTA's shared or tensor memory goes while the pair's MMAs may read it
-    if (warp == 2) tmem_free_pair(tmem, kColumns);
+    if (warp == 2) tmem_free_pair(w.tmem, kColumns);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
