@@ -129,14 +129,16 @@ struct Work {
 };
 
 template <bool GLU>
-__device__ __forceinline__ bool load_tiles(const Work& w, const CUtensorMap* map_w, const CUtensorMap* map_a) {
+__device__ __forceinline__ bool load_tiles(const Work& w, const CUtensorMap* map_w, const CUtensorMap* map_a,
+                                           const CUtensorMap* map_half) {
     Ring<kRawStages> r;
     int used = 0;   // stages armed so far, at most kRawStages
     bool ok = true;
     for (int64_t item = w.first; ok && item < w.items; item += w.step) {
         const Tile t = tile_of(w.sh.seg, w.a, w.ctiles, item);
+        // token rows in one box where the tile is full, else in boxes of 32
         const int half = t.n / 2, boxes = (half + kBoxTokens - 1) / kBoxTokens;
-        const int wrow = t.expert * w.a.N + t.channel * w.per_pair + (int)w.cta * (GLU ? kRows / 2 : kRows);
+        const int ch = t.channel * w.per_pair + (int)w.cta * (GLU ? kRows / 2 : kRows);
         const int trow = (int)t.row0 + (int)w.cta * half;
         for (int k = 0; k < w.raws; ++k, r.next()) {
             if (!mbar_wait_parked(&w.sh.raw_empty[r.stage], r.parity ^ 1)) { ok = false; break; }
@@ -144,17 +146,19 @@ __device__ __forceinline__ bool load_tiles(const Work& w, const CUtensorMap* map
             uint64_t* bar = &w.sh.raw_full[r.stage];
             mbar_arrive_expect_tx(bar, kRawA + boxes * kBoxTokens * kRawK);
             if (GLU) {
-                // 16 gates and their 16 ups in each 32 lanes
+                // a box: 16 gates and their 16 ups, the 32 lanes of an epilogue warp
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    tma_load_2d(dst + (2 * i) * 16 * kRawK, map_w, k * kRawK, wrow + 16 * i, bar);
-                    tma_load_2d(dst + (2 * i + 1) * 16 * kRawK, map_w, k * kRawK, wrow + w.outs + 16 * i, bar);
-                }
+                for (int i = 0; i < 4; ++i)
+                    tma_load_4d(dst + 32 * i * kRawK, map_w, k * kRawK, ch + 16 * i, 0, t.expert, bar);
             } else {
-                tma_load_2d(dst, map_w, k * kRawK, wrow, bar);
+                tma_load_2d(dst, map_w, k * kRawK, t.expert * w.a.N + ch, bar);
             }
-            for (int b = 0; b < boxes; ++b)
-                tma_load_2d(dst + kRawA + b * kBoxTokens * kRawK, map_a, k * kRawK, trow + b * kBoxTokens, bar);
+            if (boxes == kHalf / kBoxTokens) {
+                tma_load_2d(dst + kRawA, map_half, k * kRawK, trow, bar);
+            } else {
+                for (int b = 0; b < boxes; ++b)
+                    tma_load_2d(dst + kRawA + b * kBoxTokens * kRawK, map_a, k * kRawK, trow + b * kBoxTokens, bar);
+            }
             used = min(used + 1, kRawStages);
         }
     }
@@ -274,6 +278,15 @@ __device__ __forceinline__ bool convert(const Work& w, int warp, int half) {
     return ok;
 }
 
+// silu(gate s0) * (up s1); a gate of -inf or an exponential past the range gives 0 as the limit does.
+__device__ __forceinline__ float swiglu(float gate, float up, float s0, float s1) {
+    float e, r;
+    const float g = gate * s0;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return g * (up * s1) * r;
+}
+
 // Lane: an output channel; with gates and ups, lanes 0-15 hold the gates of lanes 16-31's ups.
 template <bool GLU>
 __device__ __forceinline__ bool epilogue(const Work& w, int warp, float* scales) {
@@ -302,15 +315,30 @@ __device__ __forceinline__ bool epilogue(const Work& w, int warp, float* scales)
             if (GLU) {
                 // lanes 0-15 finish the even tokens, lanes 16-31 the odd ones
                 const int odd = lane >> 4;
-                uint16_t* out = w.a.out + (t.row0 + c0 + odd) * outs + ch;
+                float y[16];
 #pragma unroll
-                for (int i = 0; i < 32; i += 2, out += 2 * outs) {
+                for (int i = 0; i < 32; i += 2) {
                     const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(odd ? v[i] : v[i + 1]), 16);
                     const float s = scales[c0 + i + odd];
-                    const float gate = (odd ? other : __uint_as_float(v[i])) * s * s0;
-                    const float up = (odd ? __uint_as_float(v[i + 1]) : other) * s * s1;
-                    const float y = __fdividef(gate, 1.0f + __expf(-gate)) * up;
-                    if (in && i + odd < left) *out = (uint16_t)pack_bf16x2_rn(y, 0.0f);
+                    y[i / 2] = swiglu((odd ? other : __uint_as_float(v[i])) * s, (odd ? __uint_as_float(v[i + 1]) : other) * s, s0, s1);
+                }
+                if (wide) {
+                    // neighbours trade as below: an even lane stores its pair of channels of token
+                    // i + odd, an odd lane that of token i + 2 + odd
+                    const int last = lane & 1;
+                    const uint32_t sel = last ? 0x3276u : 0x5410u;
+                    uint16_t* out = w.a.out + (t.row0 + c0 + odd + 2 * last) * outs + (ch - last);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4, out += 4 * outs) {
+                        const uint32_t p = pack_bf16x2_rn(y[i / 2], y[i / 2 + 1]);
+                        const uint32_t both = __byte_perm(p, __shfl_xor_sync(0xffffffffu, p, 1), sel);
+                        if (in && i + odd + 2 * last < left) *reinterpret_cast<uint32_t*>(out) = both;
+                    }
+                } else {
+                    uint16_t* out = w.a.out + (t.row0 + c0 + odd) * outs + ch;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2, out += 2 * outs)
+                        if (in && i + odd < left) *out = (uint16_t)pack_bf16x2_rn(y[i / 2], 0.0f);
                 }
             } else if (wide) {
                 // neighbours trade halves: an even lane stores both channels of the even token
@@ -343,7 +371,7 @@ __device__ __forceinline__ bool epilogue(const Work& w, int warp, float* scales)
 template <bool GLU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_w,
-                    const __grid_constant__ CUtensorMap map_a) {
+                    const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_half) {
     extern __shared__ uint8_t dynamic[];
     __shared__ Shared sh;
     __shared__ __align__(16) float scales[4][kTileTokens];   // of the epilogue warps
@@ -371,7 +399,7 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
                     (a.K + kRawK - 1) / kRawK, blockIdx.x >> 1, (int64_t)sh.seg.tile[a.E] * ctiles, gridDim.x >> 1};
     bool ok = true;
     if (warp == 0) {
-        if (lane == 0) ok = load_tiles<GLU>(w, &map_w, &map_a);
+        if (lane == 0) ok = load_tiles<GLU>(w, &map_w, &map_a, &map_half);
     } else if (warp == 1) {
         if (cta == 0) ok = issue_mma(w);
     } else if (warp >= 16) {
@@ -406,14 +434,28 @@ EncodeTiled encode_tiled() {
     return (EncodeTiled)p;
 }
 
-// Rows of `bytes` codes as boxes of 128 bytes x box_rows, 128-byte swizzle; zeros outside.
-bool make_map(EncodeTiled enc, CUtensorMap* map, const void* p, int64_t rows, int64_t bytes, int box_rows) {
-    const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)bytes};
-    const cuuint32_t box[2] = {kRawK, (cuuint32_t)box_rows}, unit[2] = {1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, box, unit,
+// Codes in boxes of 128 bytes x rows, 128-byte swizzle; zeros outside.
+bool make_map(EncodeTiled enc, CUtensorMap* map, const void* p, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+              const cuuint32_t* box) {
+    const cuuint32_t unit[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(p), dims, strides, box, unit,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [rows][bytes]
+bool make_rows_map(EncodeTiled enc, CUtensorMap* map, const void* p, int64_t rows, int64_t bytes, int box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)bytes};
+    const cuuint32_t box[2] = {kRawK, (cuuint32_t)box_rows};
+    return make_map(enc, map, p, 2, dims, strides, box);
+}
+
+// [E][gate, up][n][bytes], 16 gates and their ups a box
+bool make_pairs_map(EncodeTiled enc, CUtensorMap* map, const void* p, int64_t E, int64_t n, int64_t bytes) {
+    const cuuint64_t dims[4] = {(cuuint64_t)bytes, (cuuint64_t)n, 2, (cuuint64_t)E};
+    const cuuint64_t strides[3] = {(cuuint64_t)bytes, (cuuint64_t)(n * bytes), (cuuint64_t)(2 * n * bytes)};
+    const cuuint32_t box[4] = {kRawK, 16, 2, 1};
+    return make_map(enc, map, p, 4, dims, strides, box);
 }
 
 }  // namespace
@@ -421,16 +463,18 @@ bool make_map(EncodeTiled enc, CUtensorMap* map, const void* p, int64_t rows, in
 cudaError_t launch_matmul_tiles(const MatmulArgs& a, int sms, cudaStream_t st) {
     EncodeTiled enc = encode_tiled();
     if (!enc) return cudaErrorNotSupported;
-    CUtensorMap map_w, map_a;
-    if (!make_map(enc, &map_w, a.w, (int64_t)a.E * a.N, a.K, a.swiglu ? 16 : kRows) ||
-        !make_map(enc, &map_a, a.a, a.rows, a.K, kBoxTokens))
-        return cudaErrorInvalidValue;
     const int64_t per_pair = a.swiglu ? kRows : 2 * kRows, outs = a.swiglu ? a.N / 2 : a.N;
+    CUtensorMap map_w, map_a, map_half;
+    if (!(a.swiglu ? make_pairs_map(enc, &map_w, a.w, a.E, outs, a.K)
+                   : make_rows_map(enc, &map_w, a.w, (int64_t)a.E * a.N, a.K, kRows)) ||
+        !make_rows_map(enc, &map_a, a.a, a.rows, a.K, kBoxTokens) ||
+        !make_rows_map(enc, &map_half, a.a, a.rows, a.K, kHalf))
+        return cudaErrorInvalidValue;
     const int64_t most = ((a.rows + kTileTokens - 1) / kTileTokens + (a.E > 1 ? a.E : 0)) * ((outs + per_pair - 1) / per_pair);
     const int64_t pairs = most < sms / 2 ? most : sms / 2;
     auto kernel = a.swiglu ? matmul_tiles_kernel<true> : matmul_tiles_kernel<false>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(2 * pairs), kThreads, kSmem, st>>>(a, map_w, map_a);
+    kernel<<<(unsigned)(2 * pairs), kThreads, kSmem, st>>>(a, map_w, map_a, map_half);
     return cudaGetLastError();
 }
