@@ -29,25 +29,39 @@
 
 namespace {
 
-constexpr int kThreads = 768;
-constexpr int kTileTokens = 192;       // token rows of a tile, both CTAs
-constexpr int kHalf = kTileTokens / 2; // token rows that one CTA converts
 constexpr int kRows = 128;             // weight rows of a CTA
 constexpr int kRawK = 128;             // k of a TMA stage (bytes of a row)
-constexpr int kRawStages = 5;
-constexpr int kCvtStages = 4;          // 64-k stages of float16 operands
-constexpr int kRawA = kRows * kRawK, kRawB = kHalf * kRawK, kRaw = kRawA + kRawB;
-constexpr int kCvtB = kHalf * 128;     // bytes: 64 float16 a row
-constexpr uint32_t kColumns = 512, kColA = 2 * kTileTokens;
-constexpr int kSmem = 1024 + kRawStages * kRaw + kCvtStages * kCvtB;
+constexpr int kRawA = kRows * kRawK;
+constexpr uint32_t kColumns = 512;     // of tensor memory
 constexpr int kBoxTokens = 32;         // rows of a token box
+constexpr int kSets = 4;               // groups of four warps that convert in turn
+constexpr int kThreads = 32 * (8 + 4 * kSets);
 
-static_assert(kColA + kCvtStages * 32 <= kColumns, "tensor memory");
+// TILE: token rows of a tile, both CTAs.  RAW TMA stages of 128 k, CVT float16 stages of 64 k.
+template <int TILE, int RAW, int CVT>
+struct Config {
+    static constexpr int tile = TILE, half = TILE / 2;   // half: token rows that one CTA converts
+    static constexpr int raw_stages = RAW, cvt_stages = CVT;
+    static constexpr int raw_bytes = kRawA + half * kRawK;
+    static constexpr int cvt_bytes = half * 128;         // 64 float16 a row
+    static constexpr uint32_t col_a = 2 * TILE;          // weights, behind two accumulators
+    static constexpr int smem = 1024 + RAW * raw_bytes + CVT * cvt_bytes;
+    static_assert(col_a + CVT * 32 <= kColumns, "tensor memory");
+    static_assert((CVT & (CVT - 1)) == 0 && CVT % kSets == 0, "uses take stages in turn");
+    static_assert(raw_bytes % 1024 == 0 && cvt_bytes % 1024 == 0 && half % kBoxTokens == 0, "swizzled rows");
+};
 
+// Segments of many rows: the largest tile of which tensor memory holds two.
+using Thick = Config<192, 5, 4>;
+// Segments of up to 64 rows: the tile's work is the weights', so more TMA stages are in flight, and
+// the columns that smaller accumulators leave hold more weights.
+using Thin = Config<64, 7, 8>;
+
+template <class C>
 struct Shared {
     Segments seg;
-    uint64_t raw_full[kRawStages], raw_empty[kRawStages];
-    uint64_t cvt_full[kCvtStages], cvt_empty[kCvtStages];
+    uint64_t raw_full[C::raw_stages], raw_empty[C::raw_stages];
+    uint64_t cvt_full[C::cvt_stages], cvt_empty[C::cvt_stages];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drained;
     uint32_t tmem;
@@ -56,6 +70,7 @@ struct Shared {
 struct Tile { int64_t row0; int expert, m, n, channel; };   // n: MMA columns, channel: tile of output channels
 
 // Tiles of one expert are neighbours, its token tiles fastest: concurrent pairs share weights and tokens in L2.
+template <class C>
 __device__ __forceinline__ Tile tile_of(const Segments& s, const MatmulArgs& a, int ctiles, int64_t item) {
     const int e = expert_of_tile(s, a.E, (int)(item / ctiles));
     const int tiles = s.tile[e + 1] - s.tile[e];
@@ -118,31 +133,32 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // What every role of a CTA knows.
+template <class C>
 struct Work {
     const MatmulArgs& a;
-    Shared& sh;
-    uint8_t* raw;    // TMA stages: 128 weight rows, then up to 96 token rows, of 128 codes
+    Shared<C>& sh;
+    uint8_t* raw;    // TMA stages: 128 weight rows, then token rows, of 128 codes
     uint8_t* cvt;    // float16 token rows of 64 k
     uint32_t tmem, cta;
     int outs, per_pair, ctiles, raws;
     int64_t first, items, step;
 };
 
-template <bool GLU>
-__device__ __forceinline__ bool load_tiles(const Work& w, const CUtensorMap* map_w, const CUtensorMap* map_a,
+template <class C, bool GLU>
+__device__ __forceinline__ bool load_tiles(const Work<C>& w, const CUtensorMap* map_w, const CUtensorMap* map_a,
                                            const CUtensorMap* map_half) {
-    Ring<kRawStages> r;
-    int used = 0;   // stages armed so far, at most kRawStages
+    Ring<C::raw_stages> r;
+    int used = 0;   // stages armed so far, at most all
     bool ok = true;
     for (int64_t item = w.first; ok && item < w.items; item += w.step) {
-        const Tile t = tile_of(w.sh.seg, w.a, w.ctiles, item);
+        const Tile t = tile_of<C>(w.sh.seg, w.a, w.ctiles, item);
         // token rows in one box where the tile is full, else in boxes of 32
         const int half = t.n / 2, boxes = (half + kBoxTokens - 1) / kBoxTokens;
         const int ch = t.channel * w.per_pair + (int)w.cta * (GLU ? kRows / 2 : kRows);
         const int trow = (int)t.row0 + (int)w.cta * half;
         for (int k = 0; k < w.raws; ++k, r.next()) {
             if (!mbar_wait_parked(&w.sh.raw_empty[r.stage], r.parity ^ 1)) { ok = false; break; }
-            uint8_t* dst = w.raw + r.stage * kRaw;
+            uint8_t* dst = w.raw + r.stage * C::raw_bytes;
             uint64_t* bar = &w.sh.raw_full[r.stage];
             mbar_arrive_expect_tx(bar, kRawA + boxes * kBoxTokens * kRawK);
             if (GLU) {
@@ -153,13 +169,13 @@ __device__ __forceinline__ bool load_tiles(const Work& w, const CUtensorMap* map
             } else {
                 tma_load_2d(dst, map_w, k * kRawK, t.expert * w.a.N + ch, bar);
             }
-            if (boxes == kHalf / kBoxTokens) {
+            if (boxes == C::half / kBoxTokens) {
                 tma_load_2d(dst + kRawA, map_half, k * kRawK, trow, bar);
             } else {
                 for (int b = 0; b < boxes; ++b)
                     tma_load_2d(dst + kRawA + b * kBoxTokens * kRawK, map_a, k * kRawK, trow + b * kBoxTokens, bar);
             }
-            used = min(used + 1, kRawStages);
+            used = min(used + 1, C::raw_stages);
         }
     }
     // copies in flight end before the CTA does, also when a wait gave up
@@ -173,22 +189,23 @@ __device__ __forceinline__ bool load_tiles(const Work& w, const CUtensorMap* map
 // The whole warp walks the loop and one elected lane issues, so that descriptors stay in uniform
 // registers.  Whether the next stage is full is asked before the MMAs of this one are issued:
 // the answer takes longer than they do.
-__device__ __forceinline__ bool issue_mma(const Work& w) {
-    Ring<kCvtStages> c;
+template <class C>
+__device__ __forceinline__ bool issue_mma(const Work<C>& w) {
+    Ring<C::cvt_stages> c;
     Ring<2> acc;
     const uint32_t cvt0 = smem_addr(w.cvt);
     bool ready = false, ok = true;
     for (int64_t item = w.first; ok && item < w.items; item += w.step, acc.next()) {
-        const Tile t = tile_of(w.sh.seg, w.a, w.ctiles, item);
+        const Tile t = tile_of<C>(w.sh.seg, w.a, w.ctiles, item);
         const uint32_t idesc = mma_desc_f16(2 * kRows, t.n);
         if (!warp_wait(&w.sh.acc_empty[acc.stage], acc.parity ^ 1)) { ok = false; break; }
         tmem_fence_after();
-        const uint32_t d = w.tmem + acc.stage * kTileTokens;
+        const uint32_t d = w.tmem + acc.stage * C::tile;
         for (int k = 0; k < 2 * w.raws; ++k) {
             if (!ready && !warp_wait(&w.sh.cvt_full[c.stage], c.parity)) { ok = false; break; }
             tmem_fence_after();
-            const uint32_t at = w.tmem + kColA + c.stage * 32;
-            const uint64_t b = smem_desc_k128(cvt0 + c.stage * kCvtB);
+            const uint32_t at = w.tmem + C::col_a + c.stage * 32;
+            const uint64_t b = smem_desc_k128(cvt0 + c.stage * C::cvt_bytes);
             uint64_t* const empty = &w.sh.cvt_empty[c.stage];
             c.next();
             ready = __all_sync(0xffffffffu, mbar_try_wait(&w.sh.cvt_full[c.stage], c.parity));
@@ -208,73 +225,66 @@ __device__ __forceinline__ bool issue_mma(const Work& w) {
     return warp_wait(&w.sh.drained, 0) && ok;
 }
 
-// Four warps turn the weights (WEIGHTS) or the tokens of half a TMA stage (64 k) into float16;
-// `half` 0 or 1.  A stage has two converted stages, so half h uses stages h and h + 2 in turn.
-template <bool WEIGHTS>
-__device__ __forceinline__ bool convert(const Work& w, int warp, int half) {
+// Four warps turn 64 k of a stage into float16 at a time.  Use u of the converted stages is half
+// u & 1 of TMA stage u >> 1; group `set` takes every kSets-th use.
+template <class C>
+__device__ __forceinline__ bool convert(const Work<C>& w, int warp, int set) {
     const int lane = threadIdx.x & 31;
-    const uint32_t full0 = cluster_addr(smem_addr(&w.sh.cvt_full[half]), 0);
-    const uint32_t raw0 = smem_addr(w.raw);
-    const int rr = lane & 7, q = lane >> 3;
+    const uint32_t full0 = cluster_addr(smem_addr(&w.sh.cvt_full[0]), 0);
+    const int rr = lane & 7, q = lane >> 3, h = set & 1;
+    constexpr int kChunks = C::half / 32;
+    static_assert(kSets % 2 == 0, "a group keeps to one half");
     // weights: a thread per row (tensor-memory lane), its four chunks of 16 codes where the swizzle put them;
     // tokens: a lane per chunk, eight rows and four chunks a warp, free of bank conflicts
-    uint32_t from[4];
+    uint32_t from_w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        from[i] = WEIGHTS ? raw0 + (warp * 32 + lane) * kRawK + (((4 * half + i) ^ rr) * 16)
-                          : raw0 + kRawA + (warp * 8 + rr) * kRawK + (((4 * half + q) ^ rr) * 16) + i * 32 * kRawK;
-    const uint32_t to0 = smem_addr(w.cvt) + half * kCvtB + (warp * 8 + rr) * 128 + (((2 * q) ^ rr) * 16);
-    const uint32_t to1 = smem_addr(w.cvt) + half * kCvtB + (warp * 8 + rr) * 128 + (((2 * q + 1) ^ rr) * 16);
-    const uint32_t col = w.tmem + ((uint32_t)(warp * 32) << 16) + kColA + half * 32;
-    Ring<kRawStages> r;
-    Ring<2> c;   // converted stage half + 2 * c.stage
-    static_assert(kCvtStages == 4, "two halves, two stages each");
-    int64_t uses = 0;
+    for (int i = 0; i < 4; ++i) from_w[i] = smem_addr(w.raw) + (warp * 32 + lane) * kRawK + (((4 * h + i) ^ rr) * 16);
+    const uint32_t from_t = smem_addr(w.raw) + kRawA + (warp * 8 + rr) * kRawK + (((4 * h + q) ^ rr) * 16);
+    const uint32_t row = smem_addr(w.cvt) + (warp * 8 + rr) * 128;
+    const uint32_t to0 = row + (((2 * q) ^ rr) * 16), to1 = row + (((2 * q + 1) ^ rr) * 16);
+    const uint32_t col = w.tmem + ((uint32_t)(warp * 32) << 16) + C::col_a;
+    Ring<C::raw_stages> r;
+    uint32_t use = h;
     bool ok = true;
     for (int64_t item = w.first; ok && item < w.items; item += w.step) {
-        const int rows = WEIGHTS ? 0 : tile_of(w.sh.seg, w.a, w.ctiles, item).n / 2 - warp * 8;
-        uses += w.raws;
-        for (int k = 0; k < w.raws; ++k, r.next(), c.next()) {
+        const int rows = tile_of<C>(w.sh.seg, w.a, w.ctiles, item).n / 2 - warp * 8;
+        for (int k = 0; k < w.raws; ++k, use += 2, r.next()) {
+            if (use % kSets != (uint32_t)set) continue;
+            const uint32_t stage = use % C::cvt_stages, parity = (use / C::cvt_stages) & 1;
             if (!warp_wait(&w.sh.raw_full[r.stage], r.parity)) { ok = false; break; }
-            const uint32_t at = r.stage * kRaw;
-            uint64_t* const empty = &w.sh.cvt_empty[half + 2 * c.stage];
-            if (WEIGHTS) {
-                uint32_t v[32];
+            const uint32_t at = r.stage * C::raw_bytes;
+            uint32_t v[32];
+            uint4 in[kChunks];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) codes_to_f16(lds_at(from[i] + at), v + 8 * i);
-                if (!warp_wait(empty, c.parity ^ 1)) { ok = false; break; }
-                tmem_fence_after();
-                tmem_store32(col + c.stage * 64, v);
-                tmem_wait_stores();
-                tmem_fence_before();
-            } else {
-                uint4 in[kHalf / 32];
+            for (int i = 0; i < 4; ++i) codes_to_f16(lds_at(from_w[i] + at), v + 8 * i);
 #pragma unroll
-                for (int g = 0; g < kHalf / 32; ++g) in[g] = lds_at(from[g] + at);   // rows past the tile's are not used
-                if (!warp_wait(empty, c.parity ^ 1)) { ok = false; break; }
-                const uint32_t to = c.stage * 2 * kCvtB;
+            for (int g = 0; g < kChunks; ++g) in[g] = lds_at(from_t + at + g * 32 * kRawK);   // some past the tile's rows
+            if (!warp_wait(&w.sh.cvt_empty[stage], parity ^ 1)) { ok = false; break; }
+            tmem_fence_after();
+            tmem_store32(col + stage * 32, v);
+            const uint32_t to = stage * C::cvt_bytes;
 #pragma unroll
-                for (int g = 0; g < kHalf / 32; ++g) {
-                    if (g * 32 >= rows) break;
-                    uint32_t v[8];
-                    codes_to_f16(in[g], v);
-                    sts_at(to0 + to + g * 32 * 128, v[0], v[1], v[2], v[3]);
-                    sts_at(to1 + to + g * 32 * 128, v[4], v[5], v[6], v[7]);
-                }
-                fence_proxy_async_smem();
+            for (int g = 0; g < kChunks; ++g) {
+                if (g * 32 >= rows) break;
+                uint32_t f[8];
+                codes_to_f16(in[g], f);
+                sts_at(to0 + to + g * 32 * 128, f[0], f[1], f[2], f[3]);
+                sts_at(to1 + to + g * 32 * 128, f[4], f[5], f[6], f[7]);
             }
+            fence_proxy_async_smem();
+            tmem_wait_stores();
+            tmem_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive_cluster(full0 + c.stage * 16);
+                mbar_arrive_cluster(full0 + stage * 8);
                 mbar_arrive(&w.sh.raw_empty[r.stage]);
             }
         }
     }
     // the commits that free the last stages reach this CTA before it ends
-    for (int i = 0; ok && i < 2 && i < uses; ++i) {
-        c.back();
-        ok = warp_wait(&w.sh.cvt_empty[half + 2 * c.stage], c.parity);
-    }
+    use -= h;
+    for (uint32_t i = 0; ok && i < C::cvt_stages && i < use; ++i)
+        ok = warp_wait(&w.sh.cvt_empty[(use - 1 - i) % C::cvt_stages], ((use - 1 - i) / C::cvt_stages) & 1);
     return ok;
 }
 
@@ -288,8 +298,8 @@ __device__ __forceinline__ float swiglu(float gate, float up, float s0, float s1
 }
 
 // Lane: an output channel; with gates and ups, lanes 0-15 hold the gates of lanes 16-31's ups.
-template <bool GLU>
-__device__ __forceinline__ bool epilogue(const Work& w, int warp, float* scales) {
+template <class C, bool GLU>
+__device__ __forceinline__ bool epilogue(const Work<C>& w, int warp, float* scales) {
     const int lane = threadIdx.x & 31;
     const uint32_t acc_empty0 = cluster_addr(smem_addr(&w.sh.acc_empty[0]), 0);
     const int64_t outs = w.outs;
@@ -297,7 +307,7 @@ __device__ __forceinline__ bool epilogue(const Work& w, int warp, float* scales)
     const bool wide = (outs & 1) == 0 && ((uintptr_t)w.a.out & 3) == 0;
     Ring<2> acc;
     for (int64_t item = w.first; item < w.items; item += w.step, acc.next()) {
-        const Tile t = tile_of(w.sh.seg, w.a, w.ctiles, item);
+        const Tile t = tile_of<C>(w.sh.seg, w.a, w.ctiles, item);
         const int ch = t.channel * w.per_pair + (int)w.cta * (GLU ? kRows / 2 : kRows) + warp * (GLU ? 16 : 32) +
                        (GLU ? lane & 15 : lane);
         const bool in = ch < outs;
@@ -307,7 +317,7 @@ __device__ __forceinline__ bool epilogue(const Work& w, int warp, float* scales)
         __syncwarp();
         if (!warp_wait(&w.sh.acc_full[acc.stage], acc.parity)) return false;
         tmem_fence_after();
-        const uint32_t d = w.tmem + ((uint32_t)(warp * 32) << 16) + acc.stage * kTileTokens;
+        const uint32_t d = w.tmem + ((uint32_t)(warp * 32) << 16) + acc.stage * C::tile;
         for (int c0 = 0; c0 < t.m; c0 += 32) {
             uint32_t v[32];
             tmem_load32(d + c0, v);
@@ -368,20 +378,20 @@ __device__ __forceinline__ bool epilogue(const Work& w, int warp, float* scales)
     return true;
 }
 
-template <bool GLU>
+template <class C, bool GLU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_w,
                     const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_half) {
     extern __shared__ uint8_t dynamic[];
-    __shared__ Shared sh;
-    __shared__ __align__(16) float scales[4][kTileTokens];   // of the epilogue warps
+    __shared__ Shared<C> sh;
+    __shared__ __align__(16) float scales[4][C::tile];   // of the epilogue warps
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (!load_segments<kThreads>(sh.seg, a, kTileTokens)) return;   // the same answer in both CTAs
+    if (!load_segments<kThreads>(sh.seg, a, C::tile)) return;   // the same answer in both CTAs
     const uint32_t cta = cluster_rank();
     uint8_t* raw = dynamic + ((1024 - (smem_addr(dynamic) & 1023)) & 1023);
     if (tid == 0) {
-        for (int i = 0; i < kRawStages; ++i) { mbar_init(&sh.raw_full[i], 1); mbar_init(&sh.raw_empty[i], 16); }
-        for (int i = 0; i < kCvtStages; ++i) { mbar_init(&sh.cvt_full[i], 16); mbar_init(&sh.cvt_empty[i], 1); }
+        for (int i = 0; i < C::raw_stages; ++i) { mbar_init(&sh.raw_full[i], 1); mbar_init(&sh.raw_empty[i], 8); }
+        for (int i = 0; i < C::cvt_stages; ++i) { mbar_init(&sh.cvt_full[i], 8); mbar_init(&sh.cvt_empty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&sh.acc_full[i], 1); mbar_init(&sh.acc_empty[i], 8); }
         mbar_init(&sh.drained, 1);
         mbar_fence_init();
@@ -395,19 +405,17 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
     const int outs = GLU ? a.N / 2 : a.N;
     const int per_pair = GLU ? kRows : 2 * kRows;   // output channels of a tile
     const int ctiles = (outs + per_pair - 1) / per_pair;
-    const Work w = {a, sh, raw, raw + kRawStages * kRaw, sh.tmem, cta, outs, per_pair, ctiles,
+    const Work<C> w = {a, sh, raw, raw + C::raw_stages * C::raw_bytes, sh.tmem, cta, outs, per_pair, ctiles,
                     (a.K + kRawK - 1) / kRawK, blockIdx.x >> 1, (int64_t)sh.seg.tile[a.E] * ctiles, gridDim.x >> 1};
     bool ok = true;
     if (warp == 0) {
-        if (lane == 0) ok = load_tiles<GLU>(w, &map_w, &map_a, &map_half);
+        if (lane == 0) ok = load_tiles<C, GLU>(w, &map_w, &map_a, &map_half);
     } else if (warp == 1) {
         if (cta == 0) ok = issue_mma(w);
-    } else if (warp >= 16) {
-        ok = convert<false>(w, warp & 3, (warp >> 2) & 1);
     } else if (warp >= 8) {
-        ok = convert<true>(w, warp & 3, (warp >> 2) & 1);
+        ok = convert<C>(w, warp & 3, (warp >> 2) - 2);
     } else if (warp >= 4) {
-        ok = epilogue<GLU>(w, warp & 3, scales[warp & 3]);
+        ok = epilogue<C, GLU>(w, warp & 3, scales[warp & 3]);
     }
     if (!ok && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
     __syncwarp();
@@ -458,9 +466,8 @@ bool make_pairs_map(EncodeTiled enc, CUtensorMap* map, const void* p, int64_t E,
     return make_map(enc, map, p, 4, dims, strides, box);
 }
 
-}  // namespace
-
-cudaError_t launch_matmul_tiles(const MatmulArgs& a, int sms, cudaStream_t st) {
+template <class C>
+cudaError_t launch(const MatmulArgs& a, int sms, cudaStream_t st) {
     EncodeTiled enc = encode_tiled();
     if (!enc) return cudaErrorNotSupported;
     const int64_t per_pair = a.swiglu ? kRows : 2 * kRows, outs = a.swiglu ? a.N / 2 : a.N;
@@ -468,13 +475,23 @@ cudaError_t launch_matmul_tiles(const MatmulArgs& a, int sms, cudaStream_t st) {
     if (!(a.swiglu ? make_pairs_map(enc, &map_w, a.w, a.E, outs, a.K)
                    : make_rows_map(enc, &map_w, a.w, (int64_t)a.E * a.N, a.K, kRows)) ||
         !make_rows_map(enc, &map_a, a.a, a.rows, a.K, kBoxTokens) ||
-        !make_rows_map(enc, &map_half, a.a, a.rows, a.K, kHalf))
+        !make_rows_map(enc, &map_half, a.a, a.rows, a.K, C::half))
         return cudaErrorInvalidValue;
-    const int64_t most = ((a.rows + kTileTokens - 1) / kTileTokens + (a.E > 1 ? a.E : 0)) * ((outs + per_pair - 1) / per_pair);
+    const int64_t most = ((a.rows + C::tile - 1) / C::tile + (a.E > 1 ? a.E : 0)) * ((outs + per_pair - 1) / per_pair);
     const int64_t pairs = most < sms / 2 ? most : sms / 2;
-    auto kernel = a.swiglu ? matmul_tiles_kernel<true> : matmul_tiles_kernel<false>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    auto kernel = a.swiglu ? matmul_tiles_kernel<C, true> : matmul_tiles_kernel<C, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(2 * pairs), kThreads, kSmem, st>>>(a, map_w, map_a, map_half);
+    kernel<<<(unsigned)(2 * pairs), kThreads, C::smem, st>>>(a, map_w, map_a, map_half);
     return cudaGetLastError();
+}
+
+#ifndef EP_MATMUL_THIN_ROWS
+#define EP_MATMUL_THIN_ROWS 64
+#endif
+
+}  // namespace
+
+cudaError_t launch_matmul_tiles(const MatmulArgs& a, int sms, cudaStream_t st) {
+    return a.rows <= (int64_t)a.E * EP_MATMUL_THIN_ROWS ? launch<Thin>(a, sms, st) : launch<Thick>(a, sms, st);
 }
