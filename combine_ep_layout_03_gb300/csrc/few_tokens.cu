@@ -15,6 +15,7 @@
 // warp order): results do not vary from run to run.
 #include "expert_ops.cuh"
 #include "skinny.cuh"
+#include "tensor_maps.cuh"
 
 namespace {
 
@@ -88,170 +89,318 @@ __device__ __forceinline__ float routing_weight(const FewArgs& a, int token, int
     return w;
 }
 
+// Two CTAs share an SM; what the routing and the sums leave of its shared memory goes to the rings.
+constexpr int kCtasPerSm = 2;
+
+// Sizes of both kernels by the largest number of token tiles.
+template <int MAXNT>
+struct Sizes {
+    static constexpr int depth = MAXNT == 1 ? 6 : MAXNT == 2 ? 5 : 4;
+    using Ring = WeightRing<depth>;
+    static constexpr int ring_bytes = kWarps * Ring::kWarpBytes;
+    // inner: [buffer][warp][column][16 rows]; two buffers in turn, so that one barrier an item is enough, but one
+    // where 64 columns make them large
+    static constexpr int buffers = MAXNT > 2 ? 1 : 2;
+    static constexpr int inner_smem = 1024 + ring_bytes + buffers * kWarps * MAXNT * 8 * 16 * 4;
+    static constexpr int out_smem = 1024 + ring_bytes + kWarps * MAXNT * 8 * 16 * 4;   // [warp][token][16 columns]
+    static_assert(kCtasPerSm * (inner_smem + (int)sizeof(Routing) + 1536) <= 228 * 1024, "two CTAs an SM");
+};
+
+__device__ __forceinline__ uint8_t* aligned_smem(uint8_t* p) {
+    return p + ((1024 - (smem_addr(p) & 1023)) & 1023);
+}
+
+// A warp's way through the pieces of few_inner_kernel: items item, item + step, ... and in each
+// the pieces warp, warp + 8, ...
+struct InnerCursor {
+    int item, tile, piece;
+    int expert;
+    __device__ __forceinline__ void place(const Routing& r, int items, int tiles) {
+        if (item >= items) return;
+        tile = item % tiles;
+        expert = r.expert[item / tiles];
+    }
+};
+
 // An item is eight inner channels of one expert: their gate rows are rows 0-7 of the
 // 16-row tile and their up rows 8-15, so a lane ends with both of a channel.  The warps
 // share the item's k and add their parts in shared memory.
-template <bool W8, int NT>
-__device__ __forceinline__ void inner_item(const FewArgs& a, const Routing& r, int pos, int tile, float* red) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-    const int e = r.expert[pos], row0 = r.base[pos], m = r.base[pos + 1] - row0;
-    const int k_bytes = a.H * (W8 ? 1 : 2);
-    const uint8_t* r0 = a.w13 + ((int64_t)e * 2 * a.I + tile * 8 + g) * k_bytes;
-    const uint8_t* r1 = r0 + (int64_t)a.I * k_bytes;
-    const uint8_t* tok[NT];
-    float acc[NT][4];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const int col = min(j * 8 + g, m - 1);   // columns past the last token repeat it and are not stored
-        tok[j] = reinterpret_cast<const uint8_t*>(a.x) + (int64_t)r.token[row0 + col] * a.H * 2;
-        acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-    }
-    mma_pieces<W8, false, NT, 1>(acc, r0, r1, tok, 0, warp, (k_bytes + 127) / 128, kWarps, q * 16, k_bytes);
-    // red[warp][column][16 rows]
-    float* mine = red + warp * NT * 8 * 16;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        mine[(j * 8 + 2 * q) * 16 + g] = acc[j][0];
-        mine[(j * 8 + 2 * q + 1) * 16 + g] = acc[j][1];
-        mine[(j * 8 + 2 * q) * 16 + g + 8] = acc[j][2];
-        mine[(j * 8 + 2 * q + 1) * 16 + g + 8] = acc[j][3];
-    }
-    __syncthreads();
-    for (int i = tid; i < m * 8; i += kThreads) {
-        const int col = i >> 3, c = i & 7, channel = tile * 8 + c;
-        float gate = 0.0f, up = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            gate += red[(w * NT * 8 + col) * 16 + c];
-            up += red[(w * NT * 8 + col) * 16 + c + 8];
-        }
-        if constexpr (W8) {
-            const float* sc = a.w13_scales + (int64_t)e * 2 * a.I + channel;
-            gate *= sc[0];
-            up *= sc[a.I];
-        }
-        const float h = gate / (1.0f + expf(-gate)) * up * routing_weight(a, r.token[row0 + col], e);
-        const uint32_t hi = pack_bf16x2_rn(h, 0.0f) & 0xffffu;
-        uint16_t* dst = a.inner + (int64_t)(row0 + col) * 2 * a.I + channel;
-        dst[0] = (uint16_t)hi;
-        dst[a.I] = (uint16_t)pack_bf16x2_rn(h - bf16_bits_to_float(hi), 0.0f);
-    }
-    __syncthreads();
-}
-
 template <bool W8, int MAXNT>
-__global__ void __launch_bounds__(kThreads) few_inner_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) few_inner_kernel(const FewArgs a, const __grid_constant__ CUtensorMap map_w) {
+    extern __shared__ uint8_t dynamic[];
     __shared__ Routing r;
-    __shared__ float red[kWarps * MAXNT * 8 * 16];
+    using S = Sizes<MAXNT>;
+    __shared__ uint64_t bars[kWarps * S::depth];
+    uint8_t* const slots = aligned_smem(dynamic);
+    constexpr int kBuffers = S::buffers, kSums = kWarps * MAXNT * 8 * 16;
+    float* const red = reinterpret_cast<float*>(slots + S::ring_bytes);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
     build_routing(r, a);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tiles = a.I / 8;
-    const int items = r.count * tiles;
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        const int pos = item / tiles, tile = item % tiles;
-        const int m = r.base[pos + 1] - r.base[pos];
-        if (MAXNT == 1 || m <= 8) inner_item<W8, 1>(a, r, pos, tile, red);
-        else if (MAXNT == 2 || m <= 16) inner_item<W8, (MAXNT < 2 ? MAXNT : 2)>(a, r, pos, tile, red);
-        else if (m <= 32) inner_item<W8, (MAXNT < 4 ? MAXNT : 4)>(a, r, pos, tile, red);
-        else inner_item<W8, MAXNT>(a, r, pos, tile, red);
-    }
-}
-
-// The part of one expert in a warp's range of pieces, added to the warp's own sums
-// [token][16 rows].
-template <bool W8, int NT>
-__device__ __forceinline__ void out_part(const FewArgs& a, const Routing& r, int pos, int h0, int first, int end,
-                                         float* sums) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int e = r.expert[pos], row0 = r.base[pos], m = r.base[pos + 1] - row0;
-    const int k_bytes = a.I * (W8 ? 1 : 2);
-    const int ra = min(h0 + g, a.H - 1), rb = min(h0 + g + 8, a.H - 1);   // rows past H are not stored
-    const uint8_t* w = a.w2 + (int64_t)e * a.H * k_bytes;
-    const uint8_t* tok[NT];
-    float acc[NT][4];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        tok[j] = reinterpret_cast<const uint8_t*>(a.inner) + (int64_t)(row0 + min(j * 8 + g, m - 1)) * a.I * 4;
-        acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-    }
-    mma_pieces<W8, false, NT, 2>(acc, w + (int64_t)ra * k_bytes, w + (int64_t)rb * k_bytes, tok, (int64_t)a.I * 2,
-                                 first, end, 1, q * 16, k_bytes);
-    float sa = 1.0f, sb = 1.0f;
-    if constexpr (W8) {
-        sa = a.w2_scales[(int64_t)e * a.H + ra];
-        sb = a.w2_scales[(int64_t)e * a.H + rb];
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const int col = j * 8 + 2 * q + c;
-            if (col < m) {
-                float* s = sums + r.token[row0 + col] * 16 + g;
-                s[0] += sa * acc[j][c];
-                s[8] += sb * acc[j][c + 2];
-            }
+    const int tiles = a.I / 8, items = r.count * tiles, step = gridDim.x;
+    const int k_bytes = a.H * (W8 ? 1 : 2), pieces = (k_bytes + 127) / 128;
+    typename S::Ring ring(slots, bars, warp, lane);
+    InnerCursor ahead;
+    ahead.item = pieces > warp ? (int)blockIdx.x : items;
+    ahead.piece = warp;
+    ahead.place(r, items, tiles);
+    auto fetch = [&]() {
+        if (ahead.item >= items) return;
+        ring.put(lane, 2048, [&](uint8_t* slot, uint64_t* bar) {
+            tma_load_4d(slot, &map_w, ahead.piece * 128, ahead.tile * 8, 0, ahead.expert, bar);
+        });
+        ahead.piece += kWarps;
+        if (ahead.piece >= pieces) {
+            ahead.piece = warp;
+            ahead.item += step;
+            ahead.place(r, items, tiles);
         }
+    };
+    for (int d = 0; d < S::depth; ++d) fetch();
+
+    int buffer = 0;
+    for (int item = blockIdx.x; item < items; item += step, buffer ^= 1) {
+        const int pos = item / tiles, tile = item % tiles;
+        const int e = r.expert[pos], row0 = r.base[pos], m = r.base[pos + 1] - row0;
+        const int nt = (m + 7) / 8;
+        float* sums = red + (kBuffers == 2 ? buffer * kSums : 0);
+        auto run = [&](auto count) {
+            constexpr int NT = decltype(count)::value;
+            const uint8_t* tok[NT];
+            float acc[NT][4];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int col = min(j * 8 + g, m - 1);   // columns past the last token repeat it and are not stored
+                tok[j] = reinterpret_cast<const uint8_t*>(a.x) + (int64_t)r.token[row0 + col] * a.H * 2;
+                acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+            }
+            TokenPart<W8> next;   // with one tile: the tokens of the next piece
+            if (NT == 1 && warp < pieces) load_tokens<W8, false>(next, tok[0], warp, q * 16, k_bytes);
+            for (int c = warp; c < pieces; c += kWarps) {
+                uint4 lo[2], hi[2];
+                const TokenPart<W8> now = next;
+                if (NT == 1) load_tokens<W8, false>(next, tok[0], c + kWarps, q * 16, k_bytes);
+                ring.take(lo, hi);
+                mma_piece<W8, NT, 1>(acc, lo, hi, [&](int j, int) {
+                    if constexpr (NT == 1) {
+                        return now;
+                    } else {
+                        TokenPart<W8> t;
+                        load_tokens<W8, false>(t, tok[j], c, q * 16, k_bytes);
+                        return t;
+                    }
+                });
+                __syncwarp();
+                fetch();
+            }
+            float* mine = sums + warp * NT * 8 * 16;   // [warp][column][16 rows]
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                mine[(j * 8 + 2 * q) * 16 + g] = acc[j][0];
+                mine[(j * 8 + 2 * q + 1) * 16 + g] = acc[j][1];
+                mine[(j * 8 + 2 * q) * 16 + g + 8] = acc[j][2];
+                mine[(j * 8 + 2 * q + 1) * 16 + g + 8] = acc[j][3];
+            }
+            return NT * 8;
+        };
+        const int cols = with_tiles<MAXNT>(nt, run);
+        __syncthreads();
+        for (int i = tid; i < m * 8; i += kThreads) {
+            const int col = i >> 3, c = i & 7, channel = tile * 8 + c;
+            float gate = 0.0f, up = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                gate += sums[(w * cols + col) * 16 + c];
+                up += sums[(w * cols + col) * 16 + c + 8];
+            }
+            if constexpr (W8) {
+                const float* sc = a.w13_scales + (int64_t)e * 2 * a.I + channel;
+                gate *= sc[0];
+                up *= sc[a.I];
+            }
+            const float h = gate / (1.0f + expf(-gate)) * up * routing_weight(a, r.token[row0 + col], e);
+            const uint32_t hi = pack_bf16x2_rn(h, 0.0f) & 0xffffu;
+            uint16_t* dst = a.inner + (int64_t)(row0 + col) * 2 * a.I + channel;
+            dst[0] = (uint16_t)hi;
+            dst[a.I] = (uint16_t)pack_bf16x2_rn(h - bf16_bits_to_float(hi), 0.0f);
+        }
+        if (kBuffers == 1) __syncthreads();
     }
-    __syncwarp();
+    if (!ring.drain() && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
 }
 
-// A CTA owns 16 columns of the output for every token.  The pieces of all experts form
-// one line, of which each warp takes an equal stretch.
+// A CTA owns `rows` <= 16 columns of the output at a time (tiles tile, tile + grid, ...) for every
+// token.  The pieces of all experts form one line, of which each warp takes an equal stretch.
+struct OutCursor {
+    int tile, at, piece, expert;   // at: place in the line of pieces
+    __device__ __forceinline__ void place(const Routing& r, int pieces) {
+        piece = at % pieces;
+        expert = r.expert[at / pieces];
+    }
+};
+
 template <bool W8, int MAXNT>
-__global__ void __launch_bounds__(kThreads) few_out_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) few_out_kernel(const FewArgs a, int rows, const __grid_constant__ CUtensorMap map_w) {
+    extern __shared__ uint8_t dynamic[];
     __shared__ Routing r;
-    extern __shared__ float sums[];   // [warp][token][16]
-    const int tid = threadIdx.x, warp = tid >> 5;
+    using S = Sizes<MAXNT>;
+    __shared__ uint64_t bars[kWarps * S::depth];
+    uint8_t* const slots = aligned_smem(dynamic);
+    float* const sums = reinterpret_cast<float*>(slots + S::ring_bytes);   // [warp][token][16]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
     for (int i = tid; i < kWarps * a.T * 16; i += kThreads) sums[i] = 0.0f;
     build_routing(r, a);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int h0 = blockIdx.x * 16;
-    const int pieces = (a.I * (W8 ? 1 : 2) + 127) / 128;
-    const int total = r.count * pieces;
+    const int k_bytes = a.I * (W8 ? 1 : 2), pieces = (k_bytes + 127) / 128;
+    const int total = r.count * pieces, tiles = (a.H + rows - 1) / rows;
     const int begin = (int)((int64_t)total * warp / kWarps), end = (int)((int64_t)total * (warp + 1) / kWarps);
+    const int64_t plane = (int64_t)a.I * 2;
+    typename S::Ring ring(slots, bars, warp, lane);
+    OutCursor ahead;
+    ahead.tile = begin < end ? (int)blockIdx.x : tiles;
+    ahead.at = begin;
+    if (ahead.tile < tiles) ahead.place(r, pieces);
+    auto fetch = [&]() {
+        if (ahead.tile >= tiles) return;
+        ring.put(lane, 128 * rows, [&](uint8_t* slot, uint64_t* bar) {
+            tma_load_3d(slot, &map_w, ahead.piece * 128, ahead.tile * rows, ahead.expert, bar);
+        });
+        ++ahead.piece;
+        if (++ahead.at == end) {
+            ahead.at = begin;
+            ahead.tile += gridDim.x;
+            if (ahead.tile < tiles) ahead.place(r, pieces);
+        } else if (ahead.piece == pieces) {
+            ahead.place(r, pieces);
+        }
+    };
+    // the weights do not depend on the first kernel: they are on their way while it ends
+    for (int d = 0; d < S::depth; ++d) fetch();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
     float* mine = sums + warp * a.T * 16;
-    for (int at = begin; at < end;) {
-        const int pos = at / pieces, first = at % pieces, last = min(pieces, first + end - at);
-        const int m = r.base[pos + 1] - r.base[pos];
-        if (MAXNT == 1 || m <= 8) out_part<W8, 1>(a, r, pos, h0, first, last, mine);
-        else if (MAXNT == 2 || m <= 16) out_part<W8, (MAXNT < 2 ? MAXNT : 2)>(a, r, pos, h0, first, last, mine);
-        else if (m <= 32) out_part<W8, (MAXNT < 4 ? MAXNT : 4)>(a, r, pos, h0, first, last, mine);
-        else out_part<W8, MAXNT>(a, r, pos, h0, first, last, mine);
-        at += last - first;
-    }
-    __syncthreads();
-    for (int i = tid; i < a.T * 16; i += kThreads) {
-        const int t = i >> 4, h = h0 + (i & 15);
-        if (h >= a.H) continue;
-        float s = 0.0f;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int h0 = tile * rows;
+        for (int at = begin; at < end;) {
+            const int pos = at / pieces, first = at % pieces, last = min(pieces, first + end - at);
+            const int e = r.expert[pos], row0 = r.base[pos], m = r.base[pos + 1] - row0;
+            auto run = [&](auto count) {
+                constexpr int NT = decltype(count)::value;
+                const uint8_t* tok[NT];
+                float acc[NT][4];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) s += sums[w * a.T * 16 + i];
-        for (int k = 0; k < a.S; ++k) s += bf16_bits_to_float(a.shared[((int64_t)k * a.T + t) * a.H + h]);
-        a.out[(int64_t)t * a.H + h] = (uint16_t)pack_bf16x2_rn(s, 0.0f);
+                for (int j = 0; j < NT; ++j) {
+                    tok[j] = reinterpret_cast<const uint8_t*>(a.inner) + (int64_t)(row0 + min(j * 8 + g, m - 1)) * a.I * 4;
+                    acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+                }
+                TokenPart<W8> next[2];   // with one tile: the inner rows of the next piece
+                if (NT == 1) {
+                    load_tokens<W8, false>(next[0], tok[0], first, q * 16, k_bytes);
+                    load_tokens<W8, false>(next[1], tok[0] + plane, first, q * 16, k_bytes);
+                }
+                for (int c = first; c < last; ++c) {
+                    uint4 lo[2], hi[2];
+                    const TokenPart<W8> now[2] = {next[0], next[1]};
+                    if (NT == 1) {
+                        load_tokens<W8, false>(next[0], tok[0], c + 1, q * 16, k_bytes);
+                        load_tokens<W8, false>(next[1], tok[0] + plane, c + 1, q * 16, k_bytes);
+                    }
+                    ring.take(lo, hi);
+                    mma_piece<W8, NT, 2>(acc, lo, hi, [&](int j, int pl) {
+                        if constexpr (NT == 1) {
+                            return now[pl];
+                        } else {
+                            TokenPart<W8> t;
+                            load_tokens<W8, false>(t, tok[j] + pl * plane, c, q * 16, k_bytes);
+                            return t;
+                        }
+                    });
+                    __syncwarp();
+                    fetch();
+                }
+                float sa = 1.0f, sb = 1.0f;
+                if constexpr (W8) {
+                    sa = a.w2_scales[(int64_t)e * a.H + min(h0 + g, a.H - 1)];
+                    sb = a.w2_scales[(int64_t)e * a.H + min(h0 + g + 8, a.H - 1)];
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int col = j * 8 + 2 * q + c;
+                        if (col < m) {
+                            float* s = mine + r.token[row0 + col] * 16 + g;
+                            s[0] += sa * acc[j][c];
+                            s[8] += sb * acc[j][c + 2];
+                        }
+                    }
+                }
+                __syncwarp();
+                return 0;
+            };
+            with_tiles<MAXNT>((m + 7) / 8, run);
+            at += last - first;
+        }
+        __syncthreads();
+        for (int i = tid; i < a.T * 16; i += kThreads) {
+            const int t = i >> 4, h = h0 + (i & 15);
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                s += sums[w * a.T * 16 + i];
+                sums[w * a.T * 16 + i] = 0.0f;
+            }
+            if ((i & 15) >= rows || h >= a.H) continue;
+            for (int k = 0; k < a.S; ++k) s += bf16_bits_to_float(a.shared[((int64_t)k * a.T + t) * a.H + h]);
+            a.out[(int64_t)t * a.H + h] = (uint16_t)pack_bf16x2_rn(s, 0.0f);
+        }
+        __syncthreads();
     }
+    if (!ring.drain() && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
+}
+
+// Output columns of a CTA's tile, 12 to 16: those that leave the last round of CTAs fullest.
+int rows_of_tile(int H, int ctas) {
+    int best = 16;
+    int64_t least = INT64_MAX;
+    for (int rows = 16; rows >= 12; --rows) {
+        const int tiles = (H + rows - 1) / rows;
+        const int64_t time = (int64_t)((tiles + ctas - 1) / ctas) * (rows + 3);
+        if (time < least) { least = time; best = rows; }
+    }
+    return best;
 }
 
 template <bool W8, int MAXNT>
 cudaError_t launch(const FewArgs& a, int sms, cudaStream_t st) {
     const int64_t entries = (int64_t)a.T * a.K;
     const int64_t items = (entries < a.E ? entries : a.E) * (a.I / 8);
-    const int64_t most = (int64_t)sms * 4;
-    few_inner_kernel<W8, MAXNT><<<(unsigned)(items < most ? items : most), kThreads, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
+    const int ctas = sms * kCtasPerSm;
+    using S = Sizes<MAXNT>;
+    const int rows = rows_of_tile(a.H, ctas), tiles = (a.H + rows - 1) / rows;
+    const int64_t width = W8 ? 1 : 2;
+    CUtensorMap map13, map2;
+    if (!make_pairs_map(&map13, a.w13, a.E, a.I, a.H * width, 8) || !make_experts_map(&map2, a.w2, a.E, a.H, a.I * width, rows))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(few_inner_kernel<W8, MAXNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::inner_smem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(few_out_kernel<W8, MAXNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::out_smem);
     if (e != cudaSuccess) return e;
-    // The second kernel may start while the first drains: it reads the routing, then waits.
+    few_inner_kernel<W8, MAXNT><<<(unsigned)(items < ctas ? items : ctas), kThreads, S::inner_smem, st>>>(a, map13);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // The second kernel may start while the first drains: it reads the routing, fetches its first
+    // weights, then waits.
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3((unsigned)((a.H + 15) / 16));
+    cfg.gridDim = dim3((unsigned)(tiles < ctas ? tiles : ctas));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = sizeof(float) * kWarps * (size_t)a.T * 16;
+    cfg.dynamicSmemBytes = S::out_smem;
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, few_out_kernel<W8, MAXNT>, a);
+    e = cudaLaunchKernelEx(&cfg, few_out_kernel<W8, MAXNT>, a, rows, map2);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

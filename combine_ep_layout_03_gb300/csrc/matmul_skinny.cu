@@ -2,84 +2,126 @@
 // rows each, where reading the weights is the work:
 //   c[r, n] = a_scales[r] * w_scales[e, n] * sum_k a[r, k] * w[e, n, k]
 // An item is 16 weight rows (eight gates and their eight ups with swiglu) against up to
-// 64 rows of one expert: the warps of a CTA share the item's k and add their parts in
+// 32 rows of one expert: the warps of a CTA share the item's k and add their parts in
 // shared memory, in warp order.  The codes become bf16 on the way to the tensor cores,
 // which is exact, and a product of two codes is exact in float32; sums stay exact up to
 // 2^24 (1040 terms of the largest size, any number of ordinary ones).
 #include "expert_ops.cuh"
 #include "skinny.cuh"
+#include "tensor_maps.cuh"
 
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTileRows = 64;
+constexpr int kTileRows = 32;
+constexpr int kDepth = 4;                              // pieces in flight a warp
+using Ring = WeightRing<kDepth>;
+constexpr int kRingBytes = kWarps * Ring::kWarpBytes;
+constexpr int kSums = kWarps * kTileRows * 16;         // [warp][column][16 rows]
+constexpr int kSmem = 1024 + kRingBytes + 2 * kSums * (int)sizeof(float);
 
-template <bool GLU, int NT>
-__device__ __forceinline__ void matmul_item(const MatmulArgs& a, int e, int64_t row0, int m, int tile, float* red) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-    const int outs = GLU ? a.N / 2 : a.N, ch0 = tile * (GLU ? 8 : 16);
-    // rows past the last repeat it and are not stored
-    const int n0 = min(ch0 + g, outs - 1), n1 = GLU ? n0 + outs : min(ch0 + g + 8, outs - 1);
-    const uint8_t* w = a.w + (int64_t)e * a.N * a.K;
-    const uint8_t* tok[NT];
-    float acc[NT][4];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        tok[j] = a.a + (row0 + min(j * 8 + g, m - 1)) * a.K;
-        acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-    }
-    mma_pieces<true, true, NT, 1>(acc, w + (int64_t)n0 * a.K, w + (int64_t)n1 * a.K, tok, 0, warp, (a.K + 127) / 128,
-                                  kWarps, q * 16, a.K);
-    float* mine = red + warp * NT * 8 * 16;   // [warp][column][16 rows]
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        mine[(j * 8 + 2 * q) * 16 + g] = acc[j][0];
-        mine[(j * 8 + 2 * q + 1) * 16 + g] = acc[j][1];
-        mine[(j * 8 + 2 * q) * 16 + g + 8] = acc[j][2];
-        mine[(j * 8 + 2 * q + 1) * 16 + g + 8] = acc[j][3];
-    }
-    __syncthreads();
-    constexpr int per = GLU ? 8 : 16;
-    for (int i = tid; i < m * per; i += kThreads) {
-        const int col = i / per, c = i % per, ch = ch0 + c;
-        if (ch >= outs) continue;
-        float v = 0.0f, u = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-            v += red[(k * NT * 8 + col) * 16 + c];
-            if constexpr (GLU) u += red[(k * NT * 8 + col) * 16 + c + 8];
-        }
-        const int64_t row = row0 + col;
-        const float sa = a.a_scales[row];
-        const float* sw = a.w_scales + (int64_t)e * a.N + ch;
-        v = v * sa * sw[0];
-        if constexpr (GLU) v = v / (1.0f + expf(-v)) * (u * sa * sw[outs]);
-        a.out[row * outs + ch] = (uint16_t)pack_bf16x2_rn(v, 0.0f);
-    }
-    __syncthreads();
+// Where an item lies: tiles of one expert are neighbours, its token tiles fastest (they read the same weights).
+struct Item { int e, channel, first, m; };
+
+__device__ __forceinline__ Item item_of(const Segments& s, const MatmulArgs& a, int ctiles, int64_t item) {
+    Item t;
+    t.e = expert_of_tile(s, a.E, (int)(item / ctiles));
+    const int tiles = s.tile[t.e + 1] - s.tile[t.e];
+    const int local = (int)(item - (int64_t)s.tile[t.e] * ctiles);
+    t.first = local % tiles * kTileRows;
+    t.channel = local / tiles;
+    t.m = min(kTileRows, s.rows[t.e] - t.first);
+    return t;
 }
 
 template <bool GLU>
-__global__ void __launch_bounds__(kThreads) matmul_skinny_kernel(const MatmulArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) matmul_skinny_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_w) {
+    extern __shared__ uint8_t dynamic[];
+    __shared__ uint64_t bars[kWarps * kDepth];
+    uint8_t* const slots = dynamic + ((1024 - (smem_addr(dynamic) & 1023)) & 1023);
     __shared__ Segments s;
-    __shared__ float red[kWarps * kTileRows * 16];
+    float* const red = reinterpret_cast<float*>(slots + kRingBytes);   // two buffers in turn: a barrier an item
     if (!load_segments<kThreads>(s, a, kTileRows)) return;
-    const int channels = GLU ? 8 : 16, outs = GLU ? a.N / 2 : a.N;
-    const int ctiles = (outs + channels - 1) / channels;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+    constexpr int per = GLU ? 8 : 16;   // output channels of an item
+    const int outs = GLU ? a.N / 2 : a.N, ctiles = (outs + per - 1) / per, pieces = (a.K + 127) / 128;
     const int64_t items = (int64_t)s.tile[a.E] * ctiles;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        // an expert's items are neighbours, its token tiles fastest: they read the same weights
-        const int e = expert_of_tile(s, a.E, (int)(item / ctiles));
-        const int tiles = s.tile[e + 1] - s.tile[e];
-        const int local = (int)(item - (int64_t)s.tile[e] * ctiles);
-        const int first = local % tiles * kTileRows, m = min(kTileRows, s.rows[e] - first);
-        const int64_t row0 = (int64_t)s.base[e] + first;
-        if (m <= 8) matmul_item<GLU, 1>(a, e, row0, m, local / tiles, red);
-        else if (m <= 16) matmul_item<GLU, 2>(a, e, row0, m, local / tiles, red);
-        else if (m <= 32) matmul_item<GLU, 4>(a, e, row0, m, local / tiles, red);
-        else matmul_item<GLU, 8>(a, e, row0, m, local / tiles, red);
+
+    Ring ring(slots, bars, warp, lane);
+    int64_t ahead = warp < pieces ? (int64_t)blockIdx.x : items;
+    int ahead_piece = warp;
+    Item at{};
+    if (ahead < items) at = item_of(s, a, ctiles, ahead);
+    auto fetch = [&]() {
+        if (ahead >= items) return;
+        ring.put(lane, 2048, [&](uint8_t* slot, uint64_t* bar) {
+            if (GLU) tma_load_4d(slot, &map_w, ahead_piece * 128, at.channel * per, 0, at.e, bar);
+            else tma_load_3d(slot, &map_w, ahead_piece * 128, at.channel * per, at.e, bar);
+        });
+        ahead_piece += kWarps;
+        if (ahead_piece >= pieces) {
+            ahead_piece = warp;
+            ahead += gridDim.x;
+            if (ahead < items) at = item_of(s, a, ctiles, ahead);
+        }
+    };
+    for (int d = 0; d < kDepth; ++d) fetch();
+
+    int buffer = 0;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x, buffer ^= 1) {
+        const Item t = item_of(s, a, ctiles, item);
+        const int64_t row0 = (int64_t)s.base[t.e] + t.first;
+        float* sums = red + buffer * kSums;
+        auto run = [&](auto count) {
+            constexpr int NT = decltype(count)::value;
+            const uint8_t* tok[NT];
+            float acc[NT][4];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                tok[j] = a.a + (row0 + min(j * 8 + g, t.m - 1)) * a.K;   // columns past the last repeat it
+                acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+            }
+            for (int c = warp; c < pieces; c += kWarps) {
+                TokenPart<true> part[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) load_tokens<true, true>(part[j], tok[j], c, q * 16, a.K);
+                uint4 lo[2], hi[2];
+                ring.take(lo, hi);
+                mma_piece<true, NT, 1>(acc, lo, hi, [&](int j, int) { return part[j]; });
+                __syncwarp();
+                fetch();
+            }
+            float* mine = sums + warp * NT * 8 * 16;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                mine[(j * 8 + 2 * q) * 16 + g] = acc[j][0];
+                mine[(j * 8 + 2 * q + 1) * 16 + g] = acc[j][1];
+                mine[(j * 8 + 2 * q) * 16 + g + 8] = acc[j][2];
+                mine[(j * 8 + 2 * q + 1) * 16 + g + 8] = acc[j][3];
+            }
+            return NT * 8;
+        };
+        const int cols = with_tiles<4>((t.m + 7) / 8, run);
+        __syncthreads();
+        for (int i = tid; i < t.m * per; i += kThreads) {
+            const int col = i / per, c = i % per, ch = t.channel * per + c;
+            if (ch >= outs) continue;
+            float v = 0.0f, u = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                v += sums[(k * cols + col) * 16 + c];
+                if constexpr (GLU) u += sums[(k * cols + col) * 16 + c + 8];
+            }
+            const int64_t row = row0 + col;
+            const float sa = a.a_scales[row];
+            const float* sw = a.w_scales + (int64_t)t.e * a.N + ch;
+            v = v * sa * sw[0];
+            if constexpr (GLU) v = v / (1.0f + expf(-v)) * (u * sa * sw[outs]);
+            a.out[row * outs + ch] = (uint16_t)pack_bf16x2_rn(v, 0.0f);
+        }
     }
+    if (!ring.drain() && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
 }
 
 #ifndef EP_MATMUL_TILE_ROWS
@@ -93,10 +135,15 @@ bool aligned(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
 cudaError_t launch_matmul_skinny(const MatmulArgs& a, int sms, cudaStream_t st) {
     const int64_t ctiles = a.swiglu ? (a.N / 2 + 7) / 8 : (a.N + 15) / 16;
     const int64_t most_tiles = (a.rows + kTileRows - 1) / kTileRows + (a.E > 1 ? a.E : 0);
-    const int64_t items = ctiles * most_tiles, most = (int64_t)sms * 8;
-    const unsigned grid = (unsigned)(items < most ? items : most);
-    if (a.swiglu) matmul_skinny_kernel<true><<<grid, kThreads, 0, st>>>(a);
-    else matmul_skinny_kernel<false><<<grid, kThreads, 0, st>>>(a);
+    const int64_t items = ctiles * most_tiles;
+    const unsigned grid = (unsigned)(items < 2 * sms ? items : 2 * sms);
+    auto kernel = a.swiglu ? matmul_skinny_kernel<true> : matmul_skinny_kernel<false>;
+    CUtensorMap map_w;
+    if (!(a.swiglu ? make_pairs_map(&map_w, a.w, a.E, a.N / 2, a.K, 8) : make_experts_map(&map_w, a.w, a.E, a.N, a.K, 16)))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThreads, kSmem, st>>>(a, map_w);
     return cudaGetLastError();
 }
 

@@ -22,10 +22,9 @@
 // Warps: 0 TMA, 1 MMA (of the pair's first CTA), 2 tensor memory, 4-7 epilogue, 8-15 weights
 // to float16 (8-11 the first 64 k of a TMA stage, 12-15 the second), 16-23 tokens likewise: one
 // step of a warp, from its wait to its arrival, takes longer than the MMAs of 64 k.  Every wait is bounded (EP_ERR_TIMEOUT).
-#include <atomic>
-
 #include "expert_ops.cuh"
 #include "tcgen05.cuh"
+#include "tensor_maps.cuh"
 
 namespace {
 
@@ -425,57 +424,14 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
     if (warp == 2) tmem_free_pair(w.tmem, kColumns);
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-    static std::atomic<void*> entry{nullptr};
-    void* p = entry.load(std::memory_order_relaxed);
-    if (!p) {
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
-                cudaSuccess || found != cudaDriverEntryPointSuccess)
-            return nullptr;
-        entry.store(p, std::memory_order_relaxed);
-    }
-    return (EncodeTiled)p;
-}
-
-// Codes in boxes of 128 bytes x rows, 128-byte swizzle; zeros outside.
-bool make_map(EncodeTiled enc, CUtensorMap* map, const void* p, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-              const cuuint32_t* box) {
-    const cuuint32_t unit[4] = {1, 1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(p), dims, strides, box, unit,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// [rows][bytes]
-bool make_rows_map(EncodeTiled enc, CUtensorMap* map, const void* p, int64_t rows, int64_t bytes, int box_rows) {
-    const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)bytes};
-    const cuuint32_t box[2] = {kRawK, (cuuint32_t)box_rows};
-    return make_map(enc, map, p, 2, dims, strides, box);
-}
-
-// [E][gate, up][n][bytes], 16 gates and their ups a box
-bool make_pairs_map(EncodeTiled enc, CUtensorMap* map, const void* p, int64_t E, int64_t n, int64_t bytes) {
-    const cuuint64_t dims[4] = {(cuuint64_t)bytes, (cuuint64_t)n, 2, (cuuint64_t)E};
-    const cuuint64_t strides[3] = {(cuuint64_t)bytes, (cuuint64_t)(n * bytes), (cuuint64_t)(2 * n * bytes)};
-    const cuuint32_t box[4] = {kRawK, 16, 2, 1};
-    return make_map(enc, map, p, 4, dims, strides, box);
-}
-
 template <class C>
 cudaError_t launch(const MatmulArgs& a, int sms, cudaStream_t st) {
-    EncodeTiled enc = encode_tiled();
-    if (!enc) return cudaErrorNotSupported;
     const int64_t per_pair = a.swiglu ? kRows : 2 * kRows, outs = a.swiglu ? a.N / 2 : a.N;
     CUtensorMap map_w, map_a, map_half;
-    if (!(a.swiglu ? make_pairs_map(enc, &map_w, a.w, a.E, outs, a.K)
-                   : make_rows_map(enc, &map_w, a.w, (int64_t)a.E * a.N, a.K, kRows)) ||
-        !make_rows_map(enc, &map_a, a.a, a.rows, a.K, kBoxTokens) ||
-        !make_rows_map(enc, &map_half, a.a, a.rows, a.K, C::half))
+    if (!(a.swiglu ? make_pairs_map(&map_w, a.w, a.E, outs, a.K, 16)
+                   : make_rows_map(&map_w, a.w, (int64_t)a.E * a.N, a.K, kRows)) ||
+        !make_rows_map(&map_a, a.a, a.rows, a.K, kBoxTokens) ||
+        !make_rows_map(&map_half, a.a, a.rows, a.K, C::half))
         return cudaErrorInvalidValue;
     const int64_t most = ((a.rows + C::tile - 1) / C::tile + (a.E > 1 ? a.E : 0)) * ((outs + per_pair - 1) / per_pair);
     const int64_t pairs = most < sms / 2 ? most : sms / 2;

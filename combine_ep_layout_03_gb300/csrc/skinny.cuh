@@ -1,16 +1,18 @@
 // skinny.cuh -- the inner loop of matrix products with few token rows, where
-// reading the weights once is the work: 16 weight rows against up to 64 tokens a
-// warp, straight from global memory to the tensor cores.
+// reading the weights once is the work: 16 weight rows against up to 64 tokens a warp.
 //
 // mma.sync m16n8k16 takes the weights as its 16-row operand and the tokens as its 8
 // columns.  A dot product does not care in which order its terms are taken, so the
 // 16 columns k that one instruction covers need not be neighbours: each lane loads 16
 // contiguous bytes of a weight row and the same k of a token row, and feeds them to
-// consecutive instructions as they lie.  No shared memory, no shuffles; the four lanes
-// of a row cover 64 contiguous bytes, two such loads a whole 128-byte line.  The legacy
+// consecutive instructions as they lie, without a shuffle; the four lanes of a row cover 64
+// contiguous bytes, two such loads a whole 128-byte line.  The legacy
 // tensor path is ample here: at 6.8 TB/s the weights arrive at 22 bytes a clock an SM.
 #pragma once
 
+#include <type_traits>
+
+#include "tcgen05.cuh"
 #include "ep_internal.cuh"
 
 namespace {
@@ -38,92 +40,153 @@ __device__ __forceinline__ void int8x4_to_bf16(uint32_t w, uint32_t& lo, uint32_
     hi = int8x2_to_bf16x2<0x4342>(w);
 }
 
-__device__ __forceinline__ uint4 ld_weights(const uint8_t* p) {   // read once: no L1 line is kept
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
+// A warp's weights arrive through a ring of DEPTH slots of its own in shared memory, each one
+// 128-byte piece of 16 weight rows (2 KB), by TMA: one lane issues a slot's box, the warp waits
+// on the slot's mbarrier, reads, and the slot is filled again.  No warp waits for another, so the
+// ring keeps running through the barriers and sums between one unit of work and the next.
+// (cp.async in 16-byte chunks, and loads to registers, reach two thirds of the rate: what arrives
+// in 32-byte sectors is written to shared memory or registers a sector at a time, 20 accesses for
+// 512 bytes.)  Every wait is bounded; after one that gave up the ring waits for nothing more.
+template <int DEPTH>
+struct WeightRing {
+    static constexpr int kSlot = 2048, kWarpBytes = DEPTH * kSlot;
+    uint8_t* slots;
+    uint64_t* bars;
+    uint32_t lane_off;   // of this lane's chunk in a slot (row g, the first half of a piece)
+    int put_slot = 0, take_slot = 0, armed = 0;
+    uint32_t parity = 0;
+    bool ok = true;
 
-// One 128-byte piece of two weight rows (this lane's part): rows g and g + 8 of the tile.
-struct Piece { uint4 lo[2], hi[2]; };
+    // smem: 1024-byte aligned, kWarpBytes a warp; barriers: DEPTH a warp.
+    __device__ __forceinline__ WeightRing(uint8_t* smem, uint64_t* barriers, int warp, int lane)
+        : slots(smem + warp * kWarpBytes), bars(barriers + warp * DEPTH) {
+        const int g = lane >> 2, q = lane & 3;
+        lane_off = (uint32_t)__cvta_generic_to_shared(slots) + g * 128 + ((q ^ g) * 16);   // 128-byte swizzle
+        if (lane == 0) {
+            for (int i = 0; i < DEPTH; ++i) mbar_init(&bars[i], 1);
+            mbar_fence_init();
+        }
+        __syncwarp();
+    }
 
-// k_bytes: bytes of a weight row; a lane's 16 bytes past its end read as zero.
-__device__ __forceinline__ void load_piece(Piece& p, const uint8_t* r0, const uint8_t* r1, int piece, int lane_off,
-                                           int k_bytes) {
+    // load(slot, barrier) issues the box of `bytes` bytes (one lane).
+    template <class Load>
+    __device__ __forceinline__ void put(int lane, uint32_t bytes, Load load) {
+        if (lane == 0 && ok) {
+            mbar_arrive_expect_tx(&bars[put_slot], bytes);
+            load(slots + put_slot * kSlot, &bars[put_slot]);
+        }
+        ++armed;
+        put_slot = put_slot + 1 == DEPTH ? 0 : put_slot + 1;
+    }
+
+    // This lane's part of the oldest slot: rows g (lo) and g + 8 (hi) of the two 64-byte halves.
+    __device__ __forceinline__ void take(uint4 lo[2], uint4 hi[2]) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars[take_slot], parity, kMaxPolls));
+        --armed;
+        const uint32_t at = lane_off + take_slot * kSlot;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            lo[h] = lds(at ^ (h * 64));
+            hi[h] = lds((at ^ (h * 64)) + 1024);
+        }
+        if (++take_slot == DEPTH) { take_slot = 0; parity ^= 1; }
+    }
+
+    // Nothing is in flight when the CTA ends.  False: a wait gave up.
+    __device__ __forceinline__ bool drain() {
+        for (; armed > 0; --armed) {
+            ok = mbar_wait(&bars[take_slot], parity, kMaxPolls) && ok;
+            if (++take_slot == DEPTH) { take_slot = 0; parity ^= 1; }
+        }
+        return ok;
+    }
+
+    static __device__ __forceinline__ uint4 lds(uint32_t addr) {
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+        return v;
+    }
+};
+
+// The token side of one piece for a tile of eight tokens: this lane's values, as bf16 pairs.
+template <bool W8>
+struct TokenPart { uint32_t b[2][W8 ? 8 : 4]; };
+
+// tok: the token's row (bf16, or int8 with T8); a lane's values past the row's end read as zero.
+template <bool W8, bool T8>
+__device__ __forceinline__ void load_tokens(TokenPart<W8>& t, const uint8_t* tok, int piece, int lane_off, int k_bytes) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int off = piece * 128 + h * 64 + lane_off;
         const bool in = off < k_bytes;
-        p.lo[h] = in ? ld_weights(r0 + off) : make_uint4(0, 0, 0, 0);
-        p.hi[h] = in ? ld_weights(r1 + off) : make_uint4(0, 0, 0, 0);
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        if constexpr (T8) {
+            const uint4 v = in ? *reinterpret_cast<const uint4*>(tok + off) : zero;
+            int8x4_to_bf16(v.x, t.b[h][0], t.b[h][1]); int8x4_to_bf16(v.y, t.b[h][2], t.b[h][3]);
+            int8x4_to_bf16(v.z, t.b[h][4], t.b[h][5]); int8x4_to_bf16(v.w, t.b[h][6], t.b[h][7]);
+        } else {
+            const uint8_t* p = tok + (int64_t)off * (W8 ? 2 : 1);
+            const uint4 v = in ? *reinterpret_cast<const uint4*>(p) : zero;
+            t.b[h][0] = v.x; t.b[h][1] = v.y; t.b[h][2] = v.z; t.b[h][3] = v.w;
+            if constexpr (W8) {
+                const uint4 w = in ? *reinterpret_cast<const uint4*>(p + 16) : zero;
+                t.b[h][4] = w.x; t.b[h][5] = w.y; t.b[h][6] = w.z; t.b[h][7] = w.w;
+            }
+        }
     }
 }
 
-// acc += the piece's products with NT tiles of eight token rows.  tok[j]: the row of this
-// lane's column in tile j (bf16, or int8 with T8); PLANES 2 adds a second row `plane`
-// elements further (a value's remainder, see few_tokens.cu).
-template <bool W8, bool T8, int NT, int PLANES>
-__device__ __forceinline__ void mma_piece(float (*acc)[4], const Piece& p, const uint8_t* const* tok, int64_t plane,
-                                          int piece, int lane_off, int k_bytes) {
+// Calls f with the number of tiles of eight columns as a constant: 1, 2, 4 or 8, at most MAXNT.
+template <int MAXNT, class F>
+__device__ __forceinline__ int with_tiles(int tiles, F&& f) {
+    using std::integral_constant;
+    if constexpr (MAXNT >= 2) {
+        if (tiles > 1) {
+            if constexpr (MAXNT >= 8) {
+                if (tiles > 4) return f(integral_constant<int, 8>{});
+            }
+            if constexpr (MAXNT >= 4) {
+                if (tiles > 2) return f(integral_constant<int, 4>{});
+            }
+            return f(integral_constant<int, 2>{});
+        }
+    }
+    return f(integral_constant<int, 1>{});
+}
+
+// The weights of half a piece as bf16 pairs.
+template <bool W8>
+__device__ __forceinline__ void unpack_weights(const uint4& v, uint32_t* a) {
+    if constexpr (W8) {
+        int8x4_to_bf16(v.x, a[0], a[1]); int8x4_to_bf16(v.y, a[2], a[3]);
+        int8x4_to_bf16(v.z, a[4], a[5]); int8x4_to_bf16(v.w, a[6], a[7]);
+    } else {
+        a[0] = v.x; a[1] = v.y; a[2] = v.z; a[3] = v.w;
+    }
+}
+
+// acc += one piece's products with NT tiles of eight tokens.  part(j, plane) gives the token side;
+// PLANES 2 multiplies by a second set of token rows as well (a value's remainder).
+template <bool W8, int NT, int PLANES, class Part>
+__device__ __forceinline__ void mma_piece(float (*acc)[4], const uint4 lo[2], const uint4 hi[2], Part part) {
+    uint32_t a0[2][W8 ? 8 : 4], a1[2][W8 ? 8 : 4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int off = piece * 128 + h * 64 + lane_off;
-        const bool in = off < k_bytes;
-        uint32_t a0[8], a1[8];   // the lane's weights of rows g and g + 8 as bf16 pairs
-        if constexpr (W8) {
-            int8x4_to_bf16(p.lo[h].x, a0[0], a0[1]); int8x4_to_bf16(p.lo[h].y, a0[2], a0[3]);
-            int8x4_to_bf16(p.lo[h].z, a0[4], a0[5]); int8x4_to_bf16(p.lo[h].w, a0[6], a0[7]);
-            int8x4_to_bf16(p.hi[h].x, a1[0], a1[1]); int8x4_to_bf16(p.hi[h].y, a1[2], a1[3]);
-            int8x4_to_bf16(p.hi[h].z, a1[4], a1[5]); int8x4_to_bf16(p.hi[h].w, a1[6], a1[7]);
-        } else {
-            a0[0] = p.lo[h].x; a0[1] = p.lo[h].y; a0[2] = p.lo[h].z; a0[3] = p.lo[h].w;
-            a1[0] = p.hi[h].x; a1[1] = p.hi[h].y; a1[2] = p.hi[h].z; a1[3] = p.hi[h].w;
-        }
+        unpack_weights<W8>(lo[h], a0[h]);
+        unpack_weights<W8>(hi[h], a1[h]);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
 #pragma unroll
         for (int pl = 0; pl < PLANES; ++pl) {
+            const TokenPart<W8> t = part(j, pl);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                uint32_t b[8];
-                const uint4 zero = make_uint4(0, 0, 0, 0);
-                if constexpr (T8) {
-                    const uint4 v = in ? *reinterpret_cast<const uint4*>(tok[j] + off) : zero;
-                    int8x4_to_bf16(v.x, b[0], b[1]); int8x4_to_bf16(v.y, b[2], b[3]);
-                    int8x4_to_bf16(v.z, b[4], b[5]); int8x4_to_bf16(v.w, b[6], b[7]);
-                } else {
-                    const uint8_t* t = tok[j] + pl * plane + (int64_t)off * (W8 ? 2 : 1);
-                    const uint4 v = in ? *reinterpret_cast<const uint4*>(t) : zero;
-                    b[0] = v.x; b[1] = v.y; b[2] = v.z; b[3] = v.w;
-                    if constexpr (W8) {
-                        const uint4 w = in ? *reinterpret_cast<const uint4*>(t + 16) : zero;
-                        b[4] = w.x; b[5] = w.y; b[6] = w.z; b[7] = w.w;
-                    }
-                }
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < (W8 ? 4 : 2); ++i)
-                    mma_bf16(acc[j], a0[2 * i], a1[2 * i], a0[2 * i + 1], a1[2 * i + 1], b[2 * i], b[2 * i + 1]);
-            }
-        }
-    }
-}
-
-// Pieces first, first + step, ... below end, the loads of the next DEPTH pieces in flight.
-template <bool W8, bool T8, int NT, int PLANES, int DEPTH = 2>
-__device__ __forceinline__ void mma_pieces(float (*acc)[4], const uint8_t* r0, const uint8_t* r1,
-                                           const uint8_t* const* tok, int64_t plane, int first, int end, int step,
-                                           int lane_off, int k_bytes) {
-    Piece p[DEPTH];
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-        load_piece(p[d], r0, r1, first + d * step, lane_off, first + d * step < end ? k_bytes : 0);
-    for (int c = first; c < end; c += DEPTH * step) {
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-            const int now = c + d * step, next = now + DEPTH * step;
-            if (now < end) {
-                mma_piece<W8, T8, NT, PLANES>(acc, p[d], tok, plane, now, lane_off, k_bytes);
-                if (next < end) load_piece(p[d], r0, r1, next, lane_off, k_bytes);
-            }
+                    mma_bf16(acc[j], a0[h][2 * i], a1[h][2 * i], a0[h][2 * i + 1], a1[h][2 * i + 1], t.b[h][2 * i],
+                             t.b[h][2 * i + 1]);
         }
     }
 }
