@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) few_inner_kernel(const F
             for (int c = warp; c < pieces; c += kWarps) {
                 uint4 lo[2], hi[2];
                 const TokenPart<W8> now = next;
-                if (NT == 1) load_tokens<W8, false>(next, tok[0], c + kWarps, q * 16, k_bytes);
+                if (NT == 1 && c + kWarps < pieces) load_tokens<W8, false>(next, tok[0], c + kWarps, q * 16, k_bytes);
                 ring.take(lo, hi);
                 mma_piece<W8, NT, 1>(acc, lo, hi, [&](int j, int) {
                     if constexpr (NT == 1) {
@@ -283,29 +283,37 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) few_out_kernel(const Few
         for (int at = begin; at < end;) {
             const int pos = at / pieces, first = at % pieces, last = min(pieces, first + end - at);
             const int e = r.expert[pos], row0 = r.base[pos], m = r.base[pos + 1] - row0;
+            // count 0: up to four tokens, whose values and remainders share one tile of eight columns
             auto run = [&](auto count) {
-                constexpr int NT = decltype(count)::value;
+                constexpr bool kFold = decltype(count)::value == 0;
+                constexpr int NT = kFold ? 1 : decltype(count)::value, PLANES = kFold ? 1 : 2;
                 const uint8_t* tok[NT];
                 float acc[NT][4];
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    tok[j] = reinterpret_cast<const uint8_t*>(a.inner) + (int64_t)(row0 + min(j * 8 + g, m - 1)) * a.I * 4;
+                    const int col = kFold ? g & 3 : j * 8 + g;
+                    tok[j] = reinterpret_cast<const uint8_t*>(a.inner) + (int64_t)(row0 + min(col, m - 1)) * a.I * 4 +
+                             (kFold && g >= 4 ? plane : 0);
                     acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
                 }
-                TokenPart<W8> next[2];   // with one tile: the inner rows of the next piece
-                if (NT == 1) {
-                    load_tokens<W8, false>(next[0], tok[0], first, q * 16, k_bytes);
-                    load_tokens<W8, false>(next[1], tok[0] + plane, first, q * 16, k_bytes);
+                TokenPart<W8> next[PLANES];   // with one tile: the inner rows of the next piece
+                if constexpr (NT == 1) {
+#pragma unroll
+                    for (int pl = 0; pl < PLANES; ++pl)
+                        load_tokens<W8, false>(next[pl], tok[0] + pl * plane, first, q * 16, k_bytes);
                 }
                 for (int c = first; c < last; ++c) {
                     uint4 lo[2], hi[2];
-                    const TokenPart<W8> now[2] = {next[0], next[1]};
-                    if (NT == 1) {
-                        load_tokens<W8, false>(next[0], tok[0], c + 1, q * 16, k_bytes);
-                        load_tokens<W8, false>(next[1], tok[0] + plane, c + 1, q * 16, k_bytes);
+                    TokenPart<W8> now[PLANES];
+                    if constexpr (NT == 1) {
+#pragma unroll
+                        for (int pl = 0; pl < PLANES; ++pl) {
+                            now[pl] = next[pl];
+                            if (c + 1 < last) load_tokens<W8, false>(next[pl], tok[0] + pl * plane, c + 1, q * 16, k_bytes);
+                        }
                     }
                     ring.take(lo, hi);
-                    mma_piece<W8, NT, 2>(acc, lo, hi, [&](int j, int pl) {
+                    mma_piece<W8, NT, PLANES>(acc, lo, hi, [&](int j, int pl) {
                         if constexpr (NT == 1) {
                             return now[pl];
                         } else {
@@ -316,6 +324,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) few_out_kernel(const Few
                     });
                     __syncwarp();
                     fetch();
+                }
+                if constexpr (kFold) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[0][i] += __shfl_xor_sync(0xffffffffu, acc[0][i], 2);
                 }
                 float sa = 1.0f, sb = 1.0f;
                 if constexpr (W8) {
@@ -337,7 +349,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) few_out_kernel(const Few
                 __syncwarp();
                 return 0;
             };
-            with_tiles<MAXNT>((m + 7) / 8, run);
+            if (m <= 4) run(std::integral_constant<int, 0>{});
+            else with_tiles<MAXNT>((m + 7) / 8, run);
             at += last - first;
         }
         __syncthreads();

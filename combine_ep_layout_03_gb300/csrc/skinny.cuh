@@ -113,25 +113,37 @@ struct WeightRing {
 template <bool W8>
 struct TokenPart { uint32_t b[2][W8 ? 8 : 4]; };
 
-// tok: the token's row (bf16, or int8 with T8); a lane's values past the row's end read as zero.
+// tok: the token's row (bf16, or int8 with T8); a lane's values past the row's end read as zero (the
+// weights there are zeros too, but zero times what lies behind the row may not be).
 template <bool W8, bool T8>
 __device__ __forceinline__ void load_tokens(TokenPart<W8>& t, const uint8_t* tok, int piece, int lane_off, int k_bytes) {
+    constexpr int kWide = W8 && !T8 ? 2 : 1;   // bytes of a token's value to those of a weight
+    const int off = piece * 128 + lane_off;
+    const uint8_t* p = tok + (int64_t)off * kWide;
+    uint4 v[2][kWide];
+    if ((piece + 1) * 128 <= k_bytes) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < kWide; ++i) v[h][i] = *reinterpret_cast<const uint4*>(p + h * 64 * kWide + i * 16);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < kWide; ++i)
+                v[h][i] = off + h * 64 < k_bytes ? *reinterpret_cast<const uint4*>(p + h * 64 * kWide + i * 16)
+                                                 : make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int off = piece * 128 + h * 64 + lane_off;
-        const bool in = off < k_bytes;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
         if constexpr (T8) {
-            const uint4 v = in ? *reinterpret_cast<const uint4*>(tok + off) : zero;
-            int8x4_to_bf16(v.x, t.b[h][0], t.b[h][1]); int8x4_to_bf16(v.y, t.b[h][2], t.b[h][3]);
-            int8x4_to_bf16(v.z, t.b[h][4], t.b[h][5]); int8x4_to_bf16(v.w, t.b[h][6], t.b[h][7]);
+            int8x4_to_bf16(v[h][0].x, t.b[h][0], t.b[h][1]); int8x4_to_bf16(v[h][0].y, t.b[h][2], t.b[h][3]);
+            int8x4_to_bf16(v[h][0].z, t.b[h][4], t.b[h][5]); int8x4_to_bf16(v[h][0].w, t.b[h][6], t.b[h][7]);
         } else {
-            const uint8_t* p = tok + (int64_t)off * (W8 ? 2 : 1);
-            const uint4 v = in ? *reinterpret_cast<const uint4*>(p) : zero;
-            t.b[h][0] = v.x; t.b[h][1] = v.y; t.b[h][2] = v.z; t.b[h][3] = v.w;
-            if constexpr (W8) {
-                const uint4 w = in ? *reinterpret_cast<const uint4*>(p + 16) : zero;
-                t.b[h][4] = w.x; t.b[h][5] = w.y; t.b[h][6] = w.z; t.b[h][7] = w.w;
+#pragma unroll
+            for (int i = 0; i < kWide; ++i) {
+                t.b[h][4 * i] = v[h][i].x; t.b[h][4 * i + 1] = v[h][i].y;
+                t.b[h][4 * i + 2] = v[h][i].z; t.b[h][4 * i + 3] = v[h][i].w;
             }
         }
     }
