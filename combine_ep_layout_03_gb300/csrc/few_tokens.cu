@@ -89,13 +89,17 @@ __device__ __forceinline__ float routing_weight(const FewArgs& a, int token, int
     return w;
 }
 
-// Two CTAs share an SM; what the routing and the sums leave of its shared memory goes to the rings.
-constexpr int kCtasPerSm = 2;
-
-// Sizes of both kernels by the largest number of token tiles.
-template <int MAXNT>
+// Sizes of both kernels by weight type and largest number of token tiles.
+//   ctas     CTAs of an SM; what the routing and the sums leave of its shared memory goes to the rings (depth).
+//   prefetch whether the token values of the next piece are loaded under this one's products.  It helps bf16
+//            weights (one token tile, 64 tokens over 512 experts: 914 us with, 1015 us without); int8 weights
+//            need the registers for their conversion and gain more from other warps (8 tokens of 256 experts:
+//            276 us with it and two CTAs, 255 us without, 238 us without and with three CTAs).
+template <bool W8, int MAXNT>
 struct Sizes {
-    static constexpr int depth = MAXNT == 1 ? 6 : MAXNT == 2 ? 5 : 4;
+    static constexpr int ctas = W8 && MAXNT == 1 ? 3 : 2;
+    static constexpr int depth = ctas == 3 ? 3 : W8 ? (MAXNT == 2 ? 4 : 3) : MAXNT == 1 ? 6 : MAXNT == 2 ? 5 : 4;
+    static constexpr bool prefetch = !W8;
     using Ring = WeightRing<depth>;
     static constexpr int ring_bytes = kWarps * Ring::kWarpBytes;
     // inner: [buffer][warp][column][16 rows]; two buffers in turn, so that one barrier an item is enough, but one
@@ -103,7 +107,7 @@ struct Sizes {
     static constexpr int buffers = MAXNT > 2 ? 1 : 2;
     static constexpr int inner_smem = 1024 + ring_bytes + buffers * kWarps * MAXNT * 8 * 16 * 4;
     static constexpr int out_smem = 1024 + ring_bytes + kWarps * MAXNT * 8 * 16 * 4;   // [warp][token][16 columns]
-    static_assert(kCtasPerSm * (inner_smem + (int)sizeof(Routing) + 1536) <= 228 * 1024, "two CTAs an SM");
+    static_assert(ctas * (inner_smem + (int)sizeof(Routing) + 1536) <= 228 * 1024, "shared memory of an SM");
 };
 
 __device__ __forceinline__ uint8_t* aligned_smem(uint8_t* p) {
@@ -126,10 +130,10 @@ struct InnerCursor {
 // 16-row tile and their up rows 8-15, so a lane ends with both of a channel.  The warps
 // share the item's k and add their parts in shared memory.
 template <bool W8, int MAXNT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) few_inner_kernel(const FewArgs a, const __grid_constant__ CUtensorMap map_w) {
+__global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_inner_kernel(const FewArgs a, const __grid_constant__ CUtensorMap map_w) {
     extern __shared__ uint8_t dynamic[];
     __shared__ Routing r;
-    using S = Sizes<MAXNT>;
+    using S = Sizes<W8, MAXNT>;
     __shared__ uint64_t bars[kWarps * S::depth];
     uint8_t* const slots = aligned_smem(dynamic);
     constexpr int kBuffers = S::buffers, kSums = kWarps * MAXNT * 8 * 16;
@@ -175,11 +179,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) few_inner_kernel(const F
                 acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
             }
             TokenPart<W8> next;   // with one tile: the tokens of the next piece
-            if (NT == 1 && warp < pieces) load_tokens<W8, false>(next, tok[0], warp, q * 16, k_bytes);
+            constexpr bool kAhead = NT == 1 && S::prefetch;
+            if (kAhead && warp < pieces) load_tokens<W8, false>(next, tok[0], warp, q * 16, k_bytes);
             for (int c = warp; c < pieces; c += kWarps) {
                 uint4 lo[2], hi[2];
-                const TokenPart<W8> now = next;
-                if (NT == 1 && c + kWarps < pieces) load_tokens<W8, false>(next, tok[0], c + kWarps, q * 16, k_bytes);
+                TokenPart<W8> now;
+                if constexpr (kAhead) {
+                    now = next;
+                    if (c + kWarps < pieces) load_tokens<W8, false>(next, tok[0], c + kWarps, q * 16, k_bytes);
+                } else if constexpr (NT == 1) {
+                    load_tokens<W8, false>(now, tok[0], c, q * 16, k_bytes);
+                }
                 ring.take(lo, hi);
                 mma_piece<W8, NT, 1>(acc, lo, hi, [&](int j, int) {
                     if constexpr (NT == 1) {
@@ -240,10 +250,10 @@ struct OutCursor {
 };
 
 template <bool W8, int MAXNT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) few_out_kernel(const FewArgs a, int rows, const __grid_constant__ CUtensorMap map_w) {
+__global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_out_kernel(const FewArgs a, int rows, const __grid_constant__ CUtensorMap map_w) {
     extern __shared__ uint8_t dynamic[];
     __shared__ Routing r;
-    using S = Sizes<MAXNT>;
+    using S = Sizes<W8, MAXNT>;
     __shared__ uint64_t bars[kWarps * S::depth];
     uint8_t* const slots = aligned_smem(dynamic);
     float* const sums = reinterpret_cast<float*>(slots + S::ring_bytes);   // [warp][token][16]
@@ -296,8 +306,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) few_out_kernel(const Few
                              (kFold && g >= 4 ? plane : 0);
                     acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
                 }
+                constexpr bool kAhead = NT == 1 && S::prefetch;
                 TokenPart<W8> next[PLANES];   // with one tile: the inner rows of the next piece
-                if constexpr (NT == 1) {
+                if constexpr (kAhead) {
 #pragma unroll
                     for (int pl = 0; pl < PLANES; ++pl)
                         load_tokens<W8, false>(next[pl], tok[0] + pl * plane, first, q * 16, k_bytes);
@@ -308,8 +319,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) few_out_kernel(const Few
                     if constexpr (NT == 1) {
 #pragma unroll
                         for (int pl = 0; pl < PLANES; ++pl) {
-                            now[pl] = next[pl];
-                            if (c + 1 < last) load_tokens<W8, false>(next[pl], tok[0] + pl * plane, c + 1, q * 16, k_bytes);
+                            if constexpr (kAhead) {
+                                now[pl] = next[pl];
+                                if (c + 1 < last) load_tokens<W8, false>(next[pl], tok[0] + pl * plane, c + 1, q * 16, k_bytes);
+                            } else {
+                                load_tokens<W8, false>(now[pl], tok[0] + pl * plane, c, q * 16, k_bytes);
+                            }
                         }
                     }
                     ring.take(lo, hi);
@@ -387,8 +402,12 @@ template <bool W8, int MAXNT>
 cudaError_t launch(const FewArgs& a, int sms, cudaStream_t st) {
     const int64_t entries = (int64_t)a.T * a.K;
     const int64_t items = (entries < a.E ? entries : a.E) * (a.I / 8);
-    const int ctas = sms * kCtasPerSm;
-    using S = Sizes<MAXNT>;
+    using S = Sizes<W8, MAXNT>;
+    // As many CTAs as fit, or fewer if that fills the rounds of items better (one token: 8 x 128 items are
+    // 3.4 rounds of two CTAs an SM, but 2.2 of three).
+    int per_sm = S::ctas;
+    if (per_sm == 3 && (items + 3 * sms - 1) / (3 * sms) * 3 > (items + 2 * sms - 1) / (2 * sms) * 2) per_sm = 2;
+    const int ctas = sms * per_sm;
     const int rows = rows_of_tile(a.H, ctas), tiles = (a.H + rows - 1) / rows;
     const int64_t width = W8 ? 1 : 2;
     CUtensorMap map13, map2;
