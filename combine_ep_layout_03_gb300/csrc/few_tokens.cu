@@ -84,8 +84,10 @@ static_assert(kFewMaxTokens <= 64, "a token mask is 64 bits");
 // token names an expert twice).
 __device__ __forceinline__ float routing_weight(const FewArgs& a, int token, int expert) {
     float w = 0.0f;
-    for (int k = 0; k < a.K; ++k)
-        if (a.topk[token * a.K + k] == expert) w += a.topk_w[token * a.K + k];
+    for (int k = 0; k < a.K; ++k) {
+        const float v = a.topk_w[token * a.K + k];
+        w += a.topk[token * a.K + k] == expert ? v : 0.0f;
+    }
     return w;
 }
 
@@ -139,8 +141,9 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_inner_ke
     constexpr int kBuffers = S::buffers, kSums = kWarps * MAXNT * 8 * 16;
     float* const red = reinterpret_cast<float*>(slots + S::ring_bytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-    build_routing(r, a);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid == 0) prefetch_map(&map_w);
+    build_routing(r, a);
     const int tiles = a.I / 8, items = r.count * tiles, step = gridDim.x;
     const int k_bytes = a.H * (W8 ? 1 : 2), pieces = (k_bytes + 127) / 128;
     typename S::Ring ring(slots, bars, warp, lane);
@@ -168,6 +171,18 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_inner_ke
         const int e = r.expert[pos], row0 = r.base[pos], m = r.base[pos + 1] - row0;
         const int nt = (m + 7) / 8;
         float* sums = red + (kBuffers == 2 ? buffer * kSums : 0);
+        // what the sums below will be multiplied by arrives meanwhile
+        struct Factors { float gate, up, weight; };
+        auto factors = [&](int i) {
+            Factors f = {1.0f, 1.0f, routing_weight(a, r.token[row0 + (i >> 3)], e)};
+            if constexpr (W8) {
+                const float* sc = a.w13_scales + (int64_t)e * 2 * a.I + tile * 8 + (i & 7);
+                f.gate = sc[0];
+                f.up = sc[a.I];
+            }
+            return f;
+        };
+        const Factors mine = tid < m * 8 ? factors(tid) : Factors{};
         auto run = [&](auto count) {
             constexpr int NT = decltype(count)::value;
             const uint8_t* tok[NT];
@@ -203,13 +218,13 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_inner_ke
                 __syncwarp();
                 fetch();
             }
-            float* mine = sums + warp * NT * 8 * 16;   // [warp][column][16 rows]
+            float* part = sums + warp * NT * 8 * 16;   // [warp][column][16 rows]
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                mine[(j * 8 + 2 * q) * 16 + g] = acc[j][0];
-                mine[(j * 8 + 2 * q + 1) * 16 + g] = acc[j][1];
-                mine[(j * 8 + 2 * q) * 16 + g + 8] = acc[j][2];
-                mine[(j * 8 + 2 * q + 1) * 16 + g + 8] = acc[j][3];
+                part[(j * 8 + 2 * q) * 16 + g] = acc[j][0];
+                part[(j * 8 + 2 * q + 1) * 16 + g] = acc[j][1];
+                part[(j * 8 + 2 * q) * 16 + g + 8] = acc[j][2];
+                part[(j * 8 + 2 * q + 1) * 16 + g + 8] = acc[j][3];
             }
             return NT * 8;
         };
@@ -223,12 +238,9 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_inner_ke
                 gate += sums[(w * cols + col) * 16 + c];
                 up += sums[(w * cols + col) * 16 + c + 8];
             }
-            if constexpr (W8) {
-                const float* sc = a.w13_scales + (int64_t)e * 2 * a.I + channel;
-                gate *= sc[0];
-                up *= sc[a.I];
-            }
-            const float h = gate / (1.0f + expf(-gate)) * up * routing_weight(a, r.token[row0 + col], e);
+            const Factors f = i == tid ? mine : factors(i);
+            gate *= f.gate;
+            const float h = gate / (1.0f + expf(-gate)) * (up * f.up) * f.weight;
             const uint32_t hi = pack_bf16x2_rn(h, 0.0f) & 0xffffu;
             uint16_t* dst = a.inner + (int64_t)(row0 + col) * 2 * a.I + channel;
             dst[0] = (uint16_t)hi;
@@ -258,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_out_kern
     uint8_t* const slots = aligned_smem(dynamic);
     float* const sums = reinterpret_cast<float*>(slots + S::ring_bytes);   // [warp][token][16]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+    if (tid == 0) prefetch_map(&map_w);
     for (int i = tid; i < kWarps * a.T * 16; i += kThreads) sums[i] = 0.0f;
     build_routing(r, a);
     const int k_bytes = a.I * (W8 ? 1 : 2), pieces = (k_bytes + 127) / 128;
@@ -413,9 +426,9 @@ cudaError_t launch(const FewArgs& a, int sms, cudaStream_t st) {
     CUtensorMap map13, map2;
     if (!make_pairs_map(&map13, a.w13, a.E, a.I, a.H * width, 8) || !make_experts_map(&map2, a.w2, a.E, a.H, a.I * width, rows))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(few_inner_kernel<W8, MAXNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::inner_smem);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(few_out_kernel<W8, MAXNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::out_smem);
+    static std::atomic<uint64_t> inner_done{0}, out_done{0};
+    cudaError_t e = allow_smem(few_inner_kernel<W8, MAXNT>, S::inner_smem, inner_done);
+    if (e == cudaSuccess) e = allow_smem(few_out_kernel<W8, MAXNT>, S::out_smem, out_done);
     if (e != cudaSuccess) return e;
     few_inner_kernel<W8, MAXNT><<<(unsigned)(items < ctas ? items : ctas), kThreads, S::inner_smem, st>>>(a, map13);
     e = cudaGetLastError();

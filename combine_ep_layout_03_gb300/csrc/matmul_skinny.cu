@@ -42,6 +42,7 @@ __global__ void __launch_bounds__(kThreads, 2) matmul_skinny_kernel(const Matmul
     uint8_t* const slots = dynamic + ((1024 - (smem_addr(dynamic) & 1023)) & 1023);
     __shared__ Segments s;
     float* const red = reinterpret_cast<float*>(slots + kRingBytes);   // two buffers in turn: a barrier an item
+    if (threadIdx.x == 0) prefetch_map(&map_w);
     if (!load_segments<kThreads>(s, a, kTileRows)) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
     constexpr int per = GLU ? 8 : 16;   // output channels of an item
@@ -141,7 +142,8 @@ cudaError_t launch_matmul_skinny(const MatmulArgs& a, int sms, cudaStream_t st) 
     CUtensorMap map_w;
     if (!(a.swiglu ? make_pairs_map(&map_w, a.w, a.E, a.N / 2, a.K, 8) : make_experts_map(&map_w, a.w, a.E, a.N, a.K, 16)))
         return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    static std::atomic<uint64_t> done[2];
+    const cudaError_t e = allow_smem(kernel, kSmem, done[a.swiglu]);
     if (e != cudaSuccess) return e;
     kernel<<<grid, kThreads, kSmem, st>>>(a, map_w);
     return cudaGetLastError();

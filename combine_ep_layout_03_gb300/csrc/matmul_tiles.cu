@@ -385,6 +385,11 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
     __shared__ Shared<C> sh;
     __shared__ __align__(16) float scales[4][C::tile];   // of the epilogue warps
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        prefetch_map(&map_w);
+        prefetch_map(&map_a);
+        prefetch_map(&map_half);
+    }
     if (!load_segments<kThreads>(sh.seg, a, C::tile)) return;   // the same answer in both CTAs
     const uint32_t cta = cluster_rank();
     uint8_t* raw = dynamic + ((1024 - (smem_addr(dynamic) & 1023)) & 1023);
@@ -436,7 +441,8 @@ cudaError_t launch(const MatmulArgs& a, int sms, cudaStream_t st) {
     const int64_t most = ((a.rows + C::tile - 1) / C::tile + (a.E > 1 ? a.E : 0)) * ((outs + per_pair - 1) / per_pair);
     const int64_t pairs = most < sms / 2 ? most : sms / 2;
     auto kernel = a.swiglu ? matmul_tiles_kernel<C, true> : matmul_tiles_kernel<C, false>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+    static std::atomic<uint64_t> done[2];
+    const cudaError_t e = allow_smem(kernel, C::smem, done[a.swiglu]);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)(2 * pairs), kThreads, C::smem, st>>>(a, map_w, map_a, map_half);
     return cudaGetLastError();

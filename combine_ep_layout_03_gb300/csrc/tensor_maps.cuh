@@ -1,5 +1,5 @@
 // tensor_maps.cuh -- host side: tensor maps of byte matrices in boxes 128 bytes wide with the
-// 128-byte swizzle, zeros outside.  The driver's encoder is looked up at run time, so the library
+// 128-byte swizzle, zeros outside; and the shared-memory limit of kernels.  The driver's encoder is looked up at run time, so the library
 // does not link against the driver.
 #pragma once
 
@@ -57,6 +57,20 @@ inline bool make_pairs_map(CUtensorMap* map, const void* p, int64_t E, int64_t n
     const cuuint64_t strides[3] = {(cuuint64_t)bytes, (cuuint64_t)(n * bytes), (cuuint64_t)(2 * n * bytes)};
     const cuuint32_t box[4] = {128, (cuuint32_t)pairs, 2, 1};
     return make_map(map, p, 4, dims, strides, box);
+}
+
+// Allows `kernel` `bytes` of dynamic shared memory: the first time on each device, which `done`
+// (one of the kernel's own) remembers.
+template <class Kernel>
+cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (bit & done.load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 }  // namespace

@@ -147,8 +147,15 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# The current stream's handle without the stream object that torch.cuda.current_stream() makes (3 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and _raw_device is not None:
+            return _raw_stream(_raw_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -353,11 +360,14 @@ def _require(ok: bool, what: str):
         raise EPError(EP_ERR_INVALID_ARG, what)
 
 
-def _row_stride(t: torch.Tensor, rows: int, hidden: int, what: str) -> int:
+def _row_stride(t: torch.Tensor, shape, what: str) -> int:
     """Elements between the rows of a bf16 [rows, hidden] tensor whose columns lie together."""
-    _require(t.dtype == torch.bfloat16 and t.dim() == 2 and t.shape[0] == rows and t.shape[1] == hidden
-             and (hidden == 1 or t.stride(1) == 1), what)
-    return t.stride(0) if rows > 1 else hidden
+    if t.dtype is not torch.bfloat16 or t.shape != shape:
+        raise EPError(EP_ERR_INVALID_ARG, what)
+    row, column = t.stride()
+    if column != 1 and shape[1] > 1:
+        raise EPError(EP_ERR_INVALID_ARG, what)
+    return row if shape[0] > 1 else shape[1]
 
 
 def ep_rms_norm_quant(x: torch.Tensor, residual, gamma: torch.Tensor, eps: float, quant: int, h_out,
@@ -365,17 +375,22 @@ def ep_rms_norm_quant(x: torch.Tensor, residual, gamma: torch.Tensor, eps: float
     """8-bit rows of RMSNorm(x + residual) * gamma.  x, residual (or None) and h_out (or None: the
     sum is not kept) are bf16 [rows, H], rows any stride apart; data and scales as of alloc_recv,
     contiguous, of any type of the same bytes."""
-    _require(x.dim() == 2, "x: [rows, hidden]")
-    rows, hidden = x.shape
-    xs = _row_stride(x, rows, hidden, "x: bf16 [rows, hidden]")
-    rs = 0 if residual is None else _row_stride(residual, rows, hidden, "residual: as x")
-    hs = 0 if h_out is None else _row_stride(h_out, rows, hidden, "h_out: as x")
-    _require(gamma.dtype == torch.bfloat16 and gamma.numel() == hidden and gamma.is_contiguous(),
-             "gamma: bf16 [hidden]")
+    shape = x.shape
+    _require(len(shape) == 2, "x: [rows, hidden]")
+    rows, hidden = shape
+    xs = _row_stride(x, shape, "x: bf16 [rows, hidden]")
+    res, rs, h, hs = None, 0, None, 0
+    if residual is not None:
+        res, rs = residual.data_ptr(), _row_stride(residual, shape, "residual: as x")
+    if h_out is not None:
+        h, hs = h_out.data_ptr(), _row_stride(h_out, shape, "h_out: as x")
+    if gamma.dtype is not torch.bfloat16 or gamma.numel() != hidden or not gamma.is_contiguous():
+        raise EPError(EP_ERR_INVALID_ARG, "gamma: bf16 [hidden]")
     _check_rows_out(quant, rows, hidden, data, scales)
-    _check(_lib.ep_rms_norm_quant(x.data_ptr(), xs, _ptr(residual), rs, gamma.data_ptr(), eps, rows, hidden, quant,
-                                  _ptr(h_out), hs, data.data_ptr(), scales.data_ptr(), _stream(stream)),
-           "ep_rms_norm_quant")
+    status = _lib.ep_rms_norm_quant(x.data_ptr(), xs, res, rs, gamma.data_ptr(), eps, rows, hidden, quant, h, hs,
+                                    data.data_ptr(), scales.data_ptr(), _stream(stream))
+    if status:
+        _check(status, "ep_rms_norm_quant")
 
 
 # bytes of a row's scales by mode, of one hidden column (0: four bytes a row)
@@ -388,16 +403,17 @@ def _check_rows_out(quant: int, rows: int, hidden: int, data: torch.Tensor, scal
     per = _SCALE_DIVISOR.get(quant)
     if per is None:
         raise EPError(EP_ERR_UNSUPPORTED, "8-bit rows with scales: quant mode")
-    _require(data.is_contiguous() and data.nbytes >= rows * hidden, "data: [rows, hidden] bytes")
-    _require(scales.is_contiguous() and scales.nbytes >= rows * (hidden // per if per else 4),
-             "scales: as of ep_recv_row_bytes")
+    if not data.is_contiguous() or data.nbytes < rows * hidden:
+        raise EPError(EP_ERR_INVALID_ARG, "data: [rows, hidden] bytes")
+    if not scales.is_contiguous() or scales.nbytes < rows * (hidden // per if per else 4):
+        raise EPError(EP_ERR_INVALID_ARG, "scales: as of ep_recv_row_bytes")
 
 
 def ep_quant_rows(x: torch.Tensor, quant: int, data: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
     """8-bit rows of bf16 [rows, H] as ep_dispatch encodes them."""
     _require(x.dim() == 2, "x: [rows, hidden]")
     rows, hidden = x.shape
-    xs = _row_stride(x, rows, hidden, "x: bf16 [rows, hidden]")
+    xs = _row_stride(x, x.shape, "x: bf16 [rows, hidden]")
     _check_rows_out(quant, rows, hidden, data, scales)
     _check(_lib.ep_quant_rows(x.data_ptr(), xs, rows, hidden, quant, data.data_ptr(), scales.data_ptr(),
                               _stream(stream)), "ep_quant_rows")
@@ -409,20 +425,35 @@ def ep_expert_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w
     w_scales [E, N], expert_base int32 [E + 1] on the device (None: one matrix), out bf16 [rows, N],
     or [rows, N / 2] = silu(gates) * ups with swiglu.  a and a_scales may be the receive buffers of an
     int8 dispatch (uint8 of the same bytes)."""
-    _require(a.dim() == 2 and a.element_size() == 1 and a.is_contiguous(), "a: int8 [rows, K]")
-    rows, K = a.shape
-    _require(w.dim() == 3 and w.dtype == torch.int8 and w.is_contiguous() and w.shape[2] == K, "w: int8 [E, N, K]")
-    E, N = w.shape[0], w.shape[1]
-    _require(a_scales.is_contiguous() and a_scales.nbytes == 4 * rows, "a_scales: float32 [rows]")
-    _require(w_scales.dtype == torch.float32 and w_scales.is_contiguous() and w_scales.numel() == E * N,
-             "w_scales: float32 [E, N]")
-    _require((expert_base is None and E == 1) or (expert_base is not None and expert_base.dtype == torch.int32
-             and expert_base.is_contiguous() and expert_base.numel() == E + 1), "expert_base: int32 [E + 1]")
-    _require(out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == (rows, N // 2 if swiglu else N),
-             "out: bf16 [rows, N], or [rows, N / 2] with swiglu")
-    _check(_lib.ep_expert_matmul(a.data_ptr(), a_scales.data_ptr(), rows, K, w.data_ptr(), w_scales.data_ptr(), N, E,
-                                 _ptr(expert_base), 1 if swiglu else 0, out.data_ptr(), _ptr(status),
-                                 _stream(stream)), "ep_expert_matmul")
+    bad = None
+    shape, wshape = a.shape, w.shape
+    if len(shape) != 2 or a.element_size() != 1 or not a.is_contiguous():
+        bad = "a: int8 [rows, K]"
+    elif len(wshape) != 3 or w.dtype is not torch.int8 or not w.is_contiguous() or wshape[2] != shape[1]:
+        bad = "w: int8 [E, N, K]"
+    if bad:
+        raise EPError(EP_ERR_INVALID_ARG, bad)
+    rows, K = shape
+    E, N, _ = wshape
+    if not a_scales.is_contiguous() or a_scales.nbytes != 4 * rows:
+        bad = "a_scales: float32 [rows]"
+    elif w_scales.dtype is not torch.float32 or not w_scales.is_contiguous() or w_scales.numel() != E * N:
+        bad = "w_scales: float32 [E, N]"
+    elif out.dtype is not torch.bfloat16 or not out.is_contiguous() or out.shape != (rows, N // 2 if swiglu else N):
+        bad = "out: bf16 [rows, N], or [rows, N / 2] with swiglu"
+    base = None
+    if expert_base is not None:
+        base = expert_base.data_ptr()
+        if expert_base.dtype is not torch.int32 or not expert_base.is_contiguous() or expert_base.numel() != E + 1:
+            bad = "expert_base: int32 [E + 1]"
+    elif E != 1:
+        bad = "expert_base: int32 [E + 1]"
+    if bad:
+        raise EPError(EP_ERR_INVALID_ARG, bad)
+    code = _lib.ep_expert_matmul(a.data_ptr(), a_scales.data_ptr(), rows, K, w.data_ptr(), w_scales.data_ptr(), N, E,
+                                 base, 1 if swiglu else 0, out.data_ptr(), _ptr(status), _stream(stream))
+    if code:
+        _check(code, "ep_expert_matmul")
 
 
 def ep_moe_few_tokens_workspace_size(T: int, H: int, E: int, K: int, I: int) -> int:
@@ -438,32 +469,44 @@ def ep_moe_few_tokens(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: tor
     """The expert layer of up to 64 tokens: x [T, H] bf16, topk_idx [T, K] int64, topk_weights [T, K]
     float32, w13 [E, 2I, H] and w2 [E, H, I] in bf16, or in int8 with float32 row scales w13_scales
     [E, 2I] and w2_scales [E, H]; shared [S, T, H] bf16 or None; out [T, H] bf16; workspace uint8."""
+    _require(len(x.shape) == 2 and len(w13.shape) == 3 and len(topk_idx.shape) == 2, "x, w13, topk_idx: dimensions")
     T, H = x.shape
     E, I = w13.shape[0], w13.shape[1] // 2
     K = topk_idx.shape[1]
     wt = torch.bfloat16 if w13_scales is None else torch.int8
-    _require(x.dtype == torch.bfloat16 and x.is_contiguous(), "x: bf16 [T, H]")
-    _require(topk_idx.dtype == torch.int64 and topk_idx.is_contiguous() and topk_idx.shape[0] == T,
-             "topk_idx: int64 [T, K]")
-    _require(topk_weights.dtype == torch.float32 and topk_weights.is_contiguous()
-             and topk_weights.shape == topk_idx.shape, "topk_weights: float32 [T, K]")
-    _require(w13.dtype == wt and w13.is_contiguous() and w13.shape == (E, 2 * I, H), "w13: [E, 2I, H]")
-    _require(w2.dtype == wt and w2.is_contiguous() and w2.shape == (E, H, I), "w2: [E, H, I]")
-    _require((w13_scales is None) == (w2_scales is None), "w13_scales, w2_scales: both or neither")
-    if w13_scales is not None:
-        _require(w13_scales.dtype == torch.float32 and w13_scales.is_contiguous()
-                 and w13_scales.numel() == E * 2 * I, "w13_scales: float32 [E, 2I]")
-        _require(w2_scales.dtype == torch.float32 and w2_scales.is_contiguous()
-                 and w2_scales.numel() == E * H, "w2_scales: float32 [E, H]")
-    S = 0 if shared is None else shared.shape[0]
-    if shared is not None:
-        _require(shared.dtype == torch.bfloat16 and shared.is_contiguous() and shared.shape == (S, T, H),
-                 "shared: bf16 [S, T, H]")
-    _require(out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == (T, H), "out: bf16 [T, H]")
-    _check(_lib.ep_moe_few_tokens(x.data_ptr(), topk_idx.data_ptr(), topk_weights.data_ptr(), T, H, E, K, I,
-                                  w13.data_ptr(), _ptr(w13_scales), w2.data_ptr(), _ptr(w2_scales), _ptr(shared), S,
-                                  out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _ptr(status),
-                                  _stream(stream)), "ep_moe_few_tokens")
+    S, bad, s13, s2, sh = 0, None, None, None, None
+    if x.dtype is not torch.bfloat16 or not x.is_contiguous():
+        bad = "x: bf16 [T, H]"
+    elif topk_idx.dtype is not torch.int64 or not topk_idx.is_contiguous() or topk_idx.shape[0] != T:
+        bad = "topk_idx: int64 [T, K]"
+    elif (topk_weights.dtype is not torch.float32 or not topk_weights.is_contiguous()
+          or topk_weights.shape != topk_idx.shape):
+        bad = "topk_weights: float32 [T, K]"
+    elif w13.dtype is not wt or not w13.is_contiguous() or w13.shape != (E, 2 * I, H):
+        bad = "w13: [E, 2I, H]"
+    elif w2.dtype is not wt or not w2.is_contiguous() or w2.shape != (E, H, I):
+        bad = "w2: [E, H, I]"
+    elif (w13_scales is None) != (w2_scales is None):
+        bad = "w13_scales, w2_scales: both or neither"
+    elif out.dtype is not torch.bfloat16 or not out.is_contiguous() or out.shape != x.shape:
+        bad = "out: bf16 [T, H]"
+    elif w13_scales is not None:
+        s13, s2 = w13_scales.data_ptr(), w2_scales.data_ptr()
+        if w13_scales.dtype is not torch.float32 or not w13_scales.is_contiguous() or w13_scales.numel() != E * 2 * I:
+            bad = "w13_scales: float32 [E, 2I]"
+        elif w2_scales.dtype is not torch.float32 or not w2_scales.is_contiguous() or w2_scales.numel() != E * H:
+            bad = "w2_scales: float32 [E, H]"
+    if bad is None and shared is not None:
+        S, sh = shared.shape[0], shared.data_ptr()
+        if shared.dtype is not torch.bfloat16 or not shared.is_contiguous() or shared.shape != (S, T, H):
+            bad = "shared: bf16 [S, T, H]"
+    if bad:
+        raise EPError(EP_ERR_INVALID_ARG, bad)
+    code = _lib.ep_moe_few_tokens(x.data_ptr(), topk_idx.data_ptr(), topk_weights.data_ptr(), T, H, E, K, I,
+                                  w13.data_ptr(), s13, w2.data_ptr(), s2, sh, S, out.data_ptr(), workspace.data_ptr(),
+                                  workspace.nbytes, _ptr(status), _stream(stream))
+    if code:
+        _check(code, "ep_moe_few_tokens")
 
 
 # ---------------------------------------------------------------- convenience wrapper
