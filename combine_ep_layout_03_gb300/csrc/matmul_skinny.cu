@@ -125,9 +125,17 @@ __global__ void __launch_bounds__(kThreads, 2) matmul_skinny_kernel(const Matmul
     if (!ring.drain() && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
 }
 
-#ifndef EP_MATMUL_TILE_ROWS
-#define EP_MATMUL_TILE_ROWS 64
-#endif
+// Few enough rows and weights for the kernel above: its loop reads weights at about 2.9 TB/s for up
+// to eight rows an expert, 2.4 for 16 and 1.5 for 32, but starts sooner and uses every SM on a single
+// small matrix, where matmul_tiles.cu, at 5 TB/s, has a tile for few of them.  Measured (us, this
+// kernel and that): 8 rows x 4096 x 4096: 10 and 25; 32 rows: 15 and 25; 64 rows: 28 and 26;
+// 16 experts of 8 rows, 1024 x 704: 12 and 16; 128 experts of 8 rows, 4096 x 2048: 377 and 223.
+constexpr int64_t kSkinnyWork = 68 << 20;   // bytes of weights times tiles of eight rows
+
+bool is_skinny(const MatmulArgs& a) {
+    const int64_t experts = a.rows < a.E ? a.rows : a.E, rows = (a.rows + a.E - 1) / a.E;
+    return rows <= 32 && experts * a.N * a.K * ((rows + 7) / 8) <= kSkinnyWork;
+}
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
 
@@ -176,8 +184,7 @@ extern "C" ep_status ep_expert_matmul(const void* a, const float* a_scales, int6
     m.swiglu = swiglu;
     const int sms = ep_current_sms();
     if (sms <= 0) return EP_ERR_CUDA;
-    const bool tiles = rows > (int64_t)num_experts * EP_MATMUL_TILE_ROWS;
-    const cudaError_t e = tiles ? launch_matmul_tiles(m, sms, (cudaStream_t)stream)
-                                : launch_matmul_skinny(m, sms, (cudaStream_t)stream);
+    const cudaError_t e = is_skinny(m) ? launch_matmul_skinny(m, sms, (cudaStream_t)stream)
+                                       : launch_matmul_tiles(m, sms, (cudaStream_t)stream);
     return e == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }

@@ -448,12 +448,12 @@ cudaError_t launch(const MatmulArgs& a, int sms, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-#ifndef EP_MATMUL_THIN_ROWS
-#define EP_MATMUL_THIN_ROWS 64
-#endif
+// Up to this many rows an expert take the thin form.  128 experts x 4096 x 2048 of 64 rows: 226 us thin,
+// 258 us thick; 16 experts x 1024 x 1400 of 160 rows: 31 us thin, 24 us thick.
+constexpr int kThinRows = 64;
 
 }  // namespace
 
 cudaError_t launch_matmul_tiles(const MatmulArgs& a, int sms, cudaStream_t st) {
-    return a.rows <= (int64_t)a.E * EP_MATMUL_THIN_ROWS ? launch<Thin>(a, sms, st) : launch<Thick>(a, sms, st);
+    return a.rows <= (int64_t)a.E * kThinRows ? launch<Thin>(a, sms, st) : launch<Thick>(a, sms, st);
 }

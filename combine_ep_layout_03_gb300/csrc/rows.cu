@@ -22,6 +22,53 @@
 
 namespace {
 
+// Two float32 values in a register pair, for the packed arithmetic of sm_100 and later: these
+// kernels have several operations for each byte, and issue slots run out before bandwidth does.
+using f32x2 = unsigned long long;
+
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ void halves(f32x2 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// The two bf16 of a word.
+__device__ __forceinline__ f32x2 unpack2(uint32_t w) {
+    return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// max(m, |a|, |b|), NaN when any is NaN
+__device__ __forceinline__ float max_abs3(float m, f32x2 v) {
+    float a, b, r;
+    halves(v, a, b);
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
 // Sum of float32 values with its rounding error carried along: about 48 bits.
 struct Sum2 { float hi, lo; };
 
@@ -43,36 +90,41 @@ __device__ __forceinline__ uint4 ld_stream_v4(const void* p) {   // not .nc: h_o
 // Codes of 8 values t with largest magnitude m (finite, > 0) at TOP: the divisor is
 // brought near 1 by a power of two (exact), so that t * top cannot overflow.
 template <int Q>
-__device__ __forceinline__ uint2 encode_ratio(const float t[8], float m) {
+__device__ __forceinline__ uint2 encode_ratio(const f32x2 t[4], float m) {
     constexpr float top = QTraits<Q>::dmax;
     const int e = max((int)(__float_as_uint(m) >> 23) - 127, -110);
     // 2^-e: e = 127 gives the subnormal 2^-127
     const float p = e < 127 ? __uint_as_float((uint32_t)(127 - e) << 23) : 5.877471754111438e-39f;
-    const float a = __fmul_rn(top, p), b = __fmul_rn(m, p), inv = __fdiv_rn(1.0f, b);
-    float q[8];
+    const float a = __fmul_rn(top, p), b = __fmul_rn(m, p), inv = __frcp_rn(b);
+    const f32x2 a2 = pair(a, a), nb2 = pair(-b, -b), inv2 = pair(inv, inv);
+    f32x2 q[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float n = __fmul_rn(t[i], a);
-        const float q0 = __fmul_rn(n, inv);
-        q[i] = __fmaf_rn(__fmaf_rn(-q0, b, n), inv, q0);
+    for (int i = 0; i < 4; ++i) {
+        const f32x2 n = mul2(t[i], a2);
+        const f32x2 q0 = mul2(n, inv2);
+        q[i] = fma2(fma2(q0, nb2, n), inv2, q0);
     }
+    float f[8];
     if constexpr (Q == M_INT8) {
         // adding 1.5 * 2^23 rounds to nearest even and leaves the code in the low byte
-        int c[8];
+        const f32x2 magic = pair(12582912.0f, 12582912.0f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = __float_as_int(__fadd_rn(q[i], 12582912.0f));
-        return make_uint2(pack4_low_bytes(c[0], c[1], c[2], c[3]), pack4_low_bytes(c[4], c[5], c[6], c[7]));
+        for (int i = 0; i < 4; ++i) halves(add2(q[i], magic), f[2 * i], f[2 * i + 1]);
+        return make_uint2(pack4_low_bytes(__float_as_int(f[0]), __float_as_int(f[1]), __float_as_int(f[2]), __float_as_int(f[3])),
+                          pack4_low_bytes(__float_as_int(f[4]), __float_as_int(f[5]), __float_as_int(f[6]), __float_as_int(f[7])));
     } else {
         constexpr int C = QTraits<Q>::fp8;
-        return make_uint2(cvt_fp8x2<C>(q[0], q[1]) | (cvt_fp8x2<C>(q[2], q[3]) << 16),
-                          cvt_fp8x2<C>(q[4], q[5]) | (cvt_fp8x2<C>(q[6], q[7]) << 16));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) halves(q[i], f[2 * i], f[2 * i + 1]);
+        return make_uint2(cvt_fp8x2<C>(f[0], f[1]) | (cvt_fp8x2<C>(f[2], f[3]) << 16),
+                          cvt_fp8x2<C>(f[4], f[5]) | (cvt_fp8x2<C>(f[6], f[7]) << 16));
     }
 }
 
 __device__ __forceinline__ bool finite_bits(uint32_t magnitude) { return magnitude < 0x7f800000u; }
 
 // One CTA per row; thread t holds the 16-byte vectors u * blockDim + t of the row in
-// registers between the single barrier and the stores.
+// registers between the barrier and the stores.
 template <int Q, int VPT>
 __global__ void __launch_bounds__(1024) rms_norm_quant_kernel(const RowQuantArgs a) {
     using TR = QTraits<Q>;
@@ -98,13 +150,14 @@ __global__ void __launch_bounds__(1024) rms_norm_quant_kernel(const RowQuantArgs
         }
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
-            float f[8], r[8];
-            unpack8(v[u], f);
-            unpack8(w[u], r);
-            v[u].x = pack_bf16x2_rn(__fadd_rn(f[0], r[0]), __fadd_rn(f[1], r[1]));
-            v[u].y = pack_bf16x2_rn(__fadd_rn(f[2], r[2]), __fadd_rn(f[3], r[3]));
-            v[u].z = pack_bf16x2_rn(__fadd_rn(f[4], r[4]), __fadd_rn(f[5], r[5]));
-            v[u].w = pack_bf16x2_rn(__fadd_rn(f[6], r[6]), __fadd_rn(f[7], r[7]));
+            uint32_t h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float f0, f1;
+                halves(add2(unpack2(word(v[u], i)), unpack2(word(w[u], i))), f0, f1);
+                h[i] = pack_bf16x2_rn(f0, f1);
+            }
+            v[u] = make_uint4(h[0], h[1], h[2], h[3]);
         }
     }
 #pragma unroll
@@ -121,47 +174,41 @@ __global__ void __launch_bounds__(1024) rms_norm_quant_kernel(const RowQuantArgs
         }
     }
 
-    // the sum of squares, and max|t| as magnitude bits: an integer maximum, under which
-    // a NaN lies above every number and so marks its row or block
-    float t[VPT][8];
-    Sum2 s = {0.0f, 0.0f};
+    // the sum of squares, and max|t|: a maximum that keeps NaN, whose bits lie above every number's
+    f32x2 t[VPT][4], s2 = pair(0.0f, 0.0f);
     uint32_t m = 0, gm[VPT];
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
-        float f[8], c[8];
-        unpack8(v[u], f);
-        unpack8(g[u], c);
-        gm[u] = 0;
+        float mu = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if constexpr (TR::mx) sum2_add(s, __fmul_rn(f[i], f[i]), 0.0f);
-            else s.hi = __fmaf_rn(f[i], f[i], s.hi);
-            t[u][i] = __fmul_rn(f[i], c[i]);
-            gm[u] = max(gm[u], __float_as_uint(t[u][i]) & 0x7fffffffu);
+        for (int i = 0; i < 4; ++i) {
+            const f32x2 h = unpack2(word(v[u], i));
+            s2 = fma2(h, h, s2);
+            t[u][i] = mul2(h, unpack2(word(g[u], i)));
+            mu = max_abs3(mu, t[u][i]);
         }
+        gm[u] = __float_as_uint(mu);
         m = max(m, gm[u]);
     }
+    float s0, s1;
+    halves(s2, s0, s1);
+    float s = __fadd_rn(s0, s1);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float hi = __shfl_xor_sync(kFull, s.hi, o);
-        if constexpr (TR::mx) sum2_add(s, hi, __shfl_xor_sync(kFull, s.lo, o));
-        else s.hi = __fadd_rn(s.hi, hi);
-    }
+    for (int o = 16; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(kFull, s, o));
     if constexpr (TR::token) m = __reduce_max_sync(kFull, m);
     if ((tid & 31) == 0) {
-        s_sum[warp] = make_float2(s.hi, s.lo);
+        s_sum[warp].x = s;
         if constexpr (TR::token) s_max[warp] = m;
     }
     __syncthreads();
-    s = Sum2{0.0f, 0.0f};
+    s = 0.0f;
     for (int w = 0; w < nwarps; ++w) {
-        if constexpr (TR::mx) sum2_add(s, s_sum[w].x, s_sum[w].y);
-        else s.hi = __fadd_rn(s.hi, s_sum[w].x);
+        s = __fadd_rn(s, s_sum[w].x);
         if constexpr (TR::token) m = max(m, s_max[w]);
     }
     const float n = (float)a.H;
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(__fadd_rn(s.hi, s.lo), n), a.eps)));
-    const bool row_ok = finite_bits(__float_as_uint(s.hi) & 0x7fffffffu);
+    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(s, n), a.eps)));
+    const bool row_ok = finite_bits(__float_as_uint(s) & 0x7fffffffu);
     const float nan = __uint_as_float(0x7fc00000u);
     uint8_t* data = a.data + row * a.H;
 
@@ -193,41 +240,75 @@ __global__ void __launch_bounds__(1024) rms_norm_quant_kernel(const RowQuantArgs
             }
         }
     } else {
+        // The block's exponent is that of max|t| * r.  Within 2^-17 of a power of two the float32
+        // product may lie on the wrong side of it (the sum is off by up to 69 2^-24): then the CTA
+        // takes the sum again with its errors carried along, and m * r >= 2^k is decided as
+        // m^2 H >= 4^k (sum + H eps) in 64 bits.  A row in some hundreds comes to this.
+        uint32_t bm[VPT];
+        int ex[VPT];
+        bool near[VPT], any = false;
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            bm[u] = gm[u];   // 4 consecutive lanes hold a block
+            bm[u] = max(bm[u], __shfl_xor_sync(kFull, bm[u], 1));
+            bm[u] = max(bm[u], __shfl_xor_sync(kFull, bm[u], 2));
+            const uint32_t p = __float_as_uint(__fmul_rn(__uint_as_float(bm[u]), rstd));
+            const uint32_t frac = p & 0x7fffffu;
+            ex[u] = (p >> 23) == 0 ? -255 : (int)(p >> 23) - 127;
+            near[u] = row_ok && finite_bits(bm[u]) && bm[u] && (frac < 64u || frac > 0x7fffffu - 64u) && ex[u] > -120 && ex[u] < 128;
+            any = any || near[u];
+        }
+        if (__syncthreads_or(any)) {
+            Sum2 e = {0.0f, 0.0f};
+#pragma unroll
+            for (int u = 0; u < VPT; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float h0, h1;
+                    halves(unpack2(word(v[u], i)), h0, h1);
+                    sum2_add(e, __fmul_rn(h0, h0), 0.0f);   // the square of a bf16 is exact
+                    sum2_add(e, __fmul_rn(h1, h1), 0.0f);
+                }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const float hi = __shfl_xor_sync(kFull, e.hi, o);
+                sum2_add(e, hi, __shfl_xor_sync(kFull, e.lo, o));
+            }
+            if ((tid & 31) == 0) s_sum[warp] = make_float2(e.hi, e.lo);
+            __syncthreads();
+            e = Sum2{0.0f, 0.0f};
+            for (int w = 0; w < nwarps; ++w) sum2_add(e, s_sum[w].x, s_sum[w].y);
+#pragma unroll
+            for (int u = 0; u < VPT; ++u) {
+                if (!near[u]) continue;
+                const double mf = __uint_as_float(bm[u]);
+                const uint32_t frac = __float_as_uint(__fmul_rn(__uint_as_float(bm[u]), rstd)) & 0x7fffffu;
+                const int k = frac < 64u ? ex[u] : ex[u] + 1;
+                const double rhs = ldexp((double)e.hi + (double)e.lo + (double)n * (double)a.eps, 2 * k);
+                ex[u] = mf * mf * (double)n >= rhs ? k : k - 1;
+            }
+        }
+        const f32x2 r2 = pair(rstd, rstd);
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
             const int vi = u * nt + tid;
-            uint32_t bm = gm[u];   // 4 consecutive lanes hold a block
-            bm = max(bm, __shfl_xor_sync(kFull, bm, 1));
-            bm = max(bm, __shfl_xor_sync(kFull, bm, 2));
-            const float mf = __uint_as_float(bm);
-            const bool ok = row_ok && finite_bits(bm);
-            const uint32_t p = __float_as_uint(__fmul_rn(mf, rstd));
-            int ex = (int)(p >> 23) - 127;
-            const uint32_t frac = p & 0x7fffffu;
-            // Within 2^-17 of a power of two the float32 product may lie on the wrong side of
-            // it; m * r >= 2^k is then decided as m^2 H >= 4^k (sum + H eps) in 64 bits (rare).
-            if (ok && bm && (frac < 64u || frac > 0x7fffffu - 64u) && ex > -120 && ex < 128) {
-                const int k = frac < 64u ? ex : ex + 1;
-                const double lhs = (double)mf * (double)mf * (double)n;
-                const double rhs = ldexp((double)s.hi + (double)s.lo + (double)n * (double)a.eps, 2 * k);
-                ex = lhs >= rhs ? k : k - 1;
-            }
-            int se = (p >> 23) == 0 ? -127 : max(ex - TR::emax, -127);
-            se = min(se, 127);
+            const bool ok = row_ok && finite_bits(bm[u]);
+            const int se = min(max(ex[u] - TR::emax, -127), 127);
             const float mul = __uint_as_float((uint32_t)(127 - se) << 23);   // 2^-se; se = 127 only for values
                                                                              // that no finite row reaches
             uint2 c = make_uint2(0, 0);
-            if (ok && bm) {
+            if (ok && bm[u]) {
+                const f32x2 m2 = pair(mul, mul);
                 float q[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(__fmul_rn(t[u][i], rstd), mul);
+                for (int i = 0; i < 4; ++i) halves(mul2(mul2(t[u][i], r2), m2), q[2 * i], q[2 * i + 1]);
                 c.x = cvt_fp8x2<Q>(q[0], q[1]) | (cvt_fp8x2<Q>(q[2], q[3]) << 16);
                 c.y = cvt_fp8x2<Q>(q[4], q[5]) | (cvt_fp8x2<Q>(q[6], q[7]) << 16);
             }
             if (vi < a.nvec) {
                 st_v2(data + 8 * vi, c);
                 if ((vi & 3) == 0)
-                    a.scales[row * a.scale_bytes + (vi >> 2)] = (uint8_t)(!ok ? 255 : bm ? se + 127 : 0);
+                    a.scales[row * a.scale_bytes + (vi >> 2)] = (uint8_t)(!ok ? 255 : bm[u] ? se + 127 : 0);
             }
         }
     }
