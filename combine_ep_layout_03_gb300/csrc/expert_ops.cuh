@@ -15,7 +15,7 @@ struct RowQuantArgs {
     int64_t x_stride, residual_stride, h_stride;
     int64_t rows;
     int32_t H, nvec, scale_bytes;
-    float eps;
+    float eps, inv_n;          // inv_n: 1 / H
 };
 
 // Launchers return cudaGetLastError() after the launch.

@@ -121,12 +121,24 @@ __device__ __forceinline__ uint2 encode_ratio(const f32x2 t[4], float m) {
     }
 }
 
+// bf16(x + residual) of eight columns
+__device__ __forceinline__ uint4 add_rows(const uint4& x, const uint4& residual) {
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float f0, f1;
+        halves(add2(unpack2(word(x, i)), unpack2(word(residual, i))), f0, f1);
+        h[i] = pack_bf16x2_rn(f0, f1);
+    }
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
 __device__ __forceinline__ bool finite_bits(uint32_t magnitude) { return magnitude < 0x7f800000u; }
 
 // One CTA per row; thread t holds the 16-byte vectors u * blockDim + t of the row in
 // registers between the barrier and the stores.
 template <int Q, int VPT>
-__global__ void __launch_bounds__(1024) rms_norm_quant_kernel(const RowQuantArgs a) {
+__global__ void __launch_bounds__(VPT == 4 ? 256 : 1024, VPT == 4 ? 4 : 1) rms_norm_quant_kernel(const RowQuantArgs a) {
     using TR = QTraits<Q>;
     __shared__ float2 s_sum[32];
     __shared__ uint32_t s_max[32];
@@ -149,16 +161,7 @@ __global__ void __launch_bounds__(1024) rms_norm_quant_kernel(const RowQuantArgs
             w[u] = vi < a.nvec ? ld_stream_v4(res + 8 * vi) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int u = 0; u < VPT; ++u) {
-            uint32_t h[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float f0, f1;
-                halves(add2(unpack2(word(v[u], i)), unpack2(word(w[u], i))), f0, f1);
-                h[i] = pack_bf16x2_rn(f0, f1);
-            }
-            v[u] = make_uint4(h[0], h[1], h[2], h[3]);
-        }
+        for (int u = 0; u < VPT; ++u) v[u] = add_rows(v[u], w[u]);
     }
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
@@ -201,13 +204,13 @@ __global__ void __launch_bounds__(1024) rms_norm_quant_kernel(const RowQuantArgs
         if constexpr (TR::token) s_max[warp] = m;
     }
     __syncthreads();
-    s = 0.0f;
-    for (int w = 0; w < nwarps; ++w) {
-        s = __fadd_rn(s, s_sum[w].x);
-        if constexpr (TR::token) m = max(m, s_max[w]);
-    }
+    const int from = tid & 31;   // a lane for each warp's sum
+    s = from < nwarps ? s_sum[from].x : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(kFull, s, o));
+    if constexpr (TR::token) m = __reduce_max_sync(kFull, from < nwarps ? s_max[from] : 0u);
     const float n = (float)a.H;
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(s, n), a.eps)));
+    const float rstd = rsqrtf(__fmaf_rn(s, a.inv_n, a.eps));
     const bool row_ok = finite_bits(__float_as_uint(s) & 0x7fffffffu);
     const float nan = __uint_as_float(0x7fc00000u);
     uint8_t* data = a.data + row * a.H;
@@ -222,7 +225,7 @@ __global__ void __launch_bounds__(1024) rms_norm_quant_kernel(const RowQuantArgs
         }
         if (tid == 0)
             reinterpret_cast<float*>(a.scales)[row] =
-                !ok ? nan : m ? __fdiv_rn(__fmul_rn(mf, rstd), TR::dmax) : 0.0f;
+                !ok ? nan : m ? __fmul_rn(__fmul_rn(mf, rstd), 1.0f / TR::dmax) : 0.0f;
     } else if constexpr (TR::group) {
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
@@ -236,12 +239,12 @@ __global__ void __launch_bounds__(1024) rms_norm_quant_kernel(const RowQuantArgs
                 st_v2(data + 8 * vi, ok && gmax ? encode_ratio<Q>(t[u], mf) : make_uint2(0, 0));
                 if ((vi & 15) == 0)
                     reinterpret_cast<float*>(a.scales + row * a.scale_bytes)[vi >> 4] =
-                        !ok ? nan : gmax ? __fdiv_rn(__fmul_rn(mf, rstd), TR::dmax) : 0.0f;
+                        !ok ? nan : gmax ? __fmul_rn(__fmul_rn(mf, rstd), 1.0f / TR::dmax) : 0.0f;
             }
         }
     } else {
         // The block's exponent is that of max|t| * r.  Within 2^-17 of a power of two the float32
-        // product may lie on the wrong side of it (the sum is off by up to 69 2^-24): then the CTA
+        // product may lie on the wrong side of it (the sum, with 32 + 11 additions, is off by less than 2^-18): then the CTA
         // takes the sum again with its errors carried along, and m * r >= 2^k is decided as
         // m^2 H >= 4^k (sum + H eps) in 64 bits.  A row in some hundreds comes to this.
         uint32_t bm[VPT];
@@ -259,16 +262,20 @@ __global__ void __launch_bounds__(1024) rms_norm_quant_kernel(const RowQuantArgs
             any = any || near[u];
         }
         if (__syncthreads_or(any)) {
+            // h is read again (no register keeps it until here): from h_out, which may have taken an input's place
             Sum2 e = {0.0f, 0.0f};
-#pragma unroll
-            for (int u = 0; u < VPT; ++u)
+            const uint16_t* again = a.h_out ? a.h_out + row * a.h_stride : x;
+            for (int vi = tid; vi < a.nvec; vi += nt) {
+                uint4 h = ld_stream_v4(again + 8 * vi);
+                if (!a.h_out && res) h = add_rows(h, ld_stream_v4(res + 8 * vi));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float h0, h1;
-                    halves(unpack2(word(v[u], i)), h0, h1);
+                    halves(unpack2(word(h, i)), h0, h1);
                     sum2_add(e, __fmul_rn(h0, h0), 0.0f);   // the square of a bf16 is exact
                     sum2_add(e, __fmul_rn(h1, h1), 0.0f);
                 }
+            }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
                 const float hi = __shfl_xor_sync(kFull, e.hi, o);
@@ -317,7 +324,7 @@ __global__ void __launch_bounds__(1024) rms_norm_quant_kernel(const RowQuantArgs
 // The rows as they are, with the dispatch kernels' arithmetic (quant.cuh), so that the
 // codes and scales are those of a fused dispatch bit for bit.
 template <int Q, int VPT>
-__global__ void __launch_bounds__(1024) quant_rows_kernel(const RowQuantArgs a) {
+__global__ void __launch_bounds__(VPT == 4 ? 256 : 1024, VPT == 4 ? 4 : 1) quant_rows_kernel(const RowQuantArgs a) {
     using TR = QTraits<Q>;
     __shared__ uint32_t s_max[32];
     const int nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, nwarps = nt >> 5;
@@ -361,8 +368,9 @@ __global__ void __launch_bounds__(1024) quant_rows_kernel(const RowQuantArgs a) 
     }
 }
 
-// With fewer rows than SMs a row gets a thread for every vector (the shortest
-// dependent chain); otherwise about 256 threads a row, so that several rows share an SM.
+// With fewer rows than SMs, or short rows, a thread has one vector (the shortest dependent
+// chain); otherwise a row has up to 256 threads, so that several rows share an SM: rows of 7168
+// by 448 threads of two vectors took 212 us (32768 rows, int8), by 224 threads of four 139 us.
 template <int Q, template <int, int> class K>
 cudaError_t launch_rows(const RowQuantArgs& a, int sms, cudaStream_t st) {
     const int vpt = a.rows <= sms || a.nvec <= 256 ? 1 : a.nvec <= 512 ? 2 : 4;
@@ -457,6 +465,7 @@ extern "C" ep_status ep_rms_norm_quant(const void* x, int64_t x_stride, const vo
     a.h_out = (uint16_t*)h_out;
     a.h_stride = h_stride;
     a.eps = eps;
+    a.inv_n = 1.0f / (float)hidden;
     const int sms = ep_current_sms();
     if (sms <= 0) return EP_ERR_CUDA;
     return launch_rms_norm_quant(a, quant, sms, (cudaStream_t)stream) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
