@@ -368,12 +368,13 @@ __global__ void __launch_bounds__(VPT == 4 ? 256 : 1024, VPT == 4 ? 4 : 1) quant
     }
 }
 
-// With fewer rows than SMs, or short rows, a thread has one vector (the shortest dependent
-// chain); otherwise a row has up to 256 threads, so that several rows share an SM: rows of 7168
-// by 448 threads of two vectors took 212 us (32768 rows, int8), by 224 threads of four 139 us.
+// With fewer rows than SMs a thread has one vector (the shortest dependent chain); otherwise four,
+// and a row as few warps as that makes, so that many rows share an SM.  65536 x 1024 int8 without a
+// residual: 39 us by one warp a row, 55 us by four of one vector each; 65536 x 4096: 147 us by four
+// warps, 166 us by eight; 32768 x 7168: 142 us by seven, 212 us by fourteen.
 template <int Q, template <int, int> class K>
 cudaError_t launch_rows(const RowQuantArgs& a, int sms, cudaStream_t st) {
-    const int vpt = a.rows <= sms || a.nvec <= 256 ? 1 : a.nvec <= 512 ? 2 : 4;
+    const int vpt = a.rows <= sms || a.nvec <= 32 ? 1 : a.nvec <= 64 ? 2 : 4;
     const int nt = ((a.nvec + vpt - 1) / vpt + 31) / 32 * 32;
     const dim3 grid((unsigned)a.rows);
     if (vpt == 1) K<Q, 1>::run(a, grid, nt, st);
