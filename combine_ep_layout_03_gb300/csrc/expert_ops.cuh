@@ -10,6 +10,7 @@ struct RowQuantArgs {
     const uint16_t* residual;  // as x, or null
     const uint16_t* gamma;     // [H] bf16 (normalised form only)
     uint16_t* h_out;           // [rows] rows of H bf16, h_stride apart, or null
+    uint16_t* y_out;           // [rows][H] bf16 of y, or null
     uint8_t* data;             // [rows][H] codes
     uint8_t* scales;           // [rows][scale_bytes]
     int64_t x_stride, residual_stride, h_stride;

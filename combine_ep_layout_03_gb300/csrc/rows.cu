@@ -214,6 +214,21 @@ __global__ void __launch_bounds__(VPT == 4 ? 256 : 1024, VPT == 4 ? 4 : 1) rms_n
     const bool row_ok = finite_bits(__float_as_uint(s) & 0x7fffffffu);
     const float nan = __uint_as_float(0x7fc00000u);
     uint8_t* data = a.data + row * a.H;
+    if (a.y_out) {
+        const f32x2 r2 = pair(rstd, rstd);
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            const int vi = u * nt + tid;
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float y0, y1;
+                halves(mul2(t[u][i], r2), y0, y1);
+                y[i] = pack_bf16x2_rn(y0, y1);
+            }
+            if (vi < a.nvec) st_v4(a.y_out + row * a.H + 8 * vi, make_uint4(y[0], y[1], y[2], y[3]));
+        }
+    }
 
     if constexpr (TR::token) {
         const float mf = __uint_as_float(m);
@@ -450,7 +465,7 @@ cudaError_t launch_quant_rows(const RowQuantArgs& a, int quant, int sms, cudaStr
 extern "C" ep_status ep_rms_norm_quant(const void* x, int64_t x_stride, const void* residual,
                                        int64_t residual_stride, const void* gamma, float eps, int64_t rows,
                                        int32_t hidden, ep_quant_mode quant, void* h_out, int64_t h_stride,
-                                       void* data, void* scales, ep_stream_t stream) {
+                                       void* y_out, void* data, void* scales, ep_stream_t stream) {
     RowQuantArgs a{};
     const ep_status s = check_rows(x, x_stride, rows, hidden, quant, data, scales, &a);
     if (s != EP_OK) return s;
@@ -459,7 +474,9 @@ extern "C" ep_status ep_rms_norm_quant(const void* x, int64_t x_stride, const vo
     if (residual && (!aligned(residual, 16) || residual_stride < hidden || residual_stride % 8 != 0))
         return EP_ERR_INVALID_ARG;
     if (h_out && (!aligned(h_out, 16) || h_stride < hidden || h_stride % 8 != 0)) return EP_ERR_INVALID_ARG;
+    if (y_out && !aligned(y_out, 16)) return EP_ERR_INVALID_ARG;
     if (rows == 0) return EP_OK;
+    a.y_out = (uint16_t*)y_out;
     a.residual = (const uint16_t*)residual;
     a.residual_stride = residual_stride;
     a.gamma = (const uint16_t*)gamma;

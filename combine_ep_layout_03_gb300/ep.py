@@ -112,7 +112,7 @@ def _load():
         "ep_dispatch_wait": ([vp, st, vp, vp, i64, ctypes.c_uint32, vp, vp, i64, vp], st),
         "ep_combine_async": ([vp, vp, i64, vp, i64, vp], st),
         "ep_combine_wait": ([vp, vp, i64, vp, vp, i32, vp, vp], st),
-        "ep_rms_norm_quant": ([vp, i64, vp, i64, vp, ctypes.c_float, i64, i32, st, vp, i64, vp, vp, vp], st),
+        "ep_rms_norm_quant": ([vp, i64, vp, i64, vp, ctypes.c_float, i64, i32, st, vp, i64, vp, vp, vp, vp], st),
         "ep_quant_rows": ([vp, i64, i64, i32, st, vp, vp, vp], st),
         "ep_expert_matmul": ([vp, vp, i64, i32, vp, vp, i32, i32, vp, i32, vp, vp, vp], st),
         "ep_moe_few_tokens_workspace_size": ([i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)], st),
@@ -371,10 +371,11 @@ def _row_stride(t: torch.Tensor, shape, what: str) -> int:
 
 
 def ep_rms_norm_quant(x: torch.Tensor, residual, gamma: torch.Tensor, eps: float, quant: int, h_out,
-                      data: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+                      data: torch.Tensor, scales: torch.Tensor, stream=None, y_out=None) -> None:
     """8-bit rows of RMSNorm(x + residual) * gamma.  x, residual (or None) and h_out (or None: the
     sum is not kept) are bf16 [rows, H], rows any stride apart; data and scales as of alloc_recv,
-    contiguous, of any type of the same bytes."""
+    contiguous, of any type of the same bytes; y_out, where given, receives the normalised rows
+    themselves, contiguous bf16 [rows, H]."""
     shape = x.shape
     _require(len(shape) == 2, "x: [rows, hidden]")
     rows, hidden = shape
@@ -386,9 +387,11 @@ def ep_rms_norm_quant(x: torch.Tensor, residual, gamma: torch.Tensor, eps: float
         h, hs = h_out.data_ptr(), _row_stride(h_out, shape, "h_out: as x")
     if gamma.dtype is not torch.bfloat16 or gamma.numel() != hidden or not gamma.is_contiguous():
         raise EPError(EP_ERR_INVALID_ARG, "gamma: bf16 [hidden]")
+    if y_out is not None and (y_out.dtype is not torch.bfloat16 or y_out.shape != shape or not y_out.is_contiguous()):
+        raise EPError(EP_ERR_INVALID_ARG, "y_out: contiguous bf16 [rows, hidden]")
     _check_rows_out(quant, rows, hidden, data, scales)
     status = _lib.ep_rms_norm_quant(x.data_ptr(), xs, res, rs, gamma.data_ptr(), eps, rows, hidden, quant, h, hs,
-                                    data.data_ptr(), scales.data_ptr(), _stream(stream))
+                                    _ptr(y_out), data.data_ptr(), scales.data_ptr(), _stream(stream))
     if status:
         _check(status, "ep_rms_norm_quant")
 

@@ -1,0 +1,84 @@
+"""An expert layer out of this library's calls, with the experts' weights in int8.
+
+    layer = ExpertLayer(R, T, w13, w13_scales, w2, w2_scales, gamma, topk=8)
+    y = layer.norm(x, residual)                  # bf16 [R*T, H]: what the router reads
+    topk_idx, topk_weights = router(y)
+    out = layer.experts(topk_idx, topk_weights)  # bf16 [R*T, H]
+
+``norm`` adds the residual (kept in ``layer.h``), normalises, and leaves the rows in int8 as well
+(ep_rms_norm_quant).  ``experts`` takes one of two ways:
+
+  - up to 64 tokens: ep_moe_few_tokens on y, which reads the chosen experts once and moves no rows;
+  - more: layout, dispatch of the int8 rows as they are, gate and up products with SwiGLU, the
+    inner rows to int8, the down product, combine.
+
+The first way keeps activations in bf16 where the second has them in int8.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import ep
+
+FEW_TOKENS = 64
+
+
+class ExpertLayer:
+    """Buffers and weights of one layer on one GPU that holds all R ranks.
+
+    w13 [E, 2I, H] int8 (gate rows, then up rows) with w13_scales [E, 2I] float32; w2 [E, H, I] int8
+    with w2_scales [E, H]; gamma [H] bf16.  Every call runs on the current stream, or on ``stream``."""
+
+    def __init__(self, R: int, T: int, w13, w13_scales, w2, w2_scales, gamma, topk: int, eps: float = 1e-6,
+                 alpha: int = 1):
+        self.w13, self.w13_scales, self.w2, self.w2_scales, self.gamma = w13, w13_scales, w2, w2_scales, gamma
+        self.E, self.I, self.H = w13.shape[0], w13.shape[1] // 2, w13.shape[2]
+        self.N, self.K, self.eps = R * T, topk, eps
+        dev = w13.device
+        self.y = torch.empty((self.N, self.H), dtype=torch.bfloat16, device=dev)
+        self.h = torch.empty_like(self.y)
+        self.out = torch.empty_like(self.y)
+        self.rows = torch.empty((self.N, self.H), dtype=torch.int8, device=dev)
+        self.row_scales = torch.empty((self.N, 1), dtype=torch.float32, device=dev)
+        self.few = self.N <= FEW_TOKENS
+        if self.few:
+            n = ep.ep_moe_few_tokens_workspace_size(self.N, self.H, self.E, topk, self.I)
+            self.workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+            self._status = torch.zeros(1, dtype=torch.int32, device=dev)
+            return
+        self.layout = ep.EPLayout(R, T, self.H, self.E, topk, alpha, device=dev)
+        cap = self.layout.worst_rows
+        self.recv, self.recv_scales = self.layout.alloc_recv(ep.EP_QUANT_INT8_PER_TOKEN, cap, device=dev)
+        self.inner = torch.empty((cap, self.I), dtype=torch.bfloat16, device=dev)
+        self.inner_rows = torch.empty((cap, self.I), dtype=torch.int8, device=dev)
+        self.inner_scales = torch.empty((cap, 1), dtype=torch.float32, device=dev)
+        self.expert_out = torch.empty((cap, self.H), dtype=torch.bfloat16, device=dev)
+
+    def norm(self, x: torch.Tensor, residual: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """y = RMSNorm(x + residual) * gamma, bf16; the sum is kept in self.h."""
+        ep.ep_rms_norm_quant(x, residual, self.gamma, self.eps, ep.EP_QUANT_INT8_PER_TOKEN, self.h, self.rows,
+                             self.row_scales, stream, self.y)
+        return self.y
+
+    def experts(self, topk_idx: torch.Tensor, topk_weights: torch.Tensor, shared: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+        """The weighted sum of the chosen experts' outputs of the rows that norm() left, plus shared
+        rows: [S, N, H] with one rank, [R, S, T, H] for the long way (as EPLayout.combine)."""
+        if self.few:
+            if shared is not None and shared.dim() == 4:   # [R, S, T, H]
+                shared = shared.transpose(0, 1).reshape(shared.shape[1], self.N, self.H)
+            ep.ep_moe_few_tokens(self.y, topk_idx.view(self.N, self.K), topk_weights.view(self.N, self.K), self.w13,
+                                 self.w2, self.out, self.workspace, self.w13_scales, self.w2_scales, shared,
+                                 self._status, stream)
+            return self.out
+        lay, q = self.layout, ep.EP_QUANT_INT8_PER_TOKEN
+        lay.layout(topk_idx, stream)
+        lay.dispatch_ex(self.rows, q, self.recv, self.recv_scales, stream, x_scales=self.row_scales, pre_encoded=True)
+        lay.expert_matmul(self.recv, self.recv_scales, self.w13, self.w13_scales, self.inner, swiglu=True, stream=stream)
+        ep.ep_quant_rows(self.inner, q, self.inner_rows, self.inner_scales, stream)
+        lay.expert_matmul(self.inner_rows, self.inner_scales, self.w2, self.w2_scales, self.expert_out, stream=stream)
+        return lay.combine(self.expert_out, topk_weights, self.out, shared, stream)
+
+    def status(self) -> int:
+        """The first device-side error since the last layout (synchronises)."""
+        return int(self._status.item()) if self.few else self.layout.status()

@@ -507,6 +507,7 @@ ep_status ep_step_host(ep_handle* handle, ep_quant_mode quant, const int64_t* to
 /* Device.  For each of `rows` rows of `hidden` bf16 columns:
  *   h = bf16(x + residual), or x without a residual;
  *   y = h * gamma / sqrt(mean(h^2) + eps), in float32;
+ *   y_out [rows, hidden] = bf16(y), where given (a router reads it);
  *   data, scales = the codes and scales of y in the receive-row format of `quant`
  *   (row-major, ep_recv_row_bytes), which ep_dispatch_ex moves unchanged.
  * quant: EP_QUANT_INT8_PER_TOKEN, the FP8 per-token and per-group modes, or MXFP8
@@ -518,12 +519,13 @@ ep_status ep_step_host(ep_handle* handle, ep_quant_mode quant, const int64_t* to
  * with a NaN or an infinity, or whose sum of squares passes the float32 range, and a
  * group or block whose gamma holds one, gets NaN scales (MX: byte 255) and zero codes.
  * x, residual (may be NULL) and h_out (may be NULL) have their own strides between
- * rows, in elements, multiples of 8 and at least `hidden`; x, residual, gamma, h_out and
+ * rows, in elements, multiples of 8 and at least `hidden`; x, residual, gamma, h_out, y_out and
  * data are 16-byte aligned, scales 4-byte aligned.  h_out may be x or residual itself
  * (with its stride).  hidden as for ep_params; eps >= 0. */
 ep_status ep_rms_norm_quant(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
                             const void* gamma, float eps, int64_t rows, int32_t hidden, ep_quant_mode quant,
-                            void* h_out, int64_t h_stride, void* data, void* scales, ep_stream_t stream);
+                            void* h_out, int64_t h_stride, void* y_out, void* data, void* scales,
+                            ep_stream_t stream);
 
 /* Device.  The rows of x (bf16, x_stride elements apart) in the receive-row format of
  * `quant` (the modes of ep_rms_norm_quant), with the arithmetic of ep_dispatch: the same

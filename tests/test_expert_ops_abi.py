@@ -12,15 +12,15 @@ NAN = float("nan")
 
 
 def norm(x=A, xs=512, res=None, rs=0, gamma=B, eps=1e-6, rows=4, hidden=512, quant=ep.EP_QUANT_INT8_PER_TOKEN, h=None,
-         hs=0, data=C, scales=D):
-    return ep.lib.ep_rms_norm_quant(x, xs, res, rs, gamma, eps, rows, hidden, quant, h, hs, data, scales, None)
+         hs=0, y=None, data=C, scales=D):
+    return ep.lib.ep_rms_norm_quant(x, xs, res, rs, gamma, eps, rows, hidden, quant, h, hs, y, data, scales, None)
 
 
 @pytest.mark.parametrize("kw", [
     dict(x=None), dict(x=A + 2), dict(xs=504), dict(xs=513), dict(res=A + 4, rs=512), dict(res=A, rs=511),
     dict(res=A, rs=256), dict(gamma=None), dict(gamma=B + 8), dict(eps=-1.0), dict(eps=NAN), dict(rows=-1),
     dict(rows=1 << 31), dict(hidden=0), dict(hidden=500, xs=504), dict(hidden=8200, xs=8200), dict(h=A + 2, hs=512),
-    dict(h=A, hs=500), dict(data=None), dict(data=C + 8), dict(scales=None), dict(scales=D + 2),
+    dict(h=A, hs=500), dict(y=A + 8), dict(data=None), dict(data=C + 8), dict(scales=None), dict(scales=D + 2),
     dict(quant=ep.EP_QUANT_FP8_E4M3_PER_GROUP, hidden=192, xs=192), dict(quant=ep.EP_QUANT_MXFP8_E5M2, hidden=48, xs=48)])
 def test_norm_refuses(kw):
     assert norm(**kw) == ep.EP_ERR_INVALID_ARG

@@ -115,6 +115,21 @@ def test_norm_rows(quant, rows, H, add):
     check(x, res, gamma, 1e-6, quant, *run(x, res, gamma, 1e-6, quant))
 
 
+@pytest.mark.parametrize("rows,H", [(3, 512), (400, 1024), (200, 7168)])
+def test_normalised_rows_themselves(rows, H):
+    """y_out: float32 y (the root off by at most SCALE_TOL, one product more) rounded to bf16."""
+    x, res, gamma = draw(rows, H, seed=rows)
+    y = torch.empty(rows, H, dtype=torch.bfloat16, device="cuda")
+    data = torch.empty(rows, H, dtype=torch.int8, device="cuda")
+    scales = torch.empty(rows, 1, device="cuda")
+    ep.ep_rms_norm_quant(x, res, gamma, 1e-6, ep.EP_QUANT_INT8_PER_TOKEN, None, data, scales, y_out=y)
+    v = (x.float() + res.float()).to(torch.bfloat16).double()
+    want = v * gamma.double() / torch.sqrt(v.square().mean(1, keepdim=True) + float(np.float32(1e-6)))
+    assert ((y.double() - want).abs() <= (2.0 ** -8 + 2 * SCALE_TOL) * want.abs()).all()
+    ref = run(x, res, gamma, 1e-6, ep.EP_QUANT_INT8_PER_TOKEN)
+    assert torch.equal(data.view(torch.uint8), ref[0]) and torch.equal(scales.view(torch.uint8), ref[1])
+
+
 @pytest.mark.parametrize("quant", MODES)
 def test_zero_rows(quant):
     x = torch.zeros(0, 256, dtype=torch.bfloat16, device="cuda")
