@@ -36,25 +36,27 @@ constexpr int kBoxTokens = 32;         // rows of a token box
 constexpr int kSets = 4;               // groups of four warps that convert in turn
 constexpr int kThreads = 32 * (8 + 4 * kSets);
 
-// TILE: token rows of a tile, both CTAs.  RAW TMA stages of 128 k, CVT float16 stages of 64 k.
-template <int TILE, int RAW, int CVT>
+// TILE: token rows of a tile, both CTAs.  RAW TMA stages of 128 k, CVT float16 stages of HALVES * 64 k.
+template <int TILE, int RAW, int CVT, int HALVES>
 struct Config {
     static constexpr int tile = TILE, half = TILE / 2;   // half: token rows that one CTA converts
-    static constexpr int raw_stages = RAW, cvt_stages = CVT;
+    static constexpr int raw_stages = RAW, cvt_stages = CVT, halves = HALVES;
     static constexpr int raw_bytes = kRawA + half * kRawK;
-    static constexpr int cvt_bytes = half * 128;         // 64 float16 a row
+    static constexpr int half_bytes = half * 128, cvt_bytes = HALVES * half_bytes;   // rows of 64 float16, HALVES times
+    static constexpr int cvt_columns = HALVES * 32;
     static constexpr uint32_t col_a = 2 * TILE;          // weights, behind two accumulators
     static constexpr int smem = 1024 + RAW * raw_bytes + CVT * cvt_bytes;
-    static_assert(col_a + CVT * 32 <= kColumns, "tensor memory");
+    static_assert(col_a + CVT * cvt_columns <= kColumns, "tensor memory");
     static_assert((CVT & (CVT - 1)) == 0 && CVT % kSets == 0, "uses take stages in turn");
-    static_assert(raw_bytes % 1024 == 0 && cvt_bytes % 1024 == 0 && half % kBoxTokens == 0, "swizzled rows");
+    static_assert(raw_bytes % 1024 == 0 && half_bytes % 1024 == 0 && half % kBoxTokens == 0, "swizzled rows");
 };
 
 // Segments of many rows: the largest tile of which tensor memory holds two.
-using Thick = Config<192, 5, 4>;
-// Segments of up to 64 rows: the tile's work is the weights', so more TMA stages are in flight, and
-// the columns that smaller accumulators leave hold more weights.
-using Thin = Config<64, 7, 8>;
+using Thick = Config<192, 5, 4, 1>;
+// Segments of up to 64 rows: the tile's work is the weights', so more TMA stages are in flight.  The
+// MMAs of 64 k with few columns are over before the words about them have been exchanged between
+// the warps, so a stage is 128 k (tensor memory has the columns that the accumulators leave).
+using Thin = Config<64, 7, 4, 2>;
 
 template <class C>
 struct Shared {
@@ -200,17 +202,18 @@ __device__ __forceinline__ bool issue_mma(const Work<C>& w) {
         if (!warp_wait(&w.sh.acc_empty[acc.stage], acc.parity ^ 1)) { ok = false; break; }
         tmem_fence_after();
         const uint32_t d = w.tmem + acc.stage * C::tile;
-        for (int k = 0; k < 2 * w.raws; ++k) {
+        for (int k = 0; k < 2 / C::halves * w.raws; ++k) {
             if (!ready && !warp_wait(&w.sh.cvt_full[c.stage], c.parity)) { ok = false; break; }
             tmem_fence_after();
-            const uint32_t at = w.tmem + C::col_a + c.stage * 32;
+            const uint32_t at = w.tmem + C::col_a + c.stage * C::cvt_columns;
             const uint64_t b = smem_desc_k128(cvt0 + c.stage * C::cvt_bytes);
             uint64_t* const empty = &w.sh.cvt_empty[c.stage];
             c.next();
             ready = __all_sync(0xffffffffu, mbar_try_wait(&w.sh.cvt_full[c.stage], c.parity));
             if (elect_one()) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) mma_pair_f16(d, at + 8 * j, b + 2 * j, idesc, k > 0 || j > 0);
+                for (int j = 0; j < 4 * C::halves; ++j)
+                    mma_pair_f16(d, at + 8 * j, b + (j >> 2) * (C::half_bytes >> 4) + 2 * (j & 3), idesc, k > 0 || j > 0);
                 commit_pair(empty);
             }
             __syncwarp();
@@ -224,52 +227,61 @@ __device__ __forceinline__ bool issue_mma(const Work<C>& w) {
     return warp_wait(&w.sh.drained, 0) && ok;
 }
 
-// Four warps turn 64 k of a stage into float16 at a time.  Use u of the converted stages is half
-// u & 1 of TMA stage u >> 1; group `set` takes every kSets-th use.
+// Four warps turn a converted stage's codes into float16 at a time; group `set` takes every kSets-th
+// use.  With one half, use u of the converted stages is half u & 1 of TMA stage u >> 1; with two, use
+// u is TMA stage u.
 template <class C>
 __device__ __forceinline__ bool convert(const Work<C>& w, int warp, int set) {
     const int lane = threadIdx.x & 31;
     const uint32_t full0 = cluster_addr(smem_addr(&w.sh.cvt_full[0]), 0);
-    const int rr = lane & 7, q = lane >> 3, h = set & 1;
+    const int rr = lane & 7, q = lane >> 3, h0 = C::halves == 1 ? set & 1 : 0;
     constexpr int kChunks = C::half / 32;
     static_assert(kSets % 2 == 0, "a group keeps to one half");
-    // weights: a thread per row (tensor-memory lane), its four chunks of 16 codes where the swizzle put them;
-    // tokens: a lane per chunk, eight rows and four chunks a warp, free of bank conflicts
+    // weights: a thread per row (tensor-memory lane), its four chunks of 16 codes of a half where the swizzle put
+    // them; tokens: a lane per chunk, eight rows and four chunks a warp, free of bank conflicts.  The other half
+    // of a row lies 64 bytes across (rows are 128-byte aligned).
     uint32_t from_w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) from_w[i] = smem_addr(w.raw) + (warp * 32 + lane) * kRawK + (((4 * h + i) ^ rr) * 16);
-    const uint32_t from_t = smem_addr(w.raw) + kRawA + (warp * 8 + rr) * kRawK + (((4 * h + q) ^ rr) * 16);
+    for (int i = 0; i < 4; ++i) from_w[i] = smem_addr(w.raw) + (warp * 32 + lane) * kRawK + (((4 * h0 + i) ^ rr) * 16);
+    const uint32_t from_t = smem_addr(w.raw) + kRawA + (warp * 8 + rr) * kRawK + (((4 * h0 + q) ^ rr) * 16);
     const uint32_t row = smem_addr(w.cvt) + (warp * 8 + rr) * 128;
     const uint32_t to0 = row + (((2 * q) ^ rr) * 16), to1 = row + (((2 * q + 1) ^ rr) * 16);
     const uint32_t col = w.tmem + ((uint32_t)(warp * 32) << 16) + C::col_a;
     Ring<C::raw_stages> r;
-    uint32_t use = h;
+    uint32_t use = h0;
     bool ok = true;
     for (int64_t item = w.first; ok && item < w.items; item += w.step) {
         const int rows = tile_of<C>(w.sh.seg, w.a, w.ctiles, item).n / 2 - warp * 8;
-        for (int k = 0; k < w.raws; ++k, use += 2, r.next()) {
+        for (int k = 0; ok && k < w.raws; ++k, use += 2 / C::halves, r.next()) {
             if (use % kSets != (uint32_t)set) continue;
             const uint32_t stage = use % C::cvt_stages, parity = (use / C::cvt_stages) & 1;
             if (!warp_wait(&w.sh.raw_full[r.stage], r.parity)) { ok = false; break; }
             const uint32_t at = r.stage * C::raw_bytes;
-            uint32_t v[32];
-            uint4 in[kChunks];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) codes_to_f16(lds_at(from_w[i] + at), v + 8 * i);
+            for (int h = 0; h < C::halves; ++h) {
+                uint32_t v[32];
+                uint4 in[kChunks];
 #pragma unroll
-            for (int g = 0; g < kChunks; ++g) in[g] = lds_at(from_t + at + g * 32 * kRawK);   // some past the tile's rows
-            if (!warp_wait(&w.sh.cvt_empty[stage], parity ^ 1)) { ok = false; break; }
-            tmem_fence_after();
-            tmem_store32(col + stage * 32, v);
-            const uint32_t to = stage * C::cvt_bytes;
+                for (int i = 0; i < 4; ++i) codes_to_f16(lds_at((from_w[i] + at) ^ (h * 64)), v + 8 * i);
 #pragma unroll
-            for (int g = 0; g < kChunks; ++g) {
-                if (g * 32 >= rows) break;
-                uint32_t f[8];
-                codes_to_f16(in[g], f);
-                sts_at(to0 + to + g * 32 * 128, f[0], f[1], f[2], f[3]);
-                sts_at(to1 + to + g * 32 * 128, f[4], f[5], f[6], f[7]);
+                for (int g = 0; g < kChunks; ++g)   // some past the tile's rows
+                    in[g] = lds_at((from_t + at + g * 32 * kRawK) ^ (h * 64));
+                if (h == 0) {
+                    if (!warp_wait(&w.sh.cvt_empty[stage], parity ^ 1)) { ok = false; break; }
+                    tmem_fence_after();
+                }
+                tmem_store32(col + stage * C::cvt_columns + h * 32, v);
+                const uint32_t to = stage * C::cvt_bytes + h * C::half_bytes;
+#pragma unroll
+                for (int g = 0; g < kChunks; ++g) {
+                    if (g * 32 >= rows) break;
+                    uint32_t f[8];
+                    codes_to_f16(in[g], f);
+                    sts_at(to0 + to + g * 32 * 128, f[0], f[1], f[2], f[3]);
+                    sts_at(to1 + to + g * 32 * 128, f[4], f[5], f[6], f[7]);
+                }
             }
+            if (!ok) break;
             fence_proxy_async_smem();
             tmem_wait_stores();
             tmem_fence_before();
@@ -281,7 +293,7 @@ __device__ __forceinline__ bool convert(const Work<C>& w, int warp, int set) {
         }
     }
     // the commits that free the last stages reach this CTA before it ends
-    use -= h;
+    use -= h0;
     for (uint32_t i = 0; ok && i < C::cvt_stages && i < use; ++i)
         ok = warp_wait(&w.sh.cvt_empty[(use - 1 - i) % C::cvt_stages], ((use - 1 - i) / C::cvt_stages) & 1);
     return ok;
@@ -394,7 +406,7 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
     const uint32_t cta = cluster_rank();
     uint8_t* raw = dynamic + ((1024 - (smem_addr(dynamic) & 1023)) & 1023);
     if (tid == 0) {
-        for (int i = 0; i < C::raw_stages; ++i) { mbar_init(&sh.raw_full[i], 1); mbar_init(&sh.raw_empty[i], 8); }
+        for (int i = 0; i < C::raw_stages; ++i) { mbar_init(&sh.raw_full[i], 1); mbar_init(&sh.raw_empty[i], 8 / C::halves); }
         for (int i = 0; i < C::cvt_stages; ++i) { mbar_init(&sh.cvt_full[i], 8); mbar_init(&sh.cvt_empty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&sh.acc_full[i], 1); mbar_init(&sh.acc_empty[i], 8); }
         mbar_init(&sh.drained, 1);
