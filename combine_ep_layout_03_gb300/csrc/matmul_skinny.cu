@@ -74,6 +74,13 @@ __global__ void __launch_bounds__(kThreads, 2) matmul_skinny_kernel(const Matmul
         const Item t = item_of(s, a, ctiles, item);
         const int64_t row0 = (int64_t)s.base[t.e] + t.first;
         float* sums = red + buffer * kSums;
+        // the scales of this thread's first result arrive meanwhile
+        struct Scales { float row, gate, up; };
+        auto scales = [&](int i) {
+            const float* sw = a.w_scales + (int64_t)t.e * a.N + min(t.channel * per + i % per, outs - 1);
+            return Scales{a.a_scales[row0 + i / per], sw[0], GLU ? sw[outs] : 0.0f};
+        };
+        const Scales mine = tid < t.m * per ? scales(tid) : Scales{};
         auto run = [&](auto count) {
             constexpr int NT = decltype(count)::value;
             const uint8_t* tok[NT];
@@ -83,23 +90,35 @@ __global__ void __launch_bounds__(kThreads, 2) matmul_skinny_kernel(const Matmul
                 tok[j] = a.a + (row0 + min(j * 8 + g, t.m - 1)) * a.K;   // columns past the last repeat it
                 acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
             }
+            TokenPart<true> next;   // with one tile: the tokens of the next piece
+            if (NT == 1 && warp < pieces) load_tokens<true, true>(next, tok[0], warp, q * 16, a.K);
             for (int c = warp; c < pieces; c += kWarps) {
-                TokenPart<true> part[NT];
-#pragma unroll
-                for (int j = 0; j < NT; ++j) load_tokens<true, true>(part[j], tok[j], c, q * 16, a.K);
+                TokenPart<true> now;
+                if constexpr (NT == 1) {
+                    now = next;
+                    if (c + kWarps < pieces) load_tokens<true, true>(next, tok[0], c + kWarps, q * 16, a.K);
+                }
                 uint4 lo[2], hi[2];
                 ring.take(lo, hi);
-                mma_piece<true, NT, 1>(acc, lo, hi, [&](int j, int) { return part[j]; });
+                mma_piece<true, NT, 1>(acc, lo, hi, [&](int j, int) {
+                    if constexpr (NT == 1) {
+                        return now;
+                    } else {
+                        TokenPart<true> part;
+                        load_tokens<true, true>(part, tok[j], c, q * 16, a.K);
+                        return part;
+                    }
+                });
                 __syncwarp();
                 fetch();
             }
-            float* mine = sums + warp * NT * 8 * 16;
+            float* part = sums + warp * NT * 8 * 16;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                mine[(j * 8 + 2 * q) * 16 + g] = acc[j][0];
-                mine[(j * 8 + 2 * q + 1) * 16 + g] = acc[j][1];
-                mine[(j * 8 + 2 * q) * 16 + g + 8] = acc[j][2];
-                mine[(j * 8 + 2 * q + 1) * 16 + g + 8] = acc[j][3];
+                part[(j * 8 + 2 * q) * 16 + g] = acc[j][0];
+                part[(j * 8 + 2 * q + 1) * 16 + g] = acc[j][1];
+                part[(j * 8 + 2 * q) * 16 + g + 8] = acc[j][2];
+                part[(j * 8 + 2 * q + 1) * 16 + g + 8] = acc[j][3];
             }
             return NT * 8;
         };
@@ -115,10 +134,9 @@ __global__ void __launch_bounds__(kThreads, 2) matmul_skinny_kernel(const Matmul
                 if constexpr (GLU) u += sums[(k * cols + col) * 16 + c + 8];
             }
             const int64_t row = row0 + col;
-            const float sa = a.a_scales[row];
-            const float* sw = a.w_scales + (int64_t)t.e * a.N + ch;
-            v = v * sa * sw[0];
-            if constexpr (GLU) v = v / (1.0f + expf(-v)) * (u * sa * sw[outs]);
+            const Scales f = i == tid ? mine : scales(i);
+            v = v * f.row * f.gate;
+            if constexpr (GLU) v = v / (1.0f + expf(-v)) * (u * f.row * f.up);
             a.out[row * outs + ch] = (uint16_t)pack_bf16x2_rn(v, 0.0f);
         }
     }
