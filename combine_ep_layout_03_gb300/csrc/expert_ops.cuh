@@ -23,6 +23,27 @@ struct RowQuantArgs {
 cudaError_t launch_rms_norm_quant(const RowQuantArgs& a, int quant, int sms, cudaStream_t st);
 cudaError_t launch_quant_rows(const RowQuantArgs& a, int quant, int sms, cudaStream_t st);
 
+// Launches a kernel that may be set up while the one before it in the stream ends (programmatic
+// dependent launch).  It must call wait_for_previous() before it touches global memory.
+template <class... P, class... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Everything that earlier kernels of the stream wrote is visible after this.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // SMs of the current device (0 when the query fails).
 inline int ep_current_sms() {
     int dev = 0, sms = 0;

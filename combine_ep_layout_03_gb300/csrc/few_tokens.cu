@@ -141,8 +141,9 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_inner_ke
     constexpr int kBuffers = S::buffers, kSums = kWarps * MAXNT * 8 * 16;
     float* const red = reinterpret_cast<float*>(slots + S::ring_bytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) prefetch_map(&map_w);
+    wait_for_previous();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     build_routing(r, a);
     const int tiles = a.I / 8, items = r.count * tiles, step = gridDim.x;
     const int k_bytes = a.H * (W8 ? 1 : 2), pieces = (k_bytes + 127) / 128;
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_out_kern
     };
     // the weights do not depend on the first kernel: they are on their way while it ends
     for (int d = 0; d < S::depth; ++d) fetch();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
 
     float* mine = sums + warp * a.T * 16;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -430,23 +431,13 @@ cudaError_t launch(const FewArgs& a, int sms, cudaStream_t st) {
     cudaError_t e = allow_smem(few_inner_kernel<W8, MAXNT>, S::inner_smem, inner_done);
     if (e == cudaSuccess) e = allow_smem(few_out_kernel<W8, MAXNT>, S::out_smem, out_done);
     if (e != cudaSuccess) return e;
-    few_inner_kernel<W8, MAXNT><<<(unsigned)(items < ctas ? items : ctas), kThreads, S::inner_smem, st>>>(a, map13);
-    e = cudaGetLastError();
+    e = launch_overlapped(few_inner_kernel<W8, MAXNT>, dim3((unsigned)(items < ctas ? items : ctas)), kThreads, S::inner_smem, st,
+                          a, map13);
     if (e != cudaSuccess) return e;
-    // The second kernel may start while the first drains: it reads the routing, fetches its first
-    // weights, then waits.
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3((unsigned)(tiles < ctas ? tiles : ctas));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = S::out_smem;
-    cfg.stream = st;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, few_out_kernel<W8, MAXNT>, a, rows, map2);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    // The second kernel reads the routing and fetches its first weights while the first drains.  Both have waited
+    // for what came before, so neither reads them before they are there.
+    return launch_overlapped(few_out_kernel<W8, MAXNT>, dim3((unsigned)(tiles < ctas ? tiles : ctas)), kThreads, S::out_smem, st,
+                             a, rows, map2);
 }
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }

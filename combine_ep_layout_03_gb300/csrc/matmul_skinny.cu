@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(kThreads, 2) matmul_skinny_kernel(const Matmul
     __shared__ Segments s;
     float* const red = reinterpret_cast<float*>(slots + kRingBytes);   // two buffers in turn: a barrier an item
     if (threadIdx.x == 0) prefetch_map(&map_w);
+    wait_for_previous();
     if (!load_segments<kThreads>(s, a, kTileRows)) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
     constexpr int per = GLU ? 8 : 16;   // output channels of an item
@@ -171,8 +172,7 @@ cudaError_t launch_matmul_skinny(const MatmulArgs& a, int sms, cudaStream_t st) 
     static std::atomic<uint64_t> done[2];
     const cudaError_t e = allow_smem(kernel, kSmem, done[a.swiglu]);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, kSmem, st>>>(a, map_w);
-    return cudaGetLastError();
+    return launch_overlapped(kernel, dim3(grid), kThreads, kSmem, st, a, map_w);
 }
 
 extern "C" ep_status ep_expert_matmul(const void* a, const float* a_scales, int64_t rows, int32_t k, const void* w,

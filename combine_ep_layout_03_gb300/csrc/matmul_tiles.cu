@@ -402,7 +402,6 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
         prefetch_map(&map_a);
         prefetch_map(&map_half);
     }
-    if (!load_segments<kThreads>(sh.seg, a, C::tile)) return;   // the same answer in both CTAs
     const uint32_t cta = cluster_rank();
     uint8_t* raw = dynamic + ((1024 - (smem_addr(dynamic) & 1023)) & 1023);
     if (tid == 0) {
@@ -413,6 +412,8 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
         mbar_fence_init();
     }
     if (warp == 2) tmem_alloc_pair(&sh.tmem, kColumns);
+    wait_for_previous();
+    const bool fits = load_segments<kThreads>(sh.seg, a, C::tile);   // the same answer in both CTAs
     tmem_fence_before();
     __syncthreads();
     cluster_sync();
@@ -422,7 +423,7 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
     const int per_pair = GLU ? kRows : 2 * kRows;   // output channels of a tile
     const int ctiles = (outs + per_pair - 1) / per_pair;
     const Work<C> w = {a, sh, raw, raw + C::raw_stages * C::raw_bytes, sh.tmem, cta, outs, per_pair, ctiles,
-                    (a.K + kRawK - 1) / kRawK, blockIdx.x >> 1, (int64_t)sh.seg.tile[a.E] * ctiles, gridDim.x >> 1};
+                    (a.K + kRawK - 1) / kRawK, blockIdx.x >> 1, fits ? (int64_t)sh.seg.tile[a.E] * ctiles : 0, gridDim.x >> 1};
     bool ok = true;
     if (warp == 0) {
         if (lane == 0) ok = load_tiles<C, GLU>(w, &map_w, &map_a, &map_half);
@@ -456,8 +457,7 @@ cudaError_t launch(const MatmulArgs& a, int sms, cudaStream_t st) {
     static std::atomic<uint64_t> done[2];
     const cudaError_t e = allow_smem(kernel, C::smem, done[a.swiglu]);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(2 * pairs), kThreads, C::smem, st>>>(a, map_w, map_a, map_half);
-    return cudaGetLastError();
+    return launch_overlapped(kernel, dim3((unsigned)(2 * pairs)), kThreads, C::smem, st, a, map_w, map_a, map_half);
 }
 
 // Up to this many rows an expert take the thin form.  128 experts x 4096 x 2048 of 64 rows: 226 us thin,

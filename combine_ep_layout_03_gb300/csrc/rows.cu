@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 256 : 1024, VPT == 4 ? 4 : 1) rms_n
     const int64_t row = blockIdx.x;
     const uint16_t* x = a.x + row * a.x_stride;
     const uint16_t* res = a.residual ? a.residual + row * a.residual_stride : nullptr;
+    wait_for_previous();
 
     uint4 v[VPT], g[VPT];
 #pragma unroll
@@ -347,6 +348,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 256 : 1024, VPT == 4 ? 4 : 1) quant
     const uint16_t* x = a.x + row * a.x_stride;
     uint4 v[VPT];
     uint32_t m = 0;
+    wait_for_previous();
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
         const int vi = u * nt + tid;
@@ -392,23 +394,22 @@ cudaError_t launch_rows(const RowQuantArgs& a, int sms, cudaStream_t st) {
     const int vpt = a.rows <= sms || a.nvec <= 32 ? 1 : a.nvec <= 64 ? 2 : 4;
     const int nt = ((a.nvec + vpt - 1) / vpt + 31) / 32 * 32;
     const dim3 grid((unsigned)a.rows);
-    if (vpt == 1) K<Q, 1>::run(a, grid, nt, st);
-    else if (vpt == 2) K<Q, 2>::run(a, grid, nt, st);
-    else K<Q, 4>::run(a, grid, nt, st);
-    return cudaGetLastError();
+    if (vpt == 1) return K<Q, 1>::run(a, grid, nt, st);
+    if (vpt == 2) return K<Q, 2>::run(a, grid, nt, st);
+    return K<Q, 4>::run(a, grid, nt, st);
 }
 
 template <int Q, int VPT>
 struct NormKernel {
-    static void run(const RowQuantArgs& a, dim3 grid, int nt, cudaStream_t st) {
-        rms_norm_quant_kernel<Q, VPT><<<grid, nt, 0, st>>>(a);
+    static cudaError_t run(const RowQuantArgs& a, dim3 grid, int nt, cudaStream_t st) {
+        return launch_overlapped(rms_norm_quant_kernel<Q, VPT>, grid, nt, 0, st, a);
     }
 };
 
 template <int Q, int VPT>
 struct QuantKernel {
-    static void run(const RowQuantArgs& a, dim3 grid, int nt, cudaStream_t st) {
-        quant_rows_kernel<Q, VPT><<<grid, nt, 0, st>>>(a);
+    static cudaError_t run(const RowQuantArgs& a, dim3 grid, int nt, cudaStream_t st) {
+        return launch_overlapped(quant_rows_kernel<Q, VPT>, grid, nt, 0, st, a);
     }
 };
 
