@@ -76,12 +76,13 @@ __device__ __forceinline__ Tile tile_of(const Segments& s, const MatmulArgs& a, 
     const int e = expert_of_tile(s, a.E, (int)(item / ctiles));
     const int tiles = s.tile[e + 1] - s.tile[e];
     const int local = (int)(item - (int64_t)s.tile[e] * ctiles);
-    const int per = ((s.rows[e] + tiles - 1) / tiles + 31) / 32 * 32;   // equal tiles, not full ones and a rest
-    const int first = local % tiles * per;
+    // the segment's groups of 32 rows dealt out evenly: no tile is much shorter, and none pays for a row more
+    const int groups = (s.rows[e] + 31) / 32, j = local % tiles, each = groups / tiles, more = groups % tiles;
+    const int first = 32 * (j * each + min(j, more));
     Tile t;
     t.expert = e;
     t.row0 = (int64_t)s.base[e] + first;
-    t.m = min(per, s.rows[e] - first);
+    t.m = min(32 * (each + (j < more)), s.rows[e] - first);
     t.n = (t.m + 31) / 32 * 32;
     t.channel = local / tiles;
     return t;
