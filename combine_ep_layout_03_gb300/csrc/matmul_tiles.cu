@@ -48,6 +48,13 @@ struct Config {
     static constexpr int smem = 1024 + RAW * raw_bytes + CVT * cvt_bytes;
     static_assert(col_a + CVT * cvt_columns <= kColumns, "tensor memory");
     static_assert((CVT & (CVT - 1)) == 0 && CVT % kSets == 0, "uses take stages in turn");
+    // A group of warps looks at the mbarrier of every `turn`-th TMA stage only, and a parity tells two
+    // neighbouring phases apart, no more: when it asks for use i of a stage, use i - RAW must be over.
+    // It has handed over use i - turn, for which the MMAs of use i - turn - (CVT in TMA stages) were
+    // done, and with them, in order, everything before.  (With seven stages in the thin form a group
+    // could overtake a load that came late, take its stage for the next one, and free it twice.)
+    static constexpr int turn = kSets * HALVES / 2;
+    static_assert(turn + CVT * HALVES / 2 <= RAW || RAW % turn == 0, "stages that no group can lap");
     static_assert(raw_bytes % 1024 == 0 && half_bytes % 1024 == 0 && half % kBoxTokens == 0, "swizzled rows");
 };
 
@@ -56,7 +63,7 @@ using Thick = Config<192, 5, 4, 1>;
 // Segments of up to 64 rows: the tile's work is the weights', so more TMA stages are in flight.  The
 // MMAs of 64 k with few columns are over before the words about them have been exchanged between
 // the warps, so a stage is 128 k (tensor memory has the columns that the accumulators leave).
-using Thin = Config<64, 7, 4, 2>;
+using Thin = Config<64, 8, 4, 2>;
 
 template <class C>
 struct Shared {
