@@ -144,16 +144,20 @@ __global__ void __launch_bounds__(kThreads, 2) matmul_skinny_kernel(const Matmul
     if (!ring.drain() && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
 }
 
-// Few enough rows and weights for the kernel above: its loop reads weights at about 2.9 TB/s for up
-// to eight rows an expert, 2.4 for 16 and 1.5 for 32, but starts sooner and uses every SM on a single
-// small matrix, where matmul_tiles.cu, at 5 TB/s, has a tile for few of them.  Measured (us, this
-// kernel and that): 8 rows x 4096 x 4096: 10 and 25; 32 rows: 15 and 25; 64 rows: 28 and 26;
-// 16 experts of 8 rows, 1024 x 704: 12 and 16; 128 experts of 8 rows, 4096 x 2048: 377 and 223.
-constexpr int64_t kSkinnyWork = 68 << 20;   // bytes of weights times tiles of eight rows
-
-bool is_skinny(const MatmulArgs& a) {
+// Few enough rows and weights for the kernel above.  Its loop reads weights at about 3 TB/s for up to
+// eight rows an expert and less for more, but on every SM and from the start; matmul_tiles.cu reads at
+// 6 TB/s, starts later, and a round of its tiles takes as long as their k, however few they are.
+// Measured, us (this kernel, that one): 8 rows x 4096 x 4096: 7.1, 15.1; 32 rows: 12.5, 15.2;
+// 8 rows x 7168 x 4096: 10.8, 22.5; experts of 2048 x 1024: 16 of 8 rows 14.0, 11.1; 8 of 16 rows
+// 10.5, 11.1; 8 of 32 rows 15.0, 11.1; 32 of 8 rows 27.2, 17.4; 16 of 8 rows, 1024 x 1400: 13.9, 13.4.
+bool is_skinny(const MatmulArgs& a, int sms) {
     const int64_t experts = a.rows < a.E ? a.rows : a.E, rows = (a.rows + a.E - 1) / a.E;
-    return rows <= 32 && experts * a.N * a.K * ((rows + 7) / 8) <= kSkinnyWork;
+    if (rows > 32) return false;
+    const double rate[4] = {3.2, 2.7, 2.2, 1.7};   // bytes of weights a picosecond, by tiles of eight rows
+    const double here = 4.5 + 1e-6 * (double)(experts * a.N * a.K) / rate[(rows - 1) / 8];
+    const int64_t tiles = experts * (((a.swiglu ? a.N / 2 : a.N) + (a.swiglu ? 127 : 255)) / (a.swiglu ? 128 : 256));
+    const int64_t rounds = (tiles + sms / 2 - 1) / (sms / 2);
+    return here <= 6.0 + (double)rounds * a.K / 420.0;
 }
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
@@ -202,7 +206,7 @@ extern "C" ep_status ep_expert_matmul(const void* a, const float* a_scales, int6
     m.swiglu = swiglu;
     const int sms = ep_current_sms();
     if (sms <= 0) return EP_ERR_CUDA;
-    const cudaError_t e = is_skinny(m) ? launch_matmul_skinny(m, sms, (cudaStream_t)stream)
+    const cudaError_t e = is_skinny(m, sms) ? launch_matmul_skinny(m, sms, (cudaStream_t)stream)
                                        : launch_matmul_tiles(m, sms, (cudaStream_t)stream);
     return e == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }

@@ -217,7 +217,7 @@ __device__ __forceinline__ bool issue_mma(const Work<C>& w) {
             const uint64_t b = smem_desc_k128(cvt0 + c.stage * C::cvt_bytes);
             uint64_t* const empty = &w.sh.cvt_empty[c.stage];
             c.next();
-            ready = __all_sync(0xffffffffu, mbar_try_wait(&w.sh.cvt_full[c.stage], c.parity));
+            ready = __all_sync(0xffffffffu, mbar_test(&w.sh.cvt_full[c.stage], c.parity));
             if (elect_one()) {
 #pragma unroll
                 for (int j = 0; j < 4 * C::halves; ++j)
@@ -468,12 +468,19 @@ cudaError_t launch(const MatmulArgs& a, int sms, cudaStream_t st) {
     return launch_overlapped(kernel, dim3((unsigned)(2 * pairs)), kThreads, C::smem, st, a, map_w, map_a, map_half);
 }
 
-// Up to this many rows an expert take the thin form.  128 experts x 4096 x 2048 of 64 rows: 226 us thin,
-// 258 us thick; 16 experts x 1024 x 1400 of 160 rows: 31 us thin, 24 us thick.
+// Segments of up to this many rows take the thin form, and so do larger ones if its rounds of tiles, which
+// take three quarters as long, are that few (half-empty rounds cost whole ones).  Measured, us (thin,
+// thick): 128 rows x 4096 x 4096: 15.8, 22.1; 500 x 4096 x 1000: 15.7, 22.3; 2000 x 2048 x 1000: 16.9,
+// 14.9; 4000 x 2048 x 2000: 44.7, 34.1; 64 experts of 96 rows, 2048 x 1024: 49.0, 43.5; 128 experts of
+// 64 rows, 4096 x 2048: 183, 258; 16 experts of 166 rows, 1024 x 1400: 22.5, 18.6.
 constexpr int kThinRows = 64;
 
 }  // namespace
 
 cudaError_t launch_matmul_tiles(const MatmulArgs& a, int sms, cudaStream_t st) {
-    return a.rows <= (int64_t)a.E * kThinRows ? launch<Thin>(a, sms, st) : launch<Thick>(a, sms, st);
+    const int64_t rows = (a.rows + a.E - 1) / a.E, per_pair = a.swiglu ? kRows : 2 * kRows;
+    const int64_t columns = ((a.swiglu ? a.N / 2 : a.N) + per_pair - 1) / per_pair * a.E, pairs = sms / 2;
+    const int64_t thin = ((rows + Thin::tile - 1) / Thin::tile * columns + pairs - 1) / pairs;
+    const int64_t thick = ((rows + Thick::tile - 1) / Thick::tile * columns + pairs - 1) / pairs;
+    return rows <= kThinRows || 4 * thin <= 3 * thick + 1 ? launch<Thin>(a, sms, st) : launch<Thick>(a, sms, st);
 }

@@ -55,6 +55,16 @@ __device__ __forceinline__ bool mbar_wait_parked(uint64_t* bar, uint32_t parity)
     return false;
 }
 
+// Whether a phase is over, without waiting (a try_wait may hold the thread for microseconds).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+
 // One lane of a converged warp, the same one each time.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
