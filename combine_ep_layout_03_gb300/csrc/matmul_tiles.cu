@@ -171,10 +171,7 @@ __device__ __forceinline__ bool load_tiles(const Work<C>& w, const CUtensorMap* 
             uint64_t* bar = &w.sh.raw_full[r.stage];
             mbar_arrive_expect_tx(bar, kRawA + boxes * kBoxTokens * kRawK);
             if (GLU) {
-                // a box: 16 gates and their 16 ups, the 32 lanes of an epilogue warp
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tma_load_4d(dst + 32 * i * kRawK, map_w, k * kRawK, ch + 16 * i, 0, t.expert, bar);
+                tma_load_4d(dst, map_w, k * kRawK, ch, 0, t.expert, bar);   // 64 gates, then their ups
             } else {
                 tma_load_2d(dst, map_w, k * kRawK, t.expert * w.a.N + ch, bar);
             }
@@ -238,7 +235,7 @@ __device__ __forceinline__ bool issue_mma(const Work<C>& w) {
 // Four warps turn a converted stage's codes into float16 at a time; group `set` takes every kSets-th
 // use.  With one half, use u of the converted stages is half u & 1 of TMA stage u >> 1; with two, use
 // u is TMA stage u.
-template <class C>
+template <class C, bool GLU>
 __device__ __forceinline__ bool convert(const Work<C>& w, int warp, int set) {
     const int lane = threadIdx.x & 31;
     const uint32_t full0 = cluster_addr(smem_addr(&w.sh.cvt_full[0]), 0);
@@ -248,9 +245,11 @@ __device__ __forceinline__ bool convert(const Work<C>& w, int warp, int set) {
     // weights: a thread per row (tensor-memory lane), its four chunks of 16 codes of a half where the swizzle put
     // them; tokens: a lane per chunk, eight rows and four chunks a warp, free of bank conflicts.  The other half
     // of a row lies 64 bytes across (rows are 128-byte aligned).
+    // With gates and ups, lanes 0-15 of a warp take 16 gates and lanes 16-31 their ups (rows 64 further on).
+    const int weight = GLU ? warp * 16 + (lane & 15) + (lane & 16) * 4 : warp * 32 + lane;
     uint32_t from_w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) from_w[i] = smem_addr(w.raw) + (warp * 32 + lane) * kRawK + (((4 * h0 + i) ^ rr) * 16);
+    for (int i = 0; i < 4; ++i) from_w[i] = smem_addr(w.raw) + weight * kRawK + (((4 * h0 + i) ^ rr) * 16);
     const uint32_t from_t = smem_addr(w.raw) + kRawA + (warp * 8 + rr) * kRawK + (((4 * h0 + q) ^ rr) * 16);
     const uint32_t row = smem_addr(w.cvt) + (warp * 8 + rr) * 128;
     const uint32_t to0 = row + (((2 * q) ^ rr) * 16), to1 = row + (((2 * q + 1) ^ rr) * 16);
@@ -438,7 +437,7 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
     } else if (warp == 1) {
         if (cta == 0) ok = issue_mma(w);
     } else if (warp >= 8) {
-        ok = convert<C>(w, warp & 3, (warp >> 2) - 2);
+        ok = convert<C, GLU>(w, warp & 3, (warp >> 2) - 2);
     } else if (warp >= 4) {
         ok = epilogue<C, GLU>(w, warp & 3, scales[warp & 3]);
     }
@@ -454,7 +453,7 @@ template <class C>
 cudaError_t launch(const MatmulArgs& a, int sms, cudaStream_t st) {
     const int64_t per_pair = a.swiglu ? kRows : 2 * kRows, outs = a.swiglu ? a.N / 2 : a.N;
     CUtensorMap map_w, map_a, map_half;
-    if (!(a.swiglu ? make_pairs_map(&map_w, a.w, a.E, outs, a.K, 16)
+    if (!(a.swiglu ? make_pairs_map(&map_w, a.w, a.E, outs, a.K, kRows / 2)
                    : make_rows_map(&map_w, a.w, (int64_t)a.E * a.N, a.K, kRows)) ||
         !make_rows_map(&map_a, a.a, a.rows, a.K, kBoxTokens) ||
         !make_rows_map(&map_half, a.a, a.rows, a.K, C::half))
