@@ -19,9 +19,16 @@
 // columns each) fill the 512 columns of tensor memory, so a tile's epilogue runs under the
 // next tile's products.
 //
-// Warps: 0 TMA, 1 MMA (of the pair's first CTA), 2 tensor memory, 4-7 epilogue, 8-15 weights
-// to float16 (8-11 the first 64 k of a TMA stage, 12-15 the second), 16-23 tokens likewise: one
-// step of a warp, from its wait to its arrival, takes longer than the MMAs of 64 k.  Every wait is bounded (EP_ERR_TIMEOUT).
+// Warps: 0 TMA, 1 MMA (of the pair's first CTA), 2 tensor memory, 4-7 epilogue, 8-23 four groups
+// that turn the codes of weights and tokens into float16 and take the stages in turn (a group's way
+// from its wait to its arrival takes several times as long as the MMAs of a stage).  Every wait is
+// bounded (EP_ERR_TIMEOUT).
+//
+// Measured: 8192^3 633 us, 1737 TFLOP/s (0.90 of the measured float16 rate); 32 experts of 1152 rows,
+// 4096 x 2048, 373 us, 1660 TFLOP/s, with SwiGLU 376 us; a 64-k step takes some 500 clocks where its
+// MMAs take 384, with shared memory about 0.9 busy.  Thin segments read weights: 8 rows for each of 512
+// experts, 4096 x 1024, 331 us, 6.6 TB/s (0.97 of the copy bandwidth).  One tile of 128 rows takes 16 us
+// at k = 4096.
 #include "expert_ops.cuh"
 #include "tcgen05.cuh"
 #include "tensor_maps.cuh"

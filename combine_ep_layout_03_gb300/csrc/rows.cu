@@ -17,6 +17,11 @@
 // h is rounded to bf16 before the norm: that rounded row is what the residual stream
 // stores, and normalising exactly it makes the result the same whether the addition
 // was fused or not.
+//
+// Measured, against the copy bandwidth: 65536 x 4096 int8 with a residual 269 us, 1.03; without one
+// 146 us, 0.82; 32768 x 7168 MXFP8 without one 148 us, 0.71 (with: 237 us, 1.03); 1237 x 7168 in
+// groups, with one, 14 us, 0.66 (8.1 rows an SM).  With a residual the bytes bound it; without one
+// instructions do (more or fewer resident rows make it slower; issue slots are half busy).
 #include "expert_ops.cuh"
 #include "quant.cuh"
 
