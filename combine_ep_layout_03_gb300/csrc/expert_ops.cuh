@@ -24,21 +24,31 @@ cudaError_t launch_rms_norm_quant(const RowQuantArgs& a, int quant, int sms, cud
 cudaError_t launch_quant_rows(const RowQuantArgs& a, int quant, int sms, cudaStream_t st);
 
 // Launches a kernel that may be set up while the one before it in the stream ends (programmatic
-// dependent launch).  It must call wait_for_previous() before it touches global memory.
+// dependent launch).  It must call wait_for_previous() before it touches global memory.  cluster: CTAs of
+// a cluster, a divisor of the grid (1: none but what the kernel declares).
 template <class... P, class... A>
-cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A&&... args) {
+cudaError_t launch_overlapped_clusters(void (*kernel)(P...), int cluster, dim3 grid, int threads, size_t smem,
+                                       cudaStream_t st, A&&... args) {
     cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <class... P, class... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A&&... args) {
+    return launch_overlapped_clusters(kernel, 1, grid, threads, smem, st, args...);
 }
 
 // Everything that earlier kernels of the stream wrote is visible after this.

@@ -14,12 +14,14 @@
 // Sums run in a fixed order (warps take fixed pieces, their partial sums are added in
 // warp order): results do not vary from run to run.
 //
-// Measured (both kernels): 64 tokens over 512 experts of 4096 x 512, bf16: 858 us, 6.3 TB/s (0.92 of
-// the copy bandwidth); 16 tokens over 128 experts of 4096 x 1024: 309 us, 6.4 TB/s; one token 39 us,
+// Measured (both kernels): 64 tokens over 512 experts of 4096 x 512, bf16: 842 us, 6.4 TB/s (0.94 of
+// the copy bandwidth); 16 tokens over 128 experts of 4096 x 1024: 315 us, 6.5 TB/s; one token 39 us,
 // 5.1 TB/s, of which about 9 us are the two starts.  int8 weights are bound by instruction issue,
-// most of it their conversion: 8 tokens of 256 experts of 7168 x 1024 244 us, 5.2 TB/s;
-// one token of 128 experts of 4096 x 1024 32 us, 3.1 TB/s.  Many tokens on few experts are bound by
+// most of it their conversion: 8 tokens of 256 experts of 7168 x 1024 244 us, 5.1 TB/s;
+// one token of 128 experts of 4096 x 1024 34 us, 3.0 TB/s.  Many tokens on few experts are bound by
 // the token values' way to the registers: 64 tokens, all on 8 experts, 260 us at 0.8 TB/s.
+#include <algorithm>
+
 #include "expert_ops.cuh"
 #include "skinny.cuh"
 #include "tensor_maps.cuh"
@@ -123,23 +125,54 @@ __device__ __forceinline__ uint8_t* aligned_smem(uint8_t* p) {
     return p + ((1024 - (smem_addr(p) & 1023)) & 1023);
 }
 
-// A warp's way through the pieces of few_inner_kernel: items item, item + step, ... and in each
-// the pieces warp, warp + 8, ...
+// Work of few_inner_kernel.  A tile is eight inner channels of one expert: their gate rows are rows 0-7
+// of the 16 rows and their up rows 8-15, so a lane ends with both of a channel.  1 << share_log warps
+// share a tile's k and add their parts in shared memory; an item is the `sets` tiles side by side that a
+// CTA works on at a time.  Where the items past the last full round of CTAs have no more tiles than there
+// are CTAs they are dealt out tile by tile, each to all eight warps of a CTA, so that the last round is a
+// short one (6 tokens over 32 experts of 6416 x 1232, int8: 103 us for 110; no gain from tiles of a few
+// pieces, or from two short rounds for a long one: 12.7 us for 14.3, 94 for 98).
+struct InnerPlan {
+    int share_log, sets_log, tiles, groups, full, units;
+    __device__ __forceinline__ InnerPlan(int share_log, int tiles, int experts, int step, int pieces)
+        : share_log(share_log), sets_log(3 - share_log), tiles(tiles) {
+        groups = (tiles + (1 << sets_log) - 1) >> sets_log;
+        const int items = experts * groups;
+        full = items / step * step;
+        if (pieces < 2 * kWarps || (items - full) << sets_log > step) full = items;
+        units = full + ((items - full) << sets_log);
+    }
+    struct Unit { int pos, tile0, share_log; };   // place of the expert in the routing, first tile, warps of a tile
+    __device__ __forceinline__ Unit unit(int u) const {
+        const int tail = u - full, item = tail < 0 ? u : full + (tail >> sets_log);
+        const int pos = item / groups, tile0 = (item - pos * groups) << sets_log;
+        if (tail < 0) return {pos, tile0, share_log};
+        return {pos, tile0 + (tail & ((1 << sets_log) - 1)), 3};
+    }
+};
+static_assert(kWarps == 8, "share_log is at most 3");
+
+// A warp's way through its pieces: units unit, unit + step, ... and in each the pieces rank, rank + share, ...
+// of its tile, if it has one there.
 struct InnerCursor {
-    int item, tile, piece;
-    int expert;
-    __device__ __forceinline__ void place(const Routing& r, int items, int tiles) {
-        if (item >= items) return;
-        tile = item % tiles;
-        expert = r.expert[item / tiles];
+    int unit, tile, piece, expert, rank, share;
+    __device__ __forceinline__ void place(const Routing& r, const InnerPlan& p, int step, int warp, int pieces) {
+        for (; unit < p.units; unit += step) {
+            const InnerPlan::Unit n = p.unit(unit);
+            share = 1 << n.share_log;
+            rank = warp & (share - 1);
+            tile = n.tile0 + (warp >> n.share_log);
+            if (tile < p.tiles && rank < pieces) {
+                expert = r.expert[n.pos];
+                piece = rank;
+                return;
+            }
+        }
     }
 };
 
-// An item is eight inner channels of one expert: their gate rows are rows 0-7 of the
-// 16-row tile and their up rows 8-15, so a lane ends with both of a channel.  The warps
-// share the item's k and add their parts in shared memory.
 template <bool W8, int MAXNT>
-__global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_inner_kernel(const FewArgs a, const __grid_constant__ CUtensorMap map_w) {
+__global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_inner_kernel(const FewArgs a, int share_log, const __grid_constant__ CUtensorMap map_w) {
     extern __shared__ uint8_t dynamic[];
     __shared__ Routing r;
     using S = Sizes<W8, MAXNT>;
@@ -152,45 +185,47 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_inner_ke
     wait_for_previous();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     build_routing(r, a);
-    const int tiles = a.I / 8, items = r.count * tiles, step = gridDim.x;
+    const int step = gridDim.x;
     const int k_bytes = a.H * (W8 ? 1 : 2), pieces = (k_bytes + 127) / 128;
+    const InnerPlan plan(share_log, a.I / 8, r.count, step, pieces);
     typename S::Ring ring(slots, bars, warp, lane);
     InnerCursor ahead;
-    ahead.item = pieces > warp ? (int)blockIdx.x : items;
-    ahead.piece = warp;
-    ahead.place(r, items, tiles);
+    ahead.unit = blockIdx.x;
+    ahead.place(r, plan, step, warp, pieces);
     auto fetch = [&]() {
-        if (ahead.item >= items) return;
+        if (ahead.unit >= plan.units) return;
         ring.put(lane, 2048, [&](uint8_t* slot, uint64_t* bar) {
             tma_load_4d(slot, &map_w, ahead.piece * 128, ahead.tile * 8, 0, ahead.expert, bar);
         });
-        ahead.piece += kWarps;
+        ahead.piece += ahead.share;
         if (ahead.piece >= pieces) {
-            ahead.piece = warp;
-            ahead.item += step;
-            ahead.place(r, items, tiles);
+            ahead.unit += step;
+            ahead.place(r, plan, step, warp, pieces);
         }
     };
     for (int d = 0; d < S::depth; ++d) fetch();
 
     int buffer = 0;
-    for (int item = blockIdx.x; item < items; item += step, buffer ^= 1) {
-        const int pos = item / tiles, tile = item % tiles;
-        const int e = r.expert[pos], row0 = r.base[pos], m = r.base[pos + 1] - row0;
-        const int nt = (m + 7) / 8;
+    for (int u = blockIdx.x; u < plan.units; u += step, buffer ^= 1) {
+        const InnerPlan::Unit unit = plan.unit(u);
+        const int tile0 = unit.tile0, log = unit.share_log, share = 1 << log, rank = warp & (share - 1);
+        const int e = r.expert[unit.pos], row0 = r.base[unit.pos], m = r.base[unit.pos + 1] - row0;
+        const int nt = (m + 7) / 8, my_pieces = tile0 + (warp >> log) < plan.tiles ? pieces : 0;
+        const int width_log = 6 - log, width = 1 << width_log;   // channels of the unit
         float* sums = red + (kBuffers == 2 ? buffer * kSums : 0);
         // what the sums below will be multiplied by arrives meanwhile
         struct Factors { float gate, up, weight; };
         auto factors = [&](int i) {
-            Factors f = {1.0f, 1.0f, routing_weight(a, r.token[row0 + (i >> 3)], e)};
+            Factors f = {1.0f, 1.0f, routing_weight(a, r.token[row0 + (i >> width_log)], e)};
             if constexpr (W8) {
-                const float* sc = a.w13_scales + (int64_t)e * 2 * a.I + tile * 8 + (i & 7);
+                const float* sc = a.w13_scales + (int64_t)e * 2 * a.I + tile0 * 8 + (i & (width - 1));
                 f.gate = sc[0];
                 f.up = sc[a.I];
             }
             return f;
         };
-        const Factors mine = tid < m * 8 ? factors(tid) : Factors{};
+        auto in_item = [&](int i) { return i < m << width_log && tile0 * 8 + (i & (width - 1)) < a.I; };
+        const Factors mine = in_item(tid) ? factors(tid) : Factors{};
         auto run = [&](auto count) {
             constexpr int NT = decltype(count)::value;
             const uint8_t* tok[NT];
@@ -203,13 +238,13 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_inner_ke
             }
             TokenPart<W8> next;   // with one tile: the tokens of the next piece
             constexpr bool kAhead = NT == 1 && S::prefetch;
-            if (kAhead && warp < pieces) load_tokens<W8, false>(next, tok[0], warp, q * 16, k_bytes);
-            for (int c = warp; c < pieces; c += kWarps) {
+            if (kAhead && rank < my_pieces) load_tokens<W8, false>(next, tok[0], rank, q * 16, k_bytes);
+            for (int c = rank; c < my_pieces; c += share) {
                 uint4 lo[2], hi[2];
                 TokenPart<W8> now;
                 if constexpr (kAhead) {
                     now = next;
-                    if (c + kWarps < pieces) load_tokens<W8, false>(next, tok[0], c + kWarps, q * 16, k_bytes);
+                    if (c + share < pieces) load_tokens<W8, false>(next, tok[0], c + share, q * 16, k_bytes);
                 } else if constexpr (NT == 1) {
                     load_tokens<W8, false>(now, tok[0], c, q * 16, k_bytes);
                 }
@@ -238,13 +273,17 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_inner_ke
         };
         const int cols = with_tiles<MAXNT>(nt, run);
         __syncthreads();
-        for (int i = tid; i < m * 8; i += kThreads) {
-            const int col = i >> 3, c = i & 7, channel = tile * 8 + c;
+        for (int i = tid; i < m << width_log; i += kThreads) {
+            if (!in_item(i)) continue;
+            const int col = i >> width_log, at = i & (width - 1), c = at & 7, channel = tile0 * 8 + at;
+            const float* part = sums + (((at >> 3) << log) * cols + col) * 16 + c;
             float gate = 0.0f, up = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                gate += sums[(w * cols + col) * 16 + c];
-                up += sums[(w * cols + col) * 16 + c + 8];
+                if (w < share) {
+                    gate += part[w * cols * 16];
+                    up += part[w * cols * 16 + 8];
+                }
             }
             const Factors f = i == tid ? mine : factors(i);
             gate *= f.gate;
@@ -259,8 +298,9 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_inner_ke
     if (!ring.drain() && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
 }
 
-// A CTA owns `rows` <= 16 columns of the output at a time (tiles tile, tile + grid, ...) for every
-// token.  The pieces of all experts form one line, of which each warp takes an equal stretch.
+// The CTAs of a cluster (or one) own `rows` <= 16 columns of the output at a time (tiles tile, tile +
+// clusters, ...) for every token.  The pieces of all experts form one line, of which each warp takes an
+// equal stretch; a CTA adds its warps' sums, then the CTAs' sums are added in rank order.
 struct OutCursor {
     int tile, at, piece, expert;   // at: place in the line of pieces
     __device__ __forceinline__ void place(const Routing& r, int pieces) {
@@ -270,7 +310,7 @@ struct OutCursor {
 };
 
 template <bool W8, int MAXNT>
-__global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_out_kernel(const FewArgs a, int rows, const __grid_constant__ CUtensorMap map_w) {
+__global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_out_kernel(const FewArgs a, int rows, int split, const __grid_constant__ CUtensorMap map_w) {
     extern __shared__ uint8_t dynamic[];
     __shared__ Routing r;
     using S = Sizes<W8, MAXNT>;
@@ -283,11 +323,13 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_out_kern
     build_routing(r, a);
     const int k_bytes = a.I * (W8 ? 1 : 2), pieces = (k_bytes + 127) / 128;
     const int total = r.count * pieces, tiles = (a.H + rows - 1) / rows;
-    const int begin = (int)((int64_t)total * warp / kWarps), end = (int)((int64_t)total * (warp + 1) / kWarps);
+    const int first_tile = split > 1 ? (int)blockIdx.x / split : (int)blockIdx.x, step = split > 1 ? (int)gridDim.x / split : (int)gridDim.x;
+    const int rank = (int)blockIdx.x - first_tile * split, part = rank * kWarps + warp, parts = split * kWarps;
+    const int begin = (int)((uint32_t)(total * part) / (uint32_t)parts), end = (int)((uint32_t)(total * (part + 1)) / (uint32_t)parts);
     const int64_t plane = (int64_t)a.I * 2;
     typename S::Ring ring(slots, bars, warp, lane);
     OutCursor ahead;
-    ahead.tile = begin < end ? (int)blockIdx.x : tiles;
+    ahead.tile = begin < end ? first_tile : tiles;
     ahead.at = begin;
     if (ahead.tile < tiles) ahead.place(r, pieces);
     auto fetch = [&]() {
@@ -298,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_out_kern
         ++ahead.piece;
         if (++ahead.at == end) {
             ahead.at = begin;
-            ahead.tile += gridDim.x;
+            ahead.tile += step;
             if (ahead.tile < tiles) ahead.place(r, pieces);
         } else if (ahead.piece == pieces) {
             ahead.place(r, pieces);
@@ -309,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_out_kern
     wait_for_previous();
 
     float* mine = sums + warp * a.T * 16;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    for (int tile = first_tile; tile < tiles; tile += step) {
         const int h0 = tile * rows;
         for (int at = begin; at < end;) {
             const int pos = at / pieces, first = at % pieces, last = min(pieces, first + end - at);
@@ -390,61 +432,107 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_out_kern
             at += last - first;
         }
         __syncthreads();
-        for (int i = tid; i < a.T * 16; i += kThreads) {
+        if (split > 1) {   // the CTA's sum to its first warp's place, for its peers
+            for (int i = tid; i < a.T * 16; i += kThreads) {
+                float s = sums[i];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) {
+                    s += sums[w * a.T * 16 + i];
+                    sums[w * a.T * 16 + i] = 0.0f;
+                }
+                sums[i] = s;
+            }
+            __syncwarp();
+            cluster_sync();
+        }
+        for (int i = rank * kThreads + tid; i < a.T * 16; i += split * kThreads) {
             const int t = i >> 4, h = h0 + (i & 15);
             float s = 0.0f;
+            if (split > 1) {
+                for (int c = 0; c < split; ++c) s += load_of_peer(&sums[i], c);
+            } else {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                s += sums[w * a.T * 16 + i];
-                sums[w * a.T * 16 + i] = 0.0f;
+                for (int w = 0; w < kWarps; ++w) {
+                    s += sums[w * a.T * 16 + i];
+                    sums[w * a.T * 16 + i] = 0.0f;
+                }
             }
             if ((i & 15) >= rows || h >= a.H) continue;
             for (int k = 0; k < a.S; ++k) s += bf16_bits_to_float(a.shared[((int64_t)k * a.T + t) * a.H + h]);
             a.out[(int64_t)t * a.H + h] = (uint16_t)pack_bf16x2_rn(s, 0.0f);
+        }
+        if (split > 1) {
+            __syncwarp();
+            cluster_sync();   // the peers have read
+            for (int i = tid; i < a.T * 16; i += kThreads) sums[i] = 0.0f;
         }
         __syncthreads();
     }
     if (!ring.drain() && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
 }
 
-// Output columns of a CTA's tile, 12 to 16: those that leave the last round of CTAs fullest.
-int rows_of_tile(int H, int ctas) {
-    int best = 16;
+// Warps that share a tile of few_inner_kernel.  All eight keep the most CTAs busy where there are few
+// tiles (one token on 8 of 128 experts, bf16: 39.2 us with 8, 41.8 with 4); with more, fewer barriers and
+// longer stretches of k win (15 tokens over 256 experts of 4208 x 336, int8: 95 us with 4, 111 with 8;
+// 64 tokens, bf16: 861 with 4, 887 with 8), and short rows of int8 weights are better off with two
+// (32 tokens, 4096 x 1024: 305 us with 2, 311 with 4, 342 with 8; but 8 of 7168 x 1024 320, 244, 253).
+template <bool W8>
+int tile_share_log(int64_t tiles, int ctas, int pieces) {
+    int share_log = 2;
+    if (tiles <= 4 * (int64_t)ctas) share_log = 3;
+    else if (W8 && pieces <= 32 && tiles >= 32 * (int64_t)ctas) share_log = 1;
+    while (share_log > 0 && 1 << share_log > pieces) --share_log;
+    return share_log;
+}
+
+// Tiles of few_out_kernel: their columns, 12 to 16, those that leave the last round of clusters fullest;
+// and the CTAs of a cluster, up to three where there would be fewer tiles than SMs (8 tokens, 1584 columns,
+// int8: 160 us with 1, 128 with 2, 127 with 3, 135 with 4; 1024 columns, bf16: 184, 141, 129, 148; but a line
+// of 30 pieces 9.5, 11.9, 11.1).  From one tile an SM on, splitting costs more than it gives (2992 columns,
+// 56.2 us for 57.2).
+struct OutShape { int rows, split; };
+
+OutShape out_shape(int H, int sms, int ctas, int64_t most_pieces) {
+    OutShape best = {16, 1};
+    const int least_tiles = (H + 15) / 16;
+    if (least_tiles < sms && most_pieces >= 10 * kWarps) best.split = std::min(3, ctas / least_tiles);
+    const int clusters = ctas / best.split;
     int64_t least = INT64_MAX;
     for (int rows = 16; rows >= 12; --rows) {
         const int tiles = (H + rows - 1) / rows;
-        const int64_t time = (int64_t)((tiles + ctas - 1) / ctas) * (rows + 3);
-        if (time < least) { least = time; best = rows; }
+        const int64_t time = (int64_t)((tiles + clusters - 1) / clusters) * (rows + 3);
+        if (time < least) { least = time; best.rows = rows; }
     }
     return best;
 }
 
 template <bool W8, int MAXNT>
 cudaError_t launch(const FewArgs& a, int sms, cudaStream_t st) {
-    const int64_t entries = (int64_t)a.T * a.K;
-    const int64_t items = (entries < a.E ? entries : a.E) * (a.I / 8);
+    const int64_t entries = (int64_t)a.T * a.K, experts = entries < a.E ? entries : a.E, width = W8 ? 1 : 2;
+    const int64_t inner_tiles = experts * (a.I / 8);
     using S = Sizes<W8, MAXNT>;
-    // As many CTAs as fit, or fewer if that fills the rounds of items better (one token: 8 x 128 items are
+    // As many CTAs as fit, or fewer if that fills the rounds of tiles better (one token: 8 x 128 tiles are
     // 3.4 rounds of two CTAs an SM, but 2.2 of three).
     int per_sm = S::ctas;
-    if (per_sm == 3 && (items + 3 * sms - 1) / (3 * sms) * 3 > (items + 2 * sms - 1) / (2 * sms) * 2) per_sm = 2;
+    if (per_sm == 3 && (inner_tiles + 3 * sms - 1) / (3 * sms) * 3 > (inner_tiles + 2 * sms - 1) / (2 * sms) * 2) per_sm = 2;
     const int ctas = sms * per_sm;
-    const int rows = rows_of_tile(a.H, ctas), tiles = (a.H + rows - 1) / rows;
-    const int64_t width = W8 ? 1 : 2;
+    const int share_log = tile_share_log<W8>(inner_tiles, ctas, (int)((a.H * width + 127) / 128));
+    const OutShape o = out_shape(a.H, sms, ctas, experts * ((a.I * width + 127) / 128));
+    const int tiles = (a.H + o.rows - 1) / o.rows, clusters = ctas / o.split;
     CUtensorMap map13, map2;
-    if (!make_pairs_map(&map13, a.w13, a.E, a.I, a.H * width, 8) || !make_experts_map(&map2, a.w2, a.E, a.H, a.I * width, rows))
+    if (!make_pairs_map(&map13, a.w13, a.E, a.I, a.H * width, 8) || !make_experts_map(&map2, a.w2, a.E, a.H, a.I * width, o.rows))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> inner_done{0}, out_done{0};
     cudaError_t e = allow_smem(few_inner_kernel<W8, MAXNT>, S::inner_smem, inner_done);
     if (e == cudaSuccess) e = allow_smem(few_out_kernel<W8, MAXNT>, S::out_smem, out_done);
     if (e != cudaSuccess) return e;
-    e = launch_overlapped(few_inner_kernel<W8, MAXNT>, dim3((unsigned)(items < ctas ? items : ctas)), kThreads, S::inner_smem, st,
-                          a, map13);
+    e = launch_overlapped(few_inner_kernel<W8, MAXNT>, dim3((unsigned)(inner_tiles < ctas ? inner_tiles : ctas)), kThreads, S::inner_smem, st,
+                          a, share_log, map13);
     if (e != cudaSuccess) return e;
     // The second kernel reads the routing and fetches its first weights while the first drains.  Both have waited
     // for what came before, so neither reads them before they are there.
-    return launch_overlapped(few_out_kernel<W8, MAXNT>, dim3((unsigned)(tiles < ctas ? tiles : ctas)), kThreads, S::out_smem, st,
-                             a, rows, map2);
+    return launch_overlapped_clusters(few_out_kernel<W8, MAXNT>, o.split, dim3((unsigned)((tiles < clusters ? tiles : clusters) * o.split)), kThreads,
+                             S::out_smem, st, a, o.rows, o.split, map2);
 }
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }

@@ -25,6 +25,14 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The float at this place of the shared memory of CTA `rank`.
+__device__ __forceinline__ float load_of_peer(const float* local, uint32_t rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                 : "=f"(v) : "r"(cluster_addr((uint32_t)__cvta_generic_to_shared(local), rank)) : "memory");
+    return v;
+}
+
 // Arrive on a barrier of either CTA.  At the default CTA scope: a release to the whole cluster
 // waits for everything the thread has in flight (it doubled the time of a product), and is for
 // data that a thread of the other CTA reads.  Here each SM's tensor core reads what its own

@@ -101,6 +101,14 @@ def test_sizes(int8, T, H, E, K, I):
     check(make(T, H, E, K, I, int8, seed=T + H))
 
 
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("T,H,E,K,I", [(8, 272, 64, 8, 1232), (20, 272, 64, 8, 1232), (8, 1600, 64, 8, 208),
+                                       (16, 2192, 32, 8, 176), (50, 144, 128, 4, 656), (5, 2480, 16, 4, 1104)])
+def test_work_split_over_warps_and_ctas(int8, T, H, E, K, I):
+    """Tiles shared by two, four or eight warps, the last group short; output tiles of two and three CTAs."""
+    check(make(T, H, E, K, I, int8, seed=T + I, drop=0.1))
+
+
 @pytest.mark.parametrize("T,H,I", [(3, 8, 8), (7, 24, 40), (33, 1000, 104)])
 def test_odd_bf16_sizes(T, H, I):
     check(make(T, H, 6, 3, I, False, S=1, seed=I))
