@@ -24,10 +24,10 @@
 // from its wait to its arrival takes several times as long as the MMAs of a stage).  Every wait is
 // bounded (EP_ERR_TIMEOUT).
 //
-// Measured: 8192^3 633 us, 1737 TFLOP/s (0.90 of the measured float16 rate); 32 experts of 1152 rows,
-// 4096 x 2048, 373 us, 1660 TFLOP/s, with SwiGLU 376 us; a 64-k step takes some 500 clocks where its
+// Measured: 8192^3 622 us, 1767 TFLOP/s (0.91 of the measured float16 rate); 32 experts of 1152 rows,
+// 4096 x 2048, 366 us, 1690 TFLOP/s, with SwiGLU 371 us; a 64-k step takes some 500 clocks where its
 // MMAs take 384, with shared memory about 0.9 busy.  Thin segments read weights: 8 rows for each of 512
-// experts, 4096 x 1024, 331 us, 6.6 TB/s (0.97 of the copy bandwidth).  One tile of 128 rows takes 16 us
+// experts, 4096 x 1024, 319 us, 6.8 TB/s (1.00 of the copy bandwidth).  One tile of 128 rows takes 15 us
 // at k = 4096.
 #include "expert_ops.cuh"
 #include "tcgen05.cuh"
@@ -85,20 +85,31 @@ struct Shared {
 struct Tile { int64_t row0; int expert, m, n, channel; };   // n: MMA columns, channel: tile of output channels
 
 // Tiles of one expert are neighbours, its token tiles fastest: concurrent pairs share weights and tokens in L2.
-template <class C>
-__device__ __forceinline__ Tile tile_of(const Segments& s, const MatmulArgs& a, int ctiles, int64_t item) {
-    const int e = expert_of_tile(s, a.E, (int)(item / ctiles));
-    const int tiles = s.tile[e + 1] - s.tile[e];
-    const int local = (int)(item - (int64_t)s.tile[e] * ctiles);
+// The roles look tiles up between one tile's work and the next, so it has to be quick: a whole warp goes on from
+// its last expert, 32 experts at a time, and all counts are 32 bits wide (32 experts of 1152 rows, 1024 x 4096:
+// 217 us, with a binary search and 64-bit quotients 233; 512 experts of 8 rows, 4096 x 1024: 319, 331).
+// A single thread searches anew.
+template <class C, bool WARP>
+__device__ __forceinline__ Tile tile_of(const Segments& s, const MatmulArgs& a, int ctiles, int item, int& e) {
+    const int at = (int)((uint32_t)item / (uint32_t)ctiles);
+    if (WARP) {
+        for (int n = 32; n == 32; e += n)
+            n = __popc(__ballot_sync(0xffffffffu, s.tile[min(e + 1 + (int)(threadIdx.x & 31), a.E)] <= at));
+    } else {
+        e = expert_of_tile(s, a.E, at);
+    }
+    const uint32_t tiles = s.tile[e + 1] - s.tile[e];
+    const uint32_t local = item - s.tile[e] * ctiles;
     // the segment's groups of 32 rows dealt out evenly: no tile is much shorter, and none pays for a row more
-    const int groups = (s.rows[e] + 31) / 32, j = local % tiles, each = groups / tiles, more = groups % tiles;
+    const int groups = (s.rows[e] + 31) / 32, j = (int)(local % tiles), each = (int)((uint32_t)groups / tiles);
+    const int more = groups - each * (int)tiles;
     const int first = 32 * (j * each + min(j, more));
     Tile t;
     t.expert = e;
     t.row0 = (int64_t)s.base[e] + first;
     t.m = min(32 * (each + (j < more)), s.rows[e] - first);
     t.n = (t.m + 31) / 32 * 32;
-    t.channel = local / tiles;
+    t.channel = (int)(local / tiles);
     return t;
 }
 
@@ -157,7 +168,7 @@ struct Work {
     uint8_t* cvt;    // float16 token rows of 64 k
     uint32_t tmem, cta;
     int outs, per_pair, ctiles, raws;
-    int64_t first, items, step;
+    int first, items, step;
 };
 
 template <class C, bool GLU>
@@ -165,9 +176,10 @@ __device__ __forceinline__ bool load_tiles(const Work<C>& w, const CUtensorMap* 
                                            const CUtensorMap* map_half) {
     Ring<C::raw_stages> r;
     int used = 0;   // stages armed so far, at most all
+    int expert = 0;
     bool ok = true;
-    for (int64_t item = w.first; ok && item < w.items; item += w.step) {
-        const Tile t = tile_of<C>(w.sh.seg, w.a, w.ctiles, item);
+    for (int item = w.first; ok && item < w.items; item += w.step) {
+        const Tile t = tile_of<C, false>(w.sh.seg, w.a, w.ctiles, item, expert);
         // token rows in one box where the tile is full, else in boxes of 32
         const int half = t.n / 2, boxes = (half + kBoxTokens - 1) / kBoxTokens;
         const int ch = t.channel * w.per_pair + (int)w.cta * (GLU ? kRows / 2 : kRows);
@@ -208,8 +220,9 @@ __device__ __forceinline__ bool issue_mma(const Work<C>& w) {
     Ring<2> acc;
     const uint32_t cvt0 = smem_addr(w.cvt);
     bool ready = false, ok = true;
-    for (int64_t item = w.first; ok && item < w.items; item += w.step, acc.next()) {
-        const Tile t = tile_of<C>(w.sh.seg, w.a, w.ctiles, item);
+    int expert = 0;
+    for (int item = w.first; ok && item < w.items; item += w.step, acc.next()) {
+        const Tile t = tile_of<C, true>(w.sh.seg, w.a, w.ctiles, item, expert);
         const uint32_t idesc = mma_desc_f16(2 * kRows, t.n);
         if (!warp_wait(&w.sh.acc_empty[acc.stage], acc.parity ^ 1)) { ok = false; break; }
         tmem_fence_after();
@@ -263,9 +276,10 @@ __device__ __forceinline__ bool convert(const Work<C>& w, int warp, int set) {
     const uint32_t col = w.tmem + ((uint32_t)(warp * 32) << 16) + C::col_a;
     Ring<C::raw_stages> r;
     uint32_t use = h0;
+    int expert = 0;
     bool ok = true;
-    for (int64_t item = w.first; ok && item < w.items; item += w.step) {
-        const int rows = tile_of<C>(w.sh.seg, w.a, w.ctiles, item).n / 2 - warp * 8;
+    for (int item = w.first; ok && item < w.items; item += w.step) {
+        const int rows = tile_of<C, true>(w.sh.seg, w.a, w.ctiles, item, expert).n / 2 - warp * 8;
         for (int k = 0; ok && k < w.raws; ++k, use += 2 / C::halves, r.next()) {
             if (use % kSets != (uint32_t)set) continue;
             const uint32_t stage = use % C::cvt_stages, parity = (use / C::cvt_stages) & 1;
@@ -331,8 +345,9 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp, float* scal
     // two channels a store where rows keep them on four bytes
     const bool wide = (outs & 1) == 0 && ((uintptr_t)w.a.out & 3) == 0;
     Ring<2> acc;
-    for (int64_t item = w.first; item < w.items; item += w.step, acc.next()) {
-        const Tile t = tile_of<C>(w.sh.seg, w.a, w.ctiles, item);
+    int expert = 0;
+    for (int item = w.first; item < w.items; item += w.step, acc.next()) {
+        const Tile t = tile_of<C, true>(w.sh.seg, w.a, w.ctiles, item, expert);
         const int ch = t.channel * w.per_pair + (int)w.cta * (GLU ? kRows / 2 : kRows) + warp * (GLU ? 16 : 32) +
                        (GLU ? lane & 15 : lane);
         const bool in = ch < outs;
@@ -436,8 +451,10 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
     const int outs = GLU ? a.N / 2 : a.N;
     const int per_pair = GLU ? kRows : 2 * kRows;   // output channels of a tile
     const int ctiles = (outs + per_pair - 1) / per_pair;
+    // (overlapping segments can name more tiles than there is output; items + step stays a number)
+    const int64_t all = fits ? (int64_t)sh.seg.tile[a.E] * ctiles : 0, limit = INT32_MAX - (int64_t)gridDim.x;
     const Work<C> w = {a, sh, raw, raw + C::raw_stages * C::raw_bytes, sh.tmem, cta, outs, per_pair, ctiles,
-                    (a.K + kRawK - 1) / kRawK, blockIdx.x >> 1, fits ? (int64_t)sh.seg.tile[a.E] * ctiles : 0, gridDim.x >> 1};
+                    (a.K + kRawK - 1) / kRawK, (int)(blockIdx.x >> 1), (int)(all < limit ? all : limit), (int)(gridDim.x >> 1)};
     bool ok = true;
     if (warp == 0) {
         if (lane == 0) ok = load_tiles<C, GLU>(w, &map_w, &map_a, &map_half);
@@ -466,6 +483,7 @@ cudaError_t launch(const MatmulArgs& a, int sms, cudaStream_t st) {
         !make_rows_map(&map_half, a.a, a.rows, a.K, C::half))
         return cudaErrorInvalidValue;
     const int64_t most = ((a.rows + C::tile - 1) / C::tile + (a.E > 1 ? a.E : 0)) * ((outs + per_pair - 1) / per_pair);
+    if (most > INT32_MAX - sms) return cudaErrorInvalidValue;   // more output than any memory holds
     const int64_t pairs = most < sms / 2 ? most : sms / 2;
     auto kernel = a.swiglu ? matmul_tiles_kernel<C, true> : matmul_tiles_kernel<C, false>;
     static std::atomic<uint64_t> done[2];
