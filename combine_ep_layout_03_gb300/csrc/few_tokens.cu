@@ -14,12 +14,13 @@
 // Sums run in a fixed order (warps take fixed pieces, their partial sums are added in
 // warp order): results do not vary from run to run.
 //
-// Measured (both kernels): 64 tokens over 512 experts of 4096 x 512, bf16: 842 us, 6.4 TB/s (0.94 of
-// the copy bandwidth); 16 tokens over 128 experts of 4096 x 1024: 315 us, 6.5 TB/s; one token 39 us,
+// Measured (both kernels): 64 tokens over 512 experts of 4096 x 512, bf16: 835 us, 6.5 TB/s (0.95 of
+// the copy bandwidth); 16 tokens over 128 experts of 4096 x 1024: 314 us, 6.5 TB/s; one token 39 us,
 // 5.1 TB/s, of which about 9 us are the two starts.  int8 weights are bound by instruction issue,
-// most of it their conversion: 8 tokens of 256 experts of 7168 x 1024 244 us, 5.1 TB/s;
-// one token of 128 experts of 4096 x 1024 34 us, 3.0 TB/s.  Many tokens on few experts are bound by
-// the token values' way to the registers: 64 tokens, all on 8 experts, 260 us at 0.8 TB/s.
+// most of it their conversion: 8 tokens of 256 experts of 7168 x 1024 233 us, 5.3 TB/s;
+// one token of 128 experts of 4096 x 1024 33 us, 3.1 TB/s.  Many tokens on few experts are bound by
+// the token values' way from L2, each time for 16 weight rows: 64 tokens over 8 experts of 4096 x 1024,
+// bf16, 64 us by two and 135 us by eight (the weights' bytes are 30).
 #include <algorithm>
 
 #include "expert_ops.cuh"
@@ -102,14 +103,17 @@ __device__ __forceinline__ float routing_weight(const FewArgs& a, int token, int
 
 // Sizes of both kernels by weight type and largest number of token tiles.
 //   ctas     CTAs of an SM; what the routing and the sums leave of its shared memory goes to the rings (depth).
-//   prefetch whether the token values of the next piece are loaded under this one's products.  It helps bf16
-//            weights (one token tile, 64 tokens over 512 experts: 914 us with, 1015 us without); int8 weights
+//   early    token parts that are asked for before the weights of their piece are waited for.  64 tokens, bf16,
+//            over 8 experts by two: 64 us with 3, 68 with 4 (spills), 69 with 2, 96 with none.
+//   prefetch whether with one token tile those of the next piece are loaded under this one's products.  It
+//            helps bf16 weights (64 tokens over 512 experts: 914 us with, 1015 us without); int8 weights
 //            need the registers for their conversion and gain more from other warps (8 tokens of 256 experts:
 //            276 us with it and two CTAs, 255 us without, 238 us without and with three CTAs).
 template <bool W8, int MAXNT>
 struct Sizes {
     static constexpr int ctas = W8 && MAXNT == 1 ? 3 : 2;
     static constexpr int depth = ctas == 3 ? 3 : W8 ? (MAXNT == 2 ? 4 : 3) : MAXNT == 1 ? 6 : MAXNT == 2 ? 5 : 4;
+    static constexpr int early = 3;
     static constexpr bool prefetch = !W8;
     using Ring = WeightRing<depth>;
     static constexpr int ring_bytes = kWarps * Ring::kWarpBytes;
@@ -228,35 +232,32 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_inner_ke
         const Factors mine = in_item(tid) ? factors(tid) : Factors{};
         auto run = [&](auto count) {
             constexpr int NT = decltype(count)::value;
-            const uint8_t* tok[NT];
+            uint32_t tok[NT];   // offsets of the tokens' rows: half the registers of addresses
             float acc[NT][4];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const int col = min(j * 8 + g, m - 1);   // columns past the last token repeat it and are not stored
-                tok[j] = reinterpret_cast<const uint8_t*>(a.x) + (int64_t)r.token[row0 + col] * a.H * 2;
+                tok[j] = (uint32_t)(r.token[row0 + col] * a.H * 2);
                 acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
             }
-            TokenPart<W8> next;   // with one tile: the tokens of the next piece
+            auto load = [&](TokenPart<W8, false>& t, int i, int c) {
+                load_tokens<W8, false>(t, reinterpret_cast<const uint8_t*>(a.x) + tok[i % NT], c, i / NT,
+                                       q * 16, k_bytes);
+            };
             constexpr bool kAhead = NT == 1 && S::prefetch;
-            if (kAhead && rank < my_pieces) load_tokens<W8, false>(next, tok[0], rank, q * 16, k_bytes);
+            TokenQueue<W8, false, TokenPart<W8, false>::kOfPiece * NT, S::early> queue, next;   // next: with one tile, the tokens of the next piece
+            if (kAhead && rank < my_pieces) next.start([&](auto& t, int i) { load(t, i, rank); });
             for (int c = rank; c < my_pieces; c += share) {
                 uint4 lo[2], hi[2];
-                TokenPart<W8> now;
                 if constexpr (kAhead) {
-                    now = next;
-                    if (c + share < pieces) load_tokens<W8, false>(next, tok[0], c + share, q * 16, k_bytes);
-                } else if constexpr (NT == 1) {
-                    load_tokens<W8, false>(now, tok[0], c, q * 16, k_bytes);
+                    queue = next;
+                    if (c + share < pieces) next.start([&](auto& t, int i) { load(t, i, c + share); });
+                } else {
+                    queue.start([&](auto& t, int i) { load(t, i, c); });
                 }
                 ring.take(lo, hi);
-                mma_piece<W8, NT, 1>(acc, lo, hi, [&](int j, int) {
-                    if constexpr (NT == 1) {
-                        return now;
-                    } else {
-                        TokenPart<W8> t;
-                        load_tokens<W8, false>(t, tok[j], c, q * 16, k_bytes);
-                        return t;
-                    }
+                mma_piece<W8, false, NT, 1>(acc, lo, hi, [&](int i) {
+                    return queue.take(i, [&](auto& t, int n) { load(t, n, c); });
                 });
                 __syncwarp();
                 fetch();
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_out_kern
     const int first_tile = split > 1 ? (int)blockIdx.x / split : (int)blockIdx.x, step = split > 1 ? (int)gridDim.x / split : (int)gridDim.x;
     const int rank = (int)blockIdx.x - first_tile * split, part = rank * kWarps + warp, parts = split * kWarps;
     const int begin = (int)((uint32_t)(total * part) / (uint32_t)parts), end = (int)((uint32_t)(total * (part + 1)) / (uint32_t)parts);
-    const int64_t plane = (int64_t)a.I * 2;
+    const uint32_t plane = (uint32_t)a.I * 2;
     typename S::Ring ring(slots, bars, warp, lane);
     OutCursor ahead;
     ahead.tile = begin < end ? first_tile : tiles;
@@ -360,45 +361,34 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_out_kern
             auto run = [&](auto count) {
                 constexpr bool kFold = decltype(count)::value == 0;
                 constexpr int NT = kFold ? 1 : decltype(count)::value, PLANES = kFold ? 1 : 2;
-                const uint8_t* tok[NT];
+                uint32_t tok[NT];   // offsets, at most 64 tokens x 16 entries x 65536 x 4 bytes
                 float acc[NT][4];
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
                     const int col = kFold ? g & 3 : j * 8 + g;
-                    tok[j] = reinterpret_cast<const uint8_t*>(a.inner) + (int64_t)(row0 + min(col, m - 1)) * a.I * 4 +
-                             (kFold && g >= 4 ? plane : 0);
+                    tok[j] = (uint32_t)(row0 + min(col, m - 1)) * a.I * 4 + (kFold && g >= 4 ? plane : 0);
                     acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
                 }
+                constexpr int kSides = NT * PLANES;
+                auto load = [&](TokenPart<W8, false>& t, int i, int c) {
+                    const int side = i % kSides;
+                    load_tokens<W8, false>(t, reinterpret_cast<const uint8_t*>(a.inner) + tok[side / PLANES] + side % PLANES * plane,
+                                           c, i / kSides, q * 16, k_bytes);
+                };
                 constexpr bool kAhead = NT == 1 && S::prefetch;
-                TokenPart<W8> next[PLANES];   // with one tile: the inner rows of the next piece
-                if constexpr (kAhead) {
-#pragma unroll
-                    for (int pl = 0; pl < PLANES; ++pl)
-                        load_tokens<W8, false>(next[pl], tok[0] + pl * plane, first, q * 16, k_bytes);
-                }
+                TokenQueue<W8, false, TokenPart<W8, false>::kOfPiece * kSides, S::early> queue, next;   // next: with one tile, the inner rows of the next piece
+                if (kAhead) next.start([&](auto& t, int i) { load(t, i, first); });
                 for (int c = first; c < last; ++c) {
                     uint4 lo[2], hi[2];
-                    TokenPart<W8> now[PLANES];
-                    if constexpr (NT == 1) {
-#pragma unroll
-                        for (int pl = 0; pl < PLANES; ++pl) {
-                            if constexpr (kAhead) {
-                                now[pl] = next[pl];
-                                if (c + 1 < last) load_tokens<W8, false>(next[pl], tok[0] + pl * plane, c + 1, q * 16, k_bytes);
-                            } else {
-                                load_tokens<W8, false>(now[pl], tok[0] + pl * plane, c, q * 16, k_bytes);
-                            }
-                        }
+                    if constexpr (kAhead) {
+                        queue = next;
+                        if (c + 1 < last) next.start([&](auto& t, int i) { load(t, i, c + 1); });
+                    } else {
+                        queue.start([&](auto& t, int i) { load(t, i, c); });
                     }
                     ring.take(lo, hi);
-                    mma_piece<W8, NT, PLANES>(acc, lo, hi, [&](int j, int pl) {
-                        if constexpr (NT == 1) {
-                            return now[pl];
-                        } else {
-                            TokenPart<W8> t;
-                            load_tokens<W8, false>(t, tok[j] + pl * plane, c, q * 16, k_bytes);
-                            return t;
-                        }
+                    mma_piece<W8, false, NT, PLANES>(acc, lo, hi, [&](int i) {
+                        return queue.take(i, [&](auto& t, int n) { load(t, n, c); });
                     });
                     __syncwarp();
                     fetch();

@@ -94,24 +94,22 @@ __global__ void __launch_bounds__(kThreads, 2) matmul_skinny_kernel(const Matmul
                 tok[j] = a.a + (row0 + min(j * 8 + g, t.m - 1)) * a.K;   // columns past the last repeat it
                 acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
             }
-            TokenPart<true> next;   // with one tile: the tokens of the next piece
-            if (NT == 1 && warp < pieces) load_tokens<true, true>(next, tok[0], warp, q * 16, a.K);
+            auto load = [&](TokenPart<true, true>& t, int i, int c) {
+                load_tokens<true, true>(t, tok[i % NT], c, i / NT, q * 16, a.K);
+            };
+            TokenQueue<true, true, 2 * NT, 8> queue, next;   // next: with one tile, the tokens of the next piece
+            if (NT == 1 && warp < pieces) next.start([&](auto& t, int i) { load(t, i, warp); });
             for (int c = warp; c < pieces; c += kWarps) {
-                TokenPart<true> now;
                 if constexpr (NT == 1) {
-                    now = next;
-                    if (c + kWarps < pieces) load_tokens<true, true>(next, tok[0], c + kWarps, q * 16, a.K);
+                    queue = next;
+                    if (c + kWarps < pieces) next.start([&](auto& t, int i) { load(t, i, c + kWarps); });
+                } else {
+                    queue.start([&](auto& t, int i) { load(t, i, c); });
                 }
                 uint4 lo[2], hi[2];
                 ring.take(lo, hi);
-                mma_piece<true, NT, 1>(acc, lo, hi, [&](int j, int) {
-                    if constexpr (NT == 1) {
-                        return now;
-                    } else {
-                        TokenPart<true> part;
-                        load_tokens<true, true>(part, tok[j], c, q * 16, a.K);
-                        return part;
-                    }
+                mma_piece<true, true, NT, 1>(acc, lo, hi, [&](int i) {
+                    return queue.take(i, [&](auto& t, int n) { load(t, n, c); });
                 });
                 __syncwarp();
                 fetch();

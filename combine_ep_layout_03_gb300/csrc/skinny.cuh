@@ -109,43 +109,31 @@ struct WeightRing {
     }
 };
 
-// The token side of one piece for a tile of eight tokens: this lane's values, as bf16 pairs.
-template <bool W8>
-struct TokenPart { uint32_t b[2][W8 ? 8 : 4]; };
-
-// tok: the token's row (bf16, or int8 with T8); a lane's values past the row's end read as zero (the
-// weights there are zeros too, but zero times what lies behind the row may not be).
+// Part of the token side of one piece for a tile of eight tokens, this lane's values as they lie: with bf16
+// weights all of the piece, which is one 128-byte line of a token; with int8 weights half of it, so that
+// half of the weights at a time is converted and held (64 tokens over 512 experts, bf16, by halves: 886 us
+// for 856; 8 over 256 experts, int8, by whole pieces: 242 us for 233).
 template <bool W8, bool T8>
-__device__ __forceinline__ void load_tokens(TokenPart<W8>& t, const uint8_t* tok, int piece, int lane_off, int k_bytes) {
+struct TokenPart {
+    static constexpr int kOfPiece = W8 ? 2 : 1;   // parts of a piece
+    uint4 v[T8 ? 1 : 2];
+};
+
+// tok: the token's row (bf16, or int8 with T8); a lane's values past the row's end read as zero (the weights
+// there are zeros too, but zero times what lies behind the row may not be).
+template <bool W8, bool T8>
+__device__ __forceinline__ void load_tokens(TokenPart<W8, T8>& t, const uint8_t* tok, int piece, int part, int lane_off, int k_bytes) {
     constexpr int kWide = W8 && !T8 ? 2 : 1;   // bytes of a token's value to those of a weight
-    const int off = piece * 128 + lane_off;
+    const int off = piece * 128 + (W8 ? part * 64 : 0) + lane_off;
     const uint8_t* p = tok + (int64_t)off * kWide;
-    uint4 v[2][kWide];
     if ((piece + 1) * 128 <= k_bytes) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < kWide; ++i) v[h][i] = *reinterpret_cast<const uint4*>(p + h * 64 * kWide + i * 16);
+        for (int i = 0; i < (T8 ? 1 : 2); ++i) t.v[i] = *reinterpret_cast<const uint4*>(p + i * (W8 ? 16 : 64));
     } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < kWide; ++i)
-                v[h][i] = off + h * 64 < k_bytes ? *reinterpret_cast<const uint4*>(p + h * 64 * kWide + i * 16)
-                                                 : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if constexpr (T8) {
-            int8x4_to_bf16(v[h][0].x, t.b[h][0], t.b[h][1]); int8x4_to_bf16(v[h][0].y, t.b[h][2], t.b[h][3]);
-            int8x4_to_bf16(v[h][0].z, t.b[h][4], t.b[h][5]); int8x4_to_bf16(v[h][0].w, t.b[h][6], t.b[h][7]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kWide; ++i) {
-                t.b[h][4 * i] = v[h][i].x; t.b[h][4 * i + 1] = v[h][i].y;
-                t.b[h][4 * i + 2] = v[h][i].z; t.b[h][4 * i + 3] = v[h][i].w;
-            }
-        }
+        for (int i = 0; i < (T8 ? 1 : 2); ++i)
+            t.v[i] = off + (W8 ? 0 : i * 64) < k_bytes ? *reinterpret_cast<const uint4*>(p + i * (W8 ? 16 : 64))
+                                                       : make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -167,7 +155,7 @@ __device__ __forceinline__ int with_tiles(int tiles, F&& f) {
     return f(integral_constant<int, 1>{});
 }
 
-// The weights of half a piece as bf16 pairs.
+// Sixteen int8, or eight bf16, as bf16 pairs.
 template <bool W8>
 __device__ __forceinline__ void unpack_weights(const uint4& v, uint32_t* a) {
     if constexpr (W8) {
@@ -178,29 +166,56 @@ __device__ __forceinline__ void unpack_weights(const uint4& v, uint32_t* a) {
     }
 }
 
-// acc += one piece's products with NT tiles of eight tokens.  part(j, plane) gives the token side;
+// acc += one piece's products with NT tiles of eight tokens.  part(i) gives the token parts in the order of
+// use: with `sides` = NT PLANES, part i / sides of side i % sides, which is plane i % PLANES of its tile.
 // PLANES 2 multiplies by a second set of token rows as well (a value's remainder).
-template <bool W8, int NT, int PLANES, class Part>
+template <bool W8, bool T8, int NT, int PLANES, class Part>
 __device__ __forceinline__ void mma_piece(float (*acc)[4], const uint4 lo[2], const uint4 hi[2], Part part) {
-    uint32_t a0[2][W8 ? 8 : 4], a1[2][W8 ? 8 : 4];
+    constexpr int kParts = TokenPart<W8, T8>::kOfPiece, kSides = NT * PLANES;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        unpack_weights<W8>(lo[h], a0[h]);
-        unpack_weights<W8>(hi[h], a1[h]);
-    }
+    for (int h = 0; h < kParts; ++h) {
+        // an int8 part's 16 codes, or a bf16 part's two times 8 values, of each row
+        uint32_t a0[8], a1[8];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
+        for (int n = 0; n < 3 - kParts; ++n) {
+            unpack_weights<W8>(lo[h + n], a0 + 4 * n);
+            unpack_weights<W8>(hi[h + n], a1 + 4 * n);
+        }
 #pragma unroll
-        for (int pl = 0; pl < PLANES; ++pl) {
-            const TokenPart<W8> t = part(j, pl);
+        for (int i = 0; i < kSides; ++i) {
+            const TokenPart<W8, T8> t = part(h * kSides + i);
+            uint32_t b[8];
+            if constexpr (T8) {
+                unpack_weights<true>(t.v[0], b);
+            } else {
+                unpack_weights<false>(t.v[0], b);
+                unpack_weights<false>(t.v[1], b + 4);
+            }
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < (W8 ? 4 : 2); ++i)
-                    mma_bf16(acc[j], a0[h][2 * i], a1[h][2 * i], a0[h][2 * i + 1], a1[h][2 * i + 1], t.b[h][2 * i],
-                             t.b[h][2 * i + 1]);
+            for (int n = 0; n < 4; ++n)
+                mma_bf16(acc[i / PLANES], a0[2 * n], a1[2 * n], a0[2 * n + 1], a1[2 * n + 1], b[2 * n], b[2 * n + 1]);
         }
     }
 }
+
+// Token parts on their way: the first EARLY of a piece are asked for before its weights are waited for,
+// each later one when the one EARLY before it is used.
+template <bool W8, bool T8, int PARTS, int EARLY>
+struct TokenQueue {
+    static constexpr int kEarly = EARLY < PARTS ? EARLY : PARTS;
+    TokenPart<W8, T8> t[kEarly];
+    // load(part, i)
+    template <class Load>
+    __device__ __forceinline__ void start(Load load) {
+#pragma unroll
+        for (int i = 0; i < kEarly; ++i) load(t[i], i);
+    }
+    template <class Load>
+    __device__ __forceinline__ TokenPart<W8, T8> take(int i, Load load) {
+        const TokenPart<W8, T8> now = t[i % kEarly];
+        if (i + kEarly < PARTS) load(t[i % kEarly], i + kEarly);
+        return now;
+    }
+};
 
 }  // namespace
