@@ -8,11 +8,14 @@
 ``norm`` adds the residual (kept in ``layer.h``), normalises, and leaves the rows in int8 as well
 (ep_rms_norm_quant).  ``experts`` takes one of two ways:
 
-  - up to 64 tokens: ep_moe_few_tokens on y, which reads the chosen experts once and moves no rows;
+  - up to 64 tokens (``few_tokens``): ep_moe_few_tokens on y, which reads the chosen experts once and moves no rows;
   - more: layout, dispatch of the int8 rows as they are, gate and up products with SwiGLU, the
     inner rows to int8, the down product, combine.
 
-The first way keeps activations in bf16 where the second has them in int8.
+The first way keeps activations in bf16 where the second has them in int8.  From about 32 tokens on,
+the second is the faster one where the tokens choose many experts (few, more; us, 4096 x 1024, top-8:
+16 tokens over 32 experts 99, 115; 64 over 32 experts 208, 118; 16 over 128 experts 208, 215; 64 over
+128 experts 357, 299): ``few_tokens`` says up to how many take the first.
 """
 from __future__ import annotations
 
@@ -20,7 +23,7 @@ import torch
 
 from . import ep
 
-FEW_TOKENS = 64
+FEW_TOKENS = 64   # the most that ep_moe_few_tokens takes
 
 
 class ExpertLayer:
@@ -30,7 +33,7 @@ class ExpertLayer:
     with w2_scales [E, H]; gamma [H] bf16.  Every call runs on the current stream, or on ``stream``."""
 
     def __init__(self, R: int, T: int, w13, w13_scales, w2, w2_scales, gamma, topk: int, eps: float = 1e-6,
-                 alpha: int = 1):
+                 alpha: int = 1, few_tokens: int = FEW_TOKENS):
         self.w13, self.w13_scales, self.w2, self.w2_scales, self.gamma = w13, w13_scales, w2, w2_scales, gamma
         self.E, self.I, self.H = w13.shape[0], w13.shape[1] // 2, w13.shape[2]
         self.N, self.K, self.eps = R * T, topk, eps
@@ -40,7 +43,7 @@ class ExpertLayer:
         self.out = torch.empty_like(self.y)
         self.rows = torch.empty((self.N, self.H), dtype=torch.int8, device=dev)
         self.row_scales = torch.empty((self.N, 1), dtype=torch.float32, device=dev)
-        self.few = self.N <= FEW_TOKENS
+        self.few = self.N <= min(few_tokens, FEW_TOKENS)
         if self.few:
             n = ep.ep_moe_few_tokens_workspace_size(self.N, self.H, self.E, topk, self.I)
             self.workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)

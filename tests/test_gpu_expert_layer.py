@@ -87,3 +87,16 @@ def test_the_short_way(R, T):
     assert layer.status() == ep.EP_OK and layer.few
     want = plain(layer, y, idx, wts) + shared.double().sum(1).reshape(R * T, 512)
     assert (out - want).norm() <= 2.0 ** -8 * want.norm()   # every value is within half a step, 2^-8 of it
+
+
+def test_the_way_is_the_callers_choice():
+    layer, x, res, idx, wts = make(1, 40, 512, 16, 4, 256, 1, seed=3)
+    assert layer.few
+    other = ExpertLayer(1, 40, layer.w13, layer.w13_scales, layer.w2, layer.w2_scales, layer.gamma, topk=4, few_tokens=16)
+    assert not other.few
+    y = other.norm(x, res)
+    assert torch.equal(y, layer.norm(x, res))
+    out = other.experts(idx.view(1, 40, 4), wts.view(1, 40, 4)).double()
+    assert other.status() == ep.EP_OK
+    want = plain(other, y, idx, wts)
+    assert (out - want).norm() <= 0.06 * want.norm()
