@@ -19,9 +19,11 @@
 // was fused or not.
 //
 // Measured, against the copy bandwidth: 65536 x 4096 int8 with a residual 269 us, 1.03; without one
-// 146 us, 0.82; 32768 x 7168 MXFP8 without one 148 us, 0.71 (with: 237 us, 1.03); 1237 x 7168 in
+// 146 us, 0.82; 32768 x 7168 MXFP8 without one 154 us, 0.68 (with: 237 us, 1.03); 1237 x 7168 in
 // groups, with one, 14 us, 0.66 (8.1 rows an SM).  With a residual the bytes bound it; without one
 // instructions do (more or fewer resident rows make it slower; issue slots are half busy).
+#include <type_traits>
+
 #include "expert_ops.cuh"
 #include "quant.cuh"
 
@@ -83,6 +85,18 @@ __device__ __forceinline__ void sum2_add(Sum2& s, float hi, float lo) {
     const float e = __fadd_rn(__fsub_rn(s.hi, __fsub_rn(t, b)), __fsub_rn(hi, b));
     s.hi = t;
     s.lo = __fadd_rn(s.lo, __fadd_rn(e, lo));
+}
+
+// What is missing from r, an approximation of 1 / sqrt(s / n + eps): r (n - r^2 s - r^2 n eps) / 2n, with the
+// errors of the products taken along.  0 where a product leaves the range.
+__device__ __forceinline__ float rsqrt_remainder(float r, float s, float n, float inv_n, float eps) {
+    const float p = __fmul_rn(n, eps);
+    const float q = __fmul_rn(r, r), q_lo = __fmaf_rn(r, r, -q);
+    const float a = __fmul_rn(s, q), a_lo = __fmaf_rn(s, q, -a);
+    const float b = __fmul_rn(p, q), b_lo = __fmaf_rn(p, q, -b);
+    const float left = __fsub_rn(__fsub_rn(__fsub_rn(n, a), b), __fmaf_rn(__fadd_rn(s, p), q_lo, __fadd_rn(a_lo, b_lo)));
+    const float lo = __fmul_rn(__fmul_rn(r, 0.5f * inv_n), left);
+    return fabsf(lo) <= r * 0x1p-20f ? lo : 0.0f;
 }
 
 __device__ __forceinline__ uint4 ld_stream_v4(const void* p) {   // not .nc: h_out may be one of the inputs
@@ -316,29 +330,46 @@ __global__ void __launch_bounds__(VPT == 4 ? 256 : 1024, VPT == 4 ? 4 : 1) rms_n
                 ex[u] = mf * mf * (double)n >= rhs ? k : k - 1;
             }
         }
-        const f32x2 r2 = pair(rstd, rstd);
+        // t r as one rounding, from the root and its remainder: the 8-bit codes then differ from those of the real
+        // numbers about as seldom as any rounding to float32 before them allows (some 50 of 90 million; with the
+        // root alone, off by up to two steps, and a product rounded again the error of a whole output was up to
+        // twice that; 32768 x 7168 took 148 us then and takes 154 now).
+        const float rest = rsqrt_remainder(rstd, s, n, a.inv_n, a.eps);
+        // The power of two of a block goes into the root, unless some values are so far from 1 that it
+        // would leave the range.
+        auto store = [&](auto into_root) {
 #pragma unroll
-        for (int u = 0; u < VPT; ++u) {
-            const int vi = u * nt + tid;
-            const bool ok = row_ok && finite_bits(bm[u]);
-            const int se = min(max(ex[u] - TR::emax, -127), 127);
-            const float mul = __uint_as_float((uint32_t)(127 - se) << 23);   // 2^-se; se = 127 only for values
-                                                                             // that no finite row reaches
-            uint2 c = make_uint2(0, 0);
-            if (ok && bm[u]) {
-                const f32x2 m2 = pair(mul, mul);
-                float q[8];
+            for (int u = 0; u < VPT; ++u) {
+                const int vi = u * nt + tid;
+                const bool ok = row_ok && finite_bits(bm[u]);
+                const int se = min(max(ex[u] - TR::emax, -127), 127);
+                const float mul = __uint_as_float((uint32_t)(127 - se) << 23);   // 2^-se; se = 127 only for values
+                                                                                 // that no finite row reaches
+                uint2 c = make_uint2(0, 0);
+                if (ok && bm[u]) {
+                    const float rm = into_root ? rstd * mul : rstd, lo = into_root ? rest * mul : rest;
+                    const f32x2 r2 = pair(rm, rm), lo2 = pair(lo, lo), m2 = pair(mul, mul);
+                    float q[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) halves(mul2(mul2(t[u][i], r2), m2), q[2 * i], q[2 * i + 1]);
-                c.x = cvt_fp8x2<Q>(q[0], q[1]) | (cvt_fp8x2<Q>(q[2], q[3]) << 16);
-                c.y = cvt_fp8x2<Q>(q[4], q[5]) | (cvt_fp8x2<Q>(q[6], q[7]) << 16);
+                    for (int i = 0; i < 4; ++i) {
+                        const f32x2 y = fma2(t[u][i], r2, mul2(t[u][i], lo2));
+                        halves(into_root ? y : mul2(y, m2), q[2 * i], q[2 * i + 1]);
+                    }
+                    c.x = cvt_fp8x2<Q>(q[0], q[1]) | (cvt_fp8x2<Q>(q[2], q[3]) << 16);
+                    c.y = cvt_fp8x2<Q>(q[4], q[5]) | (cvt_fp8x2<Q>(q[6], q[7]) << 16);
+                }
+                if (vi < a.nvec) {
+                    st_v2(data + 8 * vi, c);
+                    if ((vi & 3) == 0)
+                        a.scales[row * a.scale_bytes + (vi >> 2)] = (uint8_t)(!ok ? 255 : bm[u] ? se + 127 : 0);
+                }
             }
-            if (vi < a.nvec) {
-                st_v2(data + 8 * vi, c);
-                if ((vi & 3) == 0)
-                    a.scales[row * a.scale_bytes + (vi >> 2)] = (uint8_t)(!ok ? 255 : bm[u] ? se + 127 : 0);
-            }
-        }
+        };
+        bool fits = rstd > 0x1p-60f && rstd < 0x1p60f;
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) fits = fits && ((ex[u] > -50 && ex[u] < 50) || !bm[u]);
+        if (fits) store(std::true_type{});
+        else store(std::false_type{});
     }
 }
 

@@ -170,6 +170,25 @@ def test_block_maximum_on_a_power_of_two(quant):
     check(x, None, gamma, 0.0, quant, data, scales, h)
 
 
+@pytest.mark.parametrize("quant", MX)
+@pytest.mark.parametrize("scale", [2.0 ** -80, 2.0 ** -45, 1.0, 2.0 ** 45, 2.0 ** 80])
+@pytest.mark.parametrize("rows,H", [(300, 1376), (64, 8192), (1, 64)])
+def test_block_codes_are_rounded_once_more_at_most(quant, scale, rows, H):
+    """Small integers, whose squares' sum is exact: then only y's own rounding to float32, 2^-24 of it (and
+    errors of 2^-40), stands between a code and the nearest one."""
+    g = torch.Generator(device="cuda").manual_seed(H)
+    x = torch.randint(-7, 8, (rows, H), device="cuda", generator=g).to(torch.bfloat16)
+    gamma = ((1 + 0.1 * torch.randn(H, device="cuda", generator=g)) * scale).to(torch.bfloat16)
+    data, scales, _ = run(x, None, gamma, 1e-6, quant)
+    v = x.double()
+    y = (v * gamma.double() / torch.sqrt(v.square().mean(1, keepdim=True) + float(np.float32(1e-6)))).view(rows, -1, 32)
+    q = y * torch.exp2(127 - scales.double())[:, :, None]
+    top = 57344.0 if quant in E5M2 else 448.0
+    q = q.clamp(-top, top)
+    codes = decode(data, quant).view(q.shape)
+    assert ((codes - q).abs() <= step_of(q, quant in E5M2) / 2 + 1.01 * 2.0 ** -24 * q.abs()).all()
+
+
 @pytest.mark.parametrize("quant", MODES)
 def test_strides_and_in_place(quant):
     wide = draw(64, 1024, seed=3)[0]
