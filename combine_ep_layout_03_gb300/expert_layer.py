@@ -36,7 +36,7 @@ class ExpertLayer:
                  alpha: int = 1, few_tokens: int = FEW_TOKENS):
         self.w13, self.w13_scales, self.w2, self.w2_scales, self.gamma = w13, w13_scales, w2, w2_scales, gamma
         self.E, self.I, self.H = w13.shape[0], w13.shape[1] // 2, w13.shape[2]
-        self.N, self.K, self.eps = R * T, topk, eps
+        self.R, self.T, self.N, self.K, self.eps = R, T, R * T, topk, eps
         dev = w13.device
         self.y = torch.empty((self.N, self.H), dtype=torch.bfloat16, device=dev)
         self.h = torch.empty_like(self.y)
@@ -65,11 +65,11 @@ class ExpertLayer:
 
     def experts(self, topk_idx: torch.Tensor, topk_weights: torch.Tensor, shared: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
-        """The weighted sum of the chosen experts' outputs of the rows that norm() left, plus shared
-        rows: [S, N, H] with one rank, [R, S, T, H] for the long way (as EPLayout.combine)."""
+        """The weighted sum of the chosen experts' outputs of the rows that norm() left, plus shared rows:
+        bf16 [R, S, T, H] (as EPLayout.combine) or [S, N, H], whichever way is taken."""
+        if shared is not None:
+            shared = self._shared_rows(shared)
         if self.few:
-            if shared is not None and shared.dim() == 4:   # [R, S, T, H]
-                shared = shared.transpose(0, 1).reshape(shared.shape[1], self.N, self.H)
             ep.ep_moe_few_tokens(self.y, topk_idx.view(self.N, self.K), topk_weights.view(self.N, self.K), self.w13,
                                  self.w2, self.out, self.workspace, self.w13_scales, self.w2_scales, shared,
                                  self._status, stream)
@@ -81,6 +81,19 @@ class ExpertLayer:
         ep.ep_quant_rows(self.inner, q, self.inner_rows, self.inner_scales, stream)
         lay.expert_matmul(self.inner_rows, self.inner_scales, self.w2, self.w2_scales, self.expert_out, stream=stream)
         return lay.combine(self.expert_out, topk_weights, self.out, shared, stream)
+
+    def _shared_rows(self, shared: torch.Tensor) -> torch.Tensor:
+        """The shared rows as this layer's way reads them: [S, N, H], or [R, S, T, H]."""
+        R, T, H = self.R, self.T, self.H
+        if shared.dim() == 3 and shared.shape[1:] == (self.N, H):
+            ranks = shared.unflatten(1, (R, T)).transpose(0, 1)
+        elif shared.dim() == 4 and (shared.shape[0], *shared.shape[2:]) == (R, T, H):
+            ranks = shared
+        else:
+            ranks = None
+        if ranks is None or shared.dtype is not torch.bfloat16:
+            raise ep.EPError(ep.EP_ERR_INVALID_ARG, "shared: bf16 [R, S, T, H] or [S, N, H]")
+        return ranks.transpose(0, 1).reshape(-1, self.N, H).contiguous() if self.few else ranks.contiguous()
 
     def status(self) -> int:
         """The first device-side error since the last layout (synchronises)."""

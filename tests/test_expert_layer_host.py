@@ -1,0 +1,68 @@
+"""What ExpertLayer hands to the library, on the CPU: its tensors are CPU tensors here, and the
+library's calls are replaced by ones that keep what they are given."""
+import pytest
+import torch
+
+from combine_ep_layout_03_gb300 import ep
+from combine_ep_layout_03_gb300.expert_layer import ExpertLayer
+
+E, H, I, K = 4, 64, 16, 2
+
+
+def make(R, T, few, monkeypatch):
+    """A layer of either way, and the list of (call, its tensors) that experts() fills."""
+    f = torch.zeros
+    layer = ExpertLayer(R, T, f(E, 2 * I, H, dtype=torch.int8), f(E, 2 * I), f(E, H, I, dtype=torch.int8), f(E, H),
+                        f(H, dtype=torch.bfloat16), K, few_tokens=64 if few else 0)
+    assert layer.few == few
+    calls = []
+
+    def keep(name):
+        def call(*args, **kw):
+            calls.append((name, args, kw))
+        return call
+
+    monkeypatch.setattr(ep, "ep_moe_few_tokens", keep("few"))
+    monkeypatch.setattr(ep, "ep_quant_rows", keep("quant_rows"))
+    if not few:
+        for name in ("layout", "dispatch_ex", "expert_matmul", "combine"):
+            monkeypatch.setattr(layer.layout, name, keep(name))
+    return layer, calls
+
+
+def routing(N):
+    return torch.zeros(N, K, dtype=torch.int64), torch.zeros(N, K)
+
+
+def shared_of(calls, few):
+    """The shared rows that the kernels were given, as [R, S, T, H] or [S, N, H]."""
+    name, args, kw = calls[-1]
+    assert name == ("few" if few else "combine")
+    return args[9] if few else args[3]
+
+
+@pytest.mark.parametrize("few", [False, True])
+@pytest.mark.parametrize("R,T,S", [(1, 8, 1), (1, 8, 3), (2, 4, 1), (2, 4, 3), (4, 1, 2)])
+@pytest.mark.parametrize("by_rank", [False, True])
+def test_shared_rows_reach_the_kernels_in_their_order(few, R, T, S, by_rank, monkeypatch):
+    """combine reads R x S x T rows, the few-token kernels S x N: both get as many as they read, each
+    token its own, whichever of the two documented shapes the caller has."""
+    layer, calls = make(R, T, few, monkeypatch)
+    ranks = torch.randn(R, S, T, H).to(torch.bfloat16)
+    tokens = ranks.transpose(0, 1).reshape(S, R * T, H)
+    layer.experts(*routing(R * T), ranks if by_rank else tokens)
+    got = shared_of(calls, few)
+    assert got.is_contiguous() and torch.equal(got, tokens if few else ranks)
+
+
+@pytest.mark.parametrize("few", [False, True])
+def test_shared_rows_of_other_shapes_are_refused(few, monkeypatch):
+    layer, calls = make(2, 4, few, monkeypatch)
+    bf = torch.bfloat16
+    for shape in ((8, H), (3, 4, H), (3, 8, H + 8), (1, 3, 8, H), (2, 3, 8, H), (2, 4, 3, H), (2, 3, 4, H // 2), (1, 2, 3, 4, H)):
+        with pytest.raises(ep.EPError) as err:
+            layer.experts(*routing(8), torch.zeros(shape, dtype=bf))
+        assert err.value.status == ep.EP_ERR_INVALID_ARG
+    with pytest.raises(ep.EPError):
+        layer.experts(*routing(8), torch.zeros(2, 3, 4, H))
+    assert not calls or calls[-1][0] not in ("few", "combine")

@@ -1,0 +1,45 @@
+"""Arguments of ExpertLayer's calls on the GPU: shared rows of both shapes on both ways.
+
+The shared rows' share is checked as the difference to a call without them: out = bf16(s + shared) with
+|s| known from the call without them to half a step, 2^-8 of it, so the two differ from the exact sum by
+2^-8 |out| + 2^-8 |s| and S + 8 float32 additions, (S + 8) 2^-23 (|s| + sum|shared|)."""
+import pytest
+import torch
+
+from combine_ep_layout_03_gb300 import ep
+from combine_ep_layout_03_gb300.expert_layer import ExpertLayer
+
+pytestmark = pytest.mark.gpu
+
+
+def make(R, T, few, H=512, E=8, K=2, I=128, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    w13 = torch.randint(-100, 101, (E, 2 * I, H), device="cuda", generator=g, dtype=torch.int8)
+    w2 = torch.randint(-100, 101, (E, H, I), device="cuda", generator=g, dtype=torch.int8)
+    s13 = torch.full((E, 2 * I), 0.02 / H ** 0.5, device="cuda")
+    s2 = torch.full((E, H), 0.02 / I ** 0.5, device="cuda")
+    layer = ExpertLayer(R, T, w13, s13, w2, s2, torch.ones(H, dtype=torch.bfloat16, device="cuda"), K,
+                        few_tokens=64 if few else 0)
+    assert layer.few == few
+    N = R * T
+    x = torch.randn(N, H, device="cuda", generator=g).to(torch.bfloat16)
+    idx = torch.rand(N, E, device="cuda", generator=g).topk(K, 1).indices
+    wts = torch.softmax(torch.randn(N, K, device="cuda", generator=g), 1)
+    return layer, x, idx, wts, g
+
+
+@pytest.mark.parametrize("few", [False, True])
+@pytest.mark.parametrize("R,T,S", [(1, 8, 3), (1, 12, 1), (2, 6, 3), (4, 2, 2)])
+@pytest.mark.parametrize("by_rank", [False, True])
+def test_shared_rows(few, R, T, S, by_rank):
+    layer, x, idx, wts, g = make(R, T, few, seed=S)
+    N, H = R * T, layer.H
+    layer.norm(x)
+    s = layer.experts(idx, wts).clone().double()
+    ranks = torch.randn(R, S, T, H, device="cuda", generator=g).to(torch.bfloat16)
+    tokens = ranks.transpose(0, 1).reshape(S, N, H)
+    out = layer.experts(idx, wts, ranks if by_rank else tokens).double()
+    assert layer.status() == ep.EP_OK
+    want = s + tokens.double().sum(0)
+    tol = 2.0 ** -8 * (out.abs() + s.abs()) + (S + 8) * 2.0 ** -23 * (s.abs() + tokens.double().abs().sum(0))
+    assert ((out - want).abs() <= tol).all()
