@@ -66,7 +66,12 @@ class ExpertLayer:
     def experts(self, topk_idx: torch.Tensor, topk_weights: torch.Tensor, shared: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
         """The weighted sum of the chosen experts' outputs of the rows that norm() left, plus shared rows:
-        bf16 [R, S, T, H] (as EPLayout.combine) or [S, N, H], whichever way is taken."""
+        bf16 [R, S, T, H] (as EPLayout.combine) or [S, N, H], whichever way is taken.  topk_idx int64 and
+        topk_weights float32, contiguous, hold K entries for each of the N tokens."""
+        for t, dtype, what in ((topk_idx, torch.int64, "topk_idx: contiguous int64 [N, K]"),
+                               (topk_weights, torch.float32, "topk_weights: contiguous float32 [N, K]")):
+            if t.dtype is not dtype or not t.is_contiguous() or t.numel() != self.N * self.K:
+                raise ep.EPError(ep.EP_ERR_INVALID_ARG, what)
         if shared is not None:
             shared = self._shared_rows(shared)
         if self.few:

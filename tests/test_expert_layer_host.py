@@ -66,3 +66,19 @@ def test_shared_rows_of_other_shapes_are_refused(few, monkeypatch):
     with pytest.raises(ep.EPError):
         layer.experts(*routing(8), torch.zeros(2, 3, 4, H))
     assert not calls or calls[-1][0] not in ("few", "combine")
+
+
+@pytest.mark.parametrize("few", [False, True])
+def test_routing_of_other_types_and_sizes_is_refused(few, monkeypatch):
+    """bf16 router weights, say, would be read as float32 past their end."""
+    layer, calls = make(2, 4, few, monkeypatch)
+    idx, wts = routing(8)
+    for a, b in ((idx.int(), wts), (idx[:4], wts), (idx.t().contiguous().t(), wts), (torch.cat([idx, idx]), wts),
+                 (idx, wts.to(torch.bfloat16)), (idx, wts.double()), (idx, wts[:4]), (idx, wts[:, :1]),
+                 (idx, wts.t().contiguous().t()), (idx, torch.zeros(8, 2 * K)[:, ::2])):
+        with pytest.raises(ep.EPError) as err:
+            layer.experts(a, b)
+        assert err.value.status == ep.EP_ERR_INVALID_ARG
+    assert not calls
+    for a, b in ((idx, wts), (idx.view(2, 4, K), wts.view(2, 4, K))):
+        layer.experts(a, b)
