@@ -19,11 +19,20 @@ the second is the faster one where the tokens choose many experts (few, more; us
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import ep
 
 FEW_TOKENS = 64   # the most that ep_moe_few_tokens takes
+
+
+def _on(stream):
+    """Inside, torch's own kernels and allocations are of a call's stream (None: the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 class ExpertLayer:
@@ -73,7 +82,7 @@ class ExpertLayer:
             if t.dtype is not dtype or not t.is_contiguous() or t.numel() != self.N * self.K:
                 raise ep.EPError(ep.EP_ERR_INVALID_ARG, what)
         if shared is not None:
-            shared = self._shared_rows(shared)
+            shared = self._shared_rows(shared, stream)
         if self.few:
             ep.ep_moe_few_tokens(self.y, topk_idx.view(self.N, self.K), topk_weights.view(self.N, self.K), self.w13,
                                  self.w2, self.out, self.workspace, self.w13_scales, self.w2_scales, shared,
@@ -87,8 +96,9 @@ class ExpertLayer:
         lay.expert_matmul(self.inner_rows, self.inner_scales, self.w2, self.w2_scales, self.expert_out, stream=stream)
         return lay.combine(self.expert_out, topk_weights, self.out, shared, stream)
 
-    def _shared_rows(self, shared: torch.Tensor) -> torch.Tensor:
-        """The shared rows as this layer's way reads them: [S, N, H], or [R, S, T, H]."""
+    def _shared_rows(self, shared: torch.Tensor, stream) -> torch.Tensor:
+        """The shared rows as this layer's way reads them: [S, N, H], or [R, S, T, H].  Where that takes a copy
+        (several ranks and several rows), it is made on the call's stream, in that stream's memory."""
         R, T, H = self.R, self.T, self.H
         if shared.dim() == 3 and shared.shape[1:] == (self.N, H):
             ranks = shared.unflatten(1, (R, T)).transpose(0, 1)
@@ -98,7 +108,8 @@ class ExpertLayer:
             ranks = None
         if ranks is None or shared.dtype is not torch.bfloat16:
             raise ep.EPError(ep.EP_ERR_INVALID_ARG, "shared: bf16 [R, S, T, H] or [S, N, H]")
-        return ranks.transpose(0, 1).reshape(-1, self.N, H).contiguous() if self.few else ranks.contiguous()
+        with _on(stream):
+            return ranks.transpose(0, 1).reshape(-1, self.N, H).contiguous() if self.few else ranks.contiguous()
 
     def status(self) -> int:
         """The first device-side error since the last layout (synchronises)."""

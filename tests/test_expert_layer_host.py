@@ -1,7 +1,10 @@
 """What ExpertLayer hands to the library, on the CPU: its tensors are CPU tensors here, and the
 library's calls are replaced by ones that keep what they are given."""
+import contextlib
+
 import pytest
 import torch
+from torch.utils._python_dispatch import TorchDispatchMode
 
 from combine_ep_layout_03_gb300 import ep
 from combine_ep_layout_03_gb300.expert_layer import ExpertLayer
@@ -82,3 +85,45 @@ def test_routing_of_other_types_and_sizes_is_refused(few, monkeypatch):
     assert not calls
     for a, b in ((idx, wts), (idx.view(2, 4, K), wts.view(2, 4, K))):
         layer.experts(a, b)
+
+
+class Streams:
+    """Stands in for torch's streams: `now` is the one that an operation would run on."""
+
+    def __init__(self, monkeypatch):
+        self.now = "current"
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: ("handle", handle))
+        monkeypatch.setattr(torch.cuda, "stream", self.enter)
+
+    @contextlib.contextmanager
+    def enter(self, stream):
+        before, self.now = self.now, stream
+        yield
+        self.now = before
+
+    @contextlib.contextmanager
+    def writes(self):
+        """The list of (operation that writes a tensor, its stream) of what runs inside."""
+        seen, streams = [], self
+
+        class Record(TorchDispatchMode):
+            def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+                if func.overloadpacket in (torch.ops.aten.clone, torch.ops.aten.copy_, torch.ops.aten._to_copy, torch.ops.aten.zero_, torch.ops.aten.fill_):
+                    seen.append((func.overloadpacket, streams.now))
+                return func(*args, **(kwargs or {}))
+
+        with Record():
+            yield seen
+
+
+@pytest.mark.parametrize("few", [False, True])
+@pytest.mark.parametrize("stream,runs_on", [(None, "current"), ("side", "side"), (1 << 40, ("handle", 1 << 40))])
+def test_shared_rows_are_reordered_on_the_calls_stream(few, stream, runs_on, monkeypatch):
+    """A copy on another stream than the kernels' may not be there yet when they read it."""
+    layer, calls = make(2, 4, few, monkeypatch)
+    streams = Streams(monkeypatch)
+    shared = torch.randn(3, 8, H).to(torch.bfloat16) if not few else torch.randn(2, 3, 4, H).to(torch.bfloat16)
+    with streams.writes() as seen:
+        layer.experts(*routing(8), shared, stream=stream)
+    copies = [s for op, s in seen if op in (torch.ops.aten.clone, torch.ops.aten.copy_)]
+    assert copies and set(copies) == {runs_on}

@@ -1,4 +1,4 @@
-"""Arguments of ExpertLayer's calls on the GPU: shared rows of both shapes on both ways.
+"""Arguments of ExpertLayer's calls on the GPU: shared rows of both shapes on both ways, and streams.
 
 The shared rows' share is checked as the difference to a call without them: out = bf16(s + shared) with
 |s| known from the call without them to half a step, 2^-8 of it, so the two differ from the exact sum by
@@ -43,3 +43,24 @@ def test_shared_rows(few, R, T, S, by_rank):
     want = s + tokens.double().sum(0)
     tol = 2.0 ** -8 * (out.abs() + s.abs()) + (S + 8) * 2.0 ** -23 * (s.abs() + tokens.double().abs().sum(0))
     assert ((out - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("few", [False, True])
+@pytest.mark.parametrize("handle", [False, True])
+def test_shared_rows_on_another_stream(few, handle):
+    """Shared rows that have to be reordered, on a stream of the call's own while the current one is busy."""
+    layer, x, idx, wts, g = make(2, 6, few, seed=9)
+    ranks = torch.randn(2, 3, 6, layer.H, device="cuda", generator=g).to(torch.bfloat16)
+    shared = ranks if few else ranks.transpose(0, 1).reshape(3, 12, layer.H)
+    layer.norm(x)
+    want = layer.experts(idx, wts, shared).clone()
+    layer.out.zero_()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)   # a tenth of a second of the current stream
+    layer.experts(idx, wts, shared, stream=side.cuda_stream if handle else side)
+    side.synchronize()
+    with torch.cuda.stream(side):
+        got = layer.out.clone()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
