@@ -84,6 +84,8 @@ class ExpertLayer:
         if shared is not None:
             shared = self._shared_rows(shared, stream)
         if self.few:
+            with _on(stream):
+                self._status.zero_()   # the layout does that on the other way
             ep.ep_moe_few_tokens(self.y, topk_idx.view(self.N, self.K), topk_weights.view(self.N, self.K), self.w13,
                                  self.w2, self.out, self.workspace, self.w13_scales, self.w2_scales, shared,
                                  self._status, stream)
@@ -111,6 +113,9 @@ class ExpertLayer:
         with _on(stream):
             return ranks.transpose(0, 1).reshape(-1, self.N, H).contiguous() if self.few else ranks.contiguous()
 
-    def status(self) -> int:
-        """The first device-side error since the last layout (synchronises)."""
-        return int(self._status.item()) if self.few else self.layout.status()
+    def status(self, stream=None) -> int:
+        """The first device-side error of the last experts() call; waits for ``stream``, the one that it ran on."""
+        if not self.few:
+            return self.layout.status(stream)
+        with _on(stream):
+            return int(self._status.item())

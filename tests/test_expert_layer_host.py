@@ -108,7 +108,8 @@ class Streams:
 
         class Record(TorchDispatchMode):
             def __torch_dispatch__(self, func, types, args=(), kwargs=None):
-                if func.overloadpacket in (torch.ops.aten.clone, torch.ops.aten.copy_, torch.ops.aten._to_copy, torch.ops.aten.zero_, torch.ops.aten.fill_):
+                if func.overloadpacket in (torch.ops.aten.clone, torch.ops.aten.copy_, torch.ops.aten._to_copy, torch.ops.aten.zero_,
+                                           torch.ops.aten._local_scalar_dense):
                     seen.append((func.overloadpacket, streams.now))
                 return func(*args, **(kwargs or {}))
 
@@ -127,3 +128,25 @@ def test_shared_rows_are_reordered_on_the_calls_stream(few, stream, runs_on, mon
         layer.experts(*routing(8), shared, stream=stream)
     copies = [s for op, s in seen if op in (torch.ops.aten.clone, torch.ops.aten.copy_)]
     assert copies and set(copies) == {runs_on}
+
+
+def test_status_is_that_of_the_last_step(monkeypatch):
+    """A bad id, a good step, another error: each step's own, cleared in the step's own stream."""
+    layer, _ = make(1, 8, True, monkeypatch)
+    streams = Streams(monkeypatch)
+    error = [0]
+
+    def few_tokens(*args):
+        status = args[10]
+        if status.item() == 0:   # the kernels keep the first error
+            status.fill_(error[0])
+
+    monkeypatch.setattr(ep, "ep_moe_few_tokens", few_tokens)
+    for error[0] in (ep.EP_ERR_BAD_EXPERT_ID, ep.EP_OK, ep.EP_ERR_TIMEOUT, ep.EP_ERR_BAD_EXPERT_ID, ep.EP_OK):
+        for stream in (None, "side"):
+            with streams.writes() as seen:
+                layer.experts(*routing(8), stream=stream)
+            assert (torch.ops.aten.zero_, stream or "current") in seen
+            with streams.writes() as seen:
+                assert layer.status(stream) == error[0]
+            assert seen == [(torch.ops.aten._local_scalar_dense, stream or "current")]

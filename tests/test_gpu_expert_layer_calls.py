@@ -64,3 +64,17 @@ def test_shared_rows_on_another_stream(few, handle):
         got = layer.out.clone()
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("few", [False, True])
+def test_status_is_that_of_the_last_step(few):
+    layer, x, idx, wts, _ = make(1, 8, few, seed=4)
+    layer.norm(x)
+    bad = idx.clone()
+    bad[3, 1] = layer.E
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (None, side):
+        for routing, want in ((idx, ep.EP_OK), (bad, ep.EP_ERR_BAD_EXPERT_ID), (idx, ep.EP_OK)):
+            layer.experts(routing, wts, stream=stream)
+            assert layer.status(stream) == want
