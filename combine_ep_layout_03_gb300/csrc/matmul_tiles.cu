@@ -327,13 +327,14 @@ __device__ __forceinline__ bool convert(const Work<C>& w, int warp, int set) {
     return ok;
 }
 
-// silu(gate s0) * (up s1); a gate of -inf or an exponential past the range gives 0 as the limit does.
+// silu(gate s0) * (up s1).  The sigmoid is multiplied in before up: where its exponential passes the range the
+// result is 0, however large gate times up would be.  (A gate of -inf gives NaN, the formula's -inf / inf.)
 __device__ __forceinline__ float swiglu(float gate, float up, float s0, float s1) {
     float e, r;
     const float g = gate * s0;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return g * (up * s1) * r;
+    return g * r * (up * s1);
 }
 
 // Lane: an output channel; with gates and ups, lanes 0-15 hold the gates of lanes 16-31's ups.
