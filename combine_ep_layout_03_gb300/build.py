@@ -16,7 +16,7 @@ LIB = os.path.join(OUT_DIR, "libeplayout.so")
 SOURCES = ["ep_api.cu", "layout.cu", "dispatch.cu", "dispatch_scaled.cu", "combine.cu", "split.cu",
            "noalloc.cu", "rows.cu", "few_tokens.cu", "matmul_skinny.cu", "matmul_tiles.cu"]
 HEADERS = ["ep_internal.cuh", "tma.cuh", "quant.cuh", "expert_ops.cuh", "skinny.cuh", "tcgen05.cuh",
-           "tensor_maps.cuh"]
+           "tensor_maps.cuh", "ring_places.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-Xptxas", "-v"]

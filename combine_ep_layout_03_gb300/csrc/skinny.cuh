@@ -14,6 +14,7 @@
 
 #include "tcgen05.cuh"
 #include "ep_internal.cuh"
+#include "ring_places.cuh"
 
 namespace {
 
@@ -46,16 +47,15 @@ __device__ __forceinline__ void int8x4_to_bf16(uint32_t w, uint32_t& lo, uint32_
 // ring keeps running through the barriers and sums between one unit of work and the next.
 // (cp.async in 16-byte chunks, and loads to registers, reach two thirds of the rate: what arrives
 // in 32-byte sectors is written to shared memory or registers a sector at a time, 20 accesses for
-// 512 bytes.)  Every wait is bounded; after one that gave up the ring waits for nothing more.
+// 512 bytes.)  Every wait is bounded; after one that gave up nothing more is loaded, and drain()
+// waits again for what is in flight.
 template <int DEPTH>
 struct WeightRing {
     static constexpr int kSlot = 2048, kWarpBytes = DEPTH * kSlot;
     uint8_t* slots;
     uint64_t* bars;
     uint32_t lane_off;   // of this lane's chunk in a slot (row g, the first half of a piece)
-    int put_slot = 0, take_slot = 0, armed = 0;
-    uint32_t parity = 0;
-    bool ok = true;
+    RingPlaces<DEPTH> places;
 
     // smem: 1024-byte aligned, kWarpBytes a warp; barriers: DEPTH a warp.
     __device__ __forceinline__ WeightRing(uint8_t* smem, uint64_t* barriers, int warp, int lane)
@@ -72,34 +72,31 @@ struct WeightRing {
     // load(slot, barrier) issues the box of `bytes` bytes (one lane).
     template <class Load>
     __device__ __forceinline__ void put(int lane, uint32_t bytes, Load load) {
-        if (lane == 0 && ok) {
-            mbar_arrive_expect_tx(&bars[put_slot], bytes);
-            load(slots + put_slot * kSlot, &bars[put_slot]);
-        }
-        ++armed;
-        put_slot = put_slot + 1 == DEPTH ? 0 : put_slot + 1;
+        places.put([&](int slot) {
+            if (lane != 0) return;
+            mbar_arrive_expect_tx(&bars[slot], bytes);
+            load(slots + slot * kSlot, &bars[slot]);
+        });
     }
 
     // This lane's part of the oldest slot: rows g (lo) and g + 8 (hi) of the two 64-byte halves.
     __device__ __forceinline__ void take(uint4 lo[2], uint4 hi[2]) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars[take_slot], parity, kMaxPolls));
-        --armed;
-        const uint32_t at = lane_off + take_slot * kSlot;
+        const uint32_t at = lane_off + kSlot * places.take([&](int slot, uint32_t parity) { return wait(slot, parity); });
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             lo[h] = lds(at ^ (h * 64));
             hi[h] = lds((at ^ (h * 64)) + 1024);
         }
-        if (++take_slot == DEPTH) { take_slot = 0; parity ^= 1; }
     }
 
     // Nothing is in flight when the CTA ends.  False: a wait gave up.
     __device__ __forceinline__ bool drain() {
-        for (; armed > 0; --armed) {
-            ok = mbar_wait(&bars[take_slot], parity, kMaxPolls) && ok;
-            if (++take_slot == DEPTH) { take_slot = 0; parity ^= 1; }
-        }
-        return ok;
+        return places.drain([&](int slot, uint32_t parity) { return wait(slot, parity); });
+    }
+
+    // The same answer in all lanes.
+    __device__ __forceinline__ bool wait(int slot, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(&bars[slot], parity, kMaxPolls));
     }
 
     static __device__ __forceinline__ uint4 lds(uint32_t addr) {
