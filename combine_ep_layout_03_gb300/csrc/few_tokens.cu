@@ -289,10 +289,13 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_inner_ke
             const Factors f = i == tid ? mine : factors(i);
             gate *= f.gate;
             const float h = gate / (1.0f + expf(-gate)) * (up * f.up) * f.weight;
-            const uint32_t hi = pack_bf16x2_rn(h, 0.0f) & 0xffffu;
+            // value and remainder; past the largest bf16 the value is the truncated one, and an infinity has none
+            uint32_t hi = pack_bf16x2_rn(h, 0.0f) & 0xffffu;
+            if ((hi & 0x7fffu) == 0x7f80u) hi = __float_as_uint(h) >> 16;
+            const float rest = (hi & 0x7fffu) == 0x7f80u ? 0.0f : h - bf16_bits_to_float(hi);
             uint16_t* dst = a.inner + (int64_t)(row0 + col) * 2 * a.I + channel;
             dst[0] = (uint16_t)hi;
-            dst[a.I] = (uint16_t)pack_bf16x2_rn(h - bf16_bits_to_float(hi), 0.0f);
+            dst[a.I] = (uint16_t)pack_bf16x2_rn(rest, 0.0f);
         }
         if (kBuffers == 1) __syncthreads();
     }

@@ -47,3 +47,46 @@ def test_products_with_swiglu(rows, experts):
     g = K * sa[:, None] * sign.float()
     u = (K * sa[:, None] * up.float()) * sw[0, half:]
     agrees(out, swiglu_of(g.double(), u.double()))
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("T,I", [(3, 16), (12, 48), (40, 272)])
+@pytest.mark.parametrize("gate,up,weight", [
+    (2.0 ** 60, 2.0 ** 80, 1.0),             # an inner value past float32: inf
+    (2.0 ** 60, -2.0 ** 80, 1.0),
+    (2.0 ** 100, 1.9921875 * 2.0 ** 27, 1.003),    # past the largest bf16, not past float32
+    (2.0 ** 100, -1.9921875 * 2.0 ** 27, 1.003),
+    (-2.0 ** 60, 2.0 ** 80, 1.0),            # the sigmoid is 0
+    (2.0 ** 20, 2.0 ** 30, 1.0),
+    (float("inf"), 1.0, 1.0), (1.0, float("-inf"), 1.0), (float("-inf"), 1.0, 1.0)])
+def test_inner_values_of_the_few_token_layer(int8, T, I, gate, up, weight):
+    """One token has such gates and ups; the others' rows stay as they are without it."""
+    H, E = 64, 2
+    x = torch.ones(T, H, dtype=torch.bfloat16, device="cuda")
+    x[:, 1:] = 0
+    odd = T // 2
+    idx = torch.zeros(T, 1, dtype=torch.int64, device="cuda")
+    idx[odd] = 1
+    wts = torch.ones(T, 1, device="cuda")
+    wts[odd] = weight
+    column = torch.where(torch.arange(H, device="cuda") % 2 == 0, 1.0, -1.0)
+    ones = torch.zeros(E, 2 * I, H, device="cuda")
+    ones[:, :, 0] = 1
+    size = torch.ones(E, 2 * I, device="cuda")
+    size[1, :I], size[1, I:] = gate, up
+    if int8:
+        w13, s13 = ones.to(torch.int8), size
+        w2, s2 = column.to(torch.int8)[None, :, None].expand(E, H, I).contiguous(), torch.full((E, H), 2.0 ** -20, device="cuda")
+    else:
+        w13, s13 = (ones * 1).to(torch.bfloat16), None
+        w13[:, :, 0] = size.to(torch.bfloat16)
+        w2, s2 = (column * 2.0 ** -20)[None, :, None].expand(E, H, I).to(torch.bfloat16).contiguous(), None
+    out = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(ep.ep_moe_few_tokens_workspace_size(T, H, E, 1, I), dtype=torch.uint8, device="cuda")
+    ep.ep_moe_few_tokens(x, idx, wts, w13, w2, out, ws, w13_scales=s13, w2_scales=s2)
+    torch.cuda.synchronize()
+    assert int8 or torch.equal(w13[1, :, 0].float(), size[1])
+    g, u = (torch.tensor(v, dtype=torch.float64, device="cuda") for v in ([1.0, gate], [1.0, up]))
+    h = swiglu_of(g, u) * torch.tensor([1.0, weight], device="cuda").double()
+    want = h[idx[:, 0], None] * column.double() * 2.0 ** -20 * I
+    agrees(out, want)
