@@ -557,7 +557,8 @@ ep_status ep_moe_few_tokens_workspace_size(int32_t num_tokens, int32_t hidden, i
  * EP_ERR_UNSUPPORTED; they take the layout, dispatch and combine path):
  *   out[t] = sum over k of topk_weights[t,k] * W2[e] (silu(Wg[e] x[t]) * (Wu[e] x[t]))
  *            + sum over s of shared[s,t],       e = topk_idx[t,k],
- * products and sums in float32, one rounding to bf16 at the end.  Entries of -1 add
+ * products and sums in float32 (of int8 codes, before the row's scale multiplies them), one
+ * rounding to bf16 at the end.  Entries of -1 add
  * nothing (their weight is not read into the sum); other ids outside [0, E) count as -1
  * and set EP_ERR_BAD_EXPERT_ID in *status (may be NULL).
  * x [T, H] bf16; topk_idx [T, K] int64; topk_weights [T, K] float32; w13 [E, 2I, H], the I

@@ -88,5 +88,5 @@ def test_inner_values_of_the_few_token_layer(int8, T, I, gate, up, weight):
     assert int8 or torch.equal(w13[1, :, 0].float(), size[1])
     g, u = (torch.tensor(v, dtype=torch.float64, device="cuda") for v in ([1.0, gate], [1.0, up]))
     h = swiglu_of(g, u) * torch.tensor([1.0, weight], device="cuda").double()
-    want = h[idx[:, 0], None] * column.double() * 2.0 ** -20 * I
-    agrees(out, want)
+    sums = h[idx[:, 0], None] * column.double() * I   # of int8 codes in float32, which the channel's scale then multiplies
+    agrees(out, (sums.float().double() if int8 else sums) * 2.0 ** -20)
