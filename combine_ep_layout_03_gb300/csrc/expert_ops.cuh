@@ -97,7 +97,8 @@ struct MatmulArgs {
 cudaError_t launch_matmul_skinny(const MatmulArgs& a, int sms, cudaStream_t st);
 
 // The segments of a grouped product in shared memory: first row and first token tile of each
-// expert.  Device data is not trusted with addresses: rows are clamped to the buffers'.
+// expert.  Device data is not trusted with addresses: the segments have to ascend inside the buffers'
+// rows, or none is worked on.  (Each inside but overlapping, their tiles could pass 32 bits together.)
 struct Segments {
     int32_t base[kMaxExperts];
     int32_t rows[kMaxExperts];
@@ -105,14 +106,14 @@ struct Segments {
     int32_t warp_sum[32];
 };
 
-// All threads of a CTA of NT threads, kMaxExperts <= 2 NT.  False: the segments need more rows than
-// there are (EP_ERR_CAPACITY is set), and nothing may be written.
+// All threads of a CTA of NT threads, kMaxExperts <= 2 NT.  False: the segments do not ascend from a first one
+// >= 0 (EP_ERR_INVALID_ARG is set) or need more rows than there are (EP_ERR_CAPACITY), and nothing may be written.
 template <int NT>
 __device__ __forceinline__ bool load_segments(Segments& s, const MatmulArgs& a, int tile_rows) {
     static_assert(kMaxExperts <= 2 * NT, "a thread holds two experts");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int tiles[2] = {0, 0};
-    bool fits = true;
+    bool ascend = true, fits = true;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int e = 2 * tid + h;
@@ -121,9 +122,8 @@ __device__ __forceinline__ bool load_segments(Segments& s, const MatmulArgs& a, 
         if (a.expert_base) {
             b = a.expert_base[e];
             end = a.expert_base[e + 1];
+            ascend = ascend && b >= 0 && b <= end;
             fits = fits && end <= a.rows;
-            b = b < 0 ? 0 : b > a.rows ? a.rows : b;
-            end = end < b ? b : end > a.rows ? a.rows : end;
         }
         s.base[e] = (int32_t)b;
         s.rows[e] = (int32_t)(end - b);
@@ -136,15 +136,18 @@ __device__ __forceinline__ bool load_segments(Segments& s, const MatmulArgs& a, 
         if (lane >= o) sum += n;
     }
     if (lane == 31) s.warp_sum[warp] = sum;
-    fits = __syncthreads_and(fits);
+    if (!__syncthreads_and(ascend && fits)) {
+        ascend = __syncthreads_and(ascend);
+        if (tid == 0 && a.status) ep_set_status(a.status, ascend ? EP_ERR_CAPACITY : EP_ERR_INVALID_ARG);
+        return false;
+    }
     for (int w = 0; w < warp; ++w) sum += s.warp_sum[w];
     const int at = sum - tiles[0] - tiles[1];
     if (2 * tid < a.E) s.tile[2 * tid] = at;
     if (2 * tid + 1 < a.E) s.tile[2 * tid + 1] = at + tiles[0];
     if (tid == NT - 1) s.tile[a.E] = sum;
-    if (!fits && tid == 0 && a.status) ep_set_status(a.status, EP_ERR_CAPACITY);
     __syncthreads();
-    return fits;
+    return true;
 }
 
 // The expert that token tile t belongs to (tiles of empty experts do not exist).

@@ -541,8 +541,9 @@ ep_status ep_quant_rows(const void* x, int64_t x_stride, int64_t rows, int32_t h
  * a [rows, k] int8 with a_scales [rows] are receive rows of EP_QUANT_INT8_PER_TOKEN (padding
  * rows have scale 0 and give zeros); w [E, n, k] int8 with w_scales [E, n]; expert_base [E+1]
  * int32 in device memory is the layout's (ep_handle_views), ascending.  `rows` is the capacity
- * of a and out: rows past expert_base[E] are neither read nor written, and if expert_base asks
- * for more than `rows`, nothing is written and *status (may be NULL) gets EP_ERR_CAPACITY.
+ * of a and out: rows past expert_base[E] are neither read nor written.  If expert_base asks for
+ * more than `rows`, or does not ascend from a first one >= 0, nothing is written and *status (may
+ * be NULL) gets EP_ERR_CAPACITY, or EP_ERR_INVALID_ARG.
  * num_experts = 1 with expert_base NULL is a plain matrix product of all rows.
  * k in [16, 65536], a multiple of 16; n in [1, 65536]; E <= 512; a and w 16-byte aligned. */
 ep_status ep_expert_matmul(const void* a, const float* a_scales, int64_t rows, int32_t k, const void* w,

@@ -90,3 +90,23 @@ def test_inner_values_of_the_few_token_layer(int8, T, I, gate, up, weight):
     h = swiglu_of(g, u) * torch.tensor([1.0, weight], device="cuda").double()
     sums = h[idx[:, 0], None] * column.double() * I   # of int8 codes in float32, which the channel's scale then multiplies
     agrees(out, (sums.float().double() if int8 else sums) * 2.0 ** -20)
+
+
+@pytest.mark.parametrize("rows,empty", [(100, 8), (100, 0), (2000, 0)])
+@pytest.mark.parametrize("bases,error", [([0, -5, 50, 100], "order"), ([90, 20, 60, 100], "order"), ([0, 100, 0, 100], "order"),
+                                         ([-1, 10, 20, 100], "order"), ([0, 150, 20, 100], "order"), ([0, 50, 101, 101], "rows"),
+                                         ([0, 0, 0, 101], "rows"), ([3, 3, 40, 100], None)])
+def test_segments_ascend_inside_the_rows(rows, empty, bases, error):
+    """Segments that overlap, or lie outside, are an error: nothing is written.  (Empty experts behind them
+    make rows an expert few, so that the small product's kernel has its turn.)"""
+    f, E = rows // 100, 3 + empty
+    bases = bases + bases[-1:] * empty
+    base = torch.tensor([b * f if b != 101 else rows + 1 for b in bases], dtype=torch.int32, device="cuda")
+    a = torch.ones(rows, 64, dtype=torch.int8, device="cuda")
+    w = torch.ones(E, 32, 64, dtype=torch.int8, device="cuda")
+    out = torch.full((rows, 32), 7.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ep.ep_expert_matmul(a, torch.ones(rows, device="cuda"), w, torch.ones(E, 32, device="cuda"), base, out, status=status)
+    assert status.item() == {None: ep.EP_OK, "order": ep.EP_ERR_INVALID_ARG, "rows": ep.EP_ERR_CAPACITY}[error]
+    first = 3 * f if error is None else rows
+    assert (out[:first] == 7).all() and (out[first:] == 64).all()
