@@ -154,6 +154,114 @@ __device__ __forceinline__ uint4 add_rows(const uint4& x, const uint4& residual)
 
 __device__ __forceinline__ bool finite_bits(uint32_t magnitude) { return magnitude < 0x7f800000u; }
 
+// h of eight columns of a row once more (no register keeps it past the first pass): from h_out, which may have
+// taken an input's place, or from the inputs.  The thread that wrote them there reads them.
+__device__ __forceinline__ uint4 row_again(const RowQuantArgs& a, int64_t row, int vi) {
+    if (a.h_out) return ld_stream_v4(a.h_out + row * a.h_stride + 8 * vi);
+    const uint4 x = ld_stream_v4(a.x + row * a.x_stride + 8 * vi);
+    return a.residual ? add_rows(x, ld_stream_v4(a.residual + row * a.residual_stride + 8 * vi)) : x;
+}
+
+// v in 32 bits for a conversion to 8 or 16 that follows: what the first rounding drops is kept in the last bit,
+// so that the second sees no tie where there is none.
+__device__ __forceinline__ float sticky(double v) {
+    const float f = __double2float_rz(v);
+    return (double)f == v ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
+
+// A row whose squares leave the range of float32 (values from 2^57 on; or, with an eps below 2^-100, values whose
+// mean square is below that too), or that is not finite: all of it in 64 bits, one vector of eight columns at a
+// time.  Such rows are rare; what counts is that the others' registers stay as they are (32768 x 7168 MXFP8: 155 us
+// without this code in the kernel, 158 with it inlined, where nothing else lives past it, 163 with it as a call,
+// 174 as a second pass over values rescaled by a power of two).
+template <int Q>
+__device__ __forceinline__ void wide_row(const RowQuantArgs& a, int64_t row) {
+    using TR = QTraits<Q>;
+    using u64 = unsigned long long;
+    __shared__ double s_sum[32];
+    __shared__ u64 s_max[32];
+    const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = nt >> 5;
+    auto load = [&](int vi, float h[8], double t[8]) {
+        float g[8];
+        unpack8(vi < a.nvec ? row_again(a, row, vi) : make_uint4(0, 0, 0, 0), h);
+        unpack8(vi < a.nvec ? __ldg(reinterpret_cast<const uint4*>(a.gamma) + vi) : make_uint4(0, 0, 0, 0), g);
+        u64 m = 0;   // bits of max|t|, NaN above all
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            t[i] = (double)h[i] * (double)g[i];
+            m = max(m, (u64)__double_as_longlong(fabs(t[i])));
+        }
+        return m;
+    };
+    float h[8];
+    double t[8], s = 0.0;
+    u64 m = 0;
+    for (int vi = tid; vi < a.nvec; vi += nt) {
+        m = max(m, load(vi, h, t));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += (double)h[i] * (double)h[i];
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(kFull, s, o);
+        m = max(m, __shfl_xor_sync(kFull, m, o));
+    }
+    if (lane == 0) { s_sum[warp] = s; s_max[warp] = m; }
+    __syncthreads();
+    s = 0.0;
+    for (int w = 0; w < nwarps; ++w) { s += s_sum[w]; m = max(m, s_max[w]); }
+    const double n = a.H, mean = s / n + (double)a.eps, r = mean == 0.0 ? 0.0 : 1.0 / sqrt(mean);   // zeros and eps 0: y = 0
+    const u64 inf = 0x7ff0000000000000ull;
+    const bool row_ok = (u64)__double_as_longlong(s) < inf;
+    for (int first = 0; first < a.nvec; first += nt) {
+        const int vi = first + tid;
+        u64 bm = load(vi, h, t);
+        if constexpr (TR::token) bm = m;
+        else   // consecutive lanes hold a group or block
+            for (int o = 1; o < (TR::group ? 16 : 4); o <<= 1) bm = max(bm, __shfl_xor_sync(kFull, bm, o));
+        if (vi >= a.nvec) continue;
+        if (a.y_out) {
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = pack_bf16x2_rn(sticky(t[2 * i] * r), sticky(t[2 * i + 1] * r));
+            st_v4(a.y_out + row * a.H + 8 * vi, make_uint4(y[0], y[1], y[2], y[3]));
+        }
+        const bool ok = row_ok && bm < inf;
+        const double mf = __longlong_as_double((long long)bm);
+        int se = -127;
+        if constexpr (TR::mx) {
+            if (ok && bm) {   // floor(log2(m r)): m^2 n >= 4^k (s + n eps) tells a power of two from what is just below
+                int k = ilogb(mf * r);
+                const double lhs = mf * mf * n, rhs = ldexp(s + n * (double)a.eps, 2 * k);
+                if (lhs < rhs) --k;
+                else if (lhs >= 4.0 * rhs) ++k;
+                se = min(max(k - TR::emax, -127), 127);
+            }
+        }
+        uint32_t c[2] = {0, 0};
+        if (ok && bm) {
+            const double up = TR::mx ? r * ldexp(1.0, -se) : 0.0;
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const double q0 = TR::mx ? t[i] * up : t[i] * (double)TR::dmax / mf;
+                const double q1 = TR::mx ? t[i + 1] * up : t[i + 1] * (double)TR::dmax / mf;
+                uint32_t two;
+                if constexpr (Q == M_INT8)
+                    two = ((uint32_t)__double2int_rn(q0) & 0xffu) | (((uint32_t)__double2int_rn(q1) & 0xffu) << 8);
+                else
+                    two = cvt_fp8x2<TR::mx ? Q : TR::fp8>(sticky(q0), sticky(q1));
+                c[i >> 2] |= two << (16 * ((i >> 1) & 1));
+            }
+        }
+        st_v2(a.data + row * a.H + 8 * vi, make_uint2(c[0], c[1]));
+        if constexpr (TR::mx) {
+            if ((vi & 3) == 0) a.scales[row * a.scale_bytes + (vi >> 2)] = (uint8_t)(!ok ? 255 : bm ? se + 127 : 0);
+        } else if (TR::group ? (vi & 15) == 0 : vi == 0) {
+            reinterpret_cast<float*>(a.scales + row * a.scale_bytes)[TR::group ? vi >> 4 : 0] =
+                !ok ? __uint_as_float(0x7fc00000u) : bm ? (float)(mf * r / (double)TR::dmax) : 0.0f;
+        }
+    }
+}
+
 // One CTA per row; thread t holds the 16-byte vectors u * blockDim + t of the row in
 // registers between the barrier and the stores.
 template <int Q, int VPT>
@@ -229,9 +337,14 @@ __global__ void __launch_bounds__(VPT == 4 ? 256 : 1024, VPT == 4 ? 4 : 1) rms_n
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(kFull, s, o));
     if constexpr (TR::token) m = __reduce_max_sync(kFull, from < nwarps ? s_max[from] : 0u);
-    const float n = (float)a.H;
-    const float rstd = rsqrtf(__fmaf_rn(s, a.inv_n, a.eps));
-    const bool row_ok = finite_bits(__float_as_uint(s) & 0x7fffffffu);
+    const float n = (float)a.H, mean = __fmaf_rn(s, a.inv_n, a.eps);
+    // from 2^-100 up to infinity, and not NaN; the same answer in every thread, as the sum is
+    constexpr uint32_t least = 27u << 23, beyond = 0x7f800000u;
+    if (__builtin_expect(__float_as_uint(mean) - least >= beyond - least, 0)) {
+        wide_row<Q>(a, row);
+        return;
+    }
+    const float rstd = rsqrtf(mean);
     const float nan = __uint_as_float(0x7fc00000u);
     uint8_t* data = a.data + row * a.H;
     if (a.y_out) {
@@ -252,7 +365,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 256 : 1024, VPT == 4 ? 4 : 1) rms_n
 
     if constexpr (TR::token) {
         const float mf = __uint_as_float(m);
-        const bool ok = row_ok && finite_bits(m);
+        const bool ok = finite_bits(m);
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
             const int vi = u * nt + tid;
@@ -269,7 +382,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 256 : 1024, VPT == 4 ? 4 : 1) rms_n
 #pragma unroll
             for (int o = 1; o < 16; o <<= 1) gmax = max(gmax, __shfl_xor_sync(kFull, gmax, o));
             const float mf = __uint_as_float(gmax);
-            const bool ok = row_ok && finite_bits(gmax);
+            const bool ok = finite_bits(gmax);
             if (vi < a.nvec) {
                 st_v2(data + 8 * vi, ok && gmax ? encode_ratio<Q>(t[u], mf) : make_uint2(0, 0));
                 if ((vi & 15) == 0)
@@ -293,16 +406,13 @@ __global__ void __launch_bounds__(VPT == 4 ? 256 : 1024, VPT == 4 ? 4 : 1) rms_n
             const uint32_t p = __float_as_uint(__fmul_rn(__uint_as_float(bm[u]), rstd));
             const uint32_t frac = p & 0x7fffffu;
             ex[u] = (p >> 23) == 0 ? -255 : (int)(p >> 23) - 127;
-            near[u] = row_ok && finite_bits(bm[u]) && bm[u] && (frac < 64u || frac > 0x7fffffu - 64u) && ex[u] > -120 && ex[u] < 128;
+            near[u] = finite_bits(bm[u]) && bm[u] && (frac < 64u || frac > 0x7fffffu - 64u) && ex[u] > -120 && ex[u] < 128;
             any = any || near[u];
         }
         if (__syncthreads_or(any)) {
-            // h is read again (no register keeps it until here): from h_out, which may have taken an input's place
             Sum2 e = {0.0f, 0.0f};
-            const uint16_t* again = a.h_out ? a.h_out + row * a.h_stride : x;
             for (int vi = tid; vi < a.nvec; vi += nt) {
-                uint4 h = ld_stream_v4(again + 8 * vi);
-                if (!a.h_out && res) h = add_rows(h, ld_stream_v4(res + 8 * vi));
+                const uint4 h = row_again(a, row, vi);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float h0, h1;
@@ -341,7 +451,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 256 : 1024, VPT == 4 ? 4 : 1) rms_n
 #pragma unroll
             for (int u = 0; u < VPT; ++u) {
                 const int vi = u * nt + tid;
-                const bool ok = row_ok && finite_bits(bm[u]);
+                const bool ok = finite_bits(bm[u]);
                 const int se = min(max(ex[u] - TR::emax, -127), 127);
                 const float mul = __uint_as_float((uint32_t)(127 - se) << 23);   // 2^-se; se = 127 only for values
                                                                                  // that no finite row reaches

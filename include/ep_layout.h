@@ -515,9 +515,10 @@ ep_status ep_step_host(ep_handle* handle, ep_quant_mode quant, const int64_t* to
  * scale = max|y| / top (top 127, 448 or 57344), or the power of two
  * 2^(floor(log2 max|y|) - emax) of 32 columns.  The norm is taken of the rounded h, the
  * row that h_out stores: the result is that of a separate addition.
- * An all-zero row (or group, or block) has zero codes and scale 0 (MX: byte 0).  A row
- * with a NaN or an infinity, or whose sum of squares passes the float32 range, and a
- * group or block whose gamma holds one, gets NaN scales (MX: byte 255) and zero codes.
+ * An all-zero row (or group, or block) has zero codes and scale 0 (MX: byte 0), and its y is 0
+ * also with eps = 0.  A row with a NaN or an infinity, and a group or block whose gamma holds
+ * one (or whose h * gamma passes the float32 range while its squares do not), gets NaN scales
+ * (MX: byte 255) and zero codes.  Squares may leave that range: such a row is taken in 64 bits.
  * x, residual (may be NULL) and h_out (may be NULL) have their own strides between
  * rows, in elements, multiples of 8 and at least `hidden`; x, residual, gamma, h_out, y_out and
  * data are 16-byte aligned, scales 4-byte aligned.  h_out may be x or residual itself
