@@ -26,6 +26,7 @@ import torch
 from . import ep
 
 FEW_TOKENS = 64   # the most that ep_moe_few_tokens takes
+STATUS_WORDS = 1024
 
 
 def _on(stream):
@@ -56,7 +57,7 @@ class ExpertLayer:
         if self.few:
             n = ep.ep_moe_few_tokens_workspace_size(self.N, self.H, self.E, topk, self.I)
             self.workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
-            self._status = torch.zeros(1, dtype=torch.int32, device=dev)
+            self._words, self._word = torch.zeros(STATUS_WORDS, dtype=torch.int32, device=dev), 0
             return
         self.layout = ep.EPLayout(R, T, self.H, self.E, topk, alpha, device=dev)
         cap = self.layout.worst_rows
@@ -84,11 +85,10 @@ class ExpertLayer:
         if shared is not None:
             shared = self._shared_rows(shared, stream)
         if self.few:
-            with _on(stream):
-                self._status.zero_()   # the layout does that on the other way
+            status = self._next_status(stream)   # (the layout clears its own on the other way)
             ep.ep_moe_few_tokens(self.y, topk_idx.view(self.N, self.K), topk_weights.view(self.N, self.K), self.w13,
                                  self.w2, self.out, self.workspace, self.w13_scales, self.w2_scales, shared,
-                                 self._status, stream)
+                                 status, stream)
             return self.out
         lay, q = self.layout, ep.EP_QUANT_INT8_PER_TOKEN
         lay.layout(topk_idx, stream)
@@ -113,9 +113,26 @@ class ExpertLayer:
         with _on(stream):
             return ranks.transpose(0, 1).reshape(-1, self.N, H).contiguous() if self.few else ranks.contiguous()
 
+    def _next_status(self, stream) -> int:
+        """The address of a cleared status word for one step of the few-token way.  To clear one in front of each
+        step would cost 2 to 10 us (28 us for 18 on a small layer, where the host is the bound): steps take words in
+        turn, which are cleared together, and captured steps have the first, cleared in their graphs."""
+        if torch.cuda.is_current_stream_capturing():
+            self._word = 0
+            with _on(stream):
+                self._words[:1].zero_()
+        else:
+            self._word += 1
+            if self._word == STATUS_WORDS:
+                self._word = 1
+                with _on(stream):
+                    self._words[1:].zero_()
+        return self._words.data_ptr() + 4 * self._word
+
     def status(self, stream=None) -> int:
-        """The first device-side error of the last experts() call; waits for ``stream``, the one that it ran on."""
+        """The first device-side error of the last experts() call (a captured one: of its last replay); waits for
+        ``stream``, the one that it ran on."""
         if not self.few:
             return self.layout.status(stream)
         with _on(stream):
-            return int(self._status.item())
+            return int(self._words[self._word].item())

@@ -1,13 +1,15 @@
 """What ExpertLayer hands to the library, on the CPU: its tensors are CPU tensors here, and the
 library's calls are replaced by ones that keep what they are given."""
 import contextlib
+import ctypes
+import random
 
 import pytest
 import torch
 from torch.utils._python_dispatch import TorchDispatchMode
 
 from combine_ep_layout_03_gb300 import ep
-from combine_ep_layout_03_gb300.expert_layer import ExpertLayer
+from combine_ep_layout_03_gb300.expert_layer import STATUS_WORDS, ExpertLayer
 
 E, H, I, K = 4, 64, 16, 2
 
@@ -25,6 +27,7 @@ def make(R, T, few, monkeypatch):
             calls.append((name, args, kw))
         return call
 
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     monkeypatch.setattr(ep, "ep_moe_few_tokens", keep("few"))
     monkeypatch.setattr(ep, "ep_quant_rows", keep("quant_rows"))
     if not few:
@@ -130,23 +133,42 @@ def test_shared_rows_are_reordered_on_the_calls_stream(few, stream, runs_on, mon
     assert copies and set(copies) == {runs_on}
 
 
-def test_status_is_that_of_the_last_step(monkeypatch):
-    """A bad id, a good step, another error: each step's own, cleared in the step's own stream."""
-    layer, _ = make(1, 8, True, monkeypatch)
-    streams = Streams(monkeypatch)
-    error = [0]
+def erring(monkeypatch):
+    """A list whose first entry the next steps of the few-token way leave in their status words."""
+    error = [ep.EP_OK]
 
     def few_tokens(*args):
-        status = args[10]
-        if status.item() == 0:   # the kernels keep the first error
-            status.fill_(error[0])
+        word = ctypes.c_int32.from_address(args[10])
+        if word.value == 0:   # the kernels keep the first error
+            word.value = error[0]
 
     monkeypatch.setattr(ep, "ep_moe_few_tokens", few_tokens)
-    for error[0] in (ep.EP_ERR_BAD_EXPERT_ID, ep.EP_OK, ep.EP_ERR_TIMEOUT, ep.EP_ERR_BAD_EXPERT_ID, ep.EP_OK):
-        for stream in (None, "side"):
+    return error
+
+
+def test_status_is_that_of_the_last_step(monkeypatch):
+    """Bad ids, good steps, other errors, over more steps than there are status words: each step's own."""
+    layer, _ = make(1, 8, True, monkeypatch)
+    streams, error, rng, clears = Streams(monkeypatch), erring(monkeypatch), random.Random(0), []
+    for step in range(2 * STATUS_WORDS + 100):
+        stream = rng.choice([None, "side"])
+        error[0] = rng.choice([ep.EP_OK, ep.EP_OK, ep.EP_ERR_BAD_EXPERT_ID, ep.EP_ERR_TIMEOUT])
+        with streams.writes() as seen:
+            layer.experts(*routing(8), stream=stream)
+        clears += [(step, on == (stream or "current")) for op, on in seen if op is torch.ops.aten.zero_]
+        with streams.writes() as seen:
+            assert layer.status(stream) == error[0]
+        assert seen == [(torch.ops.aten._local_scalar_dense, stream or "current")]
+    assert len(clears) == 2 and all(on_the_steps_stream for _, on_the_steps_stream in clears)
+
+
+def test_captured_steps_clear_their_word_in_the_graph(monkeypatch):
+    layer, _ = make(1, 8, True, monkeypatch)
+    streams, error = Streams(monkeypatch), erring(monkeypatch)
+    for capturing in (False, True, True, False, True):
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+        for error[0] in (ep.EP_ERR_BAD_EXPERT_ID, ep.EP_OK):
             with streams.writes() as seen:
-                layer.experts(*routing(8), stream=stream)
-            assert (torch.ops.aten.zero_, stream or "current") in seen
-            with streams.writes() as seen:
-                assert layer.status(stream) == error[0]
-            assert seen == [(torch.ops.aten._local_scalar_dense, stream or "current")]
+                layer.experts(*routing(8), stream="side")
+            assert [on for op, on in seen if op is torch.ops.aten.zero_] == ["side"] * capturing
+            assert layer.status("side") == error[0]

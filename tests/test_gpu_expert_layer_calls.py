@@ -78,3 +78,21 @@ def test_status_is_that_of_the_last_step(few):
         for routing, want in ((idx, ep.EP_OK), (bad, ep.EP_ERR_BAD_EXPERT_ID), (idx, ep.EP_OK)):
             layer.experts(routing, wts, stream=stream)
             assert layer.status(stream) == want
+
+
+@pytest.mark.parametrize("few", [False, True])
+def test_status_of_a_captured_step_is_that_of_its_last_replay(few):
+    layer, x, idx, wts, _ = make(1, 8, few, seed=5)
+    layer.norm(x)
+    want, routing = layer.experts(idx, wts).clone(), idx.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.experts(routing, wts)
+    for bad, error in ((False, ep.EP_OK), (True, ep.EP_ERR_BAD_EXPERT_ID), (False, ep.EP_OK)):
+        routing.copy_(idx)
+        if bad:
+            routing[3, 1] = layer.E
+        graph.replay()
+        assert layer.status() == error
+    assert torch.equal(layer.out, want)
