@@ -328,13 +328,15 @@ __device__ __forceinline__ bool convert(const Work<C>& w, int warp, int set) {
 }
 
 // silu(gate s0) * (up s1).  The sigmoid is multiplied in before up: where its exponential passes the range the
-// result is 0, however large gate times up would be.  (A gate of -inf gives NaN, the formula's -inf / inf.)
+// result is 0, however large gate times up would be.  (A gate of -inf gives NaN, the formula's -inf / inf.)  It is
+// the reciprocal of a quarter of 1 + exp, which takes none of these below 2^128 for 0, so that the result is the
+// formula's in float32 as far as that goes.
 __device__ __forceinline__ float swiglu(float gate, float up, float s0, float s1) {
     float e, r;
     const float g = gate * s0;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return g * r * (up * s1);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmaf_rn(g, -1.4426950408889634f, -2.0f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(0.25f + e));
+    return g * (0.25f * r) * (up * s1);
 }
 
 // Lane: an output channel; with gates and ups, lanes 0-15 hold the gates of lanes 16-31's ups.

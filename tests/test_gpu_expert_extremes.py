@@ -11,14 +11,15 @@ from combine_ep_layout_03_gb300 import ep
 pytestmark = pytest.mark.gpu
 
 
-def agrees(got, want):
-    """got (bf16) against want (float64 of the float32 formula, where that is finite; else its inf or NaN)."""
+def agrees(got, want, least=0.0):
+    """got (bf16) against want (float64 of the float32 formula, where that is finite; else its inf or NaN).
+    least: half a step of the smallest bf16, where results are that small."""
     got = got.double()
     assert torch.equal(torch.isnan(got), torch.isnan(want))
     inf = torch.isinf(want)
     assert torch.equal(got[inf], want[inf])
     fine = torch.isfinite(want)
-    assert ((got[fine] - want[fine]).abs() <= 2.0 ** -7 * want[fine].abs()).all()
+    assert ((got[fine] - want[fine]).abs() <= 2.0 ** -7 * want[fine].abs() + least).all()
 
 
 def swiglu_of(g, u):
@@ -29,16 +30,17 @@ def swiglu_of(g, u):
 
 
 @pytest.mark.parametrize("rows,experts", [(4, 1), (300, 1), (600, 2), (40, 16)])
-def test_products_with_swiglu(rows, experts):
+@pytest.mark.parametrize("up_scale", [1e-5, 1e-39])   # 1e-39: the largest gates by the smallest ups
+def test_products_with_swiglu(rows, experts, up_scale):
     """Gates and ups of both signs and of 1 to infinity, by each of the kernels that sizes choose."""
     K, half = 128, 72
     sign = torch.where(torch.arange(half, device="cuda") % 2 == 0, 1, -1).to(torch.int8)
     up = torch.where(torch.arange(half, device="cuda") % 3 == 0, 1, -1).to(torch.int8)
     w = torch.cat([sign, up])[None, :, None].expand(experts, 2 * half, K).contiguous()
     sw = torch.ones(experts, 2 * half, device="cuda")
-    sw[:, half:] = 1e-5
+    sw[:, half:] = up_scale
     a = torch.ones(rows, K, dtype=torch.int8, device="cuda")
-    sizes = torch.tensor([2.0 ** -7, 0.25, 1e4, 1e20, 1e23, 1e30, float("inf")], device="cuda")
+    sizes = torch.tensor([2.0 ** -7, 0.25, 1e4, 1e20, 1e23, 1e30, 2e36, float("inf")], device="cuda")
     sa = sizes[torch.arange(rows, device="cuda") % len(sizes)].contiguous()
     out = torch.zeros(rows, half, dtype=torch.bfloat16, device="cuda")
     base = torch.linspace(0, rows, experts + 1).int().cuda() if experts > 1 else None
@@ -46,7 +48,7 @@ def test_products_with_swiglu(rows, experts):
     torch.cuda.synchronize()
     g = K * sa[:, None] * sign.float()
     u = (K * sa[:, None] * up.float()) * sw[0, half:]
-    agrees(out, swiglu_of(g.double(), u.double()))
+    agrees(out, swiglu_of(g.double(), u.double()), 2.0 ** -134)
 
 
 @pytest.mark.parametrize("int8", [False, True])
@@ -110,3 +112,24 @@ def test_segments_ascend_inside_the_rows(rows, empty, bases, error):
     assert status.item() == {None: ep.EP_OK, "order": ep.EP_ERR_INVALID_ARG, "rows": ep.EP_ERR_CAPACITY}[error]
     first = 3 * f if error is None else rows
     assert (out[:first] == 7).all() and (out[first:] == 64).all()
+
+
+@pytest.mark.parametrize("rows,experts", [(4, 1), (300, 1), (600, 2), (40, 16)])
+def test_gates_far_below_zero(rows, experts):
+    """Where the sigmoid is near the smallest normal number and the ups are large: products of 1e-6 or so, the
+    same of each kernel.  (exp is within 2^-16: 88 log2 e is rounded to float32.)"""
+    K, half = 128, 40
+    gates = torch.linspace(-88.6, -80, rows, device="cuda")
+    a = torch.ones(rows, K, dtype=torch.int8, device="cuda")
+    w = torch.ones(experts, 2 * half, K, dtype=torch.int8, device="cuda")
+    sw = torch.ones(experts, 2 * half, device="cuda")
+    sw[:, half:] = -1e28
+    sa = (gates / K).contiguous()
+    out = torch.zeros(rows, half, dtype=torch.bfloat16, device="cuda")
+    base = torch.linspace(0, rows, experts + 1).int().cuda() if experts > 1 else None
+    ep.ep_expert_matmul(a, sa, w, sw, base, out, swiglu=True)
+    torch.cuda.synchronize()
+    g = (K * sa.double())[:, None].expand(rows, half)
+    want = g / (1 + torch.exp(-g)) * (g * sw[0, half:].double())
+    assert (want.abs() > 1e-8).all()
+    agrees(out, want)
