@@ -114,13 +114,11 @@ class ExpertLayer:
             return ranks.transpose(0, 1).reshape(-1, self.N, H).contiguous() if self.few else ranks.contiguous()
 
     def _next_status(self, stream) -> int:
-        """The address of a cleared status word for one step of the few-token way.  To clear one in front of each
-        step would cost 2 to 10 us (28 us for 18 on a small layer, where the host is the bound): steps take words in
-        turn, which are cleared together, and captured steps have the first, cleared in their graphs."""
+        """The address of the status word of one step of the few-token way.  To clear it in front of each step would
+        cost 2 to 10 us (28 us for 18 on a small layer, where the host is the bound): steps take words in turn, which
+        are cleared together, and captured ones share the first, which status() clears."""
         if torch.cuda.is_current_stream_capturing():
             self._word = 0
-            with _on(stream):
-                self._words[:1].zero_()
         else:
             self._word += 1
             if self._word == STATUS_WORDS:
@@ -130,9 +128,12 @@ class ExpertLayer:
         return self._words.data_ptr() + 4 * self._word
 
     def status(self, stream=None) -> int:
-        """The first device-side error of the last experts() call (a captured one: of its last replay); waits for
-        ``stream``, the one that it ran on."""
+        """The first device-side error of the last experts() call; waits for ``stream``, the one that it ran on.  Of
+        captured calls: of the replays since the last status() (few tokens), or of the last replay."""
         if not self.few:
             return self.layout.status(stream)
         with _on(stream):
-            return int(self._words[self._word].item())
+            error = int(self._words[self._word].item())
+            if error and self._word == 0:
+                self._words[:1].zero_()
+            return error

@@ -162,13 +162,21 @@ def test_status_is_that_of_the_last_step(monkeypatch):
     assert len(clears) == 2 and all(on_the_steps_stream for _, on_the_steps_stream in clears)
 
 
-def test_captured_steps_clear_their_word_in_the_graph(monkeypatch):
+def test_replays_of_captured_steps_report_each_error_once(monkeypatch):
     layer, _ = make(1, 8, True, monkeypatch)
-    streams, error = Streams(monkeypatch), erring(monkeypatch)
-    for capturing in (False, True, True, False, True):
-        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
-        for error[0] in (ep.EP_ERR_BAD_EXPERT_ID, ep.EP_OK):
-            with streams.writes() as seen:
-                layer.experts(*routing(8), stream="side")
-            assert [on for op, on in seen if op is torch.ops.aten.zero_] == ["side"] * capturing
-            assert layer.status("side") == error[0]
+    streams, error, replay = Streams(monkeypatch), erring(monkeypatch), []
+    bad = error[0] = ep.EP_ERR_BAD_EXPERT_ID
+    layer.experts(*routing(8))
+    assert layer.status() == bad
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    monkeypatch.setattr(ep, "ep_moe_few_tokens", lambda *args, keep=ep.ep_moe_few_tokens: replay.append(lambda: keep(*args)))
+    with streams.writes() as seen:
+        layer.experts(*routing(8), stream="side")
+    assert not seen   # nothing but the layer's kernels in the graph
+    for errors, want in (((ep.EP_OK,), ep.EP_OK), ((bad,), bad), ((ep.EP_OK,), ep.EP_OK), ((bad, ep.EP_OK), bad),
+                         ((ep.EP_ERR_TIMEOUT, bad), ep.EP_ERR_TIMEOUT), ((ep.EP_OK,), ep.EP_OK)):
+        for error[0] in errors:
+            replay[0]()
+        with streams.writes() as seen:
+            assert layer.status("side") == want
+        assert all(on == "side" for _, on in seen)

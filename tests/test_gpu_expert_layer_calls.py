@@ -81,7 +81,7 @@ def test_status_is_that_of_the_last_step(few):
 
 
 @pytest.mark.parametrize("few", [False, True])
-def test_status_of_a_captured_step_is_that_of_its_last_replay(few):
+def test_status_of_a_captured_step_is_that_of_its_replays(few):
     layer, x, idx, wts, _ = make(1, 8, few, seed=5)
     layer.norm(x)
     want, routing = layer.experts(idx, wts).clone(), idx.clone()
