@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_inner_ke
         }
         if (kBuffers == 1) __syncthreads();
     }
-    if (!ring.drain() && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
+    if (!ring.ok() && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
 }
 
 // The CTAs of a cluster (or one) own `rows` <= 16 columns of the output at a time (tiles tile, tile +
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<W8, MAXNT>::ctas) few_out_kern
         }
         __syncthreads();
     }
-    if (!ring.drain() && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
+    if (!ring.ok() && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
 }
 
 // Warps that share a tile of few_inner_kernel.  All eight keep the most CTAs busy where there are few

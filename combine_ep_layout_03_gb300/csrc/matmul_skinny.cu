@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 2) matmul_skinny_kernel(const Matmul
             a.out[row * outs + ch] = (uint16_t)pack_bf16x2_rn(v, 0.0f);
         }
     }
-    if (!ring.drain() && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
+    if (!ring.ok() && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
 }
 
 // Few enough rows and weights for the kernel above.  Its loop reads weights at about 3 TB/s for up to

@@ -10,20 +10,19 @@
 #define EP_PLACES inline
 #endif
 
-// A ring of DEPTH slots, filled by asynchronous copies and read in the same order.  issue(slot) starts the copy
-// into a slot; wait(slot, parity) is a bounded wait for it, false when it gave up.  After one that gave up no
-// copy is started, none is taken for read, and drain() waits once more for just those that are in flight.
+// A ring of DEPTH slots, filled by asynchronous copies and read in the same order, every one of them.  issue(slot)
+// starts the copy into a slot; wait(slot, parity) is a bounded wait for it, false when it gave up.  Where one gives
+// up, take() waits once more for it and for the others in flight there and then; no copy is started, and none
+// waited for, after that.  So nothing is in flight once all have been taken, unless a copy outlasts two waits.
 template <int DEPTH>
 struct RingPlaces {
-    int put_slot = 0, take_slot = 0, flying = 0;
+    int put_slot = 0, take_slot = 0;
     uint32_t parity = 0;
-    bool ok = true;
+    bool ok = true;   // no wait gave up
 
     template <class Issue>
     EP_PLACES void put(Issue issue) {
-        if (!ok) return;
-        issue(put_slot);
-        ++flying;
+        if (ok) issue(put_slot);
         put_slot = put_slot + 1 == DEPTH ? 0 : put_slot + 1;
     }
 
@@ -31,23 +30,17 @@ struct RingPlaces {
     template <class Wait>
     EP_PLACES int take(Wait wait) {
         const int slot = take_slot;
-        ok = ok && wait(slot, parity);
-        if (ok) next();
-        return slot;
-    }
-
-    // Nothing is in flight afterwards, unless a copy was not over after two waits.  False: a wait gave up.
-    template <class Wait>
-    EP_PLACES bool drain(Wait wait) {
-        while (flying > 0) {
-            ok = wait(take_slot, parity) && ok;
-            next();
+        const bool arrived = !ok || wait(slot, parity);
+        if (!arrived) {
+            int late = slot;
+            uint32_t of = parity;
+            do {
+                wait(late, of);
+                if (++late == DEPTH) { late = 0; of ^= 1; }
+            } while (late != put_slot);
+            ok = false;
         }
-        return ok;
-    }
-
-    EP_PLACES void next() {
-        --flying;
         if (++take_slot == DEPTH) { take_slot = 0; parity ^= 1; }
+        return slot;
     }
 };

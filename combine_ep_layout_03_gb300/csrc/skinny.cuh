@@ -47,8 +47,7 @@ __device__ __forceinline__ void int8x4_to_bf16(uint32_t w, uint32_t& lo, uint32_
 // ring keeps running through the barriers and sums between one unit of work and the next.
 // (cp.async in 16-byte chunks, and loads to registers, reach two thirds of the rate: what arrives
 // in 32-byte sectors is written to shared memory or registers a sector at a time, 20 accesses for
-// 512 bytes.)  Every wait is bounded; after one that gave up nothing more is loaded, and drain()
-// waits again for what is in flight.
+// 512 bytes.)  Every wait is bounded; ring_places.cuh says what happens after one that gave up.
 template <int DEPTH>
 struct WeightRing {
     static constexpr int kSlot = 2048, kWarpBytes = DEPTH * kSlot;
@@ -89,10 +88,8 @@ struct WeightRing {
         }
     }
 
-    // Nothing is in flight when the CTA ends.  False: a wait gave up.
-    __device__ __forceinline__ bool drain() {
-        return places.drain([&](int slot, uint32_t parity) { return wait(slot, parity); });
-    }
+    // False: a wait gave up.
+    __device__ __forceinline__ bool ok() const { return places.ok; }
 
     // The same answer in all lanes.
     __device__ __forceinline__ bool wait(int slot, uint32_t parity) {
