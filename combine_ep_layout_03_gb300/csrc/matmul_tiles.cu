@@ -327,16 +327,17 @@ __device__ __forceinline__ bool convert(const Work<C>& w, int warp, int set) {
     return ok;
 }
 
-// silu(gate s0) * (up s1).  The sigmoid is multiplied in before up: where its exponential passes the range the
-// result is 0, however large gate times up would be.  (A gate of -inf gives NaN, the formula's -inf / inf.)  It is
-// the reciprocal of a quarter of 1 + exp, which takes none of these below 2^128 for 0, so that the result is the
-// formula's in float32 as far as that goes.
-__device__ __forceinline__ float swiglu(float gate, float up, float s0, float s1) {
+// silu(gate s0) * (up s1), of quarter = s1 / 4.  Up is multiplied by the sigmoid first: where its exponential passes
+// the range the result is 0, however large gate times up would be.  (A gate of -inf gives NaN, the formula's
+// -inf / inf.)  The reciprocal of a quarter of 1 + exp is not yet one of the numbers that are taken for 0, so the
+// result is the formula's in float32 as far as that goes.  The approximations are within 2^-22, and the exponent's
+// rounding within 2^-17 where the sigmoid is smallest; the output's is 2^-8.
+__device__ __forceinline__ float swiglu(float gate, float up, float s0, float quarter) {
     float e, r;
     const float g = gate * s0;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmaf_rn(g, -1.4426950408889634f, -2.0f)));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(0.25f + e));
-    return g * (0.25f * r) * (up * s1);
+    return g * (r * (up * quarter));
 }
 
 // Lane: an output channel; with gates and ups, lanes 0-15 hold the gates of lanes 16-31's ups.
@@ -355,7 +356,7 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp, float* scal
                        (GLU ? lane & 15 : lane);
         const bool in = ch < outs;
         const float* sw = w.a.w_scales + (int64_t)t.expert * w.a.N + (in ? ch : 0);
-        const float s0 = sw[0], s1 = GLU ? sw[outs] : 0.0f;
+        const float s0 = sw[0], quarter = GLU ? 0.25f * sw[outs] : 0.0f;   // of the ups' scale
         for (int c = lane; c < t.n; c += 32) scales[c] = c < t.m ? w.a.a_scales[t.row0 + c] : 0.0f;
         __syncwarp();
         if (!warp_wait(&w.sh.acc_full[acc.stage], acc.parity)) return false;
@@ -373,7 +374,7 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp, float* scal
                 for (int i = 0; i < 32; i += 2) {
                     const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(odd ? v[i] : v[i + 1]), 16);
                     const float s = scales[c0 + i + odd];
-                    y[i / 2] = swiglu((odd ? other : __uint_as_float(v[i])) * s, (odd ? __uint_as_float(v[i + 1]) : other) * s, s0, s1);
+                    y[i / 2] = swiglu((odd ? other : __uint_as_float(v[i])) * s, (odd ? __uint_as_float(v[i + 1]) : other) * s, s0, quarter);
                 }
                 if (wide) {
                     // neighbours trade as below: an even lane stores its pair of channels of token
