@@ -14,13 +14,13 @@
 // Sums run in a fixed order (warps take fixed pieces, their partial sums are added in
 // warp order): results do not vary from run to run.
 //
-// Measured (both kernels): 64 tokens over 512 experts of 4096 x 512, bf16: 835 us, 6.5 TB/s (0.95 of
-// the copy bandwidth); 16 tokens over 128 experts of 4096 x 1024: 314 us, 6.5 TB/s; one token 39 us,
+// Measured (both kernels): 64 tokens over 512 experts of 4096 x 512, bf16: 865 us, 6.45 TB/s (0.95 of
+// the copy bandwidth); 16 tokens over 128 experts of 4096 x 1024: 316 us, 6.6 TB/s; one token 39 us,
 // 5.1 TB/s, of which about 9 us are the two starts.  int8 weights are bound by instruction issue,
 // most of it their conversion: 8 tokens of 256 experts of 7168 x 1024 233 us, 5.3 TB/s;
 // one token of 128 experts of 4096 x 1024 33 us, 3.1 TB/s.  Many tokens on few experts are bound by
 // the token values' way from L2, each time for 16 weight rows: 64 tokens over 8 experts of 4096 x 1024,
-// bf16, 64 us by two and 135 us by eight (the weights' bytes are 30).
+// bf16, 69 us by two and 139 us by eight (the weights' bytes are 30).
 #include <algorithm>
 
 #include "expert_ops.cuh"
@@ -104,7 +104,7 @@ __device__ __forceinline__ float routing_weight(const FewArgs& a, int token, int
 // Sizes of both kernels by weight type and largest number of token tiles.
 //   ctas     CTAs of an SM; what the routing and the sums leave of its shared memory goes to the rings (depth).
 //   early    token parts that are asked for before the weights of their piece are waited for.  64 tokens, bf16,
-//            over 8 experts by two: 64 us with 3, 68 with 4 (spills), 69 with 2, 96 with none.
+//            over 8 experts by two: 64 us with 3, 68 with 4 (spills), 69 with 2, 96 with none, in one run.
 //   prefetch whether with one token tile those of the next piece are loaded under this one's products.  It
 //            helps bf16 weights (64 tokens over 512 experts: 914 us with, 1015 us without); int8 weights
 //            need the registers for their conversion and gain more from other warps (8 tokens of 256 experts:

@@ -5,9 +5,9 @@
 // 32 rows of one expert: the warps of a CTA share the item's k and add their parts in
 // shared memory, in warp order.  The codes become bf16 on the way to the tensor cores,
 // which is exact, and a product of two codes is exact in float32; sums stay exact up to
-// 2^24 (1040 terms of the largest size, any number of ordinary ones).
+// 2^24 (1024 terms of the largest size, any number of ordinary ones).
 //
-// Measured: 8 rows x 4096 x 4096 7.0 us (its floor, 17 MB, is 2.5 us); 32 rows 12.7 us.  What bounds
+// Measured: 8 rows x 4096 x 4096 7.0 us (its floor, 17 MB, is 2.5 us); 32 rows 12.9 us.  What bounds
 // it is a warp's start, its first loads and its few pieces one after another; the host takes 5.1 us a call.
 #include "expert_ops.cuh"
 #include "skinny.cuh"

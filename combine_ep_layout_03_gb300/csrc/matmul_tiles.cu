@@ -24,10 +24,10 @@
 // from its wait to its arrival takes several times as long as the MMAs of a stage).  Every wait is
 // bounded (EP_ERR_TIMEOUT).
 //
-// Measured: 8192^3 622 us, 1767 TFLOP/s (0.91 of the measured float16 rate); 32 experts of 1152 rows,
-// 4096 x 2048, 366 us, 1690 TFLOP/s, with SwiGLU 371 us; a 64-k step takes some 500 clocks where its
+// Measured: 8192^3 614 us, 1791 TFLOP/s (0.93 of the measured float16 rate); 32 experts of 1152 rows,
+// 4096 x 2048, 366 us, 1690 TFLOP/s, with SwiGLU 385 us (both by the box, 359 to 382 and 374 to 403); a 64-k step takes some 500 clocks where its
 // MMAs take 384, with shared memory about 0.9 busy.  Thin segments read weights: 8 rows for each of 512
-// experts, 4096 x 1024, 319 us, 6.8 TB/s (1.00 of the copy bandwidth).  One tile of 128 rows takes 15 us
+// experts, 4096 x 1024, 324 us, 6.7 TB/s (0.99 of the copy bandwidth).  One tile of 128 rows takes 15 us
 // at k = 4096.
 #include "expert_ops.cuh"
 #include "tcgen05.cuh"

@@ -18,10 +18,14 @@
 // stores, and normalising exactly it makes the result the same whether the addition
 // was fused or not.
 //
-// Measured, against the copy bandwidth: 65536 x 4096 int8 with a residual 269 us, 1.03; without one
-// 146 us, 0.82; 32768 x 7168 MXFP8 without one 154 us, 0.68 (with: 237 us, 1.03); 1237 x 7168 in
-// groups, with one, 14 us, 0.66 (8.1 rows an SM).  With a residual the bytes bound it; without one
-// instructions do (more or fewer resident rows make it slower; issue slots are half busy).
+// Scales are float32 products of a float32 root, off by a few 2^-24 (41 at most; 5e-8 in the norm).
+//
+// Measured, against the copy bandwidth: 65536 x 4096 int8 with a residual 269 us, 1.03 (and with y_out 344 us,
+// 1.03); without one 144 us, 0.82; 32768 x 7168 MXFP8 without one 158 us, 0.67 (with: 240 us, 1.03); 1237 x 7168
+// in groups, with one, 14.2 us, 0.65 (8.1 rows an SM).  With a residual the bytes bound it.  Without one it is
+// instructions: issue slots are 0.71 busy (int8) and 0.68 (MXFP8, whose ALU pipe is 0.62), DRAM 0.65 and 0.52;
+// what is missing to full is a row's loads, sum and barrier one after another, with 0.40 to 0.45 of the warps
+// that an SM holds.  More or fewer resident rows make it slower.
 #include <type_traits>
 
 #include "expert_ops.cuh"
@@ -76,7 +80,8 @@ __device__ __forceinline__ float max_abs3(float m, f32x2 v) {
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// Sum of float32 values with its rounding error carried along: about 48 bits.
+// Sum of float32 values with its rounding error carried along (Knuth's two-term sum, and the compensated summation
+// of Ogita, Rump and Oishi): about 48 bits.
 struct Sum2 { float hi, lo; };
 
 __device__ __forceinline__ void sum2_add(Sum2& s, float hi, float lo) {
@@ -107,7 +112,8 @@ __device__ __forceinline__ uint4 ld_stream_v4(const void* p) {   // not .nc: h_o
 }
 
 // Codes of 8 values t with largest magnitude m (finite, > 0) at TOP: the divisor is
-// brought near 1 by a power of two (exact), so that t * top cannot overflow.
+// brought near 1 by a power of two (exact), so that t * top cannot overflow.  The quotient is corrected by its
+// remainder, which an FMA gives exactly (Markstein).
 template <int Q>
 __device__ __forceinline__ uint2 encode_ratio(const f32x2 t[4], float m) {
     constexpr float top = QTraits<Q>::dmax;
@@ -443,7 +449,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 256 : 1024, VPT == 4 ? 4 : 1) rms_n
         // t r as one rounding, from the root and its remainder: the 8-bit codes then differ from those of the real
         // numbers about as seldom as any rounding to float32 before them allows (some 50 of 90 million; with the
         // root alone, off by up to two steps, and a product rounded again the error of a whole output was up to
-        // twice that; 32768 x 7168 took 148 us then and takes 154 now).
+        // twice that; 32768 x 7168 took 148 us so, and 154 like this).
         const float rest = rsqrt_remainder(rstd, s, n, a.inv_n, a.eps);
         // The power of two of a block goes into the root, unless some values are so far from 1 that it
         // would leave the range.

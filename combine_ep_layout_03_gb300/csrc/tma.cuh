@@ -5,7 +5,8 @@
 // registers: a load signals an mbarrier with the bytes it delivered
 // (complete_tx), a store joins a bulk group that is committed and waited for
 // by the issuing thread.  Addresses must be 16-byte aligned and sizes
-// multiples of 16 bytes.  No cluster multicast is used anywhere.
+// multiples of 16 bytes.  No load is multicast to a cluster (the arrivals of
+// the tensor cores' commits are, tcgen05.cuh).
 #pragma once
 
 #include <stdint.h>

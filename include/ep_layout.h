@@ -537,7 +537,8 @@ ep_status ep_quant_rows(const void* x, int64_t x_stride, int64_t rows, int32_t h
 /* Device.  The 8-bit integer product of expert rows: for every row r of expert e's segment
  * [expert_base[e], expert_base[e+1])
  *   c[r,n] = a_scales[r] * w_scales[e,n] * sum_k a[r,k] * w[e,n,k],
- * sums in float32 (exact while they stay within 2^24), rounded once to bf16:
+ * sums in float32 (exact while they stay within 2^24, as 1024 terms of the largest codes do;
+ * past that an addition is off by up to 2^-23 of the sum so far), rounded once to bf16:
  *   out [rows, n] = c,  or with swiglu = 1 (n even)  out [rows, n/2] = silu(c[:, :n/2]) * c[:, n/2:].
  * a [rows, k] int8 with a_scales [rows] are receive rows of EP_QUANT_INT8_PER_TOKEN (padding
  * rows have scale 0 and give zeros); w [E, n, k] int8 with w_scales [E, n]; expert_base [E+1]
