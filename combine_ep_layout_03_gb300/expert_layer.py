@@ -111,7 +111,7 @@ class ExpertLayer:
         if ranks is None or shared.dtype is not torch.bfloat16:
             raise ep.EPError(ep.EP_ERR_INVALID_ARG, "shared: bf16 [R, S, T, H] or [S, N, H]")
         with _on(stream):
-            return ranks.transpose(0, 1).reshape(-1, self.N, H).contiguous() if self.few else ranks.contiguous()
+            return ranks.transpose(0, 1).reshape(ranks.shape[1], self.N, H).contiguous() if self.few else ranks.contiguous()
 
     def _next_status(self, stream) -> int:
         """The address of the status word of one step of the few-token way.  To clear it in front of each step would

@@ -180,3 +180,11 @@ def test_replays_of_captured_steps_report_each_error_once(monkeypatch):
         with streams.writes() as seen:
             assert layer.status("side") == want
         assert all(on == "side" for _, on in seen)
+
+
+@pytest.mark.parametrize("R,T,S", [(1, 0, 2), (2, 0, 2), (2, 4, 0)])
+def test_no_tokens_or_no_shared_rows(R, T, S, monkeypatch):
+    layer, calls = make(R, T, True, monkeypatch)
+    for shared in (torch.zeros(R, S, T, H, dtype=torch.bfloat16), torch.zeros(S, R * T, H, dtype=torch.bfloat16)):
+        layer.experts(*routing(R * T), shared)
+        assert shared_of(calls, True).shape == (S, R * T, H)
