@@ -108,8 +108,8 @@ struct Segments {
 
 // All threads of a CTA of NT threads, kMaxExperts <= 2 NT.  False: the segments do not ascend from a first one
 // >= 0 (EP_ERR_INVALID_ARG is set) or need more rows than there are (EP_ERR_CAPACITY), and nothing may be written.
-template <int NT>
-__device__ __forceinline__ bool load_segments(Segments& s, const MatmulArgs& a, int tile_rows) {
+template <int NT, class Args>
+__device__ __forceinline__ bool load_segments(Segments& s, const Args& a, int tile_rows) {
     static_assert(kMaxExperts <= 2 * NT, "a thread holds two experts");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int tiles[2] = {0, 0};

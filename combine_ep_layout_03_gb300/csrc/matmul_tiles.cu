@@ -32,6 +32,7 @@
 #include "expert_ops.cuh"
 #include "tcgen05.cuh"
 #include "tensor_maps.cuh"
+#include "expert_tiles.cuh"
 
 namespace {
 
@@ -82,37 +83,6 @@ struct Shared {
     uint32_t tmem;
 };
 
-struct Tile { int64_t row0; int expert, m, n, channel; };   // n: MMA columns, channel: tile of output channels
-
-// Tiles of one expert are neighbours, its token tiles fastest: concurrent pairs share weights and tokens in L2.
-// The roles look tiles up between one tile's work and the next, so it has to be quick: a whole warp goes on from
-// its last expert, 32 experts at a time, and all counts are 32 bits wide (32 experts of 1152 rows, 1024 x 4096:
-// 217 us, with a binary search and 64-bit quotients 233; 512 experts of 8 rows, 4096 x 1024: 319, 331).
-// A single thread searches anew.
-template <class C, bool WARP>
-__device__ __forceinline__ Tile tile_of(const Segments& s, const MatmulArgs& a, int ctiles, int item, int& e) {
-    const int at = (int)((uint32_t)item / (uint32_t)ctiles);
-    if (WARP) {
-        for (int n = 32; n == 32; e += n)
-            n = __popc(__ballot_sync(0xffffffffu, s.tile[min(e + 1 + (int)(threadIdx.x & 31), a.E)] <= at));
-    } else {
-        e = expert_of_tile(s, a.E, at);
-    }
-    const uint32_t tiles = s.tile[e + 1] - s.tile[e];
-    const uint32_t local = item - s.tile[e] * ctiles;
-    // the segment's groups of 32 rows dealt out evenly: no tile is much shorter, and none pays for a row more
-    const int groups = (s.rows[e] + 31) / 32, j = (int)(local % tiles), each = (int)((uint32_t)groups / tiles);
-    const int more = groups - each * (int)tiles;
-    const int first = 32 * (j * each + min(j, more));
-    Tile t;
-    t.expert = e;
-    t.row0 = (int64_t)s.base[e] + first;
-    t.m = min(32 * (each + (j < more)), s.rows[e] - first);
-    t.n = (t.m + 31) / 32 * 32;
-    t.channel = (int)(local / tiles);
-    return t;
-}
-
 // Two of the bytes of w (each a code + 128) as float16: 0x64xx is 1024 + xx.
 template <uint32_t SEL>
 __device__ __forceinline__ uint32_t bytes_to_f16x2(uint32_t w) {
@@ -141,24 +111,6 @@ __device__ __forceinline__ void sts_at(uint32_t addr, uint32_t a, uint32_t b, ui
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// A ring position: stage and parity of use i.
-template <int STAGES>
-struct Ring {
-    int stage = 0;
-    uint32_t parity = 0;
-    __device__ __forceinline__ void next() {
-        if (++stage == STAGES) { stage = 0; parity ^= 1; }
-    }
-    __device__ __forceinline__ void back() {
-        if (stage-- == 0) { stage = STAGES - 1; parity ^= 1; }
-    }
-};
-
-// A warp's wait, the same answer in all lanes.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait_parked(bar, parity));
-}
-
 // What every role of a CTA knows.
 template <class C>
 struct Work {
@@ -179,7 +131,7 @@ __device__ __forceinline__ bool load_tiles(const Work<C>& w, const CUtensorMap* 
     int expert = 0;
     bool ok = true;
     for (int item = w.first; ok && item < w.items; item += w.step) {
-        const Tile t = tile_of<C, false>(w.sh.seg, w.a, w.ctiles, item, expert);
+        const Tile t = tile_of<false>(w.sh.seg, w.a.E, w.ctiles, item, expert);
         // token rows in one box where the tile is full, else in boxes of 32
         const int half = t.n / 2, boxes = (half + kBoxTokens - 1) / kBoxTokens;
         const int ch = t.channel * w.per_pair + (int)w.cta * (GLU ? kRows / 2 : kRows);
@@ -222,7 +174,7 @@ __device__ __forceinline__ bool issue_mma(const Work<C>& w) {
     bool ready = false, ok = true;
     int expert = 0;
     for (int item = w.first; ok && item < w.items; item += w.step, acc.next()) {
-        const Tile t = tile_of<C, true>(w.sh.seg, w.a, w.ctiles, item, expert);
+        const Tile t = tile_of<true>(w.sh.seg, w.a.E, w.ctiles, item, expert);
         const uint32_t idesc = mma_desc_f16(2 * kRows, t.n);
         if (!warp_wait(&w.sh.acc_empty[acc.stage], acc.parity ^ 1)) { ok = false; break; }
         tmem_fence_after();
@@ -279,7 +231,7 @@ __device__ __forceinline__ bool convert(const Work<C>& w, int warp, int set) {
     int expert = 0;
     bool ok = true;
     for (int item = w.first; ok && item < w.items; item += w.step) {
-        const int rows = tile_of<C, true>(w.sh.seg, w.a, w.ctiles, item, expert).n / 2 - warp * 8;
+        const int rows = tile_of<true>(w.sh.seg, w.a.E, w.ctiles, item, expert).n / 2 - warp * 8;
         for (int k = 0; ok && k < w.raws; ++k, use += 2 / C::halves, r.next()) {
             if (use % kSets != (uint32_t)set) continue;
             const uint32_t stage = use % C::cvt_stages, parity = (use / C::cvt_stages) & 1;
@@ -327,19 +279,6 @@ __device__ __forceinline__ bool convert(const Work<C>& w, int warp, int set) {
     return ok;
 }
 
-// silu(gate s0) * (up s1), of quarter = s1 / 4.  Up is multiplied by the sigmoid first: where its exponential passes
-// the range the result is 0, however large gate times up would be.  (A gate of -inf gives NaN, the formula's
-// -inf / inf.)  The reciprocal of a quarter of 1 + exp is not yet one of the numbers that are taken for 0, so the
-// result is the formula's in float32 as far as that goes.  The approximations are within 2^-22, and the exponent's
-// rounding within 2^-17 where the sigmoid is smallest; the output's is 2^-8.
-__device__ __forceinline__ float swiglu(float gate, float up, float s0, float quarter) {
-    float e, r;
-    const float g = gate * s0;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmaf_rn(g, -1.4426950408889634f, -2.0f)));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(0.25f + e));
-    return g * (r * (up * quarter));
-}
-
 // Lane: an output channel; with gates and ups, lanes 0-15 hold the gates of lanes 16-31's ups.
 template <class C, bool GLU>
 __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp, float* scales) {
@@ -351,7 +290,7 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp, float* scal
     Ring<2> acc;
     int expert = 0;
     for (int item = w.first; item < w.items; item += w.step, acc.next()) {
-        const Tile t = tile_of<C, true>(w.sh.seg, w.a, w.ctiles, item, expert);
+        const Tile t = tile_of<true>(w.sh.seg, w.a.E, w.ctiles, item, expert);
         const int ch = t.channel * w.per_pair + (int)w.cta * (GLU ? kRows / 2 : kRows) + warp * (GLU ? 16 : 32) +
                        (GLU ? lane & 15 : lane);
         const bool in = ch < outs;

@@ -115,6 +115,8 @@ def _load():
         "ep_rms_norm_quant": ([vp, i64, vp, i64, vp, ctypes.c_float, i64, i32, st, vp, i64, vp, vp, vp, vp], st),
         "ep_quant_rows": ([vp, i64, i64, i32, st, vp, vp, vp], st),
         "ep_expert_matmul": ([vp, vp, i64, i32, vp, vp, i32, i32, vp, i32, vp, vp, vp], st),
+        "ep_swiglu_keep": ([vp, vp, i64, i32, vp, vp, vp, vp, vp], st),
+        "ep_swiglu_keep_grad": ([vp, vp, vp, vp, i64, i32, vp, vp, vp, vp, vp], st),
         "ep_moe_few_tokens_workspace_size": ([i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)], st),
         "ep_moe_few_tokens": ([vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp,
                                ctypes.c_size_t, vp, vp], st),
@@ -457,6 +459,65 @@ def ep_expert_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w
                                  base, 1 if swiglu else 0, out.data_ptr(), _ptr(status), _stream(stream))
     if code:
         _check(code, "ep_expert_matmul")
+
+
+def _rows_used(rows_used):
+    if rows_used is None:
+        return None
+    if rows_used.dtype is not torch.int32 or rows_used.numel() != 1:
+        raise EPError(EP_ERR_INVALID_ARG, "rows_used: int32 [1]")
+    return rows_used.data_ptr()
+
+
+def _keep_rows(shape, rows_of_inner, codes, scales, row_weights, what: str) -> None:
+    """The checks that ep_swiglu_keep and its gradient share; shape: of the rows [g, u]."""
+    rows, width = shape
+    bad = None
+    for t, name in rows_of_inner:
+        if t is not None and (t.dtype is not torch.bfloat16 or not t.is_contiguous() or t.shape != (rows, width // 2)):
+            bad = name + ": bf16 [rows, I]"
+    if width % 256 != 0:
+        bad = what + ": [rows, 2I], I a multiple of 128"
+    elif codes.element_size() != 1 or not codes.is_contiguous() or codes.shape != shape:
+        bad = "codes: e4m3 [rows, 2I]"
+    elif not scales.is_contiguous() or scales.nbytes != 4 * rows * (width // 128):
+        bad = "scales: float32 [rows, 2I / 128]"
+    elif row_weights is not None and (row_weights.dtype is not torch.float32 or not row_weights.is_contiguous()
+                                      or row_weights.numel() != rows):
+        bad = "row_weights: float32 [rows]"
+    if bad:
+        raise EPError(EP_ERR_INVALID_ARG, bad)
+
+
+def ep_swiglu_keep(c: torch.Tensor, inner: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, row_weights=None,
+                   rows_used=None, stream=None) -> None:
+    """inner = row_weights * silu(g) * u of bf16 rows c [rows, 2I] = [g, u], and c in 8 bits for the backward pass:
+    codes [rows, 2I] (e4m3, or bytes) and scales [rows, 2I / 128] float32 (or bytes).  rows_used: int32 [1] on the
+    device, how many of the rows hold anything (None: all)."""
+    if len(c.shape) != 2 or c.dtype is not torch.bfloat16 or not c.is_contiguous():
+        raise EPError(EP_ERR_INVALID_ARG, "c: bf16 [rows, 2I]")
+    _keep_rows(c.shape, ((inner, "inner"),), codes, scales, row_weights, "c")
+    code = _lib.ep_swiglu_keep(c.data_ptr(), _ptr(row_weights), c.shape[0], c.shape[1] // 2, _rows_used(rows_used),
+                               inner.data_ptr(), codes.data_ptr(), scales.data_ptr(), _stream(stream))
+    if code:
+        _check(code, "ep_swiglu_keep")
+
+
+def ep_swiglu_keep_grad(codes: torch.Tensor, scales: torch.Tensor, grad_inner: torch.Tensor, grad_c: torch.Tensor,
+                        inner=None, row_weights=None, row_weights_grad=None, rows_used=None, stream=None) -> None:
+    """The backward pass of ep_swiglu_keep from its codes and scales: grad_c [rows, 2I] bf16 of grad_inner [rows, I]
+    bf16, and, where given, inner [rows, I] as the codes have it and row_weights_grad [rows] float32."""
+    if len(grad_c.shape) != 2 or grad_c.dtype is not torch.bfloat16 or not grad_c.is_contiguous():
+        raise EPError(EP_ERR_INVALID_ARG, "grad_c: bf16 [rows, 2I]")
+    _keep_rows(grad_c.shape, ((grad_inner, "grad_inner"), (inner, "inner")), codes, scales, row_weights, "grad_c")
+    if row_weights_grad is not None and (row_weights_grad.dtype is not torch.float32 or not row_weights_grad.is_contiguous()
+                                         or row_weights_grad.numel() != grad_c.shape[0]):
+        raise EPError(EP_ERR_INVALID_ARG, "row_weights_grad: float32 [rows]")
+    code = _lib.ep_swiglu_keep_grad(codes.data_ptr(), scales.data_ptr(), _ptr(row_weights), grad_inner.data_ptr(),
+                                    grad_c.shape[0], grad_c.shape[1] // 2, _rows_used(rows_used), grad_c.data_ptr(),
+                                    _ptr(inner), _ptr(row_weights_grad), _stream(stream))
+    if code:
+        _check(code, "ep_swiglu_keep_grad")
 
 
 def ep_moe_few_tokens_workspace_size(T: int, H: int, E: int, K: int, I: int) -> int:

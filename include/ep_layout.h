@@ -552,6 +552,28 @@ ep_status ep_expert_matmul(const void* a, const float* a_scales, int64_t rows, i
                            const float* w_scales, int32_t n, int32_t num_experts, const int32_t* expert_base,
                            int32_t swiglu, void* out, int32_t* status, ep_stream_t stream);
 
+/* Device.  SwiGLU in training, between an expert's two products: rows [g, u] of c [rows, 2 * inner_size] bf16 give
+ *   inner [rows, inner_size] = bf16(w_r * silu(g) * u)
+ * and, for the backward pass, codes and scales of c in the receive-row format of EP_QUANT_FP8_E4M3_PER_GROUP:
+ * codes [rows, 2 * inner_size] e4m3 nearest to c / scale, ties to even, scales [rows, 2 * inner_size / 128] = max|c| /
+ * 448 of 128 columns.  row_weights [rows] float32 (NULL: 1): the routing weight of a row's token, multiplied in here,
+ * so that the combine is a plain sum.  A group of zeros has scale 0; one that holds a NaN or an infinity has a NaN
+ * scale and zero codes.  rows_used (device int32, NULL: all): rows from there on are neither read nor written
+ * (expert_base + E of a layout).  inner_size in [128, 65536], a multiple of 128; 16-byte aligned data, 4-byte
+ * aligned scales; rows * inner_size / 128 < 2^31; no output may overlap an input. */
+ep_status ep_swiglu_keep(const void* c, const float* row_weights, int64_t rows, int32_t inner_size,
+                         const int32_t* rows_used, void* inner, void* codes, float* scales, ep_stream_t stream);
+
+/* Device.  Its backward pass, from the codes: with g, u = codes * scale, dy = grad_inner [rows, inner_size] bf16 and
+ * s = 1 / (1 + exp(-g)),
+ *   grad_c [rows, 2 * inner_size] = bf16 of [w_r dy u s (1 + g (1 - s)), w_r dy g s],
+ *   inner [rows, inner_size] = bf16(w_r g s u)      (NULL: not written; the next product's weights' gradient reads it),
+ *   grad_row_weights [rows] = sum dy g s u          (float32; NULL: not written).
+ * The rest as for ep_swiglu_keep. */
+ep_status ep_swiglu_keep_grad(const void* codes, const float* scales, const float* row_weights, const void* grad_inner,
+                              int64_t rows, int32_t inner_size, const int32_t* rows_used, void* grad_c, void* inner,
+                              float* grad_row_weights, ep_stream_t stream);
+
 /* Host only: bytes of the workspace of ep_moe_few_tokens. */
 ep_status ep_moe_few_tokens_workspace_size(int32_t num_tokens, int32_t hidden, int32_t num_experts, int32_t topk,
                                            int32_t inner, size_t* bytes);
