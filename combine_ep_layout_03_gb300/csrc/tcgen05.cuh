@@ -105,6 +105,25 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
                  :: "r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(smem_addr(bar)) : "memory");
 }
 
+// The same with the bytes reported to a barrier of either CTA of the pair (bar: its cluster address).
+__device__ __forceinline__ void tma_pair_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3}], [%4];"
+                 :: "r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tma_pair_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4}], [%5];"
+                 :: "r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tma_pair_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int u, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4, %5}], [%6];"
+                 :: "r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar) : "memory");
+}
+
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t columns) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
                  :: "r"(smem_addr(slot)), "r"(columns) : "memory");
@@ -158,6 +177,24 @@ __device__ __forceinline__ void mma_pair_f16(uint32_t d, uint32_t a, uint64_t b,
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
                  "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
                  :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
+}
+
+// MN-major operand of 16-bit values, 128-byte swizzle: rows of 64 of them, one for each k, groups of eight k 1024
+// bytes apart and the next 64 of M or N `next` bytes further on.
+__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t addr, uint32_t next) {
+    return (uint64_t)((addr >> 4) & 0x3fffu) | ((uint64_t)(next >> 4) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// float32 accumulators, both operands bf16, each K-major or MN-major, M x N of the pair.
+constexpr uint32_t mma_desc_bf16(uint32_t m, uint32_t n, bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T over both CTAs of the pair; one thread of the leader.
+__device__ __forceinline__ void mma_pair_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
 }
 
 // Arrive on `bar` in both CTAs once this thread's MMAs so far have completed.

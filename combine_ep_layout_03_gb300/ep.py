@@ -115,6 +115,9 @@ def _load():
         "ep_rms_norm_quant": ([vp, i64, vp, i64, vp, ctypes.c_float, i64, i32, st, vp, i64, vp, vp, vp, vp], st),
         "ep_quant_rows": ([vp, i64, i64, i32, st, vp, vp, vp], st),
         "ep_expert_matmul": ([vp, vp, i64, i32, vp, vp, i32, i32, vp, i32, vp, vp, vp], st),
+        "ep_expert_matmul_bf16": ([vp, i64, i32, vp, i32, i32, vp, i32, vp, vp, vp], st),
+        "ep_expert_matmul_grad_rows": ([vp, i64, i32, vp, i32, i32, vp, vp, vp, vp], st),
+        "ep_expert_matmul_grad_weights": ([vp, vp, i64, i32, i32, i32, vp, i32, i32, vp, vp, vp], st),
         "ep_swiglu_keep": ([vp, vp, i64, i32, vp, vp, vp, vp, vp], st),
         "ep_swiglu_keep_grad": ([vp, vp, vp, vp, i64, i32, vp, vp, vp, vp, vp], st),
         "ep_moe_few_tokens_workspace_size": ([i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)], st),
@@ -459,6 +462,70 @@ def ep_expert_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w
                                  base, 1 if swiglu else 0, out.data_ptr(), _ptr(status), _stream(stream))
     if code:
         _check(code, "ep_expert_matmul")
+
+
+def _base_ptr(expert_base, E: int):
+    """The address of expert_base: int32 [E + 1], or None of one matrix."""
+    if expert_base is None:
+        if E != 1:
+            raise EPError(EP_ERR_INVALID_ARG, "expert_base: int32 [E + 1]")
+        return None
+    if expert_base.dtype is not torch.int32 or not expert_base.is_contiguous() or expert_base.numel() != E + 1:
+        raise EPError(EP_ERR_INVALID_ARG, "expert_base: int32 [E + 1]")
+    return expert_base.data_ptr()
+
+
+def _bf16_rows(t: torch.Tensor, shape, what: str) -> None:
+    if t.dtype is not torch.bfloat16 or not t.is_contiguous() or t.shape != shape:
+        raise EPError(EP_ERR_INVALID_ARG, what)
+
+
+def ep_expert_matmul_bf16(a: torch.Tensor, w: torch.Tensor, expert_base, out: torch.Tensor, swiglu: bool = False,
+                          status=None, stream=None) -> None:
+    """bf16 rows times bf16 expert matrices: a [rows, K], w [E, N, K], expert_base int32 [E + 1] on the device (None:
+    one matrix), out bf16 [rows, N], or [rows, N / 2] = silu(gates) * ups with swiglu."""
+    _require(len(a.shape) == 2 and len(w.shape) == 3, "a: bf16 [rows, K], w: bf16 [E, N, K]")
+    rows, K = a.shape
+    E, N, _ = w.shape
+    _bf16_rows(a, (rows, K), "a: bf16 [rows, K]")
+    _bf16_rows(w, (E, N, K), "w: bf16 [E, N, K]")
+    _bf16_rows(out, (rows, N // 2 if swiglu else N), "out: bf16 [rows, N], or [rows, N / 2] with swiglu")
+    code = _lib.ep_expert_matmul_bf16(a.data_ptr(), rows, K, w.data_ptr(), N, E, _base_ptr(expert_base, E), 1 if swiglu else 0,
+                                      out.data_ptr(), _ptr(status), _stream(stream))
+    if code:
+        _check(code, "ep_expert_matmul_bf16")
+
+
+def ep_expert_matmul_grad_rows(grad_c: torch.Tensor, w: torch.Tensor, expert_base, grad_a: torch.Tensor, status=None,
+                               stream=None) -> None:
+    """The gradient of the rows of ep_expert_matmul_bf16: grad_a [rows, K] = grad_c [rows, N] times each expert's w."""
+    _require(len(grad_c.shape) == 2 and len(w.shape) == 3, "grad_c: bf16 [rows, N], w: bf16 [E, N, K]")
+    rows, N = grad_c.shape
+    E, _, K = w.shape
+    _bf16_rows(grad_c, (rows, N), "grad_c: bf16 [rows, N]")
+    _bf16_rows(w, (E, N, K), "w: bf16 [E, N, K]")
+    _bf16_rows(grad_a, (rows, K), "grad_a: bf16 [rows, K]")
+    code = _lib.ep_expert_matmul_grad_rows(grad_c.data_ptr(), rows, N, w.data_ptr(), K, E, _base_ptr(expert_base, E),
+                                           grad_a.data_ptr(), _ptr(status), _stream(stream))
+    if code:
+        _check(code, "ep_expert_matmul_grad_rows")
+
+
+def ep_expert_matmul_grad_weights(grad_c: torch.Tensor, a: torch.Tensor, expert_base, grad_w: torch.Tensor,
+                                  accumulate: bool = False, status=None, stream=None) -> None:
+    """The gradient of the weights of ep_expert_matmul_bf16: grad_w [E, N, K], bf16 or float32, = grad_c^T a over each
+    expert's rows, or, with accumulate (float32 only), added to what grad_w holds."""
+    _require(len(grad_c.shape) == 2 and len(a.shape) == 2 and len(grad_w.shape) == 3, "grad_c, a: bf16 rows, grad_w: [E, N, K]")
+    (rows, N), K, E = grad_c.shape, a.shape[1], grad_w.shape[0]
+    _bf16_rows(grad_c, (rows, N), "grad_c: bf16 [rows, N]")
+    _bf16_rows(a, (rows, K), "a: bf16 [rows, K]")
+    if grad_w.dtype not in (torch.bfloat16, torch.float32) or not grad_w.is_contiguous() or grad_w.shape != (E, N, K):
+        raise EPError(EP_ERR_INVALID_ARG, "grad_w: bf16 or float32 [E, N, K]")
+    code = _lib.ep_expert_matmul_grad_weights(grad_c.data_ptr(), a.data_ptr(), rows, N, K, E, _base_ptr(expert_base, E),
+                                              1 if grad_w.dtype is torch.float32 else 0, 1 if accumulate else 0,
+                                              grad_w.data_ptr(), _ptr(status), _stream(stream))
+    if code:
+        _check(code, "ep_expert_matmul_grad_weights")
 
 
 def _rows_used(rows_used):

@@ -552,6 +552,30 @@ ep_status ep_expert_matmul(const void* a, const float* a_scales, int64_t rows, i
                            const float* w_scales, int32_t n, int32_t num_experts, const int32_t* expert_base,
                            int32_t swiglu, void* out, int32_t* status, ep_stream_t stream);
 
+/* Device.  The same of bf16 rows and weights without scales (receive rows of EP_QUANT_NONE):
+ *   c[r,n] = sum_k a[r,k] * w[e,n,k],
+ * sums in float32, rounded once to bf16.  a [rows, k], w [E, n, k], out [rows, n], or [rows, n / 2] with
+ * swiglu = 1.  k in [8, 65536], a multiple of 8; n in [1, 65536]; the rest as for ep_expert_matmul. */
+ep_status ep_expert_matmul_bf16(const void* a, int64_t rows, int32_t k, const void* w, int32_t n, int32_t num_experts,
+                                const int32_t* expert_base, int32_t swiglu, void* out, int32_t* status,
+                                ep_stream_t stream);
+
+/* Device.  Its gradients.  With grad_c [rows, n] bf16, the gradient of c (not of the SwiGLU's result, whose gradient
+ * is ep_swiglu_keep_grad), for the rows r of expert e's segment
+ *   grad_a[r,k] = sum_n grad_c[r,n] * w[e,n,k]                        (bf16 [rows, k]),
+ *   grad_w[e,n,k] = sum over the segment's r of grad_c[r,n] * a[r,k]  (bf16 or float32 [E, n, k]),
+ * sums in float32.  grad_w of an expert without rows is zeros.  float32_out = 1 writes float32; accumulate = 1, which
+ * needs float32_out, adds to what grad_w holds (an expert without rows is left as it is).  Rows outside the
+ * segments take no part, whatever they hold.
+ * n and k multiples of 8, in [8, 65536]; grad_c, a, w 16-byte aligned, grad_a and grad_w 4-byte aligned;
+ * segments and errors as for ep_expert_matmul.  With rows = 0, grad_w is written all the same. */
+ep_status ep_expert_matmul_grad_rows(const void* grad_c, int64_t rows, int32_t n, const void* w, int32_t k,
+                                     int32_t num_experts, const int32_t* expert_base, void* grad_a, int32_t* status,
+                                     ep_stream_t stream);
+ep_status ep_expert_matmul_grad_weights(const void* grad_c, const void* a, int64_t rows, int32_t n, int32_t k,
+                                        int32_t num_experts, const int32_t* expert_base, int32_t float32_out,
+                                        int32_t accumulate, void* grad_w, int32_t* status, ep_stream_t stream);
+
 /* Device.  SwiGLU in training, between an expert's two products: rows [g, u] of c [rows, 2 * inner_size] bf16 give
  *   inner [rows, inner_size] = bf16(w_r * silu(g) * u)
  * and, for the backward pass, codes and scales of c in the receive-row format of EP_QUANT_FP8_E4M3_PER_GROUP:

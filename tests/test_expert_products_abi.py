@@ -59,3 +59,63 @@ def test_binding_refuses_wrong_rows_to_keep():
     refused(ep.ep_swiglu_keep_grad, good, shared + [
         dict(grad_inner=f(4, 256)), dict(grad_inner=f(3, 256, dtype=bf)), dict(grad_c=f(4, 512)), dict(inner=f(4, 512, dtype=bf)),
         dict(grad_c=f(4, 1024, dtype=bf)[:, ::2]), dict(row_weights_grad=f(3)), dict(row_weights_grad=f(4, dtype=bf))])
+
+
+def product(a=A, rows=100, k=256, w=B, n=64, E=8, base=C, swiglu=0, out=D, status=None):
+    return ep.lib.ep_expert_matmul_bf16(a, rows, k, w, n, E, base, swiglu, out, status, None)
+
+
+def grad_rows(dc=A, rows=100, n=64, w=B, k=256, E=8, base=C, out=D, status=None):
+    return ep.lib.ep_expert_matmul_grad_rows(dc, rows, n, w, k, E, base, out, status, None)
+
+
+def grad_weights(dc=A, a=B, rows=100, n=64, k=256, E=8, base=C, wide=0, add=0, out=D, status=None):
+    return ep.lib.ep_expert_matmul_grad_weights(dc, a, rows, n, k, E, base, wide, add, out, status, None)
+
+
+SEGMENTS = [dict(rows=-1), dict(rows=(1 << 31) - 1), dict(k=0), dict(k=-8), dict(k=252), dict(k=65544), dict(n=0), dict(n=65537),
+            dict(E=0), dict(E=513), dict(base=None), dict(base=C + 2), dict(status=C + 2), dict(out=None), dict(out=D + 1)]
+
+
+@pytest.mark.parametrize("kw", SEGMENTS + [dict(a=None), dict(a=A + 8), dict(w=None), dict(w=B + 8), dict(n=63, swiglu=1), dict(swiglu=2)])
+def test_product_refuses(kw):
+    assert product(**kw) == ep.EP_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", SEGMENTS + [dict(dc=None), dict(dc=A + 8), dict(w=None), dict(w=B + 8), dict(n=60), dict(n=4), dict(out=D + 2)])
+def test_grad_rows_refuses(kw):
+    assert grad_rows(**kw) == ep.EP_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", SEGMENTS + [dict(dc=None), dict(dc=A + 8), dict(a=None), dict(a=B + 8), dict(n=60), dict(n=4), dict(wide=2),
+                                           dict(add=2, wide=1), dict(out=D + 2)])
+def test_grad_weights_refuses(kw):
+    assert grad_weights(**kw) == ep.EP_ERR_INVALID_ARG
+
+
+def test_sums_of_weights_gradients_are_float32():
+    assert grad_weights(add=1) == ep.EP_ERR_UNSUPPORTED
+
+
+def test_products_of_no_rows():
+    assert product(rows=0, a=None, out=None) == ep.EP_OK
+    assert grad_rows(rows=0, dc=None, out=None) == ep.EP_OK
+
+
+def test_binding_refuses_wrong_products():
+    f, bf, i4 = torch.zeros, torch.bfloat16, torch.int32
+    base = [dict(expert_base=None), dict(expert_base=f(3, dtype=i4)), dict(expert_base=f(4, dtype=torch.int64)),
+            dict(expert_base=f(8, dtype=i4)[::2])]
+    good = dict(a=f(4, 64, dtype=bf), w=f(3, 32, 64, dtype=bf), expert_base=f(4, dtype=i4), out=f(4, 32, dtype=bf))
+    refused(ep.ep_expert_matmul_bf16, good, base + [
+        dict(a=f(4, 64)), dict(a=f(64, 4, dtype=bf).t()), dict(a=f(64, dtype=bf)), dict(a=f(4, 128, dtype=bf)[:, ::2]), dict(w=f(3, 32, 64)),
+        dict(w=f(3, 32, 48, dtype=bf)), dict(w=f(32, 64, dtype=bf)), dict(w=f(3, 64, 32, dtype=bf).transpose(1, 2)), dict(out=f(4, 32)),
+        dict(out=f(4, 16, dtype=bf)), dict(out=f(3, 32, dtype=bf)), dict(swiglu=True)])
+    good = dict(grad_c=f(4, 32, dtype=bf), w=good["w"], expert_base=good["expert_base"], grad_a=f(4, 64, dtype=bf))
+    refused(ep.ep_expert_matmul_grad_rows, good, base + [
+        dict(grad_c=f(4, 32)), dict(grad_c=f(4, 16, dtype=bf)), dict(grad_c=f(32, 4, dtype=bf).t()), dict(w=f(3, 32, 64)),
+        dict(grad_a=f(4, 32, dtype=bf)), dict(grad_a=f(4, 64)), dict(grad_a=f(3, 64, dtype=bf))])
+    good = dict(grad_c=good["grad_c"], a=f(4, 64, dtype=bf), expert_base=good["expert_base"], grad_w=f(3, 32, 64, dtype=bf))
+    refused(ep.ep_expert_matmul_grad_weights, good, base + [
+        dict(grad_c=f(3, 32, dtype=bf)), dict(a=f(4, 64)), dict(a=f(64, 4, dtype=bf).t()), dict(grad_w=f(3, 32, 64, dtype=torch.float16)),
+        dict(grad_w=f(3, 64, 32, dtype=bf)), dict(grad_w=f(32, 64, dtype=bf)), dict(grad_w=f(3, 64, 32, dtype=bf).transpose(1, 2))])
