@@ -1,0 +1,392 @@
+// matmul_fp8.cu -- the FP8 product of expert rows with a scale for each block of 128, on the tensor cores:
+//   c[r, n] = sum over blocks b of 128 k:  a_scales[r, b] w_scales[e, n / 128, b] * sum_{k in b} a[r, k] w[e, n, k]
+//
+// The scales are float32 and change with every block of k, so no instruction can apply them: the sum of a block is
+// taken by tcgen05.mma kind::f8f6f4 into a fresh accumulator in tensor memory, and warps read it, multiply it by the
+// two scales and add it to sums in registers, while the next block's products go into another accumulator.
+// Tokens are the M operand: a thread has a token (a lane of tensor memory), so that a block costs it one scale, one
+// product of scales for each 128 channels, and half a packed FMA for each value.
+//
+// Tiles: 256 rows by 256 channels a pair of CTAs (cta_group::2, 512 clocks of products a block, of which the FMAs take
+// half), for segments of many rows; 128 rows by 128 channels, or fewer, a CTA otherwise.  With SwiGLU half of the
+// channels are gates and half their ups, and a thread has both.  A finished row leaves a thread's registers through a
+// row of shared memory of its own, by a bulk copy.
+//
+// Warps: epilogue first (four a CTA's 128 rows, or twice four, each with half of the channels), then TMA and MMA.  Every
+// wait is bounded (EP_ERR_TIMEOUT).
+#include "expert_ops.cuh"
+#include "expert_tiles.cuh"
+#include "row_codes.cuh"
+#include "tcgen05.cuh"
+#include "tensor_maps.cuh"
+
+namespace {
+
+struct Fp8Args {
+    const float* a_scales;       // [rows][blocks]
+    const float* w_scales;       // [E][wblocks][blocks]
+    const int32_t* expert_base;  // [E + 1] first row of each expert, or null: all rows belong to one matrix
+    int32_t* status;             // or null
+    uint16_t* out;               // [rows][outs] bf16
+    int64_t rows;
+    int32_t E;
+    int32_t outs;                // n, or n / 2 with swiglu
+    int32_t blocks;              // of 128 k
+    int32_t wblocks;             // of 128 rows of a matrix (with swiglu: of the gates, then of the ups)
+};
+
+constexpr int kBoxTokens = 32;   // rows of a small token box
+constexpr int kPart = 64;        // output columns that a thread stages at a time
+constexpr int kPitch = kPart * 2 + 16;   // bytes of its row there: 16 more than the row, so that lanes meet different banks
+
+// CTAS: of a tile; ROWS: token rows of a CTA that there is room for; N: channels of a tile; STAGES: of 128 k;
+// ACCS: accumulators in tensor memory.
+template <int CTAS, int ROWS, int N, int STAGES, int ACCS>
+struct Config {
+    static constexpr int ctas = CTAS, rows = ROWS, tile = CTAS * ROWS, n = N, stages = STAGES, accs = ACCS;
+    static constexpr int channels = N / CTAS;              // whose weights a CTA loads
+    static constexpr int groups = N > 128 ? 2 : 1;         // of four epilogue warps
+    static constexpr int width = N / groups;               // accumulators of a thread
+    static constexpr int load_warp = 4 * groups, mma_warp = load_warp + 1;
+    static constexpr int threads = groups == 2 ? 320 : 256;
+    static constexpr int bytes_a = ROWS * 128, bytes = bytes_a + channels * 128;
+    static constexpr int staged = 128 * groups * kPitch;
+    static constexpr int smem = 1024 + STAGES * bytes + staged;
+    static constexpr uint32_t columns = ACCS * N;
+    static_assert(columns <= 512 && (columns & (columns - 1)) == 0 && columns >= 32, "tensor memory");
+    static_assert(bytes_a % 1024 == 0 && bytes % 1024 == 0 && width % 32 == 0 && width <= 128, "swizzled rows; registers");
+    // an MMA reads 128 token rows, also where a stage has room for fewer: what follows is read for them, inside shared memory
+    static_assert(bytes - bytes_a + staged >= (128 - ROWS) * 128, "rows past a stage's");
+};
+
+using Thick = Config<2, 128, 256, 5, 2>;
+using Mid = Config<1, 128, 128, 6, 4>;
+using Thin = Config<1, 32, 128, 9, 4>;
+using Small = Config<1, 32, 32, 20, 8>;
+
+template <class C>
+struct Shared {
+    Segments seg;
+    uint64_t full[C::stages], empty[C::stages];   // full: of the tile's first CTA
+    uint64_t acc_full[C::accs], acc_empty[C::accs];
+    uint64_t drained;
+    uint32_t tmem;
+};
+
+template <class C>
+struct Work {
+    const Fp8Args& a;
+    Shared<C>& sh;
+    uint8_t* smem;      // stages: token rows, then weight rows
+    uint8_t* staged;    // a row of kPitch bytes for each epilogue thread
+    uint32_t tmem, cta;
+    int per_tile, ctiles;   // output channels of a tile, tiles of them
+    int first, items, step;
+};
+
+template <class C>
+__device__ __forceinline__ void load_rows(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t* own) {
+    if constexpr (C::ctas == 2) tma_pair_2d(dst, map, x, y, bar);
+    else tma_load_2d(dst, map, x, y, own);
+}
+
+template <class C>
+__device__ __forceinline__ void load_weights(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar, uint64_t* own) {
+    if constexpr (C::ctas == 2) tma_pair_3d(dst, map, x, y, z, bar);
+    else tma_load_3d(dst, map, x, y, z, own);
+}
+
+// map_w: matrices of weights (with SwiGLU the gates and the ups are one each); map_a, map_all: token rows in boxes of 32,
+// or of all that a stage has room for.
+template <class C, bool GLU>
+__device__ __forceinline__ bool load_tiles(const Work<C>& w, const CUtensorMap* map_w, const CUtensorMap* map_a, const CUtensorMap* map_all) {
+    Ring<C::stages> r;
+    const uint32_t full0 = cluster_addr(smem_addr(&w.sh.full[0]), 0);
+    int used = 0, expert = 0;   // used: stages filled so far, at most all
+    bool ok = true;
+    for (int item = w.first; ok && item < w.items; item += w.step) {
+        const Tile t = tile_of<false>(w.sh.seg, w.a.E, w.ctiles, item, expert);
+        const int mine = t.n / C::ctas, boxes = (mine + kBoxTokens - 1) / kBoxTokens;
+        const int bytes = C::channels * 128 + boxes * kBoxTokens * 128;
+        const int ch = t.channel * w.per_tile, row = (int)t.row0 + (int)w.cta * mine;
+        for (int k = 0; k < w.a.blocks; ++k, r.next()) {
+            if (!mbar_wait_parked(&w.sh.empty[r.stage], r.parity ^ 1)) { ok = false; break; }
+            uint8_t* dst = w.smem + r.stage * C::bytes;
+            uint64_t* own = &w.sh.full[r.stage];
+            const uint32_t bar = full0 + r.stage * 8;
+            if (w.cta == 0) mbar_arrive_expect_tx(own, C::ctas * bytes);
+            if constexpr (!GLU) {
+                load_weights<C>(dst + C::bytes_a, map_w, k * 128, ch + (int)w.cta * C::channels, t.expert, bar, own);
+            } else if constexpr (C::ctas == 2) {
+                load_weights<C>(dst + C::bytes_a, map_w, k * 128, ch, 2 * t.expert + (int)w.cta, bar, own);
+            } else {
+                load_weights<C>(dst + C::bytes_a, map_w, k * 128, ch, 2 * t.expert, bar, own);
+                load_weights<C>(dst + C::bytes_a + C::channels * 64, map_w, k * 128, ch, 2 * t.expert + 1, bar, own);
+            }
+            if (boxes == C::rows / kBoxTokens) {
+                load_rows<C>(dst, map_all, k * 128, row, bar, own);
+            } else {
+                for (int b = 0; b < boxes; ++b) load_rows<C>(dst + b * kBoxTokens * 128, map_a, k * 128, row + b * kBoxTokens, bar, own);
+            }
+            used = min(used + 1, C::stages);
+        }
+    }
+    // every load has arrived and been used when its stage is free again: none is in flight when the CTA ends (also
+    // when a wait gave up, here or elsewhere: a wait of seconds has passed since the last load then)
+    bool over = true;
+    for (int i = 0; over && i < used; ++i) {
+        r.back();
+        over = mbar_wait_parked(&w.sh.empty[r.stage], r.parity);
+    }
+    return ok && over;
+}
+
+template <class C>
+__device__ __forceinline__ bool issue_mma(const Work<C>& w) {
+    Ring<C::stages> r;
+    Ring<C::accs> acc;
+    const uint32_t smem0 = smem_addr(w.smem), idesc = mma_desc_e4m3(128 * C::ctas, C::n);
+    bool ready = false, ok = true;
+    int expert = 0;
+    for (int item = w.first; ok && item < w.items; item += w.step) {
+        for (int k = 0; k < w.a.blocks; ++k) {
+            if (!warp_wait(&w.sh.acc_empty[acc.stage], acc.parity ^ 1) ||
+                (!ready && !warp_wait(&w.sh.full[r.stage], r.parity))) { ok = false; break; }
+            tmem_fence_after();
+            const uint32_t at = smem0 + r.stage * C::bytes, d = w.tmem + acc.stage * C::n;
+            const uint64_t a = smem_desc_k128(at), b = smem_desc_k128(at + C::bytes_a);
+            uint64_t *const empty = &w.sh.empty[r.stage], *const full = &w.sh.acc_full[acc.stage];
+            r.next();
+            acc.next();
+            ready = __all_sync(0xffffffffu, mbar_test(&w.sh.full[r.stage], r.parity));
+            if (elect_one()) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mma_f8_ss<C::ctas>(d, a + 2 * j, b + 2 * j, idesc, j > 0);
+                commit_all<C::ctas>(empty);
+                commit_all<C::ctas>(full);
+            }
+            __syncwarp();
+        }
+    }
+    // no MMA is left when the CTAs part, also when a wait gave up
+    if (elect_one()) commit_own<C::ctas>(&w.sh.drained);
+    __syncwarp();
+    return warp_wait(&w.sh.drained, 0) && ok;
+}
+
+// 64 columns (or COLS) of a thread's row, in bf16 pairs, to out + row * outs + col.  Each thread has a row of shared memory of its own,
+// and nobody else reads it but its bulk copy; where rows are not whole 16 bytes, the warp writes its rows one by one.
+template <int COLS>
+__device__ __forceinline__ void store_part(const uint32_t y[COLS / 2], uint8_t* mine, uint16_t* row, int cols, bool in, bool bulk) {
+    const int lane = threadIdx.x & 31;
+    bulk_wait_read<0>();   // of the part before
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < COLS / 8; ++i) sts_v4(smem_addr(mine) + 16 * i, y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+    if (bulk) {
+        fence_proxy_async_smem();
+        if (in && cols > 0) bulk_store(row, mine, 2 * min(cols, COLS));
+        bulk_commit();
+        return;
+    }
+    __syncwarp();
+    const uint32_t warp_rows = smem_addr(mine) - lane * kPitch;
+    for (int r = 0; r < 32; ++r) {
+        uint16_t* to = (uint16_t*)__shfl_sync(0xffffffffu, (unsigned long long)row, r);
+        if (!__shfl_sync(0xffffffffu, (int)in, r)) continue;
+        for (int c = lane; c < min(cols, COLS); c += 32) {
+            uint16_t v;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(warp_rows + r * kPitch + 2 * c) : "memory");
+            to[c] = v;
+        }
+    }
+}
+
+template <class C, bool GLU>
+__device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
+    constexpr int kWidth = C::width, kHalf = kWidth / 2;
+    const int lane = threadIdx.x & 31, quarter = warp & 3, group = warp >> 2, mine_row = quarter * 32 + lane;
+    const uint32_t acc_empty0 = cluster_addr(smem_addr(&w.sh.acc_empty[0]), 0);
+    uint8_t* const mine = w.staged + (group * 128 + mine_row) * kPitch;
+    const int outs = w.a.outs, blocks = w.a.blocks;
+    const bool bulk = outs % 8 == 0 && ((uintptr_t)w.a.out & 15) == 0;
+    Ring<C::accs> acc;
+    int expert = 0;
+    bool ok = true;
+    for (int item = w.first; ok && item < w.items; item += w.step) {
+        const Tile t = tile_of<true>(w.sh.seg, w.a.E, w.ctiles, item, expert);
+        const int each = t.n / C::ctas, rows = min(each, t.m - (int)w.cta * each);   // this CTA's (perhaps none)
+        const bool some = quarter * 32 < rows, in = mine_row < rows;
+        const int64_t row = t.row0 + min((int)w.cta * each + mine_row, t.m - 1);
+        // output channels of this thread, and the scales' rows: of one block of 128 channels each
+        const int ch = t.channel * w.per_tile + group * (GLU ? kHalf : kWidth);
+        const int wb = min(ch, outs - 1) >> 7;
+        const float* sa = w.a.a_scales + row * blocks;
+        const float* sw = w.a.w_scales + ((int64_t)t.expert * w.a.wblocks + wb) * blocks;
+        const float* su = sw + (GLU ? (int64_t)(w.a.wblocks / 2) * blocks : 0);
+        f32x2 sum[kWidth / 2];
+#pragma unroll
+        for (int i = 0; i < kWidth / 2; ++i) sum[i] = 0;
+        float na = sa[0], nw = sw[0], nu = GLU ? su[0] : 0.0f;
+        for (int k = 0; k < blocks; ++k) {
+            const float s0 = na * nw, s1 = na * nu;
+            const f32x2 s = pair(s0, s0), u = pair(s1, s1);
+            const int next = min(k + 1, blocks - 1);
+            na = sa[next];
+            nw = sw[next];
+            if (GLU) nu = su[next];
+            if (!warp_wait(&w.sh.acc_full[acc.stage], acc.parity)) { ok = false; break; }
+            tmem_fence_after();
+            if (some) {
+                const uint32_t d = w.tmem + ((uint32_t)(quarter * 32) << 16) + acc.stage * C::n;
+#pragma unroll
+                for (int c = 0; c < kWidth / 32; ++c) {
+                    uint32_t v[32];
+                    // with two groups, each has 64 of the gates and their ups
+                    const int col = !GLU || C::groups == 1 ? group * kWidth + 32 * c
+                                                           : group * kHalf + (32 * c < kHalf ? 32 * c : C::n / 2 + 32 * c - kHalf);
+                    tmem_load32(d + col, v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sum[16 * c + i] = fma2(pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+                                               GLU && 32 * c + 2 * i >= kHalf ? u : s, sum[16 * c + i]);
+                }
+            }
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (C::ctas == 2) mbar_arrive_cluster(acc_empty0 + acc.stage * 8);
+                else mbar_arrive(&w.sh.acc_empty[acc.stage]);
+            }
+            acc.next();
+        }
+        if (!ok || !some) continue;
+        constexpr int kOuts = GLU ? kHalf : kWidth, kCols = kOuts < kPart ? kOuts : kPart;
+#pragma unroll
+        for (int p = 0; p < kOuts / kCols; ++p) {
+            uint32_t y[kCols / 2];
+#pragma unroll
+            for (int i = 0; i < kCols / 2; ++i) {
+                float a, b;
+                halves(sum[p * kCols / 2 + i], a, b);
+                if constexpr (GLU) {
+                    float g, h;
+                    halves(sum[kHalf / 2 + p * kCols / 2 + i], g, h);
+                    a = swiglu(a, g, 1.0f, 0.25f);
+                    b = swiglu(b, h, 1.0f, 0.25f);
+                }
+                y[i] = pack_bf16x2_rn(a, b);
+            }
+            store_part<kCols>(y, mine, w.a.out + row * outs + ch + p * kCols, outs - ch - p * kCols, in, bulk);
+        }
+    }
+    bulk_wait_all();
+    return ok;
+}
+
+template <class C, bool GLU>
+__global__ void __launch_bounds__(C::threads, 1)
+matmul_fp8_kernel(const Fp8Args a, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
+                  const __grid_constant__ CUtensorMap map_all) {
+    extern __shared__ uint8_t dynamic[];
+    __shared__ Shared<C> sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        prefetch_map(&map_w);
+        prefetch_map(&map_a);
+        prefetch_map(&map_all);
+    }
+    const uint32_t cta = C::ctas == 2 ? cluster_rank() : 0;
+    uint8_t* smem = dynamic + ((1024 - (smem_addr(dynamic) & 1023)) & 1023);
+    if (tid == 0) {
+        for (int i = 0; i < C::stages; ++i) { mbar_init(&sh.full[i], 1); mbar_init(&sh.empty[i], 1); }
+        for (int i = 0; i < C::accs; ++i) { mbar_init(&sh.acc_full[i], 1); mbar_init(&sh.acc_empty[i], 4 * C::groups * C::ctas); }
+        mbar_init(&sh.drained, 1);
+        mbar_fence_init();
+    }
+    if (warp == C::mma_warp) tmem_alloc<C::ctas>(&sh.tmem, C::columns);
+    wait_for_previous();
+    const bool fits = load_segments<C::threads>(sh.seg, a, C::tile);   // the same answer in both CTAs
+    tmem_fence_before();
+    __syncthreads();
+    if constexpr (C::ctas == 2) cluster_sync();
+    tmem_fence_after();
+
+    const int per_tile = GLU ? C::n / 2 : C::n, ctiles = (a.outs + per_tile - 1) / per_tile;
+    const int64_t all = fits ? (int64_t)sh.seg.tile[a.E] * ctiles : 0, limit = INT32_MAX - (int64_t)gridDim.x;   // (items + step stays a number)
+    const Work<C> w = {a, sh, smem, smem + C::stages * C::bytes, sh.tmem, cta, per_tile, ctiles,
+                       (int)(blockIdx.x / C::ctas), (int)(all < limit ? all : limit), (int)(gridDim.x / C::ctas)};
+    bool ok = true;
+    if (warp < 4 * C::groups) {
+        ok = epilogue<C, GLU>(w, warp);
+    } else if (warp == C::load_warp) {
+        if (lane == 0) ok = load_tiles<C, GLU>(w, &map_w, &map_a, &map_all);
+    } else if (warp == C::mma_warp) {
+        if (cta == 0) ok = issue_mma(w);
+    }
+    if (!ok && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    if constexpr (C::ctas == 2) cluster_sync();   // neither CTA's shared or tensor memory goes while the pair's MMAs may read it
+    if (warp == C::mma_warp) tmem_free<C::ctas>(w.tmem, C::columns);
+}
+
+template <class C, bool GLU>
+cudaError_t launch(const Fp8Args& a, const void* rows, const void* weights, int sms, cudaStream_t st) {
+    const int64_t per_tile = GLU ? C::n / 2 : C::n, k = 128 * (int64_t)a.blocks;
+    CUtensorMap map_w, map_a, map_all;
+    if (!make_experts_map(&map_w, weights, GLU ? 2 * a.E : a.E, a.outs, k, GLU && C::ctas == 1 ? C::channels / 2 : C::channels) ||
+        !make_rows_map(&map_a, rows, a.rows, k, kBoxTokens) || !make_rows_map(&map_all, rows, a.rows, k, C::rows))
+        return cudaErrorInvalidValue;
+    const int64_t most = ((a.rows + C::tile - 1) / C::tile + (a.E > 1 ? a.E : 0)) * ((a.outs + per_tile - 1) / per_tile);
+    if (most > INT32_MAX - sms) return cudaErrorInvalidValue;   // more output than any memory holds
+    const int64_t tiles = most < sms / C::ctas ? most : sms / C::ctas;
+    static std::atomic<uint64_t> done;
+    const cudaError_t e = allow_smem(matmul_fp8_kernel<C, GLU>, C::smem, done);
+    if (e != cudaSuccess) return e;
+    return launch_overlapped_clusters(matmul_fp8_kernel<C, GLU>, C::ctas, dim3((unsigned)(C::ctas * tiles)), C::threads, C::smem, st,
+                                      a, map_w, map_a, map_all);
+}
+
+template <bool GLU>
+cudaError_t run(const Fp8Args& a, const void* rows, const void* weights, int sms, cudaStream_t st) {
+    const int64_t each = (a.rows + a.E - 1) / a.E, experts = a.rows < a.E ? a.rows : a.E;
+    if (each <= 32) {
+        const int64_t per_tile = GLU ? Thin::n / 2 : Thin::n, tiles = experts * ((a.outs + per_tile - 1) / per_tile);
+        return tiles < sms ? launch<Small, GLU>(a, rows, weights, sms, st) : launch<Thin, GLU>(a, rows, weights, sms, st);
+    }
+    if (each <= 192) return launch<Mid, GLU>(a, rows, weights, sms, st);
+    return launch<Thick, GLU>(a, rows, weights, sms, st);
+}
+
+bool aligned(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
+
+}  // namespace
+
+extern "C" ep_status ep_expert_matmul_fp8(const void* a, const float* a_scales, int64_t rows, int32_t k, const void* w,
+                                          const float* w_scales, int32_t n, int32_t num_experts, const int32_t* expert_base,
+                                          int32_t swiglu, void* out, int32_t* status, ep_stream_t stream) {
+    if (rows < 0 || rows >= INT32_MAX || k < 128 || k > 65536 || k % 128 != 0 || n < 1 || n > 65536) return EP_ERR_INVALID_ARG;
+    if ((swiglu != 0 && swiglu != 1) || (swiglu && n % 2 != 0)) return EP_ERR_INVALID_ARG;
+    if (num_experts < 1 || num_experts > kMaxExperts || (num_experts > 1 && !expert_base)) return EP_ERR_INVALID_ARG;
+    if (!aligned(expert_base, 4) || !aligned(status, 4)) return EP_ERR_INVALID_ARG;
+    if (!w || !aligned(w, 16) || !w_scales || !aligned(w_scales, 4)) return EP_ERR_INVALID_ARG;
+    if (rows == 0) return EP_OK;
+    if (!a || !aligned(a, 16) || !a_scales || !aligned(a_scales, 4) || !out || !aligned(out, 2)) return EP_ERR_INVALID_ARG;
+    Fp8Args f;
+    f.a_scales = a_scales;
+    f.w_scales = w_scales;
+    f.expert_base = expert_base;
+    f.status = status;
+    f.out = (uint16_t*)out;
+    f.rows = rows;
+    f.E = num_experts;
+    f.outs = swiglu ? n / 2 : n;
+    f.blocks = k / 128;
+    f.wblocks = (swiglu ? 2 : 1) * ((f.outs + 127) / 128);
+    const int sms = ep_current_sms();
+    if (sms <= 0) return EP_ERR_CUDA;
+    const cudaError_t e = swiglu ? run<true>(f, a, w, sms, (cudaStream_t)stream) : run<false>(f, a, w, sms, (cudaStream_t)stream);
+    return e == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+}

@@ -107,10 +107,6 @@ __device__ __forceinline__ uint4 lds_at(uint32_t addr) {
     return v;
 }
 
-__device__ __forceinline__ void sts_at(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
 // What every role of a CTA knows.
 template <class C>
 struct Work {
@@ -257,8 +253,8 @@ __device__ __forceinline__ bool convert(const Work<C>& w, int warp, int set) {
                     if (g * 32 >= rows) break;
                     uint32_t f[8];
                     codes_to_f16(in[g], f);
-                    sts_at(to0 + to + g * 32 * 128, f[0], f[1], f[2], f[3]);
-                    sts_at(to1 + to + g * 32 * 128, f[4], f[5], f[6], f[7]);
+                    sts_v4(to0 + to + g * 32 * 128, f[0], f[1], f[2], f[3]);
+                    sts_v4(to1 + to + g * 32 * 128, f[4], f[5], f[6], f[7]);
                 }
             }
             if (!ok) break;

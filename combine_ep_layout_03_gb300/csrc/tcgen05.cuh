@@ -208,3 +208,55 @@ __device__ __forceinline__ void commit_leader(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                  :: "r"(smem_addr(bar)) : "memory");
 }
+
+// ---- the same for tiles of one CTA or of a pair (CTAS: 1 or 2)
+
+template <int CTAS>
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t columns) {
+    if constexpr (CTAS == 2) {
+        tmem_alloc_pair(slot, columns);
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(smem_addr(slot)), "r"(columns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+}
+
+template <int CTAS>
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
+    if constexpr (CTAS == 2) tmem_free_pair(addr, columns);
+    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(columns) : "memory");
+}
+
+// float32 accumulators, both operands e4m3 and K-major, M x N of all CTAs.
+constexpr uint32_t mma_desc_e4m3(uint32_t m, uint32_t n) { return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24); }
+
+// D[tmem] (+)= A[smem] * B[smem]^T of 32 values of 8 bits; one thread of the first CTA.
+template <int CTAS>
+__device__ __forceinline__ void mma_f8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    if constexpr (CTAS == 2)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
+}
+
+// Arrive on `bar` of this CTA once this thread's MMAs so far have completed.
+template <int CTAS>
+__device__ __forceinline__ void commit_own(uint64_t* bar) {
+    if constexpr (CTAS == 2)
+        commit_leader(bar);
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                     :: "r"(smem_addr(bar)) : "memory");
+}
+
+// The same in all CTAs of the tile.
+template <int CTAS>
+__device__ __forceinline__ void commit_all(uint64_t* bar) {
+    if constexpr (CTAS == 2) commit_pair(bar);
+    else commit_own<1>(bar);
+}

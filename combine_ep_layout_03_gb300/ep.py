@@ -115,6 +115,7 @@ def _load():
         "ep_rms_norm_quant": ([vp, i64, vp, i64, vp, ctypes.c_float, i64, i32, st, vp, i64, vp, vp, vp, vp], st),
         "ep_quant_rows": ([vp, i64, i64, i32, st, vp, vp, vp], st),
         "ep_expert_matmul": ([vp, vp, i64, i32, vp, vp, i32, i32, vp, i32, vp, vp, vp], st),
+        "ep_expert_matmul_fp8": ([vp, vp, i64, i32, vp, vp, i32, i32, vp, i32, vp, vp, vp], st),
         "ep_expert_matmul_bf16": ([vp, i64, i32, vp, i32, i32, vp, i32, vp, vp, vp], st),
         "ep_expert_matmul_grad_rows": ([vp, i64, i32, vp, i32, i32, vp, vp, vp, vp], st),
         "ep_expert_matmul_grad_weights": ([vp, vp, i64, i32, i32, i32, vp, i32, i32, vp, vp, vp], st),
@@ -478,6 +479,34 @@ def _base_ptr(expert_base, E: int):
 def _bf16_rows(t: torch.Tensor, shape, what: str) -> None:
     if t.dtype is not torch.bfloat16 or not t.is_contiguous() or t.shape != shape:
         raise EPError(EP_ERR_INVALID_ARG, what)
+
+
+def ep_expert_matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, expert_base,
+                         out: torch.Tensor, swiglu: bool = False, status=None, stream=None) -> None:
+    """e4m3 rows times e4m3 expert matrices with a float32 scale for each block of 128: a [rows, K] with a_scales [rows,
+    K / 128] (both also as the bytes of a receive buffer), w [E, N, K] with w_scales [E, ceil(N / 128), K / 128], or [E,
+    2 * ceil(N / 2 / 128), K / 128] with swiglu; expert_base int32 [E + 1] on the device (None: one matrix), out bf16
+    [rows, N], or [rows, N / 2] = silu(gates) * ups with swiglu."""
+    _require(len(a.shape) == 2 and len(w.shape) == 3, "a: e4m3 [rows, K], w: e4m3 [E, N, K]")
+    rows, K = a.shape
+    E, N, _ = w.shape
+    bad = None
+    if a.element_size() != 1 or not a.is_contiguous():
+        bad = "a: e4m3 [rows, K]"
+    elif w.dtype is not torch.float8_e4m3fn or not w.is_contiguous() or w.shape[2] != K or K % 128 != 0:
+        bad = "w: e4m3 [E, N, K], K a multiple of 128"
+    elif not a_scales.is_contiguous() or a_scales.nbytes != rows * (K // 32):
+        bad = "a_scales: float32 [rows, K / 128]"
+    elif (w_scales.dtype is not torch.float32 or not w_scales.is_contiguous()
+          or w_scales.numel() != E * (2 * ((N // 2 + 127) // 128) if swiglu else (N + 127) // 128) * (K // 128)):
+        bad = "w_scales: float32 [E, N / 128, K / 128]"
+    if bad:
+        raise EPError(EP_ERR_INVALID_ARG, bad)
+    _bf16_rows(out, (rows, N // 2 if swiglu else N), "out: bf16 [rows, N], or [rows, N / 2] with swiglu")
+    code = _lib.ep_expert_matmul_fp8(a.data_ptr(), a_scales.data_ptr(), rows, K, w.data_ptr(), w_scales.data_ptr(), N, E,
+                                     _base_ptr(expert_base, E), 1 if swiglu else 0, out.data_ptr(), _ptr(status), _stream(stream))
+    if code:
+        _check(code, "ep_expert_matmul_fp8")
 
 
 def ep_expert_matmul_bf16(a: torch.Tensor, w: torch.Tensor, expert_base, out: torch.Tensor, swiglu: bool = False,

@@ -552,6 +552,20 @@ ep_status ep_expert_matmul(const void* a, const float* a_scales, int64_t rows, i
                            const float* w_scales, int32_t n, int32_t num_experts, const int32_t* expert_base,
                            int32_t swiglu, void* out, int32_t* status, ep_stream_t stream);
 
+/* Device.  The same with FP8 (e4m3) rows and weights that have a float32 scale for each block of 128:
+ *   c[r,n] = sum over blocks b of 128 k:  a_scales[r,b] * w_scales[e, n / 128, b] * sum_{k in b} a[r,k] * w[e,n,k],
+ * out = bf16(c), or with swiglu = 1 bf16(silu(c[:, :n/2]) * c[:, n/2:]).  Products of codes are exact; the sum of a
+ * block, the product of its two scales and the sum over blocks are float32.
+ * a [rows, k] with a_scales [rows, k / 128] are receive rows of EP_QUANT_FP8_E4M3_PER_GROUP (or of
+ * ep_rms_norm_quant and ep_quant_rows in that mode); w [E, n, k] e4m3 with w_scales [E, ceil(n / 128), k / 128].
+ * With swiglu the blocks of the gates' n/2 rows and of the ups' are counted apart, as of two matrices one after
+ * the other: w_scales [E, 2 * ceil(n / 2 / 128), k / 128].
+ * k in [128, 65536], a multiple of 128; the rest, segments and errors among it, as for ep_expert_matmul.  A NaN
+ * code or scale makes NaN of the results that it enters. */
+ep_status ep_expert_matmul_fp8(const void* a, const float* a_scales, int64_t rows, int32_t k, const void* w,
+                               const float* w_scales, int32_t n, int32_t num_experts, const int32_t* expert_base,
+                               int32_t swiglu, void* out, int32_t* status, ep_stream_t stream);
+
 /* Device.  The same of bf16 rows and weights without scales (receive rows of EP_QUANT_NONE):
  *   c[r,n] = sum_k a[r,k] * w[e,n,k],
  * sums in float32, rounded once to bf16.  a [rows, k], w [E, n, k], out [rows, n], or [rows, n / 2] with

@@ -119,3 +119,30 @@ def test_binding_refuses_wrong_products():
     refused(ep.ep_expert_matmul_grad_weights, good, base + [
         dict(grad_c=f(3, 32, dtype=bf)), dict(a=f(4, 64)), dict(a=f(64, 4, dtype=bf).t()), dict(grad_w=f(3, 32, 64, dtype=torch.float16)),
         dict(grad_w=f(3, 64, 32, dtype=bf)), dict(grad_w=f(32, 64, dtype=bf)), dict(grad_w=f(3, 64, 32, dtype=bf).transpose(1, 2))])
+
+
+def fp8(a=A, sa=A, rows=100, k=256, w=B, sw=B, n=64, E=8, base=C, swiglu=0, out=D, status=None):
+    return ep.lib.ep_expert_matmul_fp8(a, sa, rows, k, w, sw, n, E, base, swiglu, out, status, None)
+
+
+@pytest.mark.parametrize("kw", SEGMENTS + [dict(a=None), dict(a=A + 8), dict(w=None), dict(w=B + 8), dict(sa=None), dict(sa=A + 2),
+                                           dict(sw=None), dict(sw=B + 2), dict(k=64), dict(k=192), dict(k=65664), dict(n=63, swiglu=1),
+                                           dict(swiglu=2)])
+def test_fp8_product_refuses(kw):
+    assert fp8(**kw) == ep.EP_ERR_INVALID_ARG
+
+
+def test_fp8_product_of_no_rows():
+    assert fp8(rows=0, a=None, sa=None, out=None) == ep.EP_OK
+
+
+def test_binding_refuses_wrong_fp8_products():
+    f, bf, e4 = torch.zeros, torch.bfloat16, torch.float8_e4m3fn
+    good = dict(a=f(4, 256, dtype=e4), a_scales=f(4, 2), w=f(3, 320, 256, dtype=e4), w_scales=f(3, 3, 2),
+                expert_base=f(4, dtype=torch.int32), out=f(4, 320, dtype=bf))
+    bads = [dict(a=f(4, 256, dtype=bf)), dict(a=f(256, 4, dtype=e4).t()), dict(a=f(4, 128, dtype=e4)), dict(a_scales=f(4, 1)),
+            dict(a_scales=f(4, 4)[:, ::2]), dict(w=f(3, 320, 256, dtype=torch.uint8)), dict(w=f(3, 256, 320, dtype=e4).transpose(1, 2)),
+            dict(w_scales=f(3, 2, 2)), dict(w_scales=f(3, 3, 2, dtype=bf)), dict(expert_base=None), dict(out=f(4, 320)),
+            dict(out=f(4, 160, dtype=bf)), dict(swiglu=True), dict(swiglu=True, out=f(4, 160, dtype=bf)),
+            dict(a=f(4, 192, dtype=e4), a_scales=f(4, 1), w=f(3, 320, 192, dtype=e4), w_scales=f(3, 3, 1))]
+    refused(ep.ep_expert_matmul_fp8, good, bads)
