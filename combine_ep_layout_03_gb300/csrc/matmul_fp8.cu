@@ -48,7 +48,10 @@ struct Config {
     static constexpr int groups = N > 128 ? 2 : 1;         // of four epilogue warps
     static constexpr int width = N / groups;               // accumulators of a thread
     static constexpr int load_warp = 4 * groups, mma_warp = load_warp + 1;
-    static constexpr int threads = groups == 2 ? 320 : 256;
+    static constexpr int threads = groups == 2 ? 384 : 256;
+    // Two groups of epilogue warps need 216 registers a thread, and the launch gives each of 384 threads 168: the four
+    // other warps hand over what they do not need (4 x 72 + 8 x 216 = 12 x 168, and no wait for registers is left open).
+    static constexpr bool split = groups == 2;
     static constexpr int bytes_a = ROWS * 128, bytes = bytes_a + channels * 128;
     static constexpr int staged = 128 * groups * kPitch;
     static constexpr int smem = 1024 + STAGES * bytes + staged;
@@ -202,6 +205,17 @@ __device__ __forceinline__ void store_part(const uint32_t y[COLS / 2], uint8_t* 
     }
 }
 
+// A row's scales of the blocks k to k + 3, as far as there are.
+__device__ __forceinline__ void scales_of(float s[4], const float* row, int k, int blocks, bool wide) {
+    if (wide) {
+        const float4 v = *reinterpret_cast<const float4*>(row + k);
+        s[0] = v.x; s[1] = v.y; s[2] = v.z; s[3] = v.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = row[min(k + i, blocks - 1)];
+    }
+}
+
 template <class C, bool GLU>
 __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
     constexpr int kWidth = C::width, kHalf = kWidth / 2;
@@ -227,28 +241,46 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
         f32x2 sum[kWidth / 2];
 #pragma unroll
         for (int i = 0; i < kWidth / 2; ++i) sum[i] = 0;
-        float na = sa[0], nw = sw[0], nu = GLU ? su[0] : 0.0f;
+        // Scales are asked for long before their block: a token's four blocks ahead, the channels' 32 blocks at a
+        // time, one a lane.
+        const bool wide = blocks % 4 == 0 && ((uintptr_t)w.a.a_scales & 15) == 0;
+        float next[4], now[4];
+        scales_of(next, sa, 0, blocks, wide);
+        float swl = 0.0f, sul = 0.0f;
         for (int k = 0; k < blocks; ++k) {
-            const float s0 = na * nw, s1 = na * nu;
+            if ((k & 3) == 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) now[i] = next[i];
+                if (k + 4 < blocks) scales_of(next, sa, k + 4, blocks, wide);
+            }
+            if ((k & 31) == 0) {
+                swl = sw[min(k + lane, blocks - 1)];
+                if (GLU) sul = su[min(k + lane, blocks - 1)];
+            }
+            const float s0 = now[0] * __shfl_sync(0xffffffffu, swl, k & 31), s1 = GLU ? now[0] * __shfl_sync(0xffffffffu, sul, k & 31) : 0.0f;
+            now[0] = now[1];
+            now[1] = now[2];
+            now[2] = now[3];
             const f32x2 s = pair(s0, s0), u = pair(s1, s1);
-            const int next = min(k + 1, blocks - 1);
-            na = sa[next];
-            nw = sw[next];
-            if (GLU) nu = su[next];
             if (!warp_wait(&w.sh.acc_full[acc.stage], acc.parity)) { ok = false; break; }
             tmem_fence_after();
             if (some) {
                 const uint32_t d = w.tmem + ((uint32_t)(quarter * 32) << 16) + acc.stage * C::n;
+                // 32 columns on their way while the ones before are added; with two groups, each has 64 of the gates
+                // and their ups
+                auto column = [&](int c) {
+                    return !GLU || C::groups == 1 ? group * kWidth + 32 * c
+                                                  : group * kHalf + (32 * c < kHalf ? 32 * c : C::n / 2 + 32 * c - kHalf);
+                };
+                uint32_t v[2][32];
+                tmem_start32(d + column(0), v[0]);
 #pragma unroll
                 for (int c = 0; c < kWidth / 32; ++c) {
-                    uint32_t v[32];
-                    // with two groups, each has 64 of the gates and their ups
-                    const int col = !GLU || C::groups == 1 ? group * kWidth + 32 * c
-                                                           : group * kHalf + (32 * c < kHalf ? 32 * c : C::n / 2 + 32 * c - kHalf);
-                    tmem_load32(d + col, v);
+                    tmem_wait_loads(v[c & 1]);
+                    if (c + 1 < kWidth / 32) tmem_start32(d + column(c + 1), v[(c + 1) & 1]);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        sum[16 * c + i] = fma2(pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+                        sum[16 * c + i] = fma2(pair(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])),
                                                GLU && 32 * c + 2 * i >= kHalf ? u : s, sum[16 * c + i]);
                 }
             }
@@ -318,11 +350,15 @@ matmul_fp8_kernel(const Fp8Args a, const __grid_constant__ CUtensorMap map_w, co
                        (int)(blockIdx.x / C::ctas), (int)(all < limit ? all : limit), (int)(gridDim.x / C::ctas)};
     bool ok = true;
     if (warp < 4 * C::groups) {
+        if constexpr (C::split) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         ok = epilogue<C, GLU>(w, warp);
-    } else if (warp == C::load_warp) {
-        if (lane == 0) ok = load_tiles<C, GLU>(w, &map_w, &map_a, &map_all);
-    } else if (warp == C::mma_warp) {
-        if (cta == 0) ok = issue_mma(w);
+    } else {
+        if constexpr (C::split) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == C::load_warp) {
+            if (lane == 0) ok = load_tiles<C, GLU>(w, &map_w, &map_a, &map_all);
+        } else if (warp == C::mma_warp) {
+            if (cta == 0) ok = issue_mma(w);
+        }
     }
     if (!ok && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
     __syncwarp();
@@ -343,7 +379,14 @@ cudaError_t launch(const Fp8Args& a, const void* rows, const void* weights, int 
     if (most > INT32_MAX - sms) return cudaErrorInvalidValue;   // more output than any memory holds
     const int64_t tiles = most < sms / C::ctas ? most : sms / C::ctas;
     static std::atomic<uint64_t> done;
-    const cudaError_t e = allow_smem(matmul_fp8_kernel<C, GLU>, C::smem, done);
+    cudaError_t e;
+    if (C::split && done.load(std::memory_order_relaxed) == 0) {   // the split counts on what the launch gives
+        cudaFuncAttributes attr;
+        e = cudaFuncGetAttributes(&attr, matmul_fp8_kernel<C, GLU>);
+        if (e != cudaSuccess) return e;
+        if (attr.numRegs != 168) return cudaErrorInvalidConfiguration;
+    }
+    e = allow_smem(matmul_fp8_kernel<C, GLU>, C::smem, done);
     if (e != cudaSuccess) return e;
     return launch_overlapped_clusters(matmul_fp8_kernel<C, GLU>, C::ctas, dim3((unsigned)(C::ctas * tiles)), C::threads, C::smem, st,
                                       a, map_w, map_a, map_all);
