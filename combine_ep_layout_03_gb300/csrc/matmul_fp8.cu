@@ -16,7 +16,6 @@
 // wait is bounded (EP_ERR_TIMEOUT).
 #include "expert_ops.cuh"
 #include "expert_tiles.cuh"
-#include "row_codes.cuh"
 #include "tcgen05.cuh"
 #include "tensor_maps.cuh"
 
@@ -36,40 +35,45 @@ struct Fp8Args {
 };
 
 constexpr int kBoxTokens = 32;   // rows of a small token box
-constexpr int kPart = 64;        // output columns that a thread stages at a time
+constexpr int kPart = 32;        // output columns that a thread stages at a time
 constexpr int kPitch = kPart * 2 + 16;   // bytes of its row there: 16 more than the row, so that lanes meet different banks
 
 // CTAS: of a tile; ROWS: token rows of a CTA that there is room for; N: channels of a tile; STAGES: of 128 k;
 // ACCS: accumulators in tensor memory.
-template <int CTAS, int ROWS, int N, int STAGES, int ACCS>
+// WIDTH: accumulators of an epilogue thread.
+template <int CTAS, int ROWS, int N, int STAGES, int ACCS, int WIDTH>
 struct Config {
     static constexpr int ctas = CTAS, rows = ROWS, tile = CTAS * ROWS, n = N, stages = STAGES, accs = ACCS;
     static constexpr int channels = N / CTAS;              // whose weights a CTA loads
-    static constexpr int groups = N > 128 ? 2 : 1;         // of four epilogue warps
-    static constexpr int width = N / groups;               // accumulators of a thread
-    static constexpr int load_warp = 4 * groups, mma_warp = load_warp + 1;
-    static constexpr int threads = groups == 2 ? 384 : 256;
-    // Two groups of epilogue warps need 216 registers a thread, and the launch gives each of 384 threads 168: the four
-    // other warps hand over what they do not need (4 x 72 + 8 x 216 = 12 x 168, and no wait for registers is left open).
-    static constexpr bool split = groups == 2;
+    static constexpr int width = WIDTH;
+    static constexpr int groups = N / width;               // of four epilogue warps
+    static constexpr int load_warp = 4 * groups, mma_warp = load_warp + 1, scale_warp = load_warp + 3;   // two MMA warps
+    static constexpr int threads = groups == 1 ? 256 : 32 * (4 * groups + 4);
     static constexpr int bytes_a = ROWS * 128, bytes = bytes_a + channels * 128;
     static constexpr int staged = 128 * groups * kPitch;
     static constexpr int smem = 1024 + STAGES * bytes + staged;
     static constexpr uint32_t columns = ACCS * N;
     static_assert(columns <= 512 && (columns & (columns - 1)) == 0 && columns >= 32, "tensor memory");
-    static_assert(bytes_a % 1024 == 0 && bytes % 1024 == 0 && width % 32 == 0 && width <= 128, "swizzled rows; registers");
+    static_assert(bytes_a % 1024 == 0 && bytes % 1024 == 0 && width % 32 == 0 && N % width == 0, "swizzled rows; registers");
     // an MMA reads 128 token rows, also where a stage has room for fewer: what follows is read for them, inside shared memory
     static_assert(bytes - bytes_a + staged >= (128 - ROWS) * 128, "rows past a stage's");
 };
 
-using Thick = Config<2, 128, 256, 5, 2>;
-using Mid = Config<1, 128, 128, 6, 4>;
-using Thin = Config<1, 32, 128, 9, 4>;
-using Small = Config<1, 32, 32, 20, 8>;
+using Thick = Config<2, 128, 256, 5, 2, 64>;
+using Mid = Config<1, 128, 128, 5, 4, 64>;
+using Thin = Config<1, 32, 128, 9, 4, 64>;
+using Small = Config<1, 32, 32, 20, 8, 32>;
+
+// The products of scales of a chunk of blocks, by token row of a CTA: of the tile's first block of channels, and of its
+// second (or of the ups).
+constexpr int kChunk = 8, kChunks = 2;
+struct Scales { float of[2][kChunk][128]; };
 
 template <class C>
 struct Shared {
     Segments seg;
+    Scales scales[kChunks];
+    uint64_t scale_full[kChunks], scale_empty[kChunks];
     uint64_t full[C::stages], empty[C::stages];   // full: of the tile's first CTA
     uint64_t acc_full[C::accs], acc_empty[C::accs];
     uint64_t drained;
@@ -144,32 +148,63 @@ __device__ __forceinline__ bool load_tiles(const Work<C>& w, const CUtensorMap* 
     return ok && over;
 }
 
+// The waits and words of the loop over blocks, which is one chain of latencies: without votes and without branches on the
+// lane (those cost 50 to 100 clocks each).  A wait is bounded by its polls, each of which may park the thread.
+__device__ __forceinline__ bool wait_block(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+                 "POLL%=:\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "@p bra OVER%=;\n\t"
+                 "add.u32 n, n, 1;\n\tsetp.lt.u32 p, n, %3;\n\t@p bra POLL%=;\n\t"
+                 "setp.ne.u32 p, 0, 0;\n"
+                 "OVER%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity), "r"(kMaxPolls) : "memory");
+    return ok != 0;
+}
+
+// One lane (of a warp that has just met) arrives on this CTA's barrier, or on either CTA's.
+__device__ __forceinline__ void arrive_one(int lane, uint64_t* bar, bool when) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}"
+                 :: "r"(smem_addr(bar)), "r"((uint32_t)(lane == 0 && when)) : "memory");
+}
+
+__device__ __forceinline__ void arrive_one_cluster(int lane, uint32_t bar, bool when) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}"
+                 :: "r"(bar), "r"((uint32_t)(lane == 0 && when)) : "memory");
+}
+
+// Two warps issue, every other block each: a block's products start a fresh accumulator, so that their order does not
+// matter, and the words to be exchanged for a block (some 350 clocks) are exchanged while the other's products run.
 template <class C>
-__device__ __forceinline__ bool issue_mma(const Work<C>& w) {
+__device__ __forceinline__ bool issue_mma(const Work<C>& w, int which) {
     Ring<C::stages> r;
     Ring<C::accs> acc;
     const uint32_t smem0 = smem_addr(w.smem), idesc = mma_desc_e4m3(128 * C::ctas, C::n);
-    bool ready = false, ok = true;
-    int expert = 0;
-    for (int item = w.first; ok && item < w.items; item += w.step) {
-        for (int k = 0; k < w.a.blocks; ++k) {
-            if (!warp_wait(&w.sh.acc_empty[acc.stage], acc.parity ^ 1) ||
-                (!ready && !warp_wait(&w.sh.full[r.stage], r.parity))) { ok = false; break; }
-            tmem_fence_after();
-            const uint32_t at = smem0 + r.stage * C::bytes, d = w.tmem + acc.stage * C::n;
-            const uint64_t a = smem_desc_k128(at), b = smem_desc_k128(at + C::bytes_a);
-            uint64_t *const empty = &w.sh.empty[r.stage], *const full = &w.sh.acc_full[acc.stage];
-            r.next();
-            acc.next();
-            ready = __all_sync(0xffffffffu, mbar_test(&w.sh.full[r.stage], r.parity));
-            if (elect_one()) {
+    if (which) {
+        r.next();
+        acc.next();
+    }
+    const int tiles = w.items > w.first ? (w.items - w.first + w.step - 1) / w.step : 0;
+    const int64_t blocks = (int64_t)tiles * w.a.blocks;
+    bool ok = true;
+    for (int64_t k = which; k < blocks; k += 2) {
+        const uint32_t at = smem0 + r.stage * C::bytes, d = w.tmem + acc.stage * C::n;
+        const uint64_t a = smem_desc_k128(at), b = smem_desc_k128(at + C::bytes_a);
+        if (!wait_block(&w.sh.full[r.stage], r.parity) || !wait_block(&w.sh.acc_empty[acc.stage], acc.parity ^ 1)) { ok = false; break; }
+        tmem_fence_after();
+        __syncwarp();
+        if (elect_one()) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) mma_f8_ss<C::ctas>(d, a + 2 * j, b + 2 * j, idesc, j > 0);
-                commit_all<C::ctas>(empty);
-                commit_all<C::ctas>(full);
-            }
-            __syncwarp();
+            for (int j = 0; j < 4; ++j) mma_f8_ss<C::ctas>(d, a + 2 * j, b + 2 * j, idesc, j > 0);
+            commit_all<C::ctas>(&w.sh.acc_full[acc.stage]);
+            commit_all<C::ctas>(&w.sh.empty[r.stage]);
         }
+        __syncwarp();
+        r.next();
+        r.next();
+        acc.next();
+        acc.next();
     }
     // no MMA is left when the CTAs part, also when a wait gave up
     if (elect_one()) commit_own<C::ctas>(&w.sh.drained);
@@ -205,15 +240,51 @@ __device__ __forceinline__ void store_part(const uint32_t y[COLS / 2], uint8_t* 
     }
 }
 
-// A row's scales of the blocks k to k + 3, as far as there are.
-__device__ __forceinline__ void scales_of(float s[4], const float* row, int k, int blocks, bool wide) {
-    if (wide) {
-        const float4 v = *reinterpret_cast<const float4*>(row + k);
-        s[0] = v.x; s[1] = v.y; s[2] = v.z; s[3] = v.w;
-    } else {
+// Scales go through shared memory, by a warp of their own: read by the threads that use them, 4 bytes of 32 rows at a
+// time, they cost more than the additions.
+template <class C, bool GLU>
+__device__ __forceinline__ bool load_scales(const Work<C>& w) {
+    const int lane = threadIdx.x & 31, blocks = w.a.blocks;
+    Ring<kChunks> r;
+    int expert = 0;
+    for (int item = w.first; item < w.items; item += w.step) {
+        const Tile t = tile_of<true>(w.sh.seg, w.a.E, w.ctiles, item, expert);
+        const int mine = t.n / C::ctas, rows = (min(mine, t.m - (int)w.cta * mine) + 31) / 32;   // in 32s (perhaps none)
+        const float* row[C::rows / 32];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = row[min(k + i, blocks - 1)];
+        for (int i = 0; i < C::rows / 32; ++i)
+            row[i] = w.a.a_scales + (t.row0 + min((int)w.cta * mine + 32 * i + lane, t.m - 1)) * blocks;
+        // lanes 0 to 15: the eight blocks of k of the first block of channels, and of the second (or of the ups)
+        const int half = (lane >> 3) & 1, ch = t.channel * w.per_tile;
+        const int wb = GLU ? (ch >> 7) + half * (w.a.wblocks / 2) : min((ch >> 7) + half, w.a.wblocks - 1);
+        const float* sw = w.a.w_scales + ((int64_t)t.expert * w.a.wblocks + wb) * blocks;
+        for (int k = 0; k < blocks; k += kChunk, r.next()) {
+            float v[C::rows / 32][kChunk];
+#pragma unroll
+            for (int i = 0; i < C::rows / 32; ++i)
+#pragma unroll
+                for (int b = 0; b < kChunk; ++b) v[i][b] = i < rows && k + b < blocks ? row[i][k + b] : 0.0f;
+            const float c = sw[min(k + (lane & 7), blocks - 1)];
+            if (!warp_wait(&w.sh.scale_empty[r.stage], r.parity ^ 1)) return false;
+            Scales& s = w.sh.scales[r.stage];
+#pragma unroll
+            for (int h = 0; h < (GLU || C::n > 128 ? 2 : 1); ++h)
+#pragma unroll
+                for (int b = 0; b < kChunk; ++b) {
+                    const float of = __shfl_sync(0xffffffffu, c, 8 * h + b);
+#pragma unroll
+                    for (int i = 0; i < C::rows / 32; ++i) s.of[h][b][32 * i + lane] = v[i][b] * of;
+                }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&w.sh.scale_full[r.stage]);
+        }
     }
+    return true;
+}
+
+// sum += s * v.  Volatile, so that it stays behind the wait for the load of v.
+__device__ __forceinline__ void add_scaled(float& sum, uint32_t v, float s) {
+    asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(sum) : "f"(__uint_as_float(v)), "f"(s));
 }
 
 template <class C, bool GLU>
@@ -225,6 +296,7 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
     const int outs = w.a.outs, blocks = w.a.blocks;
     const bool bulk = outs % 8 == 0 && ((uintptr_t)w.a.out & 15) == 0;
     Ring<C::accs> acc;
+    Ring<kChunks> scales;
     int expert = 0;
     bool ok = true;
     for (int item = w.first; ok && item < w.items; item += w.step) {
@@ -232,65 +304,52 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
         const int each = t.n / C::ctas, rows = min(each, t.m - (int)w.cta * each);   // this CTA's (perhaps none)
         const bool some = quarter * 32 < rows, in = mine_row < rows;
         const int64_t row = t.row0 + min((int)w.cta * each + mine_row, t.m - 1);
-        // output channels of this thread, and the scales' rows: of one block of 128 channels each
-        const int ch = t.channel * w.per_tile + group * (GLU ? kHalf : kWidth);
-        const int wb = min(ch, outs - 1) >> 7;
-        const float* sa = w.a.a_scales + row * blocks;
-        const float* sw = w.a.w_scales + ((int64_t)t.expert * w.a.wblocks + wb) * blocks;
-        const float* su = sw + (GLU ? (int64_t)(w.a.wblocks / 2) * blocks : 0);
-        f32x2 sum[kWidth / 2];
+        // output channels of this thread, and their block of the tile's (with SwiGLU: the gates' is the first, the ups' the second)
+        const int ch = t.channel * w.per_tile + group * (GLU ? kHalf : kWidth), cb = GLU ? 0 : group * kWidth >> 7;
+        float sum[kWidth];
 #pragma unroll
-        for (int i = 0; i < kWidth / 2; ++i) sum[i] = 0;
-        // Scales are asked for long before their block: a token's four blocks ahead, the channels' 32 blocks at a
-        // time, one a lane.
-        const bool wide = blocks % 4 == 0 && ((uintptr_t)w.a.a_scales & 15) == 0;
-        float next[4], now[4];
-        scales_of(next, sa, 0, blocks, wide);
-        float swl = 0.0f, sul = 0.0f;
+        for (int i = 0; i < kWidth; ++i) sum[i] = 0.0f;
+        // a block's products of scales are read under the block before
+        if (!wait_block(&w.sh.scale_full[scales.stage], scales.parity)) { ok = false; break; }
+        float next0 = w.sh.scales[scales.stage].of[cb][0][mine_row], next1 = GLU ? w.sh.scales[scales.stage].of[1][0][mine_row] : 0.0f;
         for (int k = 0; k < blocks; ++k) {
-            if ((k & 3) == 0) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) now[i] = next[i];
-                if (k + 4 < blocks) scales_of(next, sa, k + 4, blocks, wide);
-            }
-            if ((k & 31) == 0) {
-                swl = sw[min(k + lane, blocks - 1)];
-                if (GLU) sul = su[min(k + lane, blocks - 1)];
-            }
-            const float s0 = now[0] * __shfl_sync(0xffffffffu, swl, k & 31), s1 = GLU ? now[0] * __shfl_sync(0xffffffffu, sul, k & 31) : 0.0f;
-            now[0] = now[1];
-            now[1] = now[2];
-            now[2] = now[3];
-            const f32x2 s = pair(s0, s0), u = pair(s1, s1);
-            if (!warp_wait(&w.sh.acc_full[acc.stage], acc.parity)) { ok = false; break; }
+            const float s = next0, u = next1;
+            if (!wait_block(&w.sh.acc_full[acc.stage], acc.parity)) { ok = false; break; }
             tmem_fence_after();
-            if (some) {
-                const uint32_t d = w.tmem + ((uint32_t)(quarter * 32) << 16) + acc.stage * C::n;
-                // 32 columns on their way while the ones before are added; with two groups, each has 64 of the gates
-                // and their ups
-                auto column = [&](int c) {
-                    return !GLU || C::groups == 1 ? group * kWidth + 32 * c
-                                                  : group * kHalf + (32 * c < kHalf ? 32 * c : C::n / 2 + 32 * c - kHalf);
-                };
-                uint32_t v[2][32];
-                tmem_start32(d + column(0), v[0]);
-#pragma unroll
-                for (int c = 0; c < kWidth / 32; ++c) {
-                    tmem_wait_loads(v[c & 1]);
-                    if (c + 1 < kWidth / 32) tmem_start32(d + column(c + 1), v[(c + 1) & 1]);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        sum[16 * c + i] = fma2(pair(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])),
-                                               GLU && 32 * c + 2 * i >= kHalf ? u : s, sum[16 * c + i]);
+            const bool last = (k + 1) % kChunk == 0 || k + 1 == blocks;   // of its chunk
+            auto release = [&]() {
+                tmem_fence_before();
+                __syncwarp();
+                if (C::ctas == 1) {
+                    arrive_one(lane, &w.sh.acc_empty[acc.stage], true);
+                } else {
+                    arrive_one_cluster(lane, acc_empty0 + acc.stage * 8, true);
                 }
-            }
-            tmem_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if constexpr (C::ctas == 2) mbar_arrive_cluster(acc_empty0 + acc.stage * 8);
-                else mbar_arrive(&w.sh.acc_empty[acc.stage]);
+                arrive_one(lane, &w.sh.scale_empty[scales.stage], last);
+            };
+            if (some) {
+                const uint32_t d = w.tmem + ((uint32_t)(quarter * 32) << 16) + acc.stage * C::n + group * (GLU ? kHalf : kWidth);
+#pragma unroll
+                for (int c = 0; c < kWidth / 16; ++c) {
+                    const bool up = GLU && 16 * c >= kHalf;
+                    uint32_t v[16];
+                    tmem_start16(d + (up ? C::n / 2 - kHalf : 0) + 16 * c, v);
+                    tmem_wait_loads();
+                    if (c == kWidth / 16 - 1) release();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) add_scaled(sum[16 * c + i], v[i], up ? u : s);
+                }
+            } else {
+                release();
             }
             acc.next();
+            if (last) {
+                scales.next();
+                if (k + 1 < blocks && !wait_block(&w.sh.scale_full[scales.stage], scales.parity)) { ok = false; break; }
+            }
+            const auto& of = w.sh.scales[scales.stage].of;   // (behind the tile's last block: not used)
+            next0 = of[cb][(k + 1) % kChunk][mine_row];
+            if (GLU) next1 = of[1][(k + 1) % kChunk][mine_row];
         }
         if (!ok || !some) continue;
         constexpr int kOuts = GLU ? kHalf : kWidth, kCols = kOuts < kPart ? kOuts : kPart;
@@ -299,13 +358,10 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
             uint32_t y[kCols / 2];
 #pragma unroll
             for (int i = 0; i < kCols / 2; ++i) {
-                float a, b;
-                halves(sum[p * kCols / 2 + i], a, b);
+                float a = sum[p * kCols + 2 * i], b = sum[p * kCols + 2 * i + 1];
                 if constexpr (GLU) {
-                    float g, h;
-                    halves(sum[kHalf / 2 + p * kCols / 2 + i], g, h);
-                    a = swiglu(a, g, 1.0f, 0.25f);
-                    b = swiglu(b, h, 1.0f, 0.25f);
+                    a = swiglu(a, sum[kHalf + p * kCols + 2 * i], 1.0f, 0.25f);
+                    b = swiglu(b, sum[kHalf + p * kCols + 2 * i + 1], 1.0f, 0.25f);
                 }
                 y[i] = pack_bf16x2_rn(a, b);
             }
@@ -322,6 +378,7 @@ matmul_fp8_kernel(const Fp8Args a, const __grid_constant__ CUtensorMap map_w, co
                   const __grid_constant__ CUtensorMap map_all) {
     extern __shared__ uint8_t dynamic[];
     __shared__ Shared<C> sh;
+    static_assert(C::smem + sizeof(sh) <= 227 * 1024, "shared memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         prefetch_map(&map_w);
@@ -333,7 +390,8 @@ matmul_fp8_kernel(const Fp8Args a, const __grid_constant__ CUtensorMap map_w, co
     if (tid == 0) {
         for (int i = 0; i < C::stages; ++i) { mbar_init(&sh.full[i], 1); mbar_init(&sh.empty[i], 1); }
         for (int i = 0; i < C::accs; ++i) { mbar_init(&sh.acc_full[i], 1); mbar_init(&sh.acc_empty[i], 4 * C::groups * C::ctas); }
-        mbar_init(&sh.drained, 1);
+        for (int i = 0; i < kChunks; ++i) { mbar_init(&sh.scale_full[i], 1); mbar_init(&sh.scale_empty[i], 4 * C::groups); }
+        mbar_init(&sh.drained, 2);
         mbar_fence_init();
     }
     if (warp == C::mma_warp) tmem_alloc<C::ctas>(&sh.tmem, C::columns);
@@ -350,15 +408,13 @@ matmul_fp8_kernel(const Fp8Args a, const __grid_constant__ CUtensorMap map_w, co
                        (int)(blockIdx.x / C::ctas), (int)(all < limit ? all : limit), (int)(gridDim.x / C::ctas)};
     bool ok = true;
     if (warp < 4 * C::groups) {
-        if constexpr (C::split) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         ok = epilogue<C, GLU>(w, warp);
-    } else {
-        if constexpr (C::split) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == C::load_warp) {
-            if (lane == 0) ok = load_tiles<C, GLU>(w, &map_w, &map_a, &map_all);
-        } else if (warp == C::mma_warp) {
-            if (cta == 0) ok = issue_mma(w);
-        }
+    } else if (warp == C::load_warp) {
+        if (lane == 0) ok = load_tiles<C, GLU>(w, &map_w, &map_a, &map_all);
+    } else if (warp == C::mma_warp || warp == C::mma_warp + 1) {
+        if (cta == 0) ok = issue_mma(w, warp - C::mma_warp);
+    } else if (warp == C::scale_warp) {
+        ok = load_scales<C, GLU>(w);
     }
     if (!ok && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
     __syncwarp();
@@ -379,14 +435,7 @@ cudaError_t launch(const Fp8Args& a, const void* rows, const void* weights, int 
     if (most > INT32_MAX - sms) return cudaErrorInvalidValue;   // more output than any memory holds
     const int64_t tiles = most < sms / C::ctas ? most : sms / C::ctas;
     static std::atomic<uint64_t> done;
-    cudaError_t e;
-    if (C::split && done.load(std::memory_order_relaxed) == 0) {   // the split counts on what the launch gives
-        cudaFuncAttributes attr;
-        e = cudaFuncGetAttributes(&attr, matmul_fp8_kernel<C, GLU>);
-        if (e != cudaSuccess) return e;
-        if (attr.numRegs != 168) return cudaErrorInvalidConfiguration;
-    }
-    e = allow_smem(matmul_fp8_kernel<C, GLU>, C::smem, done);
+    const cudaError_t e = allow_smem(matmul_fp8_kernel<C, GLU>, C::smem, done);
     if (e != cudaSuccess) return e;
     return launch_overlapped_clusters(matmul_fp8_kernel<C, GLU>, C::ctas, dim3((unsigned)(C::ctas * tiles)), C::threads, C::smem, st,
                                       a, map_w, map_a, map_all);

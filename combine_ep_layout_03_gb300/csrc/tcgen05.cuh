@@ -137,6 +137,9 @@ __device__ __forceinline__ void tmem_free_pair(uint32_t addr, uint32_t columns) 
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// This warp's loads have arrived.  Only volatile code is sure to stay behind it.
+__device__ __forceinline__ void tmem_wait_loads() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
 // 32 columns of this warp's 32 lanes: register i of a lane is column i.  Nothing may read them before
 // tmem_wait_loads().
 __device__ __forceinline__ void tmem_start32(uint32_t addr, uint32_t r[32]) {
@@ -151,20 +154,18 @@ __device__ __forceinline__ void tmem_start32(uint32_t addr, uint32_t r[32]) {
                  : "r"(addr));
 }
 
-// This warp's loads have arrived: those of r among them (named here, so that their uses stay behind the wait).
-__device__ __forceinline__ void tmem_wait_loads(uint32_t r[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-                 :: "memory");
-}
-
 __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t r[32]) {
     tmem_start32(addr, r);
-    tmem_wait_loads(r);
+    tmem_wait_loads();
+}
+
+// 16 columns, as tmem_start32().
+__device__ __forceinline__ void tmem_start16(uint32_t addr, uint32_t r[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(addr));
 }
 
 __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t r[32]) {
