@@ -9,7 +9,18 @@ namespace {
 
 struct Tile { int64_t row0; int expert, m, n, channel; };   // n: MMA columns, channel: tile of output channels
 
-// Tiles of one expert are neighbours, its token tiles fastest: concurrent pairs share weights and tokens in L2.
+// In which order the tiles of a matrix are taken: token tiles in groups of eight, all channels of a group before the next
+// one, its token tiles fastest.  What runs at a time then covers about as many token tiles as channel tiles, and reads
+// few of either.
+struct Place { int tile, channel; };
+__device__ __forceinline__ Place place_of(uint32_t local, uint32_t tiles, uint32_t ctiles) {
+    constexpr uint32_t kGroup = 8;
+    const uint32_t group = tiles <= kGroup ? 0 : local / (kGroup * ctiles);
+    const uint32_t in = min(kGroup, tiles - group * kGroup), rest = local - group * kGroup * ctiles;
+    return {(int)(group * kGroup + rest % in), (int)(rest / in)};
+}
+
+// Tiles of one expert are neighbours: concurrent pairs share weights and tokens in L2.
 // The roles look tiles up between one tile's work and the next, so it has to be quick: a whole warp goes on from
 // its last expert, 32 experts at a time, and all counts are 32 bits wide (32 experts of 1152 rows, 1024 x 4096:
 // 217 us, with a binary search and 64-bit quotients 233; 512 experts of 8 rows, 4096 x 1024: 319, 331).
@@ -26,7 +37,8 @@ __device__ __forceinline__ Tile tile_of(const Segments& s, int E, int ctiles, in
     const uint32_t tiles = s.tile[e + 1] - s.tile[e];
     const uint32_t local = item - s.tile[e] * ctiles;
     // the segment's groups of 32 rows dealt out evenly: no tile is much shorter, and none pays for a row more
-    const int groups = (s.rows[e] + 31) / 32, j = (int)(local % tiles), each = (int)((uint32_t)groups / tiles);
+    const Place p = place_of(local, tiles, (uint32_t)ctiles);
+    const int groups = (s.rows[e] + 31) / 32, j = p.tile, each = (int)((uint32_t)groups / tiles);
     const int more = groups - each * (int)tiles;
     const int first = 32 * (j * each + min(j, more));
     Tile t;
@@ -34,7 +46,7 @@ __device__ __forceinline__ Tile tile_of(const Segments& s, int E, int ctiles, in
     t.row0 = (int64_t)s.base[e] + first;
     t.m = min(32 * (each + (j < more)), s.rows[e] - first);
     t.n = (t.m + 31) / 32 * 32;
-    t.channel = (int)(local / tiles);
+    t.channel = p.channel;
     return t;
 }
 

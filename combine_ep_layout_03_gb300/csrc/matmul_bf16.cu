@@ -84,8 +84,9 @@ struct Work {
             Tile t;
             e = (int)((uint32_t)item / each);
             t.expert = e;
-            t.channel = (int)(local / (uint32_t)rtiles);
-            t.row0 = (int64_t)(local % (uint32_t)rtiles) * C::tile;
+            const Place p = place_of(local, (uint32_t)rtiles, (uint32_t)ctiles);
+            t.channel = p.channel;
+            t.row0 = (int64_t)p.tile * C::tile;
             t.m = min(C::tile, a.n - (int)t.row0);
             t.n = (t.m + 31) / 32 * 32;
             steps = (sh.seg.rows[e] + kStep - 1) / kStep;
