@@ -8,7 +8,7 @@
 // rows pays for few.  The operands lie as they do in memory: an operand whose reduced index is contiguous is K-major,
 // else MN-major (w for da, both for dw), and no transposed copy is made of anything.
 //
-// Warps: 0 TMA, 1 MMA (of the pair's first CTA), 2 tensor memory, 3 ends of segments (dw), 4-7 epilogue.  Both CTAs'
+// Warps: 0 TMA, 1 MMA (of the pair's first CTA), 2 tensor memory, 3 ends of segments (dw), 4-11 epilogue.  Both CTAs'
 // loads report to the first one's barriers.  Two accumulators take turns, so a tile's epilogue runs under the next
 // one's products.  Every wait is bounded (EP_ERR_TIMEOUT).
 //
@@ -36,7 +36,8 @@ struct Bf16Args {
     int32_t wide, accumulate;    // WEIGHTS: float32 output; added to what is there
 };
 
-constexpr int kThreads = 256;
+constexpr int kGroups = 2;                // of four epilogue warps, which take every other 32 rows of a tile
+constexpr int kThreads = 32 * (4 + 4 * kGroups);
 constexpr int kRows = 128;                // channels of a CTA
 constexpr int kStep = 64;                 // of the sum a stage: 128 bytes
 constexpr int kBytesA = kRows * 128;
@@ -54,6 +55,7 @@ struct Config {
 };
 
 using Thick = Config<256, 6>;
+using Mid = Config<128, 8>;
 using Thin = Config<64, 10>;
 
 template <class C>
@@ -243,7 +245,7 @@ __device__ __forceinline__ bool issue_mma(const Work<C, F>& w) {
 
 // Lane: a channel; with gates and ups, lanes 0-15 hold the gates of lanes 16-31's ups.
 template <class C, Form F>
-__device__ __forceinline__ bool epilogue(const Work<C, F>& w, int warp) {
+__device__ __forceinline__ bool epilogue(const Work<C, F>& w, int warp, int group) {
     const int lane = threadIdx.x & 31;
     const uint32_t acc_empty0 = cluster_addr(smem_addr(&w.sh.acc_empty[0]), 0);
     const int64_t outs = w.a.outs;
@@ -266,7 +268,7 @@ __device__ __forceinline__ bool epilogue(const Work<C, F>& w, int warp) {
             tmem_fence_after();
         }
         const uint32_t d = w.tmem + ((uint32_t)(warp * 32) << 16) + acc.stage * C::tile;
-        for (int c0 = 0; c0 < t.m; c0 += 32) {
+        for (int c0 = 32 * group; c0 < t.m; c0 += 32 * kGroups) {
             uint32_t v[32];
             if (some) {
                 tmem_load32(d + c0, v);
@@ -350,6 +352,8 @@ matmul_bf16_kernel(const Bf16Args a, const __grid_constant__ CUtensorMap map_c, 
                    const __grid_constant__ CUtensorMap map_half) {
     extern __shared__ uint8_t dynamic[];
     __shared__ Shared<C> sh;
+    static_assert(C::smem + sizeof(sh) <= 227 * 1024, "shared memory");
+    static_assert(F != WEIGHTS || C::half % 64 == 0, "a box of rows of dw is 64 wide");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         prefetch_map(&map_c);
@@ -361,7 +365,7 @@ matmul_bf16_kernel(const Bf16Args a, const __grid_constant__ CUtensorMap map_c, 
     if (tid == 0) {
         // full: the first CTA's bytes announced; with segments that may end anywhere, a word of either CTA
         for (int i = 0; i < C::stages; ++i) { mbar_init(&sh.full[i], F == WEIGHTS ? 2 : 1); mbar_init(&sh.empty[i], 1); mbar_init(&sh.tail[i], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&sh.acc_full[i], 1); mbar_init(&sh.acc_empty[i], 8); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&sh.acc_full[i], 1); mbar_init(&sh.acc_empty[i], 8 * kGroups); }
         mbar_init(&sh.drained, 1);
         mbar_fence_init();
     }
@@ -387,7 +391,7 @@ matmul_bf16_kernel(const Bf16Args a, const __grid_constant__ CUtensorMap map_c, 
     } else if (warp == 3) {
         if (F == WEIGHTS) ok = clear_tails(w);
     } else if (warp >= 4) {
-        ok = epilogue(w, warp & 3);
+        ok = epilogue(w, warp & 3, (warp >> 2) - 1);
     }
     if (!ok && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
     __syncwarp();
@@ -426,17 +430,32 @@ cudaError_t launch(const Bf16Args& a, const void* c, const void* r, int sms, cud
     return launch_overlapped(matmul_bf16_kernel<C, F>, dim3((unsigned)(2 * pairs)), kThreads, C::smem, st, a, map_c, map_r, map_half);
 }
 
-constexpr int kThinRows = 64;
+// Which tile: the larger ones do more products for what they read, the smaller ones are more, and pay for fewer rows that
+// are none.  Measured, us (256, 128, 64 rows a tile):
+//   one matrix: 128 rows x 4096 x 4096: 29.3, 23.2, 23.2; 2000 x 2048 x 1000: 19.1, 17.1, 23.2; 4000 x 2048 x 2000: 29.3,
+//   39.6, 60.1; experts: 64 of 96 rows, 2048 x 1024: 73.7, 68.3, 70.4; 64 of 128, 4096 x 2048: 201, 193, 218; 128 of 200:
+//   392, 441, 734; 128 of 6 with SwiGLU: 361, 353, 334.
+//   dw: 2000 rows, 1024 x 1024: 21.2, 17.1; 16384 rows: 88.7, 72.4; 4 experts of 2000 rows, 2048 x 512: 23.2, 27.3; 128 of 64
+//   rows, 2048 x 1024: 132, 156.
+// So: 64 up to 32 rows an expert; 128 where its rounds of tiles, which take 0.8 of the time of 256's, are that few, or
+// segments are no longer than that.
+template <Form F>
+cudaError_t choose(const Bf16Args& a, const void* c, const void* r, int sms, cudaStream_t st) {
+    const int64_t per_pair = F == GLU ? kRows : 2 * kRows, ctiles = (a.outs + per_pair - 1) / per_pair, pairs = sms / 2;
+    const int64_t each = F == WEIGHTS ? a.n : (a.rows + a.E - 1) / a.E;   // rows of a segment, or of a matrix
+    if constexpr (F != WEIGHTS) {
+        if (each <= 32) return launch<Thin, F>(a, c, r, sms, st);
+    }
+    const int64_t mid = ((each + Mid::tile - 1) / Mid::tile * a.E * ctiles + pairs - 1) / pairs;
+    const int64_t thick = ((each + Thick::tile - 1) / Thick::tile * a.E * ctiles + pairs - 1) / pairs;
+    return each <= Mid::tile || 4 * mid < 5 * thick ? launch<Mid, F>(a, c, r, sms, st) : launch<Thick, F>(a, c, r, sms, st);
+}
 
 template <Form F>
 ep_status run(const Bf16Args& a, const void* c, const void* r, cudaStream_t st) {
     const int sms = ep_current_sms();
     if (sms <= 0) return EP_ERR_CUDA;
-    const bool thin = F != WEIGHTS && (a.rows + a.E - 1) / a.E <= kThinRows;
-    cudaError_t e;
-    if constexpr (F == WEIGHTS) e = launch<Thick, F>(a, c, r, sms, st);
-    else e = thin ? launch<Thin, F>(a, c, r, sms, st) : launch<Thick, F>(a, c, r, sms, st);
-    return e == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+    return choose<F>(a, c, r, sms, st) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
