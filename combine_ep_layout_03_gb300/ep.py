@@ -801,16 +801,53 @@ class EPLayout:
         ep_dispatch_ex(self.h, x, x_scales, quant, scales, scale_kind, flags, recv_data, recv_scales,
                        recv_data.numel() // db, stream)
 
-    def expert_matmul(self, data: torch.Tensor, scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
-                      out: torch.Tensor, swiglu: bool = False, stream=None) -> torch.Tensor:
-        """ep_expert_matmul over the segments of this layout; too few rows show in status()."""
+    def _segments(self) -> tuple[torch.Tensor, torch.Tensor]:
+        """expert_base [E + 1] and the status word, as views of the workspace."""
         if self._expert_base is None:
             v = ep_handle_views(self.h)
             off = v.expert_base - self.ws.data_ptr()
             self._expert_base = self.ws[off:off + 4 * (self.E + 1)].view(torch.int32)
             self._status = self.ws[:4].view(torch.int32)
-        ep_expert_matmul(data, scales, w, w_scales, self._expert_base, out, swiglu, self._status, stream)
+        return self._expert_base, self._status
+
+    @property
+    def rows_used(self) -> torch.Tensor:
+        """How many receive rows the layout uses: int32 [1] on the device."""
+        return self._segments()[0][self.E:]
+
+    def expert_matmul(self, data: torch.Tensor, scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                      out: torch.Tensor, swiglu: bool = False, stream=None) -> torch.Tensor:
+        """ep_expert_matmul over the segments of this layout; too few rows show in status()."""
+        base, status = self._segments()
+        ep_expert_matmul(data, scales, w, w_scales, base, out, swiglu, status, stream)
         return out
+
+    def expert_matmul_fp8(self, data: torch.Tensor, scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                          out: torch.Tensor, swiglu: bool = False, stream=None) -> torch.Tensor:
+        """ep_expert_matmul_fp8 over the segments of this layout."""
+        base, status = self._segments()
+        ep_expert_matmul_fp8(data, scales, w, w_scales, base, out, swiglu, status, stream)
+        return out
+
+    def expert_matmul_bf16(self, rows: torch.Tensor, w: torch.Tensor, out: torch.Tensor, swiglu: bool = False,
+                           stream=None) -> torch.Tensor:
+        """ep_expert_matmul_bf16 over the segments of this layout."""
+        base, status = self._segments()
+        ep_expert_matmul_bf16(rows, w, base, out, swiglu, status, stream)
+        return out
+
+    def expert_matmul_grad_rows(self, grad_c: torch.Tensor, w: torch.Tensor, grad_a: torch.Tensor, stream=None) -> torch.Tensor:
+        """ep_expert_matmul_grad_rows over the segments of this layout."""
+        base, status = self._segments()
+        ep_expert_matmul_grad_rows(grad_c, w, base, grad_a, status, stream)
+        return grad_a
+
+    def expert_matmul_grad_weights(self, grad_c: torch.Tensor, a: torch.Tensor, grad_w: torch.Tensor, accumulate: bool = False,
+                                   stream=None) -> torch.Tensor:
+        """ep_expert_matmul_grad_weights over the segments of this layout."""
+        base, status = self._segments()
+        ep_expert_matmul_grad_weights(grad_c, a, base, grad_w, accumulate, status, stream)
+        return grad_w
 
     def combine(self, y: torch.Tensor, topk_weights: torch.Tensor, out: torch.Tensor,
                 shared: torch.Tensor | None = None, stream=None) -> torch.Tensor:

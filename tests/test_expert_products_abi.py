@@ -146,3 +146,19 @@ def test_binding_refuses_wrong_fp8_products():
             dict(out=f(4, 160, dtype=bf)), dict(swiglu=True), dict(swiglu=True, out=f(4, 160, dtype=bf)),
             dict(a=f(4, 192, dtype=e4), a_scales=f(4, 1), w=f(3, 320, 192, dtype=e4), w_scales=f(3, 3, 1))]
     refused(ep.ep_expert_matmul_fp8, good, bads)
+
+
+def test_layers_refuse_mixed_weights():
+    from combine_ep_layout_03_gb300.expert_layer import ExpertLayer, TrainableExperts
+    f, bf, e4, i8 = torch.zeros, torch.bfloat16, torch.float8_e4m3fn, torch.int8
+    gamma, s = f(128, dtype=bf), f(4, 2, 1)
+    for w13, s13, w2, s2 in ((bf, s, bf, s), (bf, None, bf, s), (e4, None, e4, None), (i8, None, i8, None), (e4, s, i8, s), (bf, None, e4, s)):
+        with pytest.raises(ep.EPError) as e:
+            ExpertLayer(1, 100, f(4, 256, 128, dtype=w13), s13, f(4, 128, 128, dtype=w2), s2, gamma, 2)
+        assert e.value.status == ep.EP_ERR_INVALID_ARG
+    with pytest.raises(ep.EPError):   # FP8: whole blocks
+        ExpertLayer(1, 100, f(4, 128, 128, dtype=e4), s, f(4, 128, 64, dtype=e4), s, gamma, 2)
+    layer = ExpertLayer(1, 8, f(4, 256, 128, dtype=e4), s, f(4, 128, 128, dtype=e4), s, gamma, 2)
+    assert not layer.few and layer.rows.dtype is e4
+    with pytest.raises(ep.EPError):
+        TrainableExperts(1, 0, f(4, 256, 128, dtype=bf), f(4, 128, 128, dtype=bf), 2)
