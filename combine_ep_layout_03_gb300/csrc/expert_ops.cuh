@@ -95,6 +95,9 @@ struct MatmulArgs {
 };
 
 cudaError_t launch_matmul_skinny(const MatmulArgs& a, int sms, cudaStream_t st);
+// The same of FP8 rows and matrices with scales for each block of 128 (ep_expert_matmul_fp8), and of bf16 ones without.
+cudaError_t launch_matmul_skinny_fp8(const MatmulArgs& a, int sms, cudaStream_t st);
+cudaError_t launch_matmul_skinny_bf16(const MatmulArgs& a, int sms, cudaStream_t st);
 
 // The segments of a grouped product in shared memory: first row and first token tile of each
 // expert.  Device data is not trusted with addresses: the segments have to ascend inside the buffers'

@@ -430,6 +430,20 @@ cudaError_t launch(const Bf16Args& a, const void* c, const void* r, int sms, cud
     return launch_overlapped(matmul_bf16_kernel<C, F>, dim3((unsigned)(2 * pairs)), kThreads, C::smem, st, a, map_c, map_r, map_half);
 }
 
+// Few enough rows and weights for matmul_skinny.cu, which is on every SM from the start, and reads weights the slower the
+// more rows there are; a tile here takes 0.3 us for 64 k, however few its rows.
+// Measured, us in a graph (that kernel, Thin): one matrix: 8 rows x 4096 x 4096 7.1, 17.8; 32 rows 11.3, 17.8; 32 rows x 7168 x
+// 512 10.1, 27.2; experts of 2048 x 1024: 8 of 32 rows with SwiGLU 13.3, 14.4; 16 of 8 rows 14.4, 12.5; 32 of 8 rows 33.6,
+// 27.6; 64 of 4 rows, 4096 x 1024: 95.8, 87.9.
+bool few_rows(const Bf16Args& a, bool glu, int sms) {
+    const int64_t experts = a.rows < a.E ? a.rows : a.E, rows = (a.rows + a.E - 1) / a.E, per_pair = glu ? kRows : 2 * kRows;
+    if (rows > 32) return false;
+    const double rate[4] = {5.0, 4.5, 4.0, 3.5};   // bytes of weights a picosecond, by tiles of eight rows
+    const double here = 3.5 + 2e-6 * (double)(experts * a.outs * (glu ? 2 : 1)) * a.reduced / rate[(rows - 1) / 8];
+    const int64_t rounds = (experts * ((a.outs + per_pair - 1) / per_pair) + sms / 2 - 1) / (sms / 2);
+    return here <= 4.0 + 0.3 * (double)(rounds * ((a.reduced + kStep - 1) / kStep));
+}
+
 // Which tile: the larger ones do more products for what they read, the smaller ones are more, and pay for fewer rows that
 // are none.  Measured, us (256, 128, 64 rows a tile):
 //   one matrix: 128 rows x 4096 x 4096: 29.3, 23.2, 23.2; 2000 x 2048 x 1000: 19.1, 17.1, 23.2; 4000 x 2048 x 2000: 29.3,
@@ -443,6 +457,20 @@ template <Form F>
 cudaError_t choose(const Bf16Args& a, const void* c, const void* r, int sms, cudaStream_t st) {
     const int64_t per_pair = F == GLU ? kRows : 2 * kRows, ctiles = (a.outs + per_pair - 1) / per_pair, pairs = sms / 2;
     const int64_t each = F == WEIGHTS ? a.n : (a.rows + a.E - 1) / a.E;   // rows of a segment, or of a matrix
+    if constexpr (F == FORWARD || F == GLU) {
+        if (few_rows(a, F == GLU, sms)) {
+            MatmulArgs m{};
+            m.a = (const uint8_t*)r;
+            m.w = (const uint8_t*)c;
+            m.expert_base = a.expert_base;
+            m.out = (uint16_t*)a.out;
+            m.status = a.status;
+            m.rows = a.rows;
+            m.K = a.reduced; m.N = F == GLU ? 2 * a.outs : a.outs; m.E = a.E;
+            m.swiglu = F == GLU;
+            return launch_matmul_skinny_bf16(m, sms, st);
+        }
+    }
     if constexpr (F != WEIGHTS) {
         if (each <= 32) return launch<Thin, F>(a, c, r, sms, st);
     }

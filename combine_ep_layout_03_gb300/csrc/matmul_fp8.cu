@@ -62,7 +62,6 @@ struct Config {
 using Thick = Config<2, 128, 256, 5, 2, 64>;
 using Mid = Config<1, 128, 128, 5, 4, 64>;
 using Thin = Config<1, 32, 128, 9, 4, 64>;
-using Small = Config<1, 32, 32, 20, 8, 32>;
 
 // The products of scales of a chunk of blocks, by token row of a CTA: of the tile's first block of channels, and of its
 // second (or of the ups).
@@ -441,13 +440,38 @@ cudaError_t launch(const Fp8Args& a, const void* rows, const void* weights, int 
                                       a, map_w, map_a, map_all);
 }
 
+// Few enough rows and weights for matmul_skinny.cu, which is on every SM from the start, and reads weights the slower the
+// more rows there are; a tile here takes a third of a microsecond a block, however few its rows.
+// Measured, us in a graph (that kernel, Thin): one matrix, 4096 x 4096: 8 rows 6.4, 13.4; 32 rows 10.9, 15.2; 7168 x 4096 with
+// SwiGLU: 8 rows 8.9, 21.2; 32 rows 18.4, 22.0; experts of 2048 x 1024: 8 of 16 rows 10.0, 9.9; 8 of 32 with SwiGLU 15.0, 10.6;
+// 16 of 8 rows 13.8, 9.7; 32 of 8 rows 24.4, 16.1; 64 of 4 rows, 4096 x 1024: 73, 52.
+bool few_rows(const Fp8Args& a, bool glu, int sms) {
+    const int64_t experts = a.rows < a.E ? a.rows : a.E, rows = (a.rows + a.E - 1) / a.E, per_tile = glu ? Thin::n / 2 : Thin::n;
+    if (rows > 32) return false;
+    const double rate[4] = {3.3, 2.8, 2.2, 1.7};   // bytes of weights a picosecond, by tiles of eight rows
+    const double here = 3.0 + 1e-6 * (double)(experts * a.outs * (glu ? 2 : 1)) * 128 * a.blocks / rate[(rows - 1) / 8];
+    const int64_t rounds = (experts * ((a.outs + per_tile - 1) / per_tile) + sms - 1) / sms;
+    return here <= 4.0 + 0.33 * (double)(rounds * a.blocks);
+}
+
 template <bool GLU>
 cudaError_t run(const Fp8Args& a, const void* rows, const void* weights, int sms, cudaStream_t st) {
-    const int64_t each = (a.rows + a.E - 1) / a.E, experts = a.rows < a.E ? a.rows : a.E;
-    if (each <= 32) {
-        const int64_t per_tile = GLU ? Thin::n / 2 : Thin::n, tiles = experts * ((a.outs + per_tile - 1) / per_tile);
-        return tiles < sms ? launch<Small, GLU>(a, rows, weights, sms, st) : launch<Thin, GLU>(a, rows, weights, sms, st);
+    const int64_t each = (a.rows + a.E - 1) / a.E;
+    if (few_rows(a, GLU, sms)) {
+        MatmulArgs m{};
+        m.a = (const uint8_t*)rows;
+        m.a_scales = a.a_scales;
+        m.w = (const uint8_t*)weights;
+        m.w_scales = a.w_scales;
+        m.expert_base = a.expert_base;
+        m.out = a.out;
+        m.status = a.status;
+        m.rows = a.rows;
+        m.K = 128 * a.blocks; m.N = GLU ? 2 * a.outs : a.outs; m.E = a.E;
+        m.swiglu = GLU;
+        return launch_matmul_skinny_fp8(m, sms, st);
     }
+    if (each <= 32) return launch<Thin, GLU>(a, rows, weights, sms, st);
     if (each <= 192) return launch<Mid, GLU>(a, rows, weights, sms, st);
     return launch<Thick, GLU>(a, rows, weights, sms, st);
 }

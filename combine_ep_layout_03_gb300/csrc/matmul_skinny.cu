@@ -1,13 +1,15 @@
-// matmul_skinny.cu -- the 8-bit integer product of expert rows for experts with few
-// rows each, where reading the weights is the work:
-//   c[r, n] = a_scales[r] * w_scales[e, n] * sum_k a[r, k] * w[e, n, k]
+// matmul_skinny.cu -- the products of expert rows for experts with few rows each, where reading the weights is the
+// work: 8-bit integers, FP8 with scales for each block of 128, and bf16 (ep_expert_matmul and its two relatives).
+//   c[r, n] = a_scales[r] * w_scales[e, n] * sum_k a[r, k] * w[e, n, k]      (8-bit integers; others likewise)
 // An item is 16 weight rows (eight gates and their eight ups with swiglu) against up to
 // 32 rows of one expert: the warps of a CTA share the item's k and add their parts in
-// shared memory, in warp order.  The codes become bf16 on the way to the tensor cores,
+// shared memory, in warp order.  Integer codes become bf16 on the way to the tensor cores,
 // which is exact, and a product of two codes is exact in float32; sums stay exact up to
-// 2^24 (1024 terms of the largest size, any number of ordinary ones).
+// 2^24 (1024 terms of the largest size, any number of ordinary ones).  A 128-byte piece of FP8 rows is a block: its
+// sum is taken alone, scaled and added.
 //
-// Measured: 8 rows x 4096 x 4096 7.0 us (its floor, 17 MB, is 2.5 us); 32 rows 12.9 us.  What bounds
+// Measured: 8 rows x 4096 x 4096 7.0 us (its floor, 17 MB, is 2.5 us); 32 rows 12.9 us.  FP8 6.4 and 10.9 us in a graph, bf16
+// 7.1 (33 MB) and 11.3.  What bounds
 // it is a warp's start, its first loads and its few pieces one after another; the host takes 5.1 us a call.
 #include "expert_ops.cuh"
 #include "skinny.cuh"
@@ -38,7 +40,10 @@ __device__ __forceinline__ Item item_of(const Segments& s, const MatmulArgs& a, 
     return t;
 }
 
-template <bool GLU>
+// What the rows and matrices hold.
+enum Kind { INT8, FP8, BF16 };
+
+template <Kind KIND, bool GLU>
 __global__ void __launch_bounds__(kThreads, 2) matmul_skinny_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_w) {
     extern __shared__ uint8_t dynamic[];
     __shared__ uint64_t bars[kWarps * kDepth];
@@ -50,7 +55,8 @@ __global__ void __launch_bounds__(kThreads, 2) matmul_skinny_kernel(const Matmul
     if (!load_segments<kThreads>(s, a, kTileRows)) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
     constexpr int per = GLU ? 8 : 16;   // output channels of an item
-    const int outs = GLU ? a.N / 2 : a.N, ctiles = (outs + per - 1) / per, pieces = (a.K + 127) / 128;
+    const int outs = GLU ? a.N / 2 : a.N, ctiles = (outs + per - 1) / per;
+    const int row_bytes = KIND == BF16 ? 2 * a.K : a.K, pieces = (row_bytes + 127) / 128;
     const int64_t items = (int64_t)s.tile[a.E] * ctiles;
 
     Ring ring(slots, bars, warp, lane);
@@ -78,9 +84,10 @@ __global__ void __launch_bounds__(kThreads, 2) matmul_skinny_kernel(const Matmul
         const Item t = item_of(s, a, ctiles, item);
         const int64_t row0 = (int64_t)s.base[t.e] + t.first;
         float* sums = red + buffer * kSums;
-        // the scales of this thread's first result arrive meanwhile
+        // the scales of this thread's first result arrive meanwhile (FP8's change with every piece)
         struct Scales { float row, gate, up; };
         auto scales = [&](int i) {
+            if constexpr (KIND != INT8) return Scales{1.0f, 1.0f, 1.0f};
             const float* sw = a.w_scales + (int64_t)t.e * a.N + min(t.channel * per + i % per, outs - 1);
             return Scales{a.a_scales[row0 + i / per], sw[0], GLU ? sw[outs] : 0.0f};
         };
@@ -91,13 +98,22 @@ __global__ void __launch_bounds__(kThreads, 2) matmul_skinny_kernel(const Matmul
             float acc[NT][4];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                tok[j] = a.a + (row0 + min(j * 8 + g, t.m - 1)) * a.K;   // columns past the last repeat it
+                tok[j] = a.a + (row0 + min(j * 8 + g, t.m - 1)) * row_bytes;   // columns past the last repeat it
                 acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
             }
-            auto load = [&](TokenPart<true, true>& t, int i, int c) {
-                load_tokens<true, true>(t, tok[i % NT], c, i / NT, q * 16, a.K);
-            };
-            TokenQueue<true, true, 2 * NT, 8> queue, next;   // next: with one tile, the tokens of the next piece
+            constexpr bool kInt8 = KIND == INT8;
+            using Part = TokenPart<kInt8, kInt8>;
+            auto load = [&](Part& t, int i, int c) { load_tokens<kInt8, kInt8>(t, tok[i % NT], c, i / NT, q * 16, row_bytes); };
+            TokenQueue<kInt8, kInt8, Part::kOfPiece * NT, 8> queue, next;   // next: with one tile, the tokens of the next piece
+            const float* sa[KIND == FP8 ? 2 * NT : 1];   // of this lane's two columns of each tile
+            const float* sw[2];                          // of rows g and g + 8 (with SwiGLU: gates and ups)
+            if constexpr (KIND == FP8) {
+#pragma unroll
+                for (int j = 0; j < 2 * NT; ++j) sa[j] = a.a_scales + (row0 + min((j / 2) * 8 + 2 * q + (j & 1), t.m - 1)) * pieces;
+                const int blocks = (outs + 127) / 128;
+                sw[0] = a.w_scales + ((int64_t)t.e * (GLU ? 2 : 1) * blocks + (t.channel * per >> 7)) * pieces;
+                sw[1] = sw[0] + (GLU ? (int64_t)blocks * pieces : 0);
+            }
             if (NT == 1 && warp < pieces) next.start([&](auto& t, int i) { load(t, i, warp); });
             for (int c = warp; c < pieces; c += kWarps) {
                 if constexpr (NT == 1) {
@@ -106,11 +122,33 @@ __global__ void __launch_bounds__(kThreads, 2) matmul_skinny_kernel(const Matmul
                 } else {
                     queue.start([&](auto& t, int i) { load(t, i, c); });
                 }
+                float row_scale[KIND == FP8 ? 2 * NT : 1], weight_scale[2];
+                if constexpr (KIND == FP8) {
+#pragma unroll
+                    for (int j = 0; j < 2 * NT; ++j) row_scale[j] = sa[j][c];
+                    weight_scale[0] = sw[0][c];
+                    weight_scale[1] = sw[1][c];
+                }
                 uint4 lo[2], hi[2];
                 ring.take(lo, hi);
-                mma_piece<true, true, NT, 1>(acc, lo, hi, [&](int i) {
-                    return queue.take(i, [&](auto& t, int n) { load(t, n, c); });
-                });
+                auto tokens = [&](int i) { return queue.take(i, [&](auto& t, int n) { load(t, n, c); }); };
+                if constexpr (KIND == FP8) {
+                    // a piece is a block: its sum is scaled and added to the blocks' before
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const Part t = tokens(j);
+                        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            mma_e4m3(sum, lo[h].x, hi[h].x, lo[h].y, hi[h].y, t.v[h].x, t.v[h].y);
+                            mma_e4m3(sum, lo[h].z, hi[h].z, lo[h].w, hi[h].w, t.v[h].z, t.v[h].w);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[j][i] = __fmaf_rn(sum[i], row_scale[2 * j + (i & 1)] * weight_scale[i >> 1], acc[j][i]);
+                    }
+                } else {
+                    mma_piece<kInt8, kInt8, NT, 1>(acc, lo, hi, tokens);
+                }
                 __syncwarp();
                 fetch();
             }
@@ -136,9 +174,12 @@ __global__ void __launch_bounds__(kThreads, 2) matmul_skinny_kernel(const Matmul
                 if constexpr (GLU) u += sums[(k * cols + col) * 16 + c + 8];
             }
             const int64_t row = row0 + col;
-            const Scales f = i == tid ? mine : scales(i);
-            v = v * f.row * f.gate;
-            if constexpr (GLU) v = v / (1.0f + expf(-v)) * (u * f.row * f.up);
+            if constexpr (KIND == INT8) {
+                const Scales f = i == tid ? mine : scales(i);
+                v = v * f.row * f.gate;
+                u = u * f.row * f.up;
+            }
+            if constexpr (GLU) v = v / (1.0f + expf(-v)) * u;
             a.out[row * outs + ch] = (uint16_t)pack_bf16x2_rn(v, 0.0f);
         }
     }
@@ -163,22 +204,27 @@ bool is_skinny(const MatmulArgs& a, int sms) {
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
 
-}  // namespace
-
-cudaError_t launch_matmul_skinny(const MatmulArgs& a, int sms, cudaStream_t st) {
-    const int64_t ctiles = a.swiglu ? (a.N / 2 + 7) / 8 : (a.N + 15) / 16;
+template <Kind KIND>
+cudaError_t launch(const MatmulArgs& a, int sms, cudaStream_t st) {
+    const int64_t ctiles = a.swiglu ? (a.N / 2 + 7) / 8 : (a.N + 15) / 16, row_bytes = KIND == BF16 ? 2 * (int64_t)a.K : a.K;
     const int64_t most_tiles = (a.rows + kTileRows - 1) / kTileRows + (a.E > 1 ? a.E : 0);
     const int64_t items = ctiles * most_tiles;
     const unsigned grid = (unsigned)(items < 2 * sms ? items : 2 * sms);
-    auto kernel = a.swiglu ? matmul_skinny_kernel<true> : matmul_skinny_kernel<false>;
+    auto kernel = a.swiglu ? matmul_skinny_kernel<KIND, true> : matmul_skinny_kernel<KIND, false>;
     CUtensorMap map_w;
-    if (!(a.swiglu ? make_pairs_map(&map_w, a.w, a.E, a.N / 2, a.K, 8) : make_experts_map(&map_w, a.w, a.E, a.N, a.K, 16)))
+    if (!(a.swiglu ? make_pairs_map(&map_w, a.w, a.E, a.N / 2, row_bytes, 8) : make_experts_map(&map_w, a.w, a.E, a.N, row_bytes, 16)))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done[2];
     const cudaError_t e = allow_smem(kernel, kSmem, done[a.swiglu]);
     if (e != cudaSuccess) return e;
     return launch_overlapped(kernel, dim3(grid), kThreads, kSmem, st, a, map_w);
 }
+
+}  // namespace
+
+cudaError_t launch_matmul_skinny(const MatmulArgs& a, int sms, cudaStream_t st) { return launch<INT8>(a, sms, st); }
+cudaError_t launch_matmul_skinny_fp8(const MatmulArgs& a, int sms, cudaStream_t st) { return launch<FP8>(a, sms, st); }
+cudaError_t launch_matmul_skinny_bf16(const MatmulArgs& a, int sms, cudaStream_t st) { return launch<BF16>(a, sms, st); }
 
 extern "C" ep_status ep_expert_matmul(const void* a, const float* a_scales, int64_t rows, int32_t k, const void* w,
                                       const float* w_scales, int32_t n, int32_t num_experts,
