@@ -55,12 +55,19 @@ struct Config {
     static constexpr uint32_t columns = ACCS * N;
     static_assert(columns <= 512 && (columns & (columns - 1)) == 0 && columns >= 32, "tensor memory");
     static_assert(bytes_a % 1024 == 0 && bytes % 1024 == 0 && width % 32 == 0 && N % width == 0, "swizzled rows; registers");
+    // Each of the two issuing warps looks at the stages of every other block only, and a parity tells two neighbouring
+    // phases apart, no more: with an odd number of stages it meets a stage at every second of its loads.  When it asks for
+    // block b there, block b - STAGES must be over.  It has issued b - 2, for which the accumulator of b - 2 - ACCS was
+    // read, and that is done in order.  (With five stages and four accumulators a warp could take a load that came late
+    // for the next one, and free its stage twice.)
+    static_assert(STAGES % 2 == 0 || STAGES >= ACCS + 2, "stages that no warp can lap");
+    static_assert(ACCS % 2 == 0, "an accumulator is one warp's");
     // an MMA reads 128 token rows, also where a stage has room for fewer: what follows is read for them, inside shared memory
     static_assert(bytes - bytes_a + staged >= (128 - ROWS) * 128, "rows past a stage's");
 };
 
 using Thick = Config<2, 128, 256, 5, 2, 64>;
-using Mid = Config<1, 128, 128, 5, 4, 64>;
+using Mid = Config<1, 128, 128, 5, 2, 64>;
 using Thin = Config<1, 32, 128, 9, 4, 64>;
 
 // The products of scales of a chunk of blocks, by token row of a CTA: of the tile's first block of channels, and of its
@@ -147,9 +154,10 @@ __device__ __forceinline__ bool load_tiles(const Work<C>& w, const CUtensorMap* 
     return ok && over;
 }
 
-// The waits and words of the loop over blocks, which is one chain of latencies: without votes and without branches on the
-// lane (those cost 50 to 100 clocks each).  A wait is bounded by its polls, each of which may park the thread.
-__device__ __forceinline__ bool wait_block(uint64_t* bar, uint32_t parity) {
+// The waits and words of the loop over blocks, which is one chain of latencies: without branches on the lane (50 to 100
+// clocks each).  A wait is bounded by its polls, each of which may park the thread.  Its answer is the warp's: lanes need
+// not leave the loop together, and what follows (loads of tensor memory, elections) asks for a converged warp.
+__device__ __forceinline__ bool wait_block(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
                  "POLL%=:\n\t"
@@ -158,19 +166,25 @@ __device__ __forceinline__ bool wait_block(uint64_t* bar, uint32_t parity) {
                  "add.u32 n, n, 1;\n\tsetp.lt.u32 p, n, %3;\n\t@p bra POLL%=;\n\t"
                  "setp.ne.u32 p, 0, 0;\n"
                  "OVER%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity), "r"(kMaxPolls) : "memory");
-    return ok != 0;
+                 : "=r"(ok) : "r"(bar), "r"(parity), "r"(kMaxPolls) : "memory");
+    return __all_sync(0xffffffffu, ok != 0);
 }
 
-// One lane (of a warp that has just met) arrives on this CTA's barrier, or on either CTA's.
-__device__ __forceinline__ void arrive_one(int lane, uint64_t* bar, bool when) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}"
-                 :: "r"(smem_addr(bar)), "r"((uint32_t)(lane == 0 && when)) : "memory");
+// One lane of a converged warp arrives on this CTA's barrier, or on either CTA's.
+__device__ __forceinline__ void arrive_one(int lane, uint32_t bar) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}"
+                 :: "r"(bar), "r"(lane) : "memory");
 }
 
-__device__ __forceinline__ void arrive_one_cluster(int lane, uint32_t bar, bool when) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}"
-                 :: "r"(bar), "r"((uint32_t)(lane == 0 && when)) : "memory");
+__device__ __forceinline__ void arrive_one_cluster(int lane, uint32_t bar) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}"
+                 :: "r"(bar), "r"(lane) : "memory");
+}
+
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 // Two warps issue, every other block each: a block's products start a fresh accumulator, so that their order does not
@@ -190,7 +204,10 @@ __device__ __forceinline__ bool issue_mma(const Work<C>& w, int which) {
     for (int64_t k = which; k < blocks; k += 2) {
         const uint32_t at = smem0 + r.stage * C::bytes, d = w.tmem + acc.stage * C::n;
         const uint64_t a = smem_desc_k128(at), b = smem_desc_k128(at + C::bytes_a);
-        if (!wait_block(&w.sh.full[r.stage], r.parity) || !wait_block(&w.sh.acc_empty[acc.stage], acc.parity ^ 1)) { ok = false; break; }
+        if (!wait_block(smem_addr(&w.sh.full[r.stage]), r.parity) || !wait_block(smem_addr(&w.sh.acc_empty[acc.stage]), acc.parity ^ 1)) {
+            ok = false;
+            break;
+        }
         tmem_fence_after();
         __syncwarp();
         if (elect_one()) {
@@ -294,8 +311,17 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
     uint8_t* const mine = w.staged + (group * 128 + mine_row) * kPitch;
     const int outs = w.a.outs, blocks = w.a.blocks;
     const bool bulk = outs % 8 == 0 && ((uintptr_t)w.a.out & 15) == 0;
-    Ring<C::accs> acc;
+    constexpr uint32_t kUps = sizeof(w.sh.scales[0].of[0]);   // from a gates' product of scales to the ups'
+    const uint32_t acc_full = smem_addr(&w.sh.acc_full[0]);
+    const uint32_t columns = w.tmem + ((uint32_t)(quarter * 32) << 16) + group * (GLU ? kHalf : kWidth);
+    // (all lanes' loads of an accumulator are over: the wait for them is the warp's)
+    auto release = [&](uint32_t at) {
+        tmem_fence_before();
+        if (C::ctas == 1) arrive_one(lane, smem_addr(&w.sh.acc_empty[0]) + 8 * at);
+        else arrive_one_cluster(lane, acc_empty0 + 8 * at);
+    };
     Ring<kChunks> scales;
+    uint32_t use = 0;   // of the accumulators
     int expert = 0;
     bool ok = true;
     for (int item = w.first; ok && item < w.items; item += w.step) {
@@ -308,47 +334,37 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
         float sum[kWidth];
 #pragma unroll
         for (int i = 0; i < kWidth; ++i) sum[i] = 0.0f;
-        // a block's products of scales are read under the block before
-        if (!wait_block(&w.sh.scale_full[scales.stage], scales.parity)) { ok = false; break; }
-        float next0 = w.sh.scales[scales.stage].of[cb][0][mine_row], next1 = GLU ? w.sh.scales[scales.stage].of[1][0][mine_row] : 0.0f;
-        for (int k = 0; k < blocks; ++k) {
-            const float s = next0, u = next1;
-            if (!wait_block(&w.sh.acc_full[acc.stage], acc.parity)) { ok = false; break; }
-            tmem_fence_after();
-            const bool last = (k + 1) % kChunk == 0 || k + 1 == blocks;   // of its chunk
-            auto release = [&]() {
-                tmem_fence_before();
-                __syncwarp();
-                if (C::ctas == 1) {
-                    arrive_one(lane, &w.sh.acc_empty[acc.stage], true);
+        for (int k = 0; ok && k < blocks; k += kChunk, scales.next()) {
+            if (!wait_block(smem_addr(&w.sh.scale_full[scales.stage]), scales.parity)) { ok = false; break; }
+            const int n = min(kChunk, blocks - k);
+            const uint32_t of = smem_addr(&w.sh.scales[scales.stage].of[cb][0][mine_row]);
+            float s = lds_f32(of), u = GLU ? lds_f32(of + kUps) : 0.0f;
+            for (int b = 0; b < n; ++b, ++use) {
+                const uint32_t at = use % C::accs;
+                // (the next block's products of scales; behind the chunk's last one whatever is there, and not used)
+                const float next_s = lds_f32(of + (b + 1) * 512), next_u = GLU ? lds_f32(of + kUps + (b + 1) * 512) : 0.0f;
+                if (!wait_block(acc_full + 8 * at, use / C::accs & 1)) { ok = false; break; }
+                tmem_fence_after();
+                if (some) {
+                    const uint32_t d = columns + at * C::n;
+#pragma unroll
+                    for (int c = 0; c < kWidth / 16; ++c) {
+                        const bool up = GLU && 16 * c >= kHalf;
+                        uint32_t v[16];
+                        tmem_start16(d + (up ? C::n / 2 - kHalf : 0) + 16 * c, v);
+                        tmem_wait_loads();
+                        if (c == kWidth / 16 - 1) release(at);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) add_scaled(sum[16 * c + i], v[i], up ? u : s);
+                    }
                 } else {
-                    arrive_one_cluster(lane, acc_empty0 + acc.stage * 8, true);
+                    release(at);
                 }
-                arrive_one(lane, &w.sh.scale_empty[scales.stage], last);
-            };
-            if (some) {
-                const uint32_t d = w.tmem + ((uint32_t)(quarter * 32) << 16) + acc.stage * C::n + group * (GLU ? kHalf : kWidth);
-#pragma unroll
-                for (int c = 0; c < kWidth / 16; ++c) {
-                    const bool up = GLU && 16 * c >= kHalf;
-                    uint32_t v[16];
-                    tmem_start16(d + (up ? C::n / 2 - kHalf : 0) + 16 * c, v);
-                    tmem_wait_loads();
-                    if (c == kWidth / 16 - 1) release();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) add_scaled(sum[16 * c + i], v[i], up ? u : s);
-                }
-            } else {
-                release();
+                s = next_s;
+                u = next_u;
             }
-            acc.next();
-            if (last) {
-                scales.next();
-                if (k + 1 < blocks && !wait_block(&w.sh.scale_full[scales.stage], scales.parity)) { ok = false; break; }
-            }
-            const auto& of = w.sh.scales[scales.stage].of;   // (behind the tile's last block: not used)
-            next0 = of[cb][(k + 1) % kChunk][mine_row];
-            if (GLU) next1 = of[1][(k + 1) % kChunk][mine_row];
+            __syncwarp();
+            arrive_one(lane, smem_addr(&w.sh.scale_empty[scales.stage]));
         }
         if (!ok || !some) continue;
         constexpr int kOuts = GLU ? kHalf : kWidth, kCols = kOuts < kPart ? kOuts : kPart;
