@@ -12,6 +12,10 @@
 // loads report to the first one's barriers.  Two accumulators take turns, so a tile's epilogue runs under the next
 // one's products.  Every wait is bounded (EP_ERR_TIMEOUT).
 //
+// Few tiles with a long sum are shared by two or four pairs of a cluster: each takes a part of the sum, leaves its
+// accumulators in shared memory, and finishes every second or fourth 32 rows of the tile with the other parts' read from
+// there, in the order of the parts, whoever adds them.
+//
 // dw reduces over token rows, and a segment ends anywhere: the rows of its last 16 that belong to others (to the next
 // expert, or to nobody, with any contents) are set to zero in shared memory, in both operands, between their arrival
 // and their product.
@@ -34,6 +38,7 @@ struct Bf16Args {
     int32_t reduced;             // length of the sum (FORWARD, GLU: k; ROWS: n)
     int32_t n;                   // WEIGHTS: rows of a matrix
     int32_t wide, accumulate;    // WEIGHTS: float32 output; added to what is there
+    int32_t split;               // pairs that share a tile's sum: 1, 2 or 4
 };
 
 constexpr int kGroups = 2;                // of four epilogue warps, which take every other 32 rows of a tile
@@ -44,6 +49,7 @@ constexpr int kBytesA = kRows * 128;
 constexpr int kBoxTokens = 32;            // rows of a small token box
 constexpr int kBlock = 64 * 128;          // MN-major: 64 channels or rows by 64 of the sum
 constexpr uint32_t kColumns = 512;        // of tensor memory
+constexpr int kMostParts = 4;             // of a tile's sum
 
 // TILE: rows of a tile, both CTAs.
 template <int TILE, int STAGES>
@@ -75,8 +81,13 @@ struct Work {
     Shared<C>& sh;
     uint8_t* smem;      // stages: 128 channels, then rows
     uint32_t tmem, cta;
+    uint32_t lead;                  // the pair's first CTA in its cluster
+    int part;                       // of a tile's sum
     int per_pair, ctiles, rtiles;   // channels of a tile, tiles of channels, WEIGHTS: tiles of rows
     int first, items, step;
+
+    // The first of the steps of a sum that part p takes.
+    __device__ __forceinline__ int begin(int steps, int p) const { return steps * p / a.split; }
 
     // The tile, and its stages of the sum.
     template <bool WARP>
@@ -109,7 +120,7 @@ struct Work {
 template <class C, Form F>
 __device__ __forceinline__ bool load_tiles(const Work<C, F>& w, const CUtensorMap* map_c, const CUtensorMap* map_r, const CUtensorMap* map_half) {
     Ring<C::stages> r;
-    const uint32_t full0 = cluster_addr(smem_addr(&w.sh.full[0]), 0);
+    const uint32_t full0 = cluster_addr(smem_addr(&w.sh.full[0]), w.lead);
     int used = 0, expert = 0;   // used: stages filled so far, at most all
     bool ok = true;
     for (int item = w.first; ok && item < w.items; item += w.step) {
@@ -120,7 +131,7 @@ __device__ __forceinline__ bool load_tiles(const Work<C, F>& w, const CUtensorMa
         const int bytes = kBytesA + boxes * (F == WEIGHTS ? kBlock : kBoxTokens * 128);
         const int ch = t.channel * w.per_pair + (int)w.cta * (F == GLU ? kRows / 2 : kRows);
         const int row = (int)t.row0 + (int)w.cta * half;
-        for (int k = 0; k < steps; ++k, r.next()) {
+        for (int k = w.begin(steps, w.part), end = w.begin(steps, w.part + 1); k < end; ++k, r.next()) {
             if (!mbar_wait_parked(&w.sh.empty[r.stage], r.parity ^ 1)) { ok = false; break; }
             uint8_t* dst = w.smem + r.stage * C::bytes;
             uint32_t bar = full0 + r.stage * 8;
@@ -169,22 +180,23 @@ __device__ __forceinline__ bool load_tiles(const Work<C, F>& w, const CUtensorMa
 template <class C, Form F>
 __device__ __forceinline__ bool clear_tails(const Work<C, F>& w) {
     Ring<C::stages> r;
-    const uint32_t full0 = cluster_addr(smem_addr(&w.sh.full[0]), 0);
+    const uint32_t full0 = cluster_addr(smem_addr(&w.sh.full[0]), w.lead);
     uint32_t parity = 0;   // of each stage's tail barrier
     const int lane = threadIdx.x & 31;
     int expert = 0;
     for (int item = w.first; item < w.items; item += w.step) {
         int steps;
         const Tile t = w.template tile<true>(item, expert, steps);
-        if (steps == 0) continue;
-        for (int k = 0; k < steps - 1; ++k) r.next();
-        if (w.ragged(t, steps - 1)) {
+        const int begin = w.begin(steps, w.part), end = w.begin(steps, w.part + 1);
+        if (begin == end) continue;
+        for (int k = begin; k < end - 1; ++k) r.next();
+        if (w.ragged(t, end - 1)) {
             if (!warp_wait(&w.sh.tail[r.stage], (parity >> r.stage) & 1)) return false;
             parity ^= 1u << r.stage;
-            const int blocks = 2 + (t.n / 2 + 63) / 64, first = w.left(t, steps - 1), end = (first + 15) / 16 * 16;
+            const int blocks = 2 + (t.n / 2 + 63) / 64, first = w.left(t, end - 1), past = (first + 15) / 16 * 16;
             const uint32_t at = smem_addr(w.smem + r.stage * C::bytes);
-            for (int i = lane; i < blocks * (end - first) * 8; i += 32) {
-                const int piece = i & 7, row = first + (i >> 3) % (end - first), block = (i >> 3) / (end - first);
+            for (int i = lane; i < blocks * (past - first) * 8; i += 32) {
+                const int piece = i & 7, row = first + (i >> 3) % (past - first), block = (i >> 3) / (past - first);
                 asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};"
                              :: "r"(at + block * kBlock + row * 128 + piece * 16), "r"(0) : "memory");
             }
@@ -210,12 +222,13 @@ __device__ __forceinline__ bool issue_mma(const Work<C, F>& w) {
     for (int item = w.first; ok && item < w.items; item += w.step) {
         int steps;
         const Tile t = w.template tile<true>(item, expert, steps);
-        if (steps == 0) continue;
+        const int begin = w.begin(steps, w.part), end = w.begin(steps, w.part + 1);
+        if (begin == end) continue;
         const uint32_t idesc = mma_desc_bf16(2 * kRows, t.n, a_mn, b_mn);
         if (!warp_wait(&w.sh.acc_empty[acc.stage], acc.parity ^ 1)) { ok = false; break; }
         tmem_fence_after();
         const uint32_t d = w.tmem + acc.stage * C::tile;
-        for (int k = 0; k < steps; ++k) {
+        for (int k = begin; k < end; ++k) {
             if (!ready && !warp_wait(&w.sh.full[r.stage], r.parity)) { ok = false; break; }
             tmem_fence_after();
             const uint32_t at = smem0 + r.stage * C::bytes;
@@ -228,12 +241,12 @@ __device__ __forceinline__ bool issue_mma(const Work<C, F>& w) {
             if (elect_one()) {
 #pragma unroll
                 for (int j = 0; j < kStep / 16; ++j)   // 16 of the sum: 32 bytes further on, or 16 rows of 128
-                    if (j < pieces) mma_pair_f16_ss(d, a + j * (a_mn ? 128 : 2), b + j * (b_mn ? 128 : 2), idesc, k > 0 || j > 0);
-                commit_pair(empty);
+                    if (j < pieces) mma_pair_f16_ss(d, a + j * (a_mn ? 128 : 2), b + j * (b_mn ? 128 : 2), idesc, k > begin || j > 0);
+                commit_pair_of(empty, w.lead);
             }
             __syncwarp();
         }
-        if (ok && elect_one()) commit_pair(&w.sh.acc_full[acc.stage]);
+        if (ok && elect_one()) commit_pair_of(&w.sh.acc_full[acc.stage], w.lead);
         __syncwarp();
         acc.next();
     }
@@ -243,11 +256,58 @@ __device__ __forceinline__ bool issue_mma(const Work<C, F>& w) {
     return warp_wait(&w.sh.drained, 0) && ok;
 }
 
+// A part of a tile's sum: its accumulators go to shared memory, whose stages have been used by then, a column of 128
+// channels after the other.
+template <class C, Form F>
+__device__ __forceinline__ bool leave_part(const Work<C, F>& w, int warp, int group) {
+    if (w.first >= w.items) return true;
+    int steps, expert = 0;
+    const Tile t = w.template tile<true>(w.first, expert, steps);
+    if (w.begin(steps, w.part) == w.begin(steps, w.part + 1)) return true;
+    if (!warp_wait(&w.sh.acc_full[0], 0)) return false;
+    tmem_fence_after();
+    const uint32_t to = smem_addr(w.smem) + (warp * 32 + (threadIdx.x & 31)) * 4;
+    for (int c0 = 32 * group; c0 < t.m; c0 += 32 * kGroups) {
+        uint32_t v[32];
+        tmem_load32(w.tmem + ((uint32_t)(warp * 32) << 16) + c0, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) asm volatile("st.shared.u32 [%0], %1;" :: "r"(to + (c0 + i) * 512), "r"(v[i]) : "memory");
+    }
+    return true;
+}
+
+// The sum of all parts of 32 rows of a channel, at this address of each pair's shared memory.  All parts of 16 rows are asked
+// for at once: the way there and back takes most of a microsecond.
+template <class C, Form F>
+__device__ __forceinline__ void add_parts(const Work<C, F>& w, int steps, uint32_t at, uint32_t v[32]) {
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+        float x[kMostParts][16];
+#pragma unroll
+        for (int p = 0; p < kMostParts; ++p) {
+            const bool left = p < w.a.split && w.begin(steps, p) < w.begin(steps, p + 1);   // (else nothing was)
+            const uint32_t there = cluster_addr(at + h * 512, left ? 2 * p + w.cta : 0);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                x[p][i] = 0.0f;
+                if (left) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x[p][i]) : "r"(there + i * 512) : "memory");
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float sum = x[0][i];
+#pragma unroll
+            for (int p = 1; p < kMostParts; ++p) sum += x[p][i];
+            v[h + i] = __float_as_uint(sum);
+        }
+    }
+}
+
 // Lane: a channel; with gates and ups, lanes 0-15 hold the gates of lanes 16-31's ups.
 template <class C, Form F>
 __device__ __forceinline__ bool epilogue(const Work<C, F>& w, int warp, int group) {
     const int lane = threadIdx.x & 31;
-    const uint32_t acc_empty0 = cluster_addr(smem_addr(&w.sh.acc_empty[0]), 0);
+    const uint32_t acc_empty0 = cluster_addr(smem_addr(&w.sh.acc_empty[0]), w.lead);
     const int64_t outs = w.a.outs;
     uint16_t* const out16 = (uint16_t*)w.a.out;
     // two channels a store where rows keep them on four bytes
@@ -263,14 +323,16 @@ __device__ __forceinline__ bool epilogue(const Work<C, F>& w, int warp, int grou
         const bool in = ch < outs;
         const int64_t row0 = F == WEIGHTS ? (int64_t)t.expert * w.a.n + t.row0 : t.row0;
         const bool some = F != WEIGHTS || steps > 0;   // an expert without rows: zeros
-        if (some) {
+        if (some && w.a.split == 1) {   // (parts have been waited for)
             if (!warp_wait(&w.sh.acc_full[acc.stage], acc.parity)) return false;
             tmem_fence_after();
         }
         const uint32_t d = w.tmem + ((uint32_t)(warp * 32) << 16) + acc.stage * C::tile;
-        for (int c0 = 32 * group; c0 < t.m; c0 += 32 * kGroups) {
+        for (int c0 = 32 * (group + kGroups * w.part); c0 < t.m; c0 += 32 * kGroups * w.a.split) {
             uint32_t v[32];
-            if (some) {
+            if (some && w.a.split > 1) {
+                add_parts(w, steps, smem_addr(w.smem) + (warp * 32 + lane) * 4 + c0 * 512, v);
+            } else if (some) {
                 tmem_load32(d + c0, v);
             } else {
 #pragma unroll
@@ -336,7 +398,7 @@ __device__ __forceinline__ bool epilogue(const Work<C, F>& w, int warp, int grou
                     if (in && i < left) *out = (uint16_t)pack_bf16x2_rn(__uint_as_float(v[i]), 0.0f);
             }
         }
-        if (some) {
+        if (some && w.a.split == 1) {
             tmem_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(acc_empty0 + acc.stage * 8);
@@ -347,7 +409,7 @@ __device__ __forceinline__ bool epilogue(const Work<C, F>& w, int warp, int grou
 }
 
 template <class C, Form F>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 matmul_bf16_kernel(const Bf16Args a, const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_r,
                    const __grid_constant__ CUtensorMap map_half) {
     extern __shared__ uint8_t dynamic[];
@@ -360,7 +422,7 @@ matmul_bf16_kernel(const Bf16Args a, const __grid_constant__ CUtensorMap map_c, 
         prefetch_map(&map_r);
         prefetch_map(&map_half);
     }
-    const uint32_t cta = cluster_rank();
+    const uint32_t rank = cluster_rank(), cta = rank & 1;
     uint8_t* smem = dynamic + ((1024 - (smem_addr(dynamic) & 1023)) & 1023);
     if (tid == 0) {
         // full: the first CTA's bytes announced; with segments that may end anywhere, a word of either CTA
@@ -381,8 +443,8 @@ matmul_bf16_kernel(const Bf16Args a, const __grid_constant__ CUtensorMap map_c, 
     const int ctiles = (a.outs + per_pair - 1) / per_pair, rtiles = F == WEIGHTS ? (a.n + C::tile - 1) / C::tile : 0;
     const int64_t all = !fits ? 0 : F == WEIGHTS ? (int64_t)a.E * ctiles * rtiles : (int64_t)sh.seg.tile[a.E] * ctiles;
     const int64_t limit = INT32_MAX - (int64_t)gridDim.x;   // (items + step stays a number)
-    const Work<C, F> w = {a, sh, smem, sh.tmem, cta, per_pair, ctiles, rtiles,
-                          (int)(blockIdx.x >> 1), (int)(all < limit ? all : limit), (int)(gridDim.x >> 1)};
+    const Work<C, F> w = {a, sh, smem, sh.tmem, cta, rank - cta, (int)(rank >> 1), per_pair, ctiles, rtiles,
+                          (int)(blockIdx.x / (2 * a.split)), (int)(all < limit ? all : limit), (int)(gridDim.x / (2 * a.split))};
     bool ok = true;
     if (warp == 0) {
         if (lane == 0) ok = load_tiles(w, &map_c, &map_r, &map_half);
@@ -391,7 +453,13 @@ matmul_bf16_kernel(const Bf16Args a, const __grid_constant__ CUtensorMap map_c, 
     } else if (warp == 3) {
         if (F == WEIGHTS) ok = clear_tails(w);
     } else if (warp >= 4) {
-        ok = epilogue(w, warp & 3, (warp >> 2) - 1);
+        ok = a.split == 1 ? epilogue(w, warp & 3, (warp >> 2) - 1) : leave_part(w, warp & 3, (warp >> 2) - 1);
+    }
+    if (a.split > 1) {   // all parts are there; then each finishes its share of the tile
+        __syncwarp();
+        __syncthreads();
+        cluster_sync();
+        if (warp >= 4) ok = epilogue(w, warp & 3, (warp >> 2) - 1) && ok;
     }
     if (!ok && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
     __syncwarp();
@@ -401,9 +469,44 @@ matmul_bf16_kernel(const Bf16Args a, const __grid_constant__ CUtensorMap map_c, 
     if (warp == 2) tmem_free_pair(w.tmem, kColumns);
 }
 
+// How many tiles can be shared by `split` pairs each at a time: clusters that the device holds, asked once for each
+// device and kernel (152 SMs hold fewer clusters of eight than 19).
+template <class C, Form F>
+int64_t clusters_of(int split) {
+    static std::atomic<int> known[64][2];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::atomic<int>& mine = known[dev][split == 4];
+    int n = mine.load(std::memory_order_relaxed);
+    if (n == 0) {
+        static std::atomic<uint64_t> done;
+        if (allow_smem(matmul_bf16_kernel<C, F>, C::smem, done) != cudaSuccess) return 0;
+        cudaLaunchConfig_t cfg{};
+        cudaLaunchAttribute attr{};
+        cfg.gridDim = dim3((unsigned)(2 * split) * 64);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = C::smem;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = (unsigned)(2 * split);
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, matmul_bf16_kernel<C, F>, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            n = 0;
+        }
+        mine.store(n > 0 ? n : -1, std::memory_order_relaxed);
+#ifdef SHOWCL
+        printf("clusters of %d pairs: %d\n", split, n);
+#endif
+    }
+    return n > 0 ? n : 0;
+}
+
 // c: the channels' operand, r: the rows' one.
 template <class C, Form F>
-cudaError_t launch(const Bf16Args& a, const void* c, const void* r, int sms, cudaStream_t st) {
+cudaError_t launch(const Bf16Args& a, const void* c, const void* r, int split, int sms, cudaStream_t st) {
+    static_assert(C::tile * 512 <= C::stages * C::bytes, "accumulators in the stages' place");
     const int64_t per_pair = F == GLU ? kRows : 2 * kRows, ctiles = (a.outs + per_pair - 1) / per_pair;
     CUtensorMap map_c, map_r, map_half;
     bool ok;
@@ -423,11 +526,14 @@ cudaError_t launch(const Bf16Args& a, const void* c, const void* r, int sms, cud
     const int64_t rtiles = F == WEIGHTS ? (int64_t)a.E * ((a.n + C::tile - 1) / C::tile) : (a.rows + C::tile - 1) / C::tile + (a.E > 1 ? a.E : 0);
     const int64_t most = rtiles * ctiles;
     if (most > INT32_MAX - sms) return cudaErrorInvalidValue;   // more output than any memory holds
-    const int64_t pairs = most < sms / 2 ? most : sms / 2;
+    Bf16Args b = a;
+    b.split = split;
+    const int64_t tiles = b.split > 1 || most < sms / 2 ? most : sms / 2;   // (a shared tile has a cluster of its own)
     static std::atomic<uint64_t> done;
     const cudaError_t e = allow_smem(matmul_bf16_kernel<C, F>, C::smem, done);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(matmul_bf16_kernel<C, F>, dim3((unsigned)(2 * pairs)), kThreads, C::smem, st, a, map_c, map_r, map_half);
+    return launch_overlapped_clusters(matmul_bf16_kernel<C, F>, 2 * b.split, dim3((unsigned)(2 * b.split * tiles)), kThreads, C::smem, st, b,
+                                      map_c, map_r, map_half);
 }
 
 // Few enough rows and weights for matmul_skinny.cu, which is on every SM from the start, and reads weights the slower the
@@ -444,19 +550,36 @@ bool few_rows(const Bf16Args& a, bool glu, int sms) {
     return here <= 4.0 + 0.3 * (double)(rounds * ((a.reduced + kStep - 1) / kStep));
 }
 
-// Which tile: the larger ones do more products for what they read, the smaller ones are more, and pay for fewer rows that
-// are none.  Measured, us (256, 128, 64 rows a tile):
+// Which tile, and how many pairs share its sum: whatever is over first by this estimate in us, of rounds of tiles of so many
+// steps of 64.  The larger tiles do more products for what they read, the smaller ones are more, and pay for fewer rows that
+// are none; to share a sum takes a meeting, and clusters that find room.
+// Measured, us (256, 128, 64 rows a tile):
 //   one matrix: 128 rows x 4096 x 4096: 29.3, 23.2, 23.2; 2000 x 2048 x 1000: 19.1, 17.1, 23.2; 4000 x 2048 x 2000: 29.3,
 //   39.6, 60.1; experts: 64 of 96 rows, 2048 x 1024: 73.7, 68.3, 70.4; 64 of 128, 4096 x 2048: 201, 193, 218; 128 of 200:
 //   392, 441, 734; 128 of 6 with SwiGLU: 361, 353, 334.
 //   dw: 2000 rows, 1024 x 1024: 21.2, 17.1; 16384 rows: 88.7, 72.4; 4 experts of 2000 rows, 2048 x 512: 23.2, 27.3; 128 of 64
 //   rows, 2048 x 1024: 132, 156.
-// So: 64 up to 32 rows an expert; 128 where its rounds of tiles, which take 0.8 of the time of 256's, are that few, or
-// segments are no longer than that.
+// Measured, us in a graph (one, two, four pairs): 50 rows x 4096 x 512: 21.1, 15.8, 13.2; 300 x 7168 x 512 with SwiGLU: 35.8,
+// 23.5, 18.2; 128 x 2048 x 1024: 11.8, 11.4, 11.9; dw of 13922 rows, 992 x 376: 59.6, 35.5, 24.9; of 1000 rows, 512 x 512: 9.9,
+// 10.2, 11.2.
+struct Plan {
+    int tile = 0, split = 1;
+    double us = 1e30;
+    // tiles: that there may be
+    template <class C, Form F>
+    void consider(double per_step, int64_t tiles, int64_t steps, int sms) {
+        const double meeting[3] = {0.0, 2.8, 4.2};
+        for (int s = 0; s < 3; ++s) {
+            if (s > 0 && (tiles > sms / 4 || steps < 16 || tiles > clusters_of<C, F>(1 << s))) break;
+            const int64_t rounds = (tiles + sms / 2 - 1) / (sms / 2), part = (steps + (1 << s) - 1) >> s;
+            const double t = (double)(rounds * part) * per_step + meeting[s];
+            if (t < us) us = t, tile = C::tile, split = 1 << s;
+        }
+    }
+};
+
 template <Form F>
 cudaError_t choose(const Bf16Args& a, const void* c, const void* r, int sms, cudaStream_t st) {
-    const int64_t per_pair = F == GLU ? kRows : 2 * kRows, ctiles = (a.outs + per_pair - 1) / per_pair, pairs = sms / 2;
-    const int64_t each = F == WEIGHTS ? a.n : (a.rows + a.E - 1) / a.E;   // rows of a segment, or of a matrix
     if constexpr (F == FORWARD || F == GLU) {
         if (few_rows(a, F == GLU, sms)) {
             MatmulArgs m{};
@@ -471,12 +594,20 @@ cudaError_t choose(const Bf16Args& a, const void* c, const void* r, int sms, cud
             return launch_matmul_skinny_bf16(m, sms, st);
         }
     }
+    const int64_t per_pair = F == GLU ? kRows : 2 * kRows, ctiles = (a.outs + per_pair - 1) / per_pair;
+    const int64_t each = F == WEIGHTS ? a.n : (a.rows + a.E - 1) / a.E;   // rows of a segment, or of a matrix
+    const int64_t steps = ((F == WEIGHTS ? (a.rows + a.E - 1) / a.E : a.reduced) + kStep - 1) / kStep;
+    Plan plan;
     if constexpr (F != WEIGHTS) {
-        if (each <= 32) return launch<Thin, F>(a, c, r, sms, st);
+        if (each <= 32) plan.consider<Thin, F>(0.22, (each + Thin::tile - 1) / Thin::tile * a.E * ctiles, steps, sms);
     }
-    const int64_t mid = ((each + Mid::tile - 1) / Mid::tile * a.E * ctiles + pairs - 1) / pairs;
-    const int64_t thick = ((each + Thick::tile - 1) / Thick::tile * a.E * ctiles + pairs - 1) / pairs;
-    return each <= Mid::tile || 4 * mid < 5 * thick ? launch<Mid, F>(a, c, r, sms, st) : launch<Thick, F>(a, c, r, sms, st);
+    plan.consider<Mid, F>(0.24, (each + Mid::tile - 1) / Mid::tile * a.E * ctiles, steps, sms);
+    if (each > Mid::tile) plan.consider<Thick, F>(0.30, (each + Thick::tile - 1) / Thick::tile * a.E * ctiles, steps, sms);
+    if (plan.tile == Thick::tile) return launch<Thick, F>(a, c, r, plan.split, sms, st);
+    if constexpr (F != WEIGHTS) {
+        if (plan.tile == Thin::tile) return launch<Thin, F>(a, c, r, plan.split, sms, st);
+    }
+    return launch<Mid, F>(a, c, r, plan.split, sms, st);
 }
 
 template <Form F>

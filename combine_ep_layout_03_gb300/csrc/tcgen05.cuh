@@ -220,6 +220,12 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
                  :: "r"(smem_addr(bar)), "h"((uint16_t)3) : "memory");
 }
 
+// The same where the pair is the CTAs `lead` and `lead` + 1 of a larger cluster.
+__device__ __forceinline__ void commit_pair_of(uint64_t* bar, uint32_t lead) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 :: "r"(smem_addr(bar)), "h"((uint16_t)(3u << lead)) : "memory");
+}
+
 // The same on this CTA's barrier alone.
 __device__ __forceinline__ void commit_leader(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"

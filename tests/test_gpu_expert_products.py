@@ -264,3 +264,18 @@ def test_many_tiles():
     g = torch.Generator().manual_seed(4)
     counts = torch.randint(0, 500, (24,), generator=g).tolist()
     check_all(make(counts, 600, 1032, seed=6))
+
+
+@pytest.mark.parametrize("counts,N,K", [([100], 72, 4104), ([40, 300], 264, 2000), ([33], 2504, 264), ([3001], 72, 136), ([2], 520, 8200),
+                                        ([1999, 0, 1, 60, 4000], 264, 72), ([1700, 1555], 40, 520), ([16384], 136, 264)])
+def test_long_sums_of_few_tiles(counts, N, K):
+    """Sums that several pairs of CTAs share: of k, of n, and of rows; segments that some of them find nothing of."""
+    c = make(counts, N, K, seed=N + K)
+    check_all(c)
+    check_forward(c, True)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    check_grad_weights(c, torch.float32, torch.randn(len(counts), N, K, device="cuda", generator=g))
+    for call in (forward, grad_rows, lambda c: grad_weights(c, torch.float32)):   # the order of parts is fixed
+        first = call(c)
+        used = torch.isfinite(first)
+        assert all(torch.equal(torch.where(used, first, 0), torch.where(used, call(c), 0)) for _ in range(3))
