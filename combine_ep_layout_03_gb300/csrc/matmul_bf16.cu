@@ -127,7 +127,10 @@ __device__ __forceinline__ bool load_tiles(const Work<C, F>& w, const CUtensorMa
         int steps;
         const Tile t = w.template tile<false>(item, expert, steps);
         const int half = t.n / 2;
-        const int boxes = F == WEIGHTS ? (half + 63) / 64 : (half + kBoxTokens - 1) / kBoxTokens;
+        // rows in one box where the tile is nearly full (each box takes its time to issue, and rows that are not the
+        // tile's do no harm), else in boxes of 32
+        const int filled = (half + kBoxTokens - 1) / kBoxTokens, all = C::half / kBoxTokens;
+        const int boxes = F == WEIGHTS ? (half + 63) / 64 : 2 * filled > all ? all : filled;
         const int bytes = kBytesA + boxes * (F == WEIGHTS ? kBlock : kBoxTokens * 128);
         const int ch = t.channel * w.per_pair + (int)w.cta * (F == GLU ? kRows / 2 : kRows);
         const int row = (int)t.row0 + (int)w.cta * half;
@@ -155,8 +158,8 @@ __device__ __forceinline__ bool load_tiles(const Work<C, F>& w, const CUtensorMa
                 for (int i = 0; i < 2; ++i) tma_pair_2d(dst + i * kBlock, map_c, (ch + 64 * i) * 2, sum0, bar);
                 for (int i = 0; i < boxes; ++i) tma_pair_2d(dst + kBytesA + i * kBlock, map_r, (row + 64 * i) * 2, sum0, bar);
             }
-            if constexpr (F != WEIGHTS) {   // rows in one box where the tile is full, else in boxes of 32
-                if (boxes == C::half / kBoxTokens) {
+            if constexpr (F != WEIGHTS) {
+                if (boxes == all) {
                     tma_pair_2d(dst + kBytesA, map_half, k * 128, row, bar);
                 } else {
                     for (int b = 0; b < boxes; ++b)
@@ -536,18 +539,17 @@ cudaError_t launch(const Bf16Args& a, const void* c, const void* r, int split, i
                                       map_c, map_r, map_half);
 }
 
-// Few enough rows and weights for matmul_skinny.cu, which is on every SM from the start, and reads weights the slower the
-// more rows there are; a tile here takes 0.3 us for 64 k, however few its rows.
+// What few rows take in matmul_skinny.cu, in us: its items are 16 channels by 32 rows, so much for each round of items and for
+// each eight 128-byte pieces of a row.
 // Measured, us in a graph (that kernel, Thin): one matrix: 8 rows x 4096 x 4096 7.1, 17.8; 32 rows 11.3, 17.8; 32 rows x 7168 x
 // 512 10.1, 27.2; experts of 2048 x 1024: 8 of 32 rows with SwiGLU 13.3, 14.4; 16 of 8 rows 14.4, 12.5; 32 of 8 rows 33.6,
 // 27.6; 64 of 4 rows, 4096 x 1024: 95.8, 87.9.
-bool few_rows(const Bf16Args& a, bool glu, int sms) {
-    const int64_t experts = a.rows < a.E ? a.rows : a.E, rows = (a.rows + a.E - 1) / a.E, per_pair = glu ? kRows : 2 * kRows;
-    if (rows > 32) return false;
-    const double rate[4] = {5.0, 4.5, 4.0, 3.5};   // bytes of weights a picosecond, by tiles of eight rows
-    const double here = 3.5 + 2e-6 * (double)(experts * a.outs * (glu ? 2 : 1)) * a.reduced / rate[(rows - 1) / 8];
-    const int64_t rounds = (experts * ((a.outs + per_pair - 1) / per_pair) + sms / 2 - 1) / (sms / 2);
-    return here <= 4.0 + 0.3 * (double)(rounds * ((a.reduced + kStep - 1) / kStep));
+double few_rows_us(const Bf16Args& a, bool glu, int sms) {
+    const int64_t experts = a.rows < a.E ? a.rows : a.E, each = (a.rows + a.E - 1) / a.E;
+    if (each > 32) return 1e30;
+    const double more[4] = {1.0, 1.15, 1.35, 1.6};   // by tiles of eight rows
+    const double rounds = (double)(experts * ((a.outs + (glu ? 7 : 15)) / (glu ? 8 : 16))) / (2 * sms);
+    return 3.0 + (rounds > 0.6 ? rounds : 0.6) * (0.9 + 0.75 * ((a.reduced + 511) / 512) * more[(each - 1) / 8]);
 }
 
 // Which tile, and how many pairs share its sum: whatever is over first by this estimate in us, of rounds of tiles of so many
@@ -580,8 +582,18 @@ struct Plan {
 
 template <Form F>
 cudaError_t choose(const Bf16Args& a, const void* c, const void* r, int sms, cudaStream_t st) {
+    const int64_t per_pair = F == GLU ? kRows : 2 * kRows, ctiles = (a.outs + per_pair - 1) / per_pair;
+    const int64_t each = F == WEIGHTS ? a.n : (a.rows + a.E - 1) / a.E;   // rows of a segment, or of a matrix
+    const int64_t E = F == WEIGHTS || a.rows > a.E ? a.E : a.rows;
+    const int64_t steps = ((F == WEIGHTS ? (a.rows + a.E - 1) / a.E : a.reduced) + kStep - 1) / kStep;
+    Plan plan;
+    if constexpr (F != WEIGHTS) {
+        if (each <= 32) plan.consider<Thin, F>(0.22, (each + Thin::tile - 1) / Thin::tile * E * ctiles, steps, sms);
+    }
+    plan.consider<Mid, F>(0.24, (each + Mid::tile - 1) / Mid::tile * E * ctiles, steps, sms);
+    if (each > Mid::tile) plan.consider<Thick, F>(0.30, (each + Thick::tile - 1) / Thick::tile * E * ctiles, steps, sms);
     if constexpr (F == FORWARD || F == GLU) {
-        if (few_rows(a, F == GLU, sms)) {
+        if (few_rows_us(a, F == GLU, sms) <= 4.0 + plan.us) {
             MatmulArgs m{};
             m.a = (const uint8_t*)r;
             m.w = (const uint8_t*)c;
@@ -594,15 +606,6 @@ cudaError_t choose(const Bf16Args& a, const void* c, const void* r, int sms, cud
             return launch_matmul_skinny_bf16(m, sms, st);
         }
     }
-    const int64_t per_pair = F == GLU ? kRows : 2 * kRows, ctiles = (a.outs + per_pair - 1) / per_pair;
-    const int64_t each = F == WEIGHTS ? a.n : (a.rows + a.E - 1) / a.E;   // rows of a segment, or of a matrix
-    const int64_t steps = ((F == WEIGHTS ? (a.rows + a.E - 1) / a.E : a.reduced) + kStep - 1) / kStep;
-    Plan plan;
-    if constexpr (F != WEIGHTS) {
-        if (each <= 32) plan.consider<Thin, F>(0.22, (each + Thin::tile - 1) / Thin::tile * a.E * ctiles, steps, sms);
-    }
-    plan.consider<Mid, F>(0.24, (each + Mid::tile - 1) / Mid::tile * a.E * ctiles, steps, sms);
-    if (each > Mid::tile) plan.consider<Thick, F>(0.30, (each + Thick::tile - 1) / Thick::tile * a.E * ctiles, steps, sms);
     if (plan.tile == Thick::tile) return launch<Thick, F>(a, c, r, plan.split, sms, st);
     if constexpr (F != WEIGHTS) {
         if (plan.tile == Thin::tile) return launch<Thin, F>(a, c, r, plan.split, sms, st);

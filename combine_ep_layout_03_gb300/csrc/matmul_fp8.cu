@@ -8,7 +8,7 @@
 // product of scales for each 128 channels, and half a packed FMA for each value.
 //
 // Tiles: 256 rows by 256 channels a pair of CTAs (cta_group::2, 512 clocks of products a block, of which the FMAs take
-// half), for segments of many rows; 128 rows by 128 channels, or fewer, a CTA otherwise.  With SwiGLU half of the
+// half), for segments of many rows; 128 rows by 128 channels, or fewer of either, a CTA otherwise.  With SwiGLU half of the
 // channels are gates and half their ups, and a thread has both.  A finished row leaves a thread's registers through a
 // row of shared memory of its own, by a bulk copy.
 //
@@ -68,6 +68,7 @@ struct Config {
 
 using Thick = Config<2, 128, 256, 5, 2, 64>;
 using Mid = Config<1, 128, 128, 5, 2, 64>;
+using Small = Config<1, 128, 32, 8, 8, 32>;
 using Thin = Config<1, 32, 128, 9, 4, 64>;
 
 // The products of scales of a chunk of blocks, by token row of a CTA: of the tile's first block of channels, and of its
@@ -119,7 +120,10 @@ __device__ __forceinline__ bool load_tiles(const Work<C>& w, const CUtensorMap* 
     bool ok = true;
     for (int item = w.first; ok && item < w.items; item += w.step) {
         const Tile t = tile_of<false>(w.sh.seg, w.a.E, w.ctiles, item, expert);
-        const int mine = t.n / C::ctas, boxes = (mine + kBoxTokens - 1) / kBoxTokens;
+        // rows in one box where the tile is nearly full (each box takes its time to issue, and rows that are not the
+        // tile's do no harm), else in boxes of 32
+        const int mine = t.n / C::ctas, filled = (mine + kBoxTokens - 1) / kBoxTokens;
+        const int boxes = 2 * filled > C::rows / kBoxTokens ? C::rows / kBoxTokens : filled;
         const int bytes = C::channels * 128 + boxes * kBoxTokens * 128;
         const int ch = t.channel * w.per_tile, row = (int)t.row0 + (int)w.cta * mine;
         for (int k = 0; k < w.a.blocks; ++k, r.next()) {
@@ -456,24 +460,47 @@ cudaError_t launch(const Fp8Args& a, const void* rows, const void* weights, int 
                                       a, map_w, map_a, map_all);
 }
 
-// Few enough rows and weights for matmul_skinny.cu, which is on every SM from the start, and reads weights the slower the
-// more rows there are; a tile here takes a third of a microsecond a block, however few its rows.
-// Measured, us in a graph (that kernel, Thin): one matrix, 4096 x 4096: 8 rows 6.4, 13.4; 32 rows 10.9, 15.2; 7168 x 4096 with
+// The way that is over first by this estimate in us, of rounds of tiles: so much for each block of k and for each tile.  Few
+// rows may take matmul_skinny.cu instead, whose items are 16 channels by 32 rows: so much for each round of items and for
+// each eight 128-byte pieces of a row.
+// Measured, us in a graph (Thick, Mid, Small):
+//   one matrix: 100 rows x 4096 x 4096: 23.1, 14.3, 10.9; 500 x 4096 x 1024: 22.0, 14.6, 11.1; 1000 x 2048 x 2048: 15.1, 10.5, 21.6;
+//   4000 x 2048 x 2048 with SwiGLU: 26.2, 31.8, 76.9; experts: 8 of 128 rows, 2944 x 330: 18.9, 11.4, 9.2; 16 of 166, 4096 x
+//   2048: 46.6, 64.8, 167; 64 of 100, 2048 x 1024: 53.6, 40.4, 68.8; 128 of 200, 4096 x 2048 with SwiGLU: 275, 419, 1393; 32 of
+//   640, 128 x 592 with SwiGLU: 19.0, 18.7, 44.4.
+// Measured, us in a graph (few rows' kernel, Thin): one matrix, 4096 x 4096: 8 rows 6.4, 13.4; 32 rows 10.9, 15.2; 7168 x 4096 with
 // SwiGLU: 8 rows 8.9, 21.2; 32 rows 18.4, 22.0; experts of 2048 x 1024: 8 of 16 rows 10.0, 9.9; 8 of 32 with SwiGLU 15.0, 10.6;
 // 16 of 8 rows 13.8, 9.7; 32 of 8 rows 24.4, 16.1; 64 of 4 rows, 4096 x 1024: 73, 52.
-bool few_rows(const Fp8Args& a, bool glu, int sms) {
-    const int64_t experts = a.rows < a.E ? a.rows : a.E, rows = (a.rows + a.E - 1) / a.E, per_tile = glu ? Thin::n / 2 : Thin::n;
-    if (rows > 32) return false;
-    const double rate[4] = {3.3, 2.8, 2.2, 1.7};   // bytes of weights a picosecond, by tiles of eight rows
-    const double here = 3.0 + 1e-6 * (double)(experts * a.outs * (glu ? 2 : 1)) * 128 * a.blocks / rate[(rows - 1) / 8];
-    const int64_t rounds = (experts * ((a.outs + per_tile - 1) / per_tile) + sms - 1) / sms;
-    return here <= 4.0 + 0.33 * (double)(rounds * a.blocks);
-}
+template <bool GLU>
+struct Plan {
+    const Fp8Args& a;
+    const int sms;
+    int tile = 0, n = 0;
+    double us = 1e30;
+    template <class C>
+    void consider(double block, double of_tile) {
+        const int64_t each = (a.rows + a.E - 1) / a.E, experts = a.rows < a.E ? a.rows : a.E, per_tile = GLU ? C::n / 2 : C::n;
+        const int64_t tiles = (each + C::tile - 1) / C::tile * experts * ((a.outs + per_tile - 1) / per_tile);
+        const double t = 2.0 + (double)((tiles + sms / C::ctas - 1) / (sms / C::ctas)) * (a.blocks * block + of_tile);
+        if (t < us) us = t, tile = C::tile, n = C::n;
+    }
+    bool is_few_rows() const {
+        const int64_t each = (a.rows + a.E - 1) / a.E, experts = a.rows < a.E ? a.rows : a.E;
+        if (each > 32) return false;
+        const double more[4] = {1.0, 1.25, 1.7, 2.1};   // by tiles of eight rows
+        const double rounds = (double)(experts * ((a.outs + (GLU ? 7 : 15)) / (GLU ? 8 : 16))) / (2 * sms);
+        return 3.0 + (rounds > 0.6 ? rounds : 0.6) * (0.9 + 1.05 * ((a.blocks + 7) / 8) * more[(each - 1) / 8]) <= us;
+    }
+};
 
 template <bool GLU>
 cudaError_t run(const Fp8Args& a, const void* rows, const void* weights, int sms, cudaStream_t st) {
-    const int64_t each = (a.rows + a.E - 1) / a.E;
-    if (few_rows(a, GLU, sms)) {
+    Plan<GLU> plan{a, sms};
+    if ((a.rows + a.E - 1) / a.E <= Thin::tile) plan.template consider<Thin>(0.32, 2.0);
+    plan.template consider<Small>(0.20, 1.8);
+    plan.template consider<Mid>(0.38, 2.0);
+    plan.template consider<Thick>(0.54, 3.1);
+    if (plan.is_few_rows()) {
         MatmulArgs m{};
         m.a = (const uint8_t*)rows;
         m.a_scales = a.a_scales;
@@ -487,9 +514,9 @@ cudaError_t run(const Fp8Args& a, const void* rows, const void* weights, int sms
         m.swiglu = GLU;
         return launch_matmul_skinny_fp8(m, sms, st);
     }
-    if (each <= 32) return launch<Thin, GLU>(a, rows, weights, sms, st);
-    if (each <= 192) return launch<Mid, GLU>(a, rows, weights, sms, st);
-    return launch<Thick, GLU>(a, rows, weights, sms, st);
+    if (plan.tile == Thin::tile) return launch<Thin, GLU>(a, rows, weights, sms, st);
+    if (plan.tile == Thick::tile) return launch<Thick, GLU>(a, rows, weights, sms, st);
+    return plan.n == Small::n ? launch<Small, GLU>(a, rows, weights, sms, st) : launch<Mid, GLU>(a, rows, weights, sms, st);
 }
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }

@@ -90,7 +90,7 @@ def configurations():
 
 
 def test_the_configurations_are_sound():
-    assert len(configurations()) == 3
+    assert len(configurations()) == 4
     for c in configurations():
         assert sound(*c)
         assert not any(lapped(*c, seed) for seed in range(400))
