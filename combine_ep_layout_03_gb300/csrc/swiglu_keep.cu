@@ -115,21 +115,25 @@ __device__ __forceinline__ uint2 ld_nc_v2(const void* p) {
     return v;
 }
 
-// A warp per row, 256 gates and their ups at a time, so that the weight's gradient is a sum within the warp.  Many
+// LANES threads a row, eight gates and their ups each at a time: a warp, so that the weight's gradient is a sum within it;
+// half a warp where a row has no more than 128 gates; a CTA where there are few rows, whose warps' sums are added in their
+// order (9 rows of 2 x 2688: 7.9 us by warps).  Many
 // resident warps, each with few loads in flight: 205 us for 131072 rows of 2 x 1024 (three CTAs an SM, which hold as many
 // loads: 275; six 236).
+template <int LANES>
 __global__ void __launch_bounds__(kThreads, 5) swiglu_keep_grad_kernel(const KeepArgs a) {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x % LANES;
     wait_for_previous();
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (row >= rows_of(a)) return;
+    const int64_t row = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+    const bool in = row < rows_of(a);
+    if (LANES >= 32 && !in) return;   // (halves of a warp stay together for their sums)
     const int inner = a.groups * 128;
-    const float weight = a.weights ? a.weights[row] : 1.0f;
+    const float weight = in && a.weights ? a.weights[row] : 1.0f;
     const uint8_t* codes = a.codes + row * inner * 2;
     const float* scales = a.scales + row * a.groups * 2;
     float sum = 0.0f;
 #pragma unroll 1
-    for (int col = lane * 8; col < inner; col += 256) {
+    for (int col = in ? lane * 8 : inner; col < inner; col += LANES * 8) {
         const uint2 gc = ld_nc_v2(codes + col), uc = ld_nc_v2(codes + inner + col);
         const uint4 dv = ld_nc_v4(a.dy + row * inner + col);
         const float gs = scales[col >> 7], us = scales[a.groups + (col >> 7)];
@@ -163,8 +167,22 @@ __global__ void __launch_bounds__(kThreads, 5) swiglu_keep_grad_kernel(const Kee
     }
     if (!a.dweights) return;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    if (lane == 0) a.dweights[row] = sum;
+    for (int o = (LANES < 32 ? LANES : 32) / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if constexpr (LANES > 32) {
+        __shared__ float sums[LANES / 32];
+        if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = sum;
+        __syncthreads();
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < LANES / 32; ++i) sum += sums[i];
+    }
+    if (lane == 0 && in) a.dweights[row] = sum;
+}
+
+template <int LANES>
+cudaError_t launch_grad(const KeepArgs& a, cudaStream_t st) {
+    const int64_t each = kThreads / LANES, blocks = (a.rows + each - 1) / each;
+    return launch_overlapped(swiglu_keep_grad_kernel<LANES>, dim3((unsigned)blocks), kThreads, 0, st, a);
 }
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
@@ -216,7 +234,9 @@ extern "C" ep_status ep_swiglu_keep_grad(const void* codes, const float* scales,
     a.dweights = grad_row_weights;
     a.rows = (int32_t)rows;
     a.groups = inner_size / 128;
-    const int64_t blocks = (rows + kThreads / 32 - 1) / (kThreads / 32);
-    return launch_overlapped(swiglu_keep_grad_kernel, dim3((unsigned)blocks), kThreads, 0, (cudaStream_t)stream, a) == cudaSuccess
-               ? EP_OK : EP_ERR_CUDA;
+    // a warp a row fills 152 SMs from 1216 rows on; up to that many, a row of more than two turns has a CTA
+    const cudaError_t e = a.groups == 1 ? launch_grad<16>(a, (cudaStream_t)stream)
+                          : rows <= 1216 && a.groups > 4 ? launch_grad<kThreads>(a, (cudaStream_t)stream)
+                                                         : launch_grad<32>(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }

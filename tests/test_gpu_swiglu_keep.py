@@ -214,6 +214,13 @@ def test_streams_and_graphs():
     assert (out[0][33:] == 0).all() and (dc[33:] == 0).all() and (dw[33:] == 0).all()
 
 
+@pytest.mark.parametrize("rows,inner", [(1216, 640), (1217, 640), (1300, 1024), (1216, 128), (3, 65536)])
+def test_rows_by_ctas_and_by_warps(rows, inner):
+    s = make(rows, inner, seed=rows)
+    check_back(s, *check_keep(s))
+    assert torch.equal(back(s, *keep(s)[1:])[2], back(s, *keep(s)[1:])[2])
+
+
 def test_many_rows():
     s = make(70000, 128, seed=9)
     check_back(s, *check_keep(s))
