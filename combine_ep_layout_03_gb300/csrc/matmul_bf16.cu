@@ -553,7 +553,7 @@ double few_rows_us(const Bf16Args& a, bool glu, int sms) {
 }
 
 // Which tile, and how many pairs share its sum: whatever is over first by this estimate in us, of rounds of tiles of so many
-// steps of 64.  The larger tiles do more products for what they read, the smaller ones are more, and pay for fewer rows that
+// steps of 64 and of their way out.  The larger tiles do more products for what they read, the smaller ones are more, and pay for fewer rows that
 // are none; to share a sum takes a meeting, and clusters that find room.
 // Measured, us (256, 128, 64 rows a tile):
 //   one matrix: 128 rows x 4096 x 4096: 29.3, 23.2, 23.2; 2000 x 2048 x 1000: 19.1, 17.1, 23.2; 4000 x 2048 x 2000: 29.3,
@@ -569,12 +569,14 @@ struct Plan {
     double us = 1e30;
     // tiles: that there may be
     template <class C, Form F>
-    void consider(double per_step, int64_t tiles, int64_t steps, int sms) {
-        const double meeting[3] = {0.0, 2.8, 4.2};
+    void consider(double per_step, double per_row, int64_t tiles, int64_t steps, int sms) {
+        const double meeting[3] = {0.0, 2.8, 4.2}, store = per_row * C::tile;
         for (int s = 0; s < 3; ++s) {
             if (s > 0 && (tiles > sms / 4 || steps < 16 || tiles > clusters_of<C, F>(1 << s))) break;
             const int64_t rounds = (tiles + sms / 2 - 1) / (sms / 2), part = (steps + (1 << s) - 1) >> s;
-            const double t = (double)(rounds * part) * per_step + meeting[s];
+            // a tile is stored under the next one's products
+            const double sum = (double)part * per_step, longer = sum > store ? sum : store;
+            const double t = (double)rounds * (longer + 0.35) + sum + store - longer + meeting[s];
             if (t < us) us = t, tile = C::tile, split = 1 << s;
         }
     }
@@ -585,13 +587,21 @@ cudaError_t choose(const Bf16Args& a, const void* c, const void* r, int sms, cud
     const int64_t per_pair = F == GLU ? kRows : 2 * kRows, ctiles = (a.outs + per_pair - 1) / per_pair;
     const int64_t each = F == WEIGHTS ? a.n : (a.rows + a.E - 1) / a.E;   // rows of a segment, or of a matrix
     const int64_t E = F == WEIGHTS || a.rows > a.E ? a.E : a.rows;
+    // tiles of rows, of segments that end inside one
+    auto rtiles = [&](int64_t tile) {
+        if (F == WEIGHTS || E == 1) return (each + tile - 1) / tile * E;
+        const int64_t n = a.rows / tile + (3 * E + 4) / 5;
+        return n > E ? n : E;
+    };
     const int64_t steps = ((F == WEIGHTS ? (a.rows + a.E - 1) / a.E : a.reduced) + kStep - 1) / kStep;
+    // a CTA's part of a tile leaves at about 27 bytes a clock in float32, 16 in bf16 (whose rows are 64 bytes a warp)
+    const double per_row = a.wide ? 0.0102 : F == GLU ? 0.004 : 0.008;
     Plan plan;
     if constexpr (F != WEIGHTS) {
-        if (each <= 32) plan.consider<Thin, F>(0.22, (each + Thin::tile - 1) / Thin::tile * E * ctiles, steps, sms);
+        if (each <= 32) plan.consider<Thin, F>(0.22, per_row, rtiles(Thin::tile) * ctiles, steps, sms);
     }
-    plan.consider<Mid, F>(0.24, (each + Mid::tile - 1) / Mid::tile * E * ctiles, steps, sms);
-    if (each > Mid::tile) plan.consider<Thick, F>(0.30, (each + Thick::tile - 1) / Thick::tile * E * ctiles, steps, sms);
+    plan.consider<Mid, F>(0.24, per_row, rtiles(Mid::tile) * ctiles, steps, sms);
+    if (each > Mid::tile) plan.consider<Thick, F>(0.30, per_row, rtiles(Thick::tile) * ctiles, steps, sms);
     if constexpr (F == FORWARD || F == GLU) {
         if (few_rows_us(a, F == GLU, sms) <= 4.0 + plan.us) {
             MatmulArgs m{};
