@@ -19,6 +19,11 @@
 // dw reduces over token rows, and a segment ends anywhere: the rows of its last 16 that belong to others (to the next
 // expert, or to nobody, with any contents) are set to zero in shared memory, in both operands, between their arrival
 // and their product.
+//
+// Measured: 8192^3 578 us, 1902 TFLOP/s (0.99 of the measured rate); 128 experts of 1088 rows, 4096 x 2048: 1520 us one after
+// the other (at 1390 MHz and the power limit; 1310 after a rest), dw of the same 1410 to 1630; 6 rows for each of 128 experts,
+// 4096 x 2 x 1024: 308 us, 7.0 TB/s.  Large tiles are bound by the tensor cores (0.96 of a CTA's time) and by power; short sums
+// by a tile's way out, of which an SM stores 27 bytes a clock in float32 and 16 in bf16.
 #include "expert_ops.cuh"
 #include "expert_tiles.cuh"
 #include "tcgen05.cuh"

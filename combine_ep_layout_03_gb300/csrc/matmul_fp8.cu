@@ -4,16 +4,24 @@
 // The scales are float32 and change with every block of k, so no instruction can apply them: the sum of a block is
 // taken by tcgen05.mma kind::f8f6f4 into a fresh accumulator in tensor memory, and warps read it, multiply it by the
 // two scales and add it to sums in registers, while the next block's products go into another accumulator.
-// Tokens are the M operand: a thread has a token (a lane of tensor memory), so that a block costs it one scale, one
-// product of scales for each 128 channels, and half a packed FMA for each value.
+// Tokens are the M operand: a thread has a token (a lane of tensor memory), so that a block costs it one product of
+// scales for each 128 channels and one FMA for each value.
 //
 // Tiles: 256 rows by 256 channels a pair of CTAs (cta_group::2, 512 clocks of products a block, of which the FMAs take
 // half), for segments of many rows; 128 rows by 128 channels, or fewer of either, a CTA otherwise.  With SwiGLU half of the
 // channels are gates and half their ups, and a thread has both.  A finished row leaves a thread's registers through a
 // row of shared memory of its own, by a bulk copy.
 //
-// Warps: epilogue first (four a CTA's 128 rows, or twice four, each with half of the channels), then TMA and MMA.  Every
-// wait is bounded (EP_ERR_TIMEOUT).
+// Warps: four of the epilogue for 64 channels (128 rows), then one for TMA, two that issue MMAs, every other block each,
+// and one that brings the products of scales to shared memory (read where they are used, four bytes of 32 rows at a
+// time, they cost more than the FMAs).  Every wait is bounded (EP_ERR_TIMEOUT).
+//
+// Measured: 8192^3 468 us, 2350 TFLOP/s (without scales a library product takes 283); 128 experts of 1024 rows, 4096 x 2
+// x 1024 with SwiGLU 1187 us (at 1970 MHz and the power limit, as the library's product is at 1460 MHz); thin segments read
+// weights: 8 rows for each of 512 experts, 4096 x 1024, 324 us, 6.7 TB/s.  What bounds the large tile is a warp's way through a
+// block, some 1050 clocks: wait, four reads of tensor memory with their FMAs, the word that the accumulator is free.  With
+// everything else as it is, 8192^3 took 320 us without the epilogue's waits, reads and FMAs, as much with the reads alone,
+// 392 with the FMAs alone, and 496 with both (then 517 in all).
 #include "expert_ops.cuh"
 #include "expert_tiles.cuh"
 #include "tcgen05.cuh"
