@@ -353,8 +353,9 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
             float s = lds_f32(of), u = GLU ? lds_f32(of + kUps) : 0.0f;
             for (int b = 0; b < n; ++b, ++use) {
                 const uint32_t at = use % C::accs;
-                // (the next block's products of scales; behind the chunk's last one whatever is there, and not used)
-                const float next_s = lds_f32(of + (b + 1) * 512), next_u = GLU ? lds_f32(of + kUps + (b + 1) * 512) : 0.0f;
+                // the next block's products of scales (behind the chunk's last one its own again, and not used)
+                const uint32_t after = of + min(b + 1, kChunk - 1) * 512;
+                const float next_s = lds_f32(after), next_u = GLU ? lds_f32(after + kUps) : 0.0f;
                 if (!wait_block(acc_full + 8 * at, use / C::accs & 1)) { ok = false; break; }
                 tmem_fence_after();
                 if (some) {

@@ -221,7 +221,7 @@ class TrainableExperts:
         lay.layout(topk_idx, stream)
         lay.dispatch(x, ep.EP_QUANT_NONE, self.rows.view(torch.uint8), None, stream)
         lay.expert_matmul_bf16(self.rows, self.w13, self.c, stream=stream)
-        with _on(stream):
+        with _on(stream), torch.no_grad():   # (the router's weights may belong to a graph of its own)
             # rows that no token fills have weight 0, whatever the step before had there
             self.row_weights.zero_().scatter_(0, self._entries(), topk_weights.view(-1))
             out = torch.empty((self.N, self.H), dtype=torch.bfloat16, device=x.device)
@@ -242,7 +242,7 @@ class TrainableExperts:
         lay.expert_matmul_grad_weights(self.expert_out, self.inner, self.grad_w2, accumulate=True, stream=stream)
         lay.expert_matmul_grad_weights(self.c, self.rows, self.grad_w13, accumulate=True, stream=stream)
         lay.expert_matmul_grad_rows(self.c, self.w13, self.grad_rows, stream)
-        with _on(stream):
+        with _on(stream), torch.no_grad():
             grad_x = torch.empty((self.N, self.H), dtype=torch.bfloat16, device=grad_out.device)
             grad_weights = self.row_weights_grad[self._entries()].view(self.N, self.K)
         return lay.combine(self.grad_rows, self.ones, grad_x, None, stream), grad_weights

@@ -184,3 +184,35 @@ def test_receive_rows_of_a_layout():
     got = call(c)
     c.update(a=data.view(torch.float8_e4m3fn), sa=scales.view(torch.float32), base=base.tolist())
     assert torch.equal(got, check(c))
+
+
+@pytest.mark.parametrize("counts", [[5, 9], [60, 20], [300, 500]])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_outputs_at_odd_addresses(counts, swiglu):
+    """An output that lies on two bytes only has the values of one that lies on sixteen."""
+    c = make(counts, 272, 256, swiglu, seed=3)
+    rows, width = c["a"].shape[0], 136 if swiglu else 272
+    ref = call(c)
+    for shift in (1, 4):
+        flat = torch.full((rows * width + 8,), 7.0, dtype=torch.bfloat16, device="cuda")
+        out = flat[shift:shift + rows * width].view(rows, width)
+        ep.ep_expert_matmul_fp8(c["a"], c["sa"], c["w"], c["sw"], c["expert_base"], out, swiglu=swiglu)
+        assert torch.equal(out, ref) and (flat[:shift] == 7).all() and (flat[shift + rows * width:] == 7).all()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 codes of rows and outputs: the last ones are those of the rows alone."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rows, N, K = 530000, 4096, 4224
+    a = torch.empty(rows, K, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    a.view(torch.uint8).zero_()
+    sa = torch.zeros(rows, K // 128, device="cuda")
+    a[-300:], sa[-300:] = codes_of(g, 300, K), torch.rand(300, K // 128, device="cuda", generator=g)
+    w, sw = codes_of(g, 2, N, K), torch.rand(2, N // 128, K // 128, device="cuda", generator=g)
+    base = torch.tensor([0, rows - 300, rows], dtype=torch.int32, device="cuda")
+    out = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_matmul_fp8(a, sa, w, sw, base, out)
+    assert (out[rows // 2] == 0).all()
+    c = dict(a=a[-300:], sa=sa[-300:], w=w[1:], sw=sw[1:], base=[0, 300], swiglu=False, dense=True)
+    alone = check(c)
+    assert torch.equal(out[-300:], alone)

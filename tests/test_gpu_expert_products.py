@@ -279,3 +279,42 @@ def test_long_sums_of_few_tiles(counts, N, K):
         first = call(c)
         used = torch.isfinite(first)
         assert all(torch.equal(torch.where(used, first, 0), torch.where(used, call(c), 0)) for _ in range(3))
+
+
+@pytest.mark.parametrize("counts,swiglu", [([5, 9], False), ([5, 9], True), ([150, 200], False), ([150, 200], True), ([600], False)])
+def test_outputs_at_odd_addresses(counts, swiglu):
+    """An output that lies on two bytes only has the values of one that lies on sixteen."""
+    c = make(counts, 264, 96, seed=3)
+    rows, width = c["a"].shape[0], 132 if swiglu else 264
+    ref, used = forward(c, swiglu), c["base"][-1]
+    for shift in (1, 2, 3):
+        flat = torch.full((rows * width + 8,), 7.0, dtype=torch.bfloat16, device="cuda")
+        out = flat[shift:shift + rows * width].view(rows, width)
+        ep.ep_expert_matmul_bf16(c["a"], c["w"], c["expert_base"], out, swiglu=swiglu)
+        assert torch.equal(out, ref) and (out[used:] == 7).all() and (flat[:shift] == 7).all() and (flat[shift + rows * width:] == 7).all()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values of rows, of outputs, and of gradients: the last ones are those of the rows alone."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rows, N, K = 270000, 8192, 64
+    base = torch.tensor([0, 100, rows - 300, rows], dtype=torch.int32, device="cuda")
+    a = torch.randn(rows, K, device="cuda", generator=g).to(torch.bfloat16)
+    w = (torch.randn(3, N, K, device="cuda", generator=g) / 8).to(torch.bfloat16)
+    out = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_matmul_bf16(a, w, base, out)
+    last = torch.empty(300, N, dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_matmul_bf16(a[-300:], w[2:], None, last)
+    assert torch.equal(out[-300:], last)
+    z = a[-300:].double() @ w[2].double().t()
+    within(last, z, K * U * (a[-300:].double().abs() @ w[2].double().abs().t()) * 2 + 2.0 ** -8 * z.abs(), "last rows")
+    da, da_last = torch.empty_like(a), torch.empty(300, K, dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_matmul_grad_rows(out, w, base, da)
+    ep.ep_expert_matmul_grad_rows(last, w[2:], None, da_last)
+    d, m = last.double(), w[2].double()
+    for got in (da[-300:], da_last):
+        z, dz = d @ m, N * U * (d.abs() @ m.abs())
+        within(got, z, dz + 2.0 ** -8 * (z.abs() + dz), "gradient of the last rows")
+    dw = torch.empty(3, N, K, dtype=torch.float32, device="cuda")
+    ep.ep_expert_matmul_grad_weights(out, a, base, dw)
+    within(dw[2], d.t() @ a[-300:].double(), 302 * U * (d.abs().t() @ a[-300:].double().abs()), "gradient of the last matrix")

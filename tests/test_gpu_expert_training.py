@@ -227,6 +227,19 @@ def test_steps_add_up_and_leave_nothing_behind():
     assert torch.equal(s.layer.grad_w13, w13 + w13) and torch.equal(s.layer.grad_w2, w2 + w2)
 
 
+def test_router_weights_of_a_graph_of_their_own():
+    """Weights that require gradients (a softmax over the router's output) leave no graph behind in the layer."""
+    s = Step(1, 60, 256, 8, 2, 128, 1, seed=3)
+    ref = s.run()
+    logits = torch.log(s.wts).requires_grad_()
+    s.wts = torch.softmax(logits, 1)
+    for _ in range(2):
+        out, grad_x, grad_wts = s.run()
+        assert not (out.requires_grad or grad_x.requires_grad or grad_wts.requires_grad or s.layer.row_weights.requires_grad)
+    s.wts.backward(grad_wts)
+    assert torch.isfinite(logits.grad).all() and (out - ref[0]).double().norm() <= 4 * BF16 * ref[0].double().norm()
+
+
 def test_no_entry_has_an_expert():
     s = Step(1, 20, 256, 4, 2, 128, 1, drop=2.0)
     out, grad_x, grad_wts = s.run()

@@ -224,3 +224,24 @@ def test_rows_by_ctas_and_by_warps(rows, inner):
 def test_many_rows():
     s = make(70000, 128, seed=9)
     check_back(s, *check_keep(s))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values: the last rows are those of the rows alone."""
+    rows, I, n = 530000, 2176, 40
+    s = make(n, I, seed=3, spare=0)
+    c = torch.zeros(rows, 2 * I, dtype=torch.bfloat16, device="cuda")
+    c[-n:] = s["c"]
+    w = torch.ones(rows, device="cuda")
+    w[-n:] = s["w"]
+    big = dict(c=c, w=w, dy=torch.zeros(rows, I, dtype=torch.bfloat16, device="cuda"), rows=rows, inner=I, total=rows)
+    big["dy"][-n:] = s["dy"]
+    got, want = keep(big, used=None), keep(s, used=None)
+    assert all(torch.equal(a[-n:].view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
+    grads = back(big, *got[1:], used=None), back(s, *want[1:], used=None)
+    for a, b in zip(*grads):
+        if a.dim() == 2:
+            assert torch.equal(a[-n:], b)
+        else:   # sums by warps and by CTAs
+            assert ((a[-n:] - b).abs() <= 1e-4 * (1 + b.abs())).all()
+    assert (grads[0][0][:-n] == 0).all()
