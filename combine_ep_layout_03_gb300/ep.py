@@ -465,20 +465,18 @@ def ep_expert_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w
         _check(code, "ep_expert_matmul")
 
 
+# Small calls are as long as their checks here, so these stand in line, and each attribute is asked for once.
+_BF16, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+
 def _base_ptr(expert_base, E: int):
     """The address of expert_base: int32 [E + 1], or None of one matrix."""
     if expert_base is None:
-        if E != 1:
-            raise EPError(EP_ERR_INVALID_ARG, "expert_base: int32 [E + 1]")
-        return None
-    if expert_base.dtype is not torch.int32 or not expert_base.is_contiguous() or expert_base.numel() != E + 1:
-        raise EPError(EP_ERR_INVALID_ARG, "expert_base: int32 [E + 1]")
-    return expert_base.data_ptr()
-
-
-def _bf16_rows(t: torch.Tensor, shape, what: str) -> None:
-    if t.dtype is not torch.bfloat16 or not t.is_contiguous() or t.shape != shape:
-        raise EPError(EP_ERR_INVALID_ARG, what)
+        if E == 1:
+            return None
+    elif expert_base.dtype is torch.int32 and expert_base.is_contiguous() and expert_base.numel() == E + 1:
+        return expert_base.data_ptr()
+    raise EPError(EP_ERR_INVALID_ARG, "expert_base: int32 [E + 1]")
 
 
 def ep_expert_matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, expert_base,
@@ -487,22 +485,25 @@ def ep_expert_matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
     K / 128] (both also as the bytes of a receive buffer), w [E, N, K] with w_scales [E, ceil(N / 128), K / 128], or [E,
     2 * ceil(N / 2 / 128), K / 128] with swiglu; expert_base int32 [E + 1] on the device (None: one matrix), out bf16
     [rows, N], or [rows, N / 2] = silu(gates) * ups with swiglu."""
-    _require(len(a.shape) == 2 and len(w.shape) == 3, "a: e4m3 [rows, K], w: e4m3 [E, N, K]")
-    rows, K = a.shape
-    E, N, _ = w.shape
-    bad = None
+    shape, wshape = a.shape, w.shape
+    if len(shape) != 2 or len(wshape) != 3:
+        raise EPError(EP_ERR_INVALID_ARG, "a: e4m3 [rows, K], w: e4m3 [E, N, K]")
+    rows, K = shape
+    E, N, wk = wshape
+    outs = N // 2 if swiglu else N
+    blocks, bad = (outs + 127) // 128 * (2 if swiglu else 1), None
     if a.element_size() != 1 or not a.is_contiguous():
         bad = "a: e4m3 [rows, K]"
-    elif w.dtype is not torch.float8_e4m3fn or not w.is_contiguous() or w.shape[2] != K or K % 128 != 0:
+    elif w.dtype is not _E4M3 or not w.is_contiguous() or wk != K or K % 128 != 0:
         bad = "w: e4m3 [E, N, K], K a multiple of 128"
     elif not a_scales.is_contiguous() or a_scales.nbytes != rows * (K // 32):
         bad = "a_scales: float32 [rows, K / 128]"
-    elif (w_scales.dtype is not torch.float32 or not w_scales.is_contiguous()
-          or w_scales.numel() != E * (2 * ((N // 2 + 127) // 128) if swiglu else (N + 127) // 128) * (K // 128)):
+    elif w_scales.dtype is not _F32 or not w_scales.is_contiguous() or w_scales.numel() != E * blocks * (K // 128):
         bad = "w_scales: float32 [E, N / 128, K / 128]"
+    elif out.dtype is not _BF16 or not out.is_contiguous() or out.shape != (rows, outs):
+        bad = "out: bf16 [rows, N], or [rows, N / 2] with swiglu"
     if bad:
         raise EPError(EP_ERR_INVALID_ARG, bad)
-    _bf16_rows(out, (rows, N // 2 if swiglu else N), "out: bf16 [rows, N], or [rows, N / 2] with swiglu")
     code = _lib.ep_expert_matmul_fp8(a.data_ptr(), a_scales.data_ptr(), rows, K, w.data_ptr(), w_scales.data_ptr(), N, E,
                                      _base_ptr(expert_base, E), 1 if swiglu else 0, out.data_ptr(), _ptr(status), _stream(stream))
     if code:
@@ -513,12 +514,20 @@ def ep_expert_matmul_bf16(a: torch.Tensor, w: torch.Tensor, expert_base, out: to
                           status=None, stream=None) -> None:
     """bf16 rows times bf16 expert matrices: a [rows, K], w [E, N, K], expert_base int32 [E + 1] on the device (None:
     one matrix), out bf16 [rows, N], or [rows, N / 2] = silu(gates) * ups with swiglu."""
-    _require(len(a.shape) == 2 and len(w.shape) == 3, "a: bf16 [rows, K], w: bf16 [E, N, K]")
-    rows, K = a.shape
-    E, N, _ = w.shape
-    _bf16_rows(a, (rows, K), "a: bf16 [rows, K]")
-    _bf16_rows(w, (E, N, K), "w: bf16 [E, N, K]")
-    _bf16_rows(out, (rows, N // 2 if swiglu else N), "out: bf16 [rows, N], or [rows, N / 2] with swiglu")
+    shape, wshape = a.shape, w.shape
+    if len(shape) != 2 or len(wshape) != 3:
+        raise EPError(EP_ERR_INVALID_ARG, "a: bf16 [rows, K], w: bf16 [E, N, K]")
+    rows, K = shape
+    E, N, wk = wshape
+    bad = None
+    if a.dtype is not _BF16 or not a.is_contiguous():
+        bad = "a: bf16 [rows, K]"
+    elif w.dtype is not _BF16 or not w.is_contiguous() or wk != K:
+        bad = "w: bf16 [E, N, K]"
+    elif out.dtype is not _BF16 or not out.is_contiguous() or out.shape != (rows, N // 2 if swiglu else N):
+        bad = "out: bf16 [rows, N], or [rows, N / 2] with swiglu"
+    if bad:
+        raise EPError(EP_ERR_INVALID_ARG, bad)
     code = _lib.ep_expert_matmul_bf16(a.data_ptr(), rows, K, w.data_ptr(), N, E, _base_ptr(expert_base, E), 1 if swiglu else 0,
                                       out.data_ptr(), _ptr(status), _stream(stream))
     if code:
@@ -528,12 +537,20 @@ def ep_expert_matmul_bf16(a: torch.Tensor, w: torch.Tensor, expert_base, out: to
 def ep_expert_matmul_grad_rows(grad_c: torch.Tensor, w: torch.Tensor, expert_base, grad_a: torch.Tensor, status=None,
                                stream=None) -> None:
     """The gradient of the rows of ep_expert_matmul_bf16: grad_a [rows, K] = grad_c [rows, N] times each expert's w."""
-    _require(len(grad_c.shape) == 2 and len(w.shape) == 3, "grad_c: bf16 [rows, N], w: bf16 [E, N, K]")
-    rows, N = grad_c.shape
-    E, _, K = w.shape
-    _bf16_rows(grad_c, (rows, N), "grad_c: bf16 [rows, N]")
-    _bf16_rows(w, (E, N, K), "w: bf16 [E, N, K]")
-    _bf16_rows(grad_a, (rows, K), "grad_a: bf16 [rows, K]")
+    shape, wshape = grad_c.shape, w.shape
+    if len(shape) != 2 or len(wshape) != 3:
+        raise EPError(EP_ERR_INVALID_ARG, "grad_c: bf16 [rows, N], w: bf16 [E, N, K]")
+    rows, N = shape
+    E, wn, K = wshape
+    bad = None
+    if grad_c.dtype is not _BF16 or not grad_c.is_contiguous():
+        bad = "grad_c: bf16 [rows, N]"
+    elif w.dtype is not _BF16 or not w.is_contiguous() or wn != N:
+        bad = "w: bf16 [E, N, K]"
+    elif grad_a.dtype is not _BF16 or not grad_a.is_contiguous() or grad_a.shape != (rows, K):
+        bad = "grad_a: bf16 [rows, K]"
+    if bad:
+        raise EPError(EP_ERR_INVALID_ARG, bad)
     code = _lib.ep_expert_matmul_grad_rows(grad_c.data_ptr(), rows, N, w.data_ptr(), K, E, _base_ptr(expert_base, E),
                                            grad_a.data_ptr(), _ptr(status), _stream(stream))
     if code:
@@ -544,45 +561,41 @@ def ep_expert_matmul_grad_weights(grad_c: torch.Tensor, a: torch.Tensor, expert_
                                   accumulate: bool = False, status=None, stream=None) -> None:
     """The gradient of the weights of ep_expert_matmul_bf16: grad_w [E, N, K], bf16 or float32, = grad_c^T a over each
     expert's rows, or, with accumulate (float32 only), added to what grad_w holds."""
-    _require(len(grad_c.shape) == 2 and len(a.shape) == 2 and len(grad_w.shape) == 3, "grad_c, a: bf16 rows, grad_w: [E, N, K]")
-    (rows, N), K, E = grad_c.shape, a.shape[1], grad_w.shape[0]
-    _bf16_rows(grad_c, (rows, N), "grad_c: bf16 [rows, N]")
-    _bf16_rows(a, (rows, K), "a: bf16 [rows, K]")
-    if grad_w.dtype not in (torch.bfloat16, torch.float32) or not grad_w.is_contiguous() or grad_w.shape != (E, N, K):
-        raise EPError(EP_ERR_INVALID_ARG, "grad_w: bf16 or float32 [E, N, K]")
+    shape, ashape, wshape = grad_c.shape, a.shape, grad_w.shape
+    if len(shape) != 2 or len(ashape) != 2 or len(wshape) != 3:
+        raise EPError(EP_ERR_INVALID_ARG, "grad_c: bf16 [rows, N], a: bf16 [rows, K], grad_w: [E, N, K]")
+    rows, N = shape
+    E, wn, K = wshape
+    bad, wide = None, grad_w.dtype is _F32
+    if grad_c.dtype is not _BF16 or not grad_c.is_contiguous():
+        bad = "grad_c: bf16 [rows, N]"
+    elif a.dtype is not _BF16 or not a.is_contiguous() or ashape != (rows, K):
+        bad = "a: bf16 [rows, K]"
+    elif not (wide or grad_w.dtype is _BF16) or not grad_w.is_contiguous() or wn != N:
+        bad = "grad_w: bf16 or float32 [E, N, K]"
+    if bad:
+        raise EPError(EP_ERR_INVALID_ARG, bad)
     code = _lib.ep_expert_matmul_grad_weights(grad_c.data_ptr(), a.data_ptr(), rows, N, K, E, _base_ptr(expert_base, E),
-                                              1 if grad_w.dtype is torch.float32 else 0, 1 if accumulate else 0,
-                                              grad_w.data_ptr(), _ptr(status), _stream(stream))
+                                              1 if wide else 0, 1 if accumulate else 0, grad_w.data_ptr(), _ptr(status),
+                                              _stream(stream))
     if code:
         _check(code, "ep_expert_matmul_grad_weights")
 
 
-def _rows_used(rows_used):
-    if rows_used is None:
-        return None
-    if rows_used.dtype is not torch.int32 or rows_used.numel() != 1:
-        raise EPError(EP_ERR_INVALID_ARG, "rows_used: int32 [1]")
-    return rows_used.data_ptr()
-
-
-def _keep_rows(shape, rows_of_inner, codes, scales, row_weights, what: str) -> None:
-    """The checks that ep_swiglu_keep and its gradient share; shape: of the rows [g, u]."""
+def _keep_rows(shape, codes, scales, row_weights, rows_used):
+    """What is wrong with what ep_swiglu_keep and its gradient share, for rows [g, u] of this shape (None: nothing)."""
     rows, width = shape
-    bad = None
-    for t, name in rows_of_inner:
-        if t is not None and (t.dtype is not torch.bfloat16 or not t.is_contiguous() or t.shape != (rows, width // 2)):
-            bad = name + ": bf16 [rows, I]"
     if width % 256 != 0:
-        bad = what + ": [rows, 2I], I a multiple of 128"
-    elif codes.element_size() != 1 or not codes.is_contiguous() or codes.shape != shape:
-        bad = "codes: e4m3 [rows, 2I]"
-    elif not scales.is_contiguous() or scales.nbytes != 4 * rows * (width // 128):
-        bad = "scales: float32 [rows, 2I / 128]"
-    elif row_weights is not None and (row_weights.dtype is not torch.float32 or not row_weights.is_contiguous()
-                                      or row_weights.numel() != rows):
-        bad = "row_weights: float32 [rows]"
-    if bad:
-        raise EPError(EP_ERR_INVALID_ARG, bad)
+        return "I: a multiple of 128"
+    if codes.element_size() != 1 or not codes.is_contiguous() or codes.shape != shape:
+        return "codes: e4m3 [rows, 2I]"
+    if not scales.is_contiguous() or scales.nbytes != rows * width // 32:
+        return "scales: float32 [rows, 2I / 128]"
+    if row_weights is not None and (row_weights.dtype is not _F32 or not row_weights.is_contiguous() or row_weights.numel() != rows):
+        return "row_weights: float32 [rows]"
+    if rows_used is not None and (rows_used.dtype is not torch.int32 or rows_used.numel() != 1):
+        return "rows_used: int32 [1]"
+    return None
 
 
 def ep_swiglu_keep(c: torch.Tensor, inner: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, row_weights=None,
@@ -590,11 +603,17 @@ def ep_swiglu_keep(c: torch.Tensor, inner: torch.Tensor, codes: torch.Tensor, sc
     """inner = row_weights * silu(g) * u of bf16 rows c [rows, 2I] = [g, u], and c in 8 bits for the backward pass:
     codes [rows, 2I] (e4m3, or bytes) and scales [rows, 2I / 128] float32 (or bytes).  rows_used: int32 [1] on the
     device, how many of the rows hold anything (None: all)."""
-    if len(c.shape) != 2 or c.dtype is not torch.bfloat16 or not c.is_contiguous():
+    shape = c.shape
+    if len(shape) != 2 or c.dtype is not _BF16 or not c.is_contiguous():
         raise EPError(EP_ERR_INVALID_ARG, "c: bf16 [rows, 2I]")
-    _keep_rows(c.shape, ((inner, "inner"),), codes, scales, row_weights, "c")
-    code = _lib.ep_swiglu_keep(c.data_ptr(), _ptr(row_weights), c.shape[0], c.shape[1] // 2, _rows_used(rows_used),
-                               inner.data_ptr(), codes.data_ptr(), scales.data_ptr(), _stream(stream))
+    rows, width = shape
+    bad = _keep_rows(shape, codes, scales, row_weights, rows_used)
+    if inner.dtype is not _BF16 or not inner.is_contiguous() or inner.shape != (rows, width // 2):
+        bad = "inner: bf16 [rows, I]"
+    if bad:
+        raise EPError(EP_ERR_INVALID_ARG, bad)
+    code = _lib.ep_swiglu_keep(c.data_ptr(), _ptr(row_weights), rows, width // 2, _ptr(rows_used), inner.data_ptr(),
+                               codes.data_ptr(), scales.data_ptr(), _stream(stream))
     if code:
         _check(code, "ep_swiglu_keep")
 
@@ -603,15 +622,24 @@ def ep_swiglu_keep_grad(codes: torch.Tensor, scales: torch.Tensor, grad_inner: t
                         inner=None, row_weights=None, row_weights_grad=None, rows_used=None, stream=None) -> None:
     """The backward pass of ep_swiglu_keep from its codes and scales: grad_c [rows, 2I] bf16 of grad_inner [rows, I]
     bf16, and, where given, inner [rows, I] as the codes have it and row_weights_grad [rows] float32."""
-    if len(grad_c.shape) != 2 or grad_c.dtype is not torch.bfloat16 or not grad_c.is_contiguous():
+    shape = grad_c.shape
+    if len(shape) != 2 or grad_c.dtype is not _BF16 or not grad_c.is_contiguous():
         raise EPError(EP_ERR_INVALID_ARG, "grad_c: bf16 [rows, 2I]")
-    _keep_rows(grad_c.shape, ((grad_inner, "grad_inner"), (inner, "inner")), codes, scales, row_weights, "grad_c")
-    if row_weights_grad is not None and (row_weights_grad.dtype is not torch.float32 or not row_weights_grad.is_contiguous()
-                                         or row_weights_grad.numel() != grad_c.shape[0]):
-        raise EPError(EP_ERR_INVALID_ARG, "row_weights_grad: float32 [rows]")
-    code = _lib.ep_swiglu_keep_grad(codes.data_ptr(), scales.data_ptr(), _ptr(row_weights), grad_inner.data_ptr(),
-                                    grad_c.shape[0], grad_c.shape[1] // 2, _rows_used(rows_used), grad_c.data_ptr(),
-                                    _ptr(inner), _ptr(row_weights_grad), _stream(stream))
+    rows, width = shape
+    half = (rows, width // 2)
+    bad = _keep_rows(shape, codes, scales, row_weights, rows_used)
+    if grad_inner.dtype is not _BF16 or not grad_inner.is_contiguous() or grad_inner.shape != half:
+        bad = "grad_inner: bf16 [rows, I]"
+    elif inner is not None and (inner.dtype is not _BF16 or not inner.is_contiguous() or inner.shape != half):
+        bad = "inner: bf16 [rows, I]"
+    elif row_weights_grad is not None and (row_weights_grad.dtype is not _F32 or not row_weights_grad.is_contiguous()
+                                           or row_weights_grad.numel() != rows):
+        bad = "row_weights_grad: float32 [rows]"
+    if bad:
+        raise EPError(EP_ERR_INVALID_ARG, bad)
+    code = _lib.ep_swiglu_keep_grad(codes.data_ptr(), scales.data_ptr(), _ptr(row_weights), grad_inner.data_ptr(), rows,
+                                    width // 2, _ptr(rows_used), grad_c.data_ptr(), _ptr(inner), _ptr(row_weights_grad),
+                                    _stream(stream))
     if code:
         _check(code, "ep_swiglu_keep_grad")
 
