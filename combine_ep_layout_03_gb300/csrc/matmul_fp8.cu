@@ -9,14 +9,15 @@
 //
 // Tiles: 256 rows by 256 channels a pair of CTAs (cta_group::2, 512 clocks of products a block, of which the FMAs take
 // half), for segments of many rows; 128 rows by 128 channels, or fewer of either, a CTA otherwise.  With SwiGLU half of the
-// channels are gates and half their ups, and a thread has both.  A finished row leaves a thread's registers through a
-// row of shared memory of its own, by a bulk copy.
+// channels are gates and half their ups, and a thread has both.  A finished row leaves through a row of shared memory of its
+// own, from which a warp stores whole 16 bytes (by a bulk copy of each row, 64 experts of 512 rows, 256 x 1024, took 40.5 us
+// in a graph where they now take 29.2, and a single tile 4.9 where it takes 3.9).
 //
 // Warps: four of the epilogue for 64 channels (128 rows), then one for TMA, two that issue MMAs, every other block each,
 // and one that brings the products of scales to shared memory (read where they are used, four bytes of 32 rows at a
 // time, they cost more than the FMAs).  Every wait is bounded (EP_ERR_TIMEOUT).
 //
-// Measured: 8192^3 468 us, 2350 TFLOP/s (without scales a library product takes 283); 128 experts of 1024 rows, 4096 x 2
+// Measured: 8192^3 461 us, 2380 TFLOP/s (without scales a library product takes 283); 128 experts of 1024 rows, 4096 x 2
 // x 1024 with SwiGLU 1187 us (at 1970 MHz and the power limit, as the library's product is at 1460 MHz); thin segments read
 // weights: 8 rows for each of 512 experts, 4096 x 1024, 324 us, 6.7 TB/s.  What bounds the large tile is a warp's way through a
 // block, some 1050 clocks: wait, four reads of tensor memory with their FMAs, the word that the accumulator is free.  With
@@ -193,6 +194,12 @@ __device__ __forceinline__ void arrive_one_cluster(int lane, uint32_t bar) {
                  :: "r"(bar), "r"(lane) : "memory");
 }
 
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ float lds_f32(uint32_t addr) {
     float v;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -240,30 +247,33 @@ __device__ __forceinline__ bool issue_mma(const Work<C>& w, int which) {
     return warp_wait(&w.sh.drained, 0) && ok;
 }
 
-// 64 columns (or COLS) of a thread's row, in bf16 pairs, to out + row * outs + col.  Each thread has a row of shared memory of its own,
-// and nobody else reads it but its bulk copy; where rows are not whole 16 bytes, the warp writes its rows one by one.
+// COLS columns of a warp's rows, in bf16 pairs, to out + row * outs + col.  They pass through rows of shared memory of the warp's own,
+// so that its lanes store whole 16 bytes, the rows' pieces side by side; where rows are not whole 16 bytes, it writes its rows one by one.
+// row: of lane 0; rows: of the warp's 32 that are there.
 template <int COLS>
-__device__ __forceinline__ void store_part(const uint32_t y[COLS / 2], uint8_t* mine, uint16_t* row, int cols, bool in, bool bulk) {
+__device__ __forceinline__ void store_part(const uint32_t y[COLS / 2], uint8_t* mine, uint16_t* row, int64_t outs, int cols, int rows, bool whole) {
     const int lane = threadIdx.x & 31;
-    bulk_wait_read<0>();   // of the part before
-    __syncwarp();
+    __syncwarp();   // the part before has been read
 #pragma unroll
     for (int i = 0; i < COLS / 8; ++i) sts_v4(smem_addr(mine) + 16 * i, y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-    if (bulk) {
-        fence_proxy_async_smem();
-        if (in && cols > 0) bulk_store(row, mine, 2 * min(cols, COLS));
-        bulk_commit();
-        return;
-    }
     __syncwarp();
     const uint32_t warp_rows = smem_addr(mine) - lane * kPitch;
-    for (int r = 0; r < 32; ++r) {
-        uint16_t* to = (uint16_t*)__shfl_sync(0xffffffffu, (unsigned long long)row, r);
-        if (!__shfl_sync(0xffffffffu, (int)in, r)) continue;
+    if (whole) {
+        constexpr int kLanes = COLS / 8, kRows = 32 / kLanes;   // of a row's piece; rows at a time
+        const int r = lane / kLanes, c = 8 * (lane % kLanes);
+        uint16_t* to = row + r * outs + c;
+#pragma unroll
+        for (int i = 0; i < 32; i += kRows, to += kRows * outs) {
+            const uint4 v = lds_v4(warp_rows + (r + i) * kPitch + 2 * c);
+            if (r + i < rows && c < cols) *reinterpret_cast<uint4*>(to) = v;
+        }
+        return;
+    }
+    for (int r = 0; r < min(rows, 32); ++r, row += outs) {
         for (int c = lane; c < min(cols, COLS); c += 32) {
             uint16_t v;
             asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(warp_rows + r * kPitch + 2 * c) : "memory");
-            to[c] = v;
+            row[c] = v;
         }
     }
 }
@@ -322,7 +332,7 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
     const uint32_t acc_empty0 = cluster_addr(smem_addr(&w.sh.acc_empty[0]), 0);
     uint8_t* const mine = w.staged + (group * 128 + mine_row) * kPitch;
     const int outs = w.a.outs, blocks = w.a.blocks;
-    const bool bulk = outs % 8 == 0 && ((uintptr_t)w.a.out & 15) == 0;
+    const bool whole = outs % 8 == 0 && ((uintptr_t)w.a.out & 15) == 0;
     constexpr uint32_t kUps = sizeof(w.sh.scales[0].of[0]);   // from a gates' product of scales to the ups'
     const uint32_t acc_full = smem_addr(&w.sh.acc_full[0]);
     const uint32_t columns = w.tmem + ((uint32_t)(quarter * 32) << 16) + group * (GLU ? kHalf : kWidth);
@@ -338,11 +348,9 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
     bool ok = true;
     for (int item = w.first; ok && item < w.items; item += w.step) {
         const Tile t = tile_of<true>(w.sh.seg, w.a.E, w.ctiles, item, expert);
-        const int each = t.n / C::ctas, rows = min(each, t.m - (int)w.cta * each);   // this CTA's (perhaps none)
-        const bool some = quarter * 32 < rows, in = mine_row < rows;
-        const int64_t row = t.row0 + min((int)w.cta * each + mine_row, t.m - 1);
-        // output channels of this thread, and their block of the tile's (with SwiGLU: the gates' is the first, the ups' the second)
-        const int ch = t.channel * w.per_tile + group * (GLU ? kHalf : kWidth), cb = GLU ? 0 : group * kWidth >> 7;
+        const int each = t.n / C::ctas;
+        const bool some = quarter * 32 < min(each, t.m - (int)w.cta * each);   // of this CTA's rows (perhaps none)
+        const int cb = GLU ? 0 : group * kWidth >> 7;   // the thread's channels' block of the tile's (with SwiGLU: the gates' is the first, the ups' the second)
         float sum[kWidth];
 #pragma unroll
         for (int i = 0; i < kWidth; ++i) sum[i] = 0.0f;
@@ -353,9 +361,6 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
             float s = lds_f32(of), u = GLU ? lds_f32(of + kUps) : 0.0f;
             for (int b = 0; b < n; ++b, ++use) {
                 const uint32_t at = use % C::accs;
-                // the next block's products of scales (behind the chunk's last one its own again, and not used)
-                const uint32_t after = of + min(b + 1, kChunk - 1) * 512;
-                const float next_s = lds_f32(after), next_u = GLU ? lds_f32(after + kUps) : 0.0f;
                 if (!wait_block(acc_full + 8 * at, use / C::accs & 1)) { ok = false; break; }
                 tmem_fence_after();
                 if (some) {
@@ -373,13 +378,22 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
                 } else {
                     release(at);
                 }
-                s = next_s;
-                u = next_u;
+                // the next block's products of scales (behind the chunk's last one its own again, and not used)
+                const uint32_t after = of + min(b + 1, kChunk - 1) * 512;
+                s = lds_f32(after);
+                if (GLU) u = lds_f32(after + kUps);
             }
             __syncwarp();
             arrive_one(lane, smem_addr(&w.sh.scale_empty[scales.stage]));
         }
         if (!ok || !some) continue;
+        // where the tile lies, looked up again: kept over the loop, it would cost the registers that the sums need
+        int again = item;
+        asm volatile("" : "+r"(again));
+        const Tile o = tile_of<true>(w.sh.seg, w.a.E, w.ctiles, again, expert);
+        const int first = (int)w.cta * (o.n / C::ctas) + quarter * 32, rows = min(o.n / C::ctas - quarter * 32, o.m - first);   // of the warp
+        const int ch = o.channel * w.per_tile + group * (GLU ? kHalf : kWidth);   // of the thread
+        const int64_t row = o.row0 + first;
         constexpr int kOuts = GLU ? kHalf : kWidth, kCols = kOuts < kPart ? kOuts : kPart;
 #pragma unroll
         for (int p = 0; p < kOuts / kCols; ++p) {
@@ -393,10 +407,9 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
                 }
                 y[i] = pack_bf16x2_rn(a, b);
             }
-            store_part<kCols>(y, mine, w.a.out + row * outs + ch + p * kCols, outs - ch - p * kCols, in, bulk);
+            store_part<kCols>(y, mine, w.a.out + row * outs + ch + p * kCols, outs, outs - ch - p * kCols, rows, whole);
         }
     }
-    bulk_wait_all();
     return ok;
 }
 
