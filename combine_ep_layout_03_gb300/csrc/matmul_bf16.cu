@@ -23,11 +23,14 @@
 // Measured: 8192^3 578 us, 1902 TFLOP/s (0.99 of the measured rate); 128 experts of 1088 rows, 4096 x 2048: 1520 us one after
 // the other (at 1390 MHz and the power limit; 1310 after a rest), dw of the same 1410 to 1630; 6 rows for each of 128 experts,
 // 4096 x 2 x 1024: 308 us, 7.0 TB/s.  Large tiles are bound by the tensor cores (0.96 of a CTA's time) and by power; short sums
-// by a tile's way out, of which an SM stores 27 bytes a clock in float32 and 16 in bf16.
+// by a tile's way out, of which an SM stores 27 bytes a clock in float32 and 16 in bf16 (whose instructions take as long as its
+// stores: without the stores themselves dw of 16 experts of 16 rows took 19 us where it took 22).
 #include "expert_ops.cuh"
 #include "expert_tiles.cuh"
 #include "tcgen05.cuh"
 #include "tensor_maps.cuh"
+
+#include <type_traits>
 
 namespace {
 
@@ -44,6 +47,7 @@ struct Bf16Args {
     int32_t n;                   // WEIGHTS: rows of a matrix
     int32_t wide, accumulate;    // WEIGHTS: float32 output; added to what is there
     int32_t split;               // pairs that share a tile's sum: 1, 2 or 4
+    Divisor ctiles, rtiles;      // tiles of channels; WEIGHTS: of a matrix's rows
 };
 
 constexpr int kGroups = 2;                // of four epilogue warps, which take every other 32 rows of a tile
@@ -88,7 +92,7 @@ struct Work {
     uint32_t tmem, cta;
     uint32_t lead;                  // the pair's first CTA in its cluster
     int part;                       // of a tile's sum
-    int per_pair, ctiles, rtiles;   // channels of a tile, tiles of channels, WEIGHTS: tiles of rows
+    int per_pair;                   // channels of a tile
     int first, items, step;
 
     // The first of the steps of a sum that part p takes.
@@ -98,11 +102,11 @@ struct Work {
     template <bool WARP>
     __device__ __forceinline__ Tile tile(int item, int& e, int& steps) const {
         if constexpr (F == WEIGHTS) {
-            const uint32_t each = (uint32_t)(ctiles * rtiles), local = (uint32_t)item % each;
+            const uint32_t at = (uint32_t)item / a.ctiles, matrix = at / a.rtiles, before = matrix * a.rtiles.of;
             Tile t;
-            e = (int)((uint32_t)item / each);
+            e = (int)matrix;
             t.expert = e;
-            const Place p = place_of(local, (uint32_t)rtiles, (uint32_t)ctiles);
+            const Place p = place_of((uint32_t)item - before * a.ctiles.of, at - before, a.rtiles.of, a.ctiles.of);
             t.channel = p.channel;
             t.row0 = (int64_t)p.tile * C::tile;
             t.m = min(C::tile, a.n - (int)t.row0);
@@ -111,7 +115,7 @@ struct Work {
             return t;
         } else {
             steps = (a.reduced + kStep - 1) / kStep;
-            return tile_of<WARP>(sh.seg, a.E, ctiles, item, e);
+            return tile_of<WARP>(sh.seg, a.E, a.ctiles, item, e);
         }
     }
     // Of the sum in step k, at most 64.
@@ -311,13 +315,94 @@ __device__ __forceinline__ void add_parts(const Work<C, F>& w, int steps, uint32
     }
 }
 
+// The address of row i, `pitch` bytes each.  Volatile, so that the 32 offsets are not kept from one tile to the next: with them the
+// registers did not do, and 16 experts of 16 rows, dw of 1024 x 1408 in float32, took 28 us in a graph where it takes 18.8.
+__device__ __forceinline__ void* row_at(void* base, uint32_t pitch, int i) {
+    uint64_t p;
+    asm volatile("mad.wide.u32 %0, %1, %2, %3;" : "=l"(p) : "r"(pitch), "r"(i), "l"(base));
+    return (void*)p;
+}
+
+// 32 rows of a warp's channels, of which this lane's first n are stored (ALL: all 32, in every lane); ch: of this lane.
+template <Form F, bool ADD, class ALL>
+__device__ __forceinline__ void store_rows(const Bf16Args& a, const uint32_t v[32], int64_t row0, int ch, int n, bool wide, ALL) {
+    constexpr bool all = ALL::value;
+    const int lane = threadIdx.x & 31;
+    if (F == WEIGHTS && a.wide) {
+        const uint32_t pitch = 4 * (uint32_t)a.outs;
+        void* const to = (float*)a.out + row0 * a.outs + ch;
+        if (ADD) {
+            float* const out = (float*)to;
+            float before[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) before[i] = all || i < n ? out[i * (int64_t)a.outs] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (all || i < n) out[i * (int64_t)a.outs] = before[i] + __uint_as_float(v[i]);
+        } else {
+            // one row's address from the last one's: no offsets are kept
+            void* row = to;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                if (all || i < n) *(float*)row = __uint_as_float(v[i]);
+                asm volatile("add.s64 %0, %0, %1;" : "+l"(row) : "l"((uint64_t)pitch));
+            }
+        }
+        return;
+    }
+    const uint32_t pitch = 2 * (uint32_t)a.outs;
+    uint16_t* const out = (uint16_t*)a.out + row0 * a.outs + ch;
+    if (F == GLU) {
+        // lanes 0-15 finish the even rows, lanes 16-31 the odd ones
+        const int odd = lane >> 4;
+        float y[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(odd ? v[i] : v[i + 1]), 16);
+            y[i / 2] = swiglu(odd ? other : __uint_as_float(v[i]), odd ? __uint_as_float(v[i + 1]) : other, 1.0f, 0.25f);
+        }
+        if (wide) {
+            // neighbours trade as below: an even lane stores its pair of channels of row i + odd, an odd lane that of
+            // row i + 2 + odd
+            const int last = lane & 1, mine = odd + 2 * last;
+            const uint32_t sel = last ? 0x3276u : 0x5410u;
+            void* const to = out + (int64_t)mine * a.outs - last;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const uint32_t p = pack_bf16x2_rn(y[i / 2], y[i / 2 + 1]);
+                const uint32_t both = __byte_perm(p, __shfl_xor_sync(0xffffffffu, p, 1), sel);
+                if (all || i + mine < n) *(uint32_t*)row_at(to, pitch, i) = both;
+            }
+        } else {
+            void* const to = out + (int64_t)odd * a.outs;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+                if (all || i + odd < n) *(uint16_t*)row_at(to, pitch, i) = (uint16_t)pack_bf16x2_rn(y[i / 2], 0.0f);
+        }
+    } else if (wide) {
+        // neighbours trade halves: an even lane stores both channels of the even row
+        const int odd = lane & 1;
+        const uint32_t sel = odd ? 0x3276u : 0x5410u;
+        void* const to = out + (int64_t)odd * a.outs - odd;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            const uint32_t y = pack_bf16x2_rn(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            const uint32_t both = __byte_perm(y, __shfl_xor_sync(0xffffffffu, y, 1), sel);
+            if (all || i + odd < n) *(uint32_t*)row_at(to, pitch, i) = both;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (all || i < n) *(uint16_t*)row_at(out, pitch, i) = (uint16_t)pack_bf16x2_rn(__uint_as_float(v[i]), 0.0f);
+    }
+}
+
 // Lane: a channel; with gates and ups, lanes 0-15 hold the gates of lanes 16-31's ups.
-template <class C, Form F>
+template <class C, Form F, bool ADD>
 __device__ __forceinline__ bool epilogue(const Work<C, F>& w, int warp, int group) {
     const int lane = threadIdx.x & 31;
     const uint32_t acc_empty0 = cluster_addr(smem_addr(&w.sh.acc_empty[0]), w.lead);
     const int64_t outs = w.a.outs;
-    uint16_t* const out16 = (uint16_t*)w.a.out;
     // two channels a store where rows keep them on four bytes
     const bool wide = (outs & 1) == 0 && ((uintptr_t)w.a.out & 3) == 0;
     Ring<2> acc;
@@ -325,12 +410,19 @@ __device__ __forceinline__ bool epilogue(const Work<C, F>& w, int warp, int grou
     for (int item = w.first; item < w.items; item += w.step) {
         int steps;
         const Tile t = w.template tile<true>(item, expert, steps);
-        if (F == WEIGHTS && steps == 0 && w.a.accumulate) continue;
+        if (ADD && steps == 0) continue;
         const int ch = t.channel * w.per_pair + (int)w.cta * (F == GLU ? kRows / 2 : kRows) + warp * (F == GLU ? 16 : 32) +
                        (F == GLU ? lane & 15 : lane);
         const bool in = ch < outs;
         const int64_t row0 = F == WEIGHTS ? (int64_t)t.expert * w.a.n + t.row0 : t.row0;
         const bool some = F != WEIGHTS || steps > 0;   // an expert without rows: zeros
+        if (ADD && ch - lane < outs) {
+            // what the tile is added to, on its way to L2 under the products, a row a lane: 128 experts of 64 rows, 2048 x 1024:
+            // 339 us in a graph, 461 without (its bytes take 324); of 500 rows 455, 465 (of the next tile instead 397, 546)
+            const float* to = (const float*)w.a.out + row0 * outs + ch - lane;
+            for (int c0 = 32 * (group + kGroups * w.part) + lane; c0 < t.m; c0 += 32 * kGroups * w.a.split)
+                asm volatile("prefetch.global.L2 [%0];" :: "l"(to + c0 * outs));
+        }
         if (some && w.a.split == 1) {   // (parts have been waited for)
             if (!warp_wait(&w.sh.acc_full[acc.stage], acc.parity)) return false;
             tmem_fence_after();
@@ -346,65 +438,10 @@ __device__ __forceinline__ bool epilogue(const Work<C, F>& w, int warp, int grou
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = 0;
             }
-            const int left = t.m - c0;
-            if (F == GLU) {
-                // lanes 0-15 finish the even rows, lanes 16-31 the odd ones
-                const int odd = lane >> 4;
-                float y[16];
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(odd ? v[i] : v[i + 1]), 16);
-                    y[i / 2] = swiglu(odd ? other : __uint_as_float(v[i]), odd ? __uint_as_float(v[i + 1]) : other, 1.0f, 0.25f);
-                }
-                if (wide) {
-                    // neighbours trade as below: an even lane stores its pair of channels of row i + odd, an odd
-                    // lane that of row i + 2 + odd
-                    const int last = lane & 1;
-                    const uint32_t sel = last ? 0x3276u : 0x5410u;
-                    uint16_t* out = out16 + (row0 + c0 + odd + 2 * last) * outs + (ch - last);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4, out += 4 * outs) {
-                        const uint32_t p = pack_bf16x2_rn(y[i / 2], y[i / 2 + 1]);
-                        const uint32_t both = __byte_perm(p, __shfl_xor_sync(0xffffffffu, p, 1), sel);
-                        if (in && i + odd + 2 * last < left) *reinterpret_cast<uint32_t*>(out) = both;
-                    }
-                } else {
-                    uint16_t* out = out16 + (row0 + c0 + odd) * outs + ch;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2, out += 2 * outs)
-                        if (in && i + odd < left) *out = (uint16_t)pack_bf16x2_rn(y[i / 2], 0.0f);
-                }
-            } else if (F == WEIGHTS && w.a.wide) {
-                float* out = (float*)w.a.out + (row0 + c0) * outs + ch;
-                if (w.a.accumulate) {
-                    float before[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) before[i] = in && i < left ? out[i * outs] : 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (in && i < left) out[i * outs] = before[i] + __uint_as_float(v[i]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (in && i < left) out[i * outs] = __uint_as_float(v[i]);
-                }
-            } else if (wide) {
-                // neighbours trade halves: an even lane stores both channels of the even row
-                const int odd = lane & 1;
-                const uint32_t sel = odd ? 0x3276u : 0x5410u;
-                uint16_t* out = out16 + (row0 + c0 + odd) * outs + (ch - odd);
-#pragma unroll
-                for (int i = 0; i < 32; i += 2, out += 2 * outs) {
-                    const uint32_t y = pack_bf16x2_rn(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                    const uint32_t both = __byte_perm(y, __shfl_xor_sync(0xffffffffu, y, 1), sel);
-                    if (in && i + odd < left) *reinterpret_cast<uint32_t*>(out) = both;
-                }
-            } else {
-                uint16_t* out = out16 + (row0 + c0) * outs + ch;
-#pragma unroll
-                for (int i = 0; i < 32; ++i, out += outs)
-                    if (in && i < left) *out = (uint16_t)pack_bf16x2_rn(__uint_as_float(v[i]), 0.0f);
-            }
+            // rows of the 32 that this lane stores, and whether that is all of them for the whole warp
+            const int n = in ? t.m - c0 : 0;
+            if (__all_sync(0xffffffffu, n >= 32)) store_rows<F, ADD>(w.a, v, row0 + c0, ch, 32, wide, std::true_type());
+            else store_rows<F, ADD>(w.a, v, row0 + c0, ch, n, wide, std::false_type());
         }
         if (some && w.a.split == 1) {
             tmem_fence_before();
@@ -416,7 +453,7 @@ __device__ __forceinline__ bool epilogue(const Work<C, F>& w, int warp, int grou
     return true;
 }
 
-template <class C, Form F>
+template <class C, Form F, bool ADD>   // ADD: WEIGHTS, to what is there
 __global__ void __launch_bounds__(kThreads, 1)
 matmul_bf16_kernel(const Bf16Args a, const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_r,
                    const __grid_constant__ CUtensorMap map_half) {
@@ -448,10 +485,9 @@ matmul_bf16_kernel(const Bf16Args a, const __grid_constant__ CUtensorMap map_c, 
     tmem_fence_after();
 
     const int per_pair = F == GLU ? kRows : 2 * kRows;
-    const int ctiles = (a.outs + per_pair - 1) / per_pair, rtiles = F == WEIGHTS ? (a.n + C::tile - 1) / C::tile : 0;
-    const int64_t all = !fits ? 0 : F == WEIGHTS ? (int64_t)a.E * ctiles * rtiles : (int64_t)sh.seg.tile[a.E] * ctiles;
+    const int64_t all = !fits ? 0 : (F == WEIGHTS ? (int64_t)a.E * a.rtiles.of : (int64_t)sh.seg.tile[a.E]) * a.ctiles.of;
     const int64_t limit = INT32_MAX - (int64_t)gridDim.x;   // (items + step stays a number)
-    const Work<C, F> w = {a, sh, smem, sh.tmem, cta, rank - cta, (int)(rank >> 1), per_pair, ctiles, rtiles,
+    const Work<C, F> w = {a, sh, smem, sh.tmem, cta, rank - cta, (int)(rank >> 1), per_pair,
                           (int)(blockIdx.x / (2 * a.split)), (int)(all < limit ? all : limit), (int)(gridDim.x / (2 * a.split))};
     bool ok = true;
     if (warp == 0) {
@@ -461,13 +497,13 @@ matmul_bf16_kernel(const Bf16Args a, const __grid_constant__ CUtensorMap map_c, 
     } else if (warp == 3) {
         if (F == WEIGHTS) ok = clear_tails(w);
     } else if (warp >= 4) {
-        ok = a.split == 1 ? epilogue(w, warp & 3, (warp >> 2) - 1) : leave_part(w, warp & 3, (warp >> 2) - 1);
+        ok = a.split == 1 ? epilogue<C, F, ADD>(w, warp & 3, (warp >> 2) - 1) : leave_part(w, warp & 3, (warp >> 2) - 1);
     }
     if (a.split > 1) {   // all parts are there; then each finishes its share of the tile
         __syncwarp();
         __syncthreads();
         cluster_sync();
-        if (warp >= 4) ok = epilogue(w, warp & 3, (warp >> 2) - 1) && ok;
+        if (warp >= 4) ok = epilogue<C, F, ADD>(w, warp & 3, (warp >> 2) - 1) && ok;
     }
     if (!ok && a.status) ep_set_status(a.status, EP_ERR_TIMEOUT);
     __syncwarp();
@@ -488,7 +524,7 @@ int64_t clusters_of(int split) {
     int n = mine.load(std::memory_order_relaxed);
     if (n == 0) {
         static std::atomic<uint64_t> done;
-        if (allow_smem(matmul_bf16_kernel<C, F>, C::smem, done) != cudaSuccess) return 0;
+        if (allow_smem(matmul_bf16_kernel<C, F, false>, C::smem, done) != cudaSuccess) return 0;
         cudaLaunchConfig_t cfg{};
         cudaLaunchAttribute attr{};
         cfg.gridDim = dim3((unsigned)(2 * split) * 64);
@@ -499,14 +535,11 @@ int64_t clusters_of(int split) {
         attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, matmul_bf16_kernel<C, F>, &cfg) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveClusters(&n, matmul_bf16_kernel<C, F, false>, &cfg) != cudaSuccess) {
             (void)cudaGetLastError();
             n = 0;
         }
         mine.store(n > 0 ? n : -1, std::memory_order_relaxed);
-#ifdef SHOWCL
-        printf("clusters of %d pairs: %d\n", split, n);
-#endif
     }
     return n > 0 ? n : 0;
 }
@@ -536,11 +569,17 @@ cudaError_t launch(const Bf16Args& a, const void* c, const void* r, int split, i
     if (most > INT32_MAX - sms) return cudaErrorInvalidValue;   // more output than any memory holds
     Bf16Args b = a;
     b.split = split;
+    b.ctiles = divisor((uint32_t)ctiles);
+    b.rtiles = divisor((uint32_t)(F == WEIGHTS ? (a.n + C::tile - 1) / C::tile : 1));
     const int64_t tiles = b.split > 1 || most < sms / 2 ? most : sms / 2;   // (a shared tile has a cluster of its own)
-    static std::atomic<uint64_t> done;
-    const cudaError_t e = allow_smem(matmul_bf16_kernel<C, F>, C::smem, done);
+    auto kernel = matmul_bf16_kernel<C, F, false>;
+    if constexpr (F == WEIGHTS) {
+        if (a.accumulate) kernel = matmul_bf16_kernel<C, F, true>;
+    }
+    static std::atomic<uint64_t> done[2];
+    const cudaError_t e = allow_smem(kernel, C::smem, done[a.accumulate]);
     if (e != cudaSuccess) return e;
-    return launch_overlapped_clusters(matmul_bf16_kernel<C, F>, 2 * b.split, dim3((unsigned)(2 * b.split * tiles)), kThreads, C::smem, st, b,
+    return launch_overlapped_clusters(kernel, 2 * b.split, dim3((unsigned)(2 * b.split * tiles)), kThreads, C::smem, st, b,
                                       map_c, map_r, map_half);
 }
 

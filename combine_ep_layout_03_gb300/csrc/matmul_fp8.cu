@@ -41,6 +41,7 @@ struct Fp8Args {
     int32_t outs;                // n, or n / 2 with swiglu
     int32_t blocks;              // of 128 k
     int32_t wblocks;             // of 128 rows of a matrix (with swiglu: of the gates, then of the ups)
+    Divisor ctiles;              // tiles of output channels
 };
 
 constexpr int kBoxTokens = 32;   // rows of a small token box
@@ -103,7 +104,7 @@ struct Work {
     uint8_t* smem;      // stages: token rows, then weight rows
     uint8_t* staged;    // a row of kPitch bytes for each epilogue thread
     uint32_t tmem, cta;
-    int per_tile, ctiles;   // output channels of a tile, tiles of them
+    int per_tile;       // output channels
     int first, items, step;
 };
 
@@ -128,7 +129,7 @@ __device__ __forceinline__ bool load_tiles(const Work<C>& w, const CUtensorMap* 
     int used = 0, expert = 0;   // used: stages filled so far, at most all
     bool ok = true;
     for (int item = w.first; ok && item < w.items; item += w.step) {
-        const Tile t = tile_of<false>(w.sh.seg, w.a.E, w.ctiles, item, expert);
+        const Tile t = tile_of<false>(w.sh.seg, w.a.E, w.a.ctiles, item, expert);
         // rows in one box where the tile is nearly full (each box takes its time to issue, and rows that are not the
         // tile's do no harm), else in boxes of 32
         const int mine = t.n / C::ctas, filled = (mine + kBoxTokens - 1) / kBoxTokens;
@@ -192,12 +193,6 @@ __device__ __forceinline__ void arrive_one(int lane, uint32_t bar) {
 __device__ __forceinline__ void arrive_one_cluster(int lane, uint32_t bar) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}"
                  :: "r"(bar), "r"(lane) : "memory");
-}
-
-__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-    return v;
 }
 
 __device__ __forceinline__ float lds_f32(uint32_t addr) {
@@ -286,7 +281,7 @@ __device__ __forceinline__ bool load_scales(const Work<C>& w) {
     Ring<kChunks> r;
     int expert = 0;
     for (int item = w.first; item < w.items; item += w.step) {
-        const Tile t = tile_of<true>(w.sh.seg, w.a.E, w.ctiles, item, expert);
+        const Tile t = tile_of<true>(w.sh.seg, w.a.E, w.a.ctiles, item, expert);
         const int mine = t.n / C::ctas, rows = (min(mine, t.m - (int)w.cta * mine) + 31) / 32;   // in 32s (perhaps none)
         const float* row[C::rows / 32];
 #pragma unroll
@@ -347,7 +342,7 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
     int expert = 0;
     bool ok = true;
     for (int item = w.first; ok && item < w.items; item += w.step) {
-        const Tile t = tile_of<true>(w.sh.seg, w.a.E, w.ctiles, item, expert);
+        const Tile t = tile_of<true>(w.sh.seg, w.a.E, w.a.ctiles, item, expert);
         const int each = t.n / C::ctas;
         const bool some = quarter * 32 < min(each, t.m - (int)w.cta * each);   // of this CTA's rows (perhaps none)
         const int cb = GLU ? 0 : group * kWidth >> 7;   // the thread's channels' block of the tile's (with SwiGLU: the gates' is the first, the ups' the second)
@@ -390,7 +385,7 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
         // where the tile lies, looked up again: kept over the loop, it would cost the registers that the sums need
         int again = item;
         asm volatile("" : "+r"(again));
-        const Tile o = tile_of<true>(w.sh.seg, w.a.E, w.ctiles, again, expert);
+        const Tile o = tile_of<true>(w.sh.seg, w.a.E, w.a.ctiles, again, expert);
         const int first = (int)w.cta * (o.n / C::ctas) + quarter * 32, rows = min(o.n / C::ctas - quarter * 32, o.m - first);   // of the warp
         const int ch = o.channel * w.per_tile + group * (GLU ? kHalf : kWidth);   // of the thread
         const int64_t row = o.row0 + first;
@@ -443,9 +438,9 @@ matmul_fp8_kernel(const Fp8Args a, const __grid_constant__ CUtensorMap map_w, co
     if constexpr (C::ctas == 2) cluster_sync();
     tmem_fence_after();
 
-    const int per_tile = GLU ? C::n / 2 : C::n, ctiles = (a.outs + per_tile - 1) / per_tile;
-    const int64_t all = fits ? (int64_t)sh.seg.tile[a.E] * ctiles : 0, limit = INT32_MAX - (int64_t)gridDim.x;   // (items + step stays a number)
-    const Work<C> w = {a, sh, smem, smem + C::stages * C::bytes, sh.tmem, cta, per_tile, ctiles,
+    const int per_tile = GLU ? C::n / 2 : C::n;
+    const int64_t all = fits ? (int64_t)sh.seg.tile[a.E] * a.ctiles.of : 0, limit = INT32_MAX - (int64_t)gridDim.x;   // (items + step stays a number)
+    const Work<C> w = {a, sh, smem, smem + C::stages * C::bytes, sh.tmem, cta, per_tile,
                        (int)(blockIdx.x / C::ctas), (int)(all < limit ? all : limit), (int)(gridDim.x / C::ctas)};
     bool ok = true;
     if (warp < 4 * C::groups) {
@@ -467,19 +462,21 @@ matmul_fp8_kernel(const Fp8Args a, const __grid_constant__ CUtensorMap map_w, co
 
 template <class C, bool GLU>
 cudaError_t launch(const Fp8Args& a, const void* rows, const void* weights, int sms, cudaStream_t st) {
-    const int64_t per_tile = GLU ? C::n / 2 : C::n, k = 128 * (int64_t)a.blocks;
+    const int64_t per_tile = GLU ? C::n / 2 : C::n, ctiles = (a.outs + per_tile - 1) / per_tile, k = 128 * (int64_t)a.blocks;
     CUtensorMap map_w, map_a, map_all;
     if (!make_experts_map(&map_w, weights, GLU ? 2 * a.E : a.E, a.outs, k, GLU && C::ctas == 1 ? C::channels / 2 : C::channels) ||
         !make_rows_map(&map_a, rows, a.rows, k, kBoxTokens) || !make_rows_map(&map_all, rows, a.rows, k, C::rows))
         return cudaErrorInvalidValue;
-    const int64_t most = ((a.rows + C::tile - 1) / C::tile + (a.E > 1 ? a.E : 0)) * ((a.outs + per_tile - 1) / per_tile);
+    const int64_t most = ((a.rows + C::tile - 1) / C::tile + (a.E > 1 ? a.E : 0)) * ctiles;
     if (most > INT32_MAX - sms) return cudaErrorInvalidValue;   // more output than any memory holds
     const int64_t tiles = most < sms / C::ctas ? most : sms / C::ctas;
+    Fp8Args b = a;
+    b.ctiles = divisor((uint32_t)ctiles);
     static std::atomic<uint64_t> done;
     const cudaError_t e = allow_smem(matmul_fp8_kernel<C, GLU>, C::smem, done);
     if (e != cudaSuccess) return e;
     return launch_overlapped_clusters(matmul_fp8_kernel<C, GLU>, C::ctas, dim3((unsigned)(C::ctas * tiles)), C::threads, C::smem, st,
-                                      a, map_w, map_a, map_all);
+                                      b, map_w, map_a, map_all);
 }
 
 // The way that is over first by this estimate in us, of rounds of tiles: so much for each block of k and for each tile.  Few
@@ -555,7 +552,7 @@ extern "C" ep_status ep_expert_matmul_fp8(const void* a, const float* a_scales, 
     if (!w || !aligned(w, 16) || !w_scales || !aligned(w_scales, 4)) return EP_ERR_INVALID_ARG;
     if (rows == 0) return EP_OK;
     if (!a || !aligned(a, 16) || !a_scales || !aligned(a_scales, 4) || !out || !aligned(out, 2)) return EP_ERR_INVALID_ARG;
-    Fp8Args f;
+    Fp8Args f{};
     f.a_scales = a_scales;
     f.w_scales = w_scales;
     f.expert_base = expert_base;

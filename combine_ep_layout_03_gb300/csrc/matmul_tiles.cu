@@ -115,7 +115,9 @@ struct Work {
     uint8_t* raw;    // TMA stages: 128 weight rows, then token rows, of 128 codes
     uint8_t* cvt;    // float16 token rows of 64 k
     uint32_t tmem, cta;
-    int outs, per_pair, ctiles, raws;
+    int outs, per_pair;
+    Divisor ctiles;   // tiles of channels
+    int raws;
     int first, items, step;
 };
 
@@ -359,7 +361,7 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp, float* scal
 
 template <class C, bool GLU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_w,
+matmul_tiles_kernel(const MatmulArgs a, const Divisor ctiles, const __grid_constant__ CUtensorMap map_w,
                     const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_half) {
     extern __shared__ uint8_t dynamic[];
     __shared__ Shared<C> sh;
@@ -389,9 +391,8 @@ matmul_tiles_kernel(const MatmulArgs a, const __grid_constant__ CUtensorMap map_
 
     const int outs = GLU ? a.N / 2 : a.N;
     const int per_pair = GLU ? kRows : 2 * kRows;   // output channels of a tile
-    const int ctiles = (outs + per_pair - 1) / per_pair;
     // (overlapping segments can name more tiles than there is output; items + step stays a number)
-    const int64_t all = fits ? (int64_t)sh.seg.tile[a.E] * ctiles : 0, limit = INT32_MAX - (int64_t)gridDim.x;
+    const int64_t all = fits ? (int64_t)sh.seg.tile[a.E] * ctiles.of : 0, limit = INT32_MAX - (int64_t)gridDim.x;
     const Work<C> w = {a, sh, raw, raw + C::raw_stages * C::raw_bytes, sh.tmem, cta, outs, per_pair, ctiles,
                     (a.K + kRawK - 1) / kRawK, (int)(blockIdx.x >> 1), (int)(all < limit ? all : limit), (int)(gridDim.x >> 1)};
     bool ok = true;
@@ -421,14 +422,15 @@ cudaError_t launch(const MatmulArgs& a, int sms, cudaStream_t st) {
         !make_rows_map(&map_a, a.a, a.rows, a.K, kBoxTokens) ||
         !make_rows_map(&map_half, a.a, a.rows, a.K, C::half))
         return cudaErrorInvalidValue;
-    const int64_t most = ((a.rows + C::tile - 1) / C::tile + (a.E > 1 ? a.E : 0)) * ((outs + per_pair - 1) / per_pair);
+    const int64_t ctiles = (outs + per_pair - 1) / per_pair, most = ((a.rows + C::tile - 1) / C::tile + (a.E > 1 ? a.E : 0)) * ctiles;
     if (most > INT32_MAX - sms) return cudaErrorInvalidValue;   // more output than any memory holds
     const int64_t pairs = most < sms / 2 ? most : sms / 2;
     auto kernel = a.swiglu ? matmul_tiles_kernel<C, true> : matmul_tiles_kernel<C, false>;
     static std::atomic<uint64_t> done[2];
     const cudaError_t e = allow_smem(kernel, C::smem, done[a.swiglu]);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(kernel, dim3((unsigned)(2 * pairs)), kThreads, C::smem, st, a, map_w, map_a, map_half);
+    return launch_overlapped(kernel, dim3((unsigned)(2 * pairs)), kThreads, C::smem, st, a, divisor((uint32_t)ctiles),
+                             map_w, map_a, map_half);
 }
 
 // Segments of up to this many rows take the thin form, and so do larger ones if its rounds of tiles, which
