@@ -483,13 +483,13 @@ cudaError_t launch(const Fp8Args& a, const void* rows, const void* weights, int 
 // rows may take matmul_skinny.cu instead, whose items are 16 channels by 32 rows: so much for each round of items and for
 // each eight 128-byte pieces of a row.
 // Measured, us in a graph (Thick, Mid, Small):
-//   one matrix: 100 rows x 4096 x 4096: 23.1, 14.3, 10.9; 500 x 4096 x 1024: 22.0, 14.6, 11.1; 1000 x 2048 x 2048: 15.1, 10.5, 21.6;
-//   4000 x 2048 x 2048 with SwiGLU: 26.2, 31.8, 76.9; experts: 8 of 128 rows, 2944 x 330: 18.9, 11.4, 9.2; 16 of 166, 4096 x
-//   2048: 46.6, 64.8, 167; 64 of 100, 2048 x 1024: 53.6, 40.4, 68.8; 128 of 200, 4096 x 2048 with SwiGLU: 275, 419, 1393; 32 of
-//   640, 128 x 592 with SwiGLU: 19.0, 18.7, 44.4.
-// Measured, us in a graph (few rows' kernel, Thin): one matrix, 4096 x 4096: 8 rows 6.4, 13.4; 32 rows 10.9, 15.2; 7168 x 4096 with
-// SwiGLU: 8 rows 8.9, 21.2; 32 rows 18.4, 22.0; experts of 2048 x 1024: 8 of 16 rows 10.0, 9.9; 8 of 32 with SwiGLU 15.0, 10.6;
-// 16 of 8 rows 13.8, 9.7; 32 of 8 rows 24.4, 16.1; 64 of 4 rows, 4096 x 1024: 73, 52.
+//   one matrix: 100 rows x 4096 x 4096: 21.5, 12.7, 10.3; 500 x 4096 x 1024: 21.2, 12.9, 10.4; 1000 x 2048 x 2048: 14.5, 8.9, 18.9;
+//   4000 x 2048 x 2048 with SwiGLU: 24.9, 26.0, 60.1; experts: 8 of 128 rows, 2944 x 330: 18.4, 11.2, 9.1; 16 of 166, 4096 x
+//   2048: 42.6, 47.9, 101; of 1024 x 1400 with SwiGLU: 17.4, 14.9, 28.9; 64 of 100, 2048 x 1024: 45.3, 34.0, 57.8; 64 of 512, 256 x
+//   1024: 28.4, 29.3, 64.1; 128 of 200, 4096 x 2048 with SwiGLU: 266, 310, 873; 32 of 640, 128 x 592 with SwiGLU: 16.0, 12.8, 23.2.
+// Measured, us in a graph (few rows' kernel, Thin): one matrix, 4096 x 4096: 8 rows 6.6, 12.1; 32 rows 11.1, 12.1; 7168 x 4096 with
+// SwiGLU: 8 rows 8.8, 19.8; 32 rows 18.3, 19.7; 1024 x 8192: 16 rows 6.8, 5.7; experts of 2048 x 1024: 8 of 16 rows 9.9, 8.4; 8 of
+// 32 with SwiGLU 14.9, 9.3; 16 of 8 rows 13.9, 8.6; 32 of 8 rows 24.3, 14.0; 64 of 4 rows, 4096 x 1024: 73.7, 49.5.
 template <bool GLU>
 struct Plan {
     const Fp8Args& a;
@@ -500,7 +500,7 @@ struct Plan {
     void consider(double block, double of_tile) {
         const int64_t each = (a.rows + a.E - 1) / a.E, experts = a.rows < a.E ? a.rows : a.E, per_tile = GLU ? C::n / 2 : C::n;
         const int64_t tiles = (each + C::tile - 1) / C::tile * experts * ((a.outs + per_tile - 1) / per_tile);
-        const double t = 2.0 + (double)((tiles + sms / C::ctas - 1) / (sms / C::ctas)) * (a.blocks * block + of_tile);
+        const double t = 2.8 + (double)((tiles + sms / C::ctas - 1) / (sms / C::ctas)) * (a.blocks * block + of_tile);
         if (t < us) us = t, tile = C::tile, n = C::n;
     }
     bool is_few_rows() const {
@@ -515,10 +515,10 @@ struct Plan {
 template <bool GLU>
 cudaError_t run(const Fp8Args& a, const void* rows, const void* weights, int sms, cudaStream_t st) {
     Plan<GLU> plan{a, sms};
-    if ((a.rows + a.E - 1) / a.E <= Thin::tile) plan.template consider<Thin>(0.32, 2.0);
-    plan.template consider<Small>(0.20, 1.8);
-    plan.template consider<Mid>(0.38, 2.0);
-    plan.template consider<Thick>(0.54, 3.1);
+    if ((a.rows + a.E - 1) / a.E <= Thin::tile) plan.template consider<Thin>(0.29, 0.8);
+    else plan.template consider<Small>(0.19, 1.1);   // (for so few rows it was never first)
+    plan.template consider<Mid>(0.31, 1.5);
+    plan.template consider<Thick>(0.52, 2.9);
     if (plan.is_few_rows()) {
         MatmulArgs m{};
         m.a = (const uint8_t*)rows;
