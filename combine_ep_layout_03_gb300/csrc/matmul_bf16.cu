@@ -23,7 +23,7 @@
 // Measured: 8192^3 578 us, 1902 TFLOP/s (0.99 of the measured rate); 128 experts of 1088 rows, 4096 x 2048: 1520 us one after
 // the other (at 1390 MHz and the power limit; 1310 after a rest), dw of the same 1410 to 1630; 6 rows for each of 128 experts,
 // 4096 x 2 x 1024: 308 us, 7.0 TB/s.  Large tiles are bound by the tensor cores (0.96 of a CTA's time) and by power; short sums
-// by a tile's way out, of which an SM stores 27 bytes a clock in float32 and 16 in bf16 (whose instructions take as long as its
+// by a tile's way out, of which an SM stores some 27 bytes a clock in float32 and 24 in bf16 (whose instructions take as long as its
 // stores: without the stores themselves dw of 16 experts of 16 rows took 19 us where it took 22).
 #include "expert_ops.cuh"
 #include "expert_tiles.cuh"
@@ -599,12 +599,12 @@ double few_rows_us(const Bf16Args& a, bool glu, int sms) {
 // Which tile, and how many pairs share its sum: whatever is over first by this estimate in us, of rounds of tiles of so many
 // steps of 64 and of their way out.  The larger tiles do more products for what they read, the smaller ones are more, and pay for fewer rows that
 // are none; to share a sum takes a meeting, and clusters that find room.
-// Measured, us (256, 128, 64 rows a tile):
-//   one matrix: 128 rows x 4096 x 4096: 29.3, 23.2, 23.2; 2000 x 2048 x 1000: 19.1, 17.1, 23.2; 4000 x 2048 x 2000: 29.3,
-//   39.6, 60.1; experts: 64 of 96 rows, 2048 x 1024: 73.7, 68.3, 70.4; 64 of 128, 4096 x 2048: 201, 193, 218; 128 of 200:
-//   392, 441, 734; 128 of 6 with SwiGLU: 361, 353, 334.
-//   dw: 2000 rows, 1024 x 1024: 21.2, 17.1; 16384 rows: 88.7, 72.4; 4 experts of 2000 rows, 2048 x 512: 23.2, 27.3; 128 of 64
-//   rows, 2048 x 1024: 132, 156.
+// Measured, us in a graph (256, 128, 64 rows a tile):
+//   one matrix: 500 rows x 4096 x 1024: 22.9, 18.4, 18.4; 1000 x 2048 x 2048: 14.7, 12.6, 19.2; 4000 x 2048 x 2048 with SwiGLU: 25.9,
+//   42.8, 69.2; experts: 64 of 100 rows, 2048 x 1024: 58.4, 54.2, 59.7; 16 of 166, 4096 x 2048: 55.3, 67.3, 87.3; 64 of 512, 256 x
+//   1024: 26.5, 33.2, 51.3; 128 of 200, 4096 x 2048 with SwiGLU: 377, 572, 983; 32 of 64, 1024 x 2048 with SwiGLU: 31.5, 31.3, 30.2.
+//   dw: 2000 rows, 1024 x 1024: 17.6, 14.8; 16384 rows: 93.2, 75.9; 4 experts of 2000 rows, 2048 x 512: 17.1, 22.8; 128 of 64
+//   rows, 2048 x 1024: 108, 130, in float32 199, 200.
 // Measured, us in a graph (one, two, four pairs): 50 rows x 4096 x 512: 21.1, 15.8, 13.2; 300 x 7168 x 512 with SwiGLU: 35.8,
 // 23.5, 18.2; 128 x 2048 x 1024: 11.8, 11.4, 11.9; dw of 13922 rows, 992 x 376: 59.6, 35.5, 24.9; of 1000 rows, 512 x 512: 9.9,
 // 10.2, 11.2.
@@ -620,7 +620,7 @@ struct Plan {
             const int64_t rounds = (tiles + sms / 2 - 1) / (sms / 2), part = (steps + (1 << s) - 1) >> s;
             // a tile is stored under the next one's products
             const double sum = (double)part * per_step, longer = sum > store ? sum : store;
-            const double t = (double)rounds * (longer + 0.35) + sum + store - longer + meeting[s];
+            const double t = (double)rounds * (longer + 0.45) + sum + store - longer + meeting[s];
             if (t < us) us = t, tile = C::tile, split = 1 << s;
         }
     }
@@ -638,8 +638,9 @@ cudaError_t choose(const Bf16Args& a, const void* c, const void* r, int sms, cud
         return n > E ? n : E;
     };
     const int64_t steps = ((F == WEIGHTS ? (a.rows + a.E - 1) / a.E : a.reduced) + kStep - 1) / kStep;
-    // a CTA's part of a tile leaves at about 27 bytes a clock in float32, 16 in bf16 (whose rows are 64 bytes a warp)
-    const double per_row = a.wide ? 0.0102 : F == GLU ? 0.004 : 0.008;
+    // a CTA's part of a tile leaves at about 27 bytes a clock in float32, 24 in bf16.  (Us in a graph, 256 rows a tile, 128: 128 experts
+    // of 200 rows, 256 x 512: 13.6, 17.2; dw of 16 experts of 166 rows, 1024 x 1408: 18.2, 20.2.)
+    const double per_row = a.wide ? 0.0102 : F == GLU ? 0.004 : 0.0055;
     Plan plan;
     if constexpr (F != WEIGHTS) {
         if (each <= 32) plan.consider<Thin, F>(0.22, per_row, rtiles(Thin::tile) * ctiles, steps, sms);

@@ -18,9 +18,9 @@
 // time, they cost more than the FMAs).  Every wait is bounded (EP_ERR_TIMEOUT).
 //
 // Measured: 8192^3 461 us, 2380 TFLOP/s (without scales a library product takes 283); 128 experts of 1024 rows, 4096 x 2
-// x 1024 with SwiGLU 1187 us (at 1970 MHz and the power limit, as the library's product is at 1460 MHz); thin segments read
-// weights: 8 rows for each of 512 experts, 4096 x 1024, 324 us, 6.7 TB/s.  What bounds the large tile is a warp's way through a
-// block, some 1050 clocks: wait, four reads of tensor memory with their FMAs, the word that the accumulator is free.  With
+// x 1024 with SwiGLU 1143 us (at 1970 MHz and the power limit, as the library's product is at 1460 MHz); thin segments read
+// weights: 8 rows for each of 512 experts, 4096 x 1024, 316 us, 6.8 TB/s.  What bounds the large tile is a warp's way through a
+// block, some 1020 clocks: wait, four reads of tensor memory with their FMAs, the word that the accumulator is free.  With
 // everything else as it is, 8192^3 took 320 us without the epilogue's waits, reads and FMAs, as much with the reads alone,
 // 392 with the FMAs alone, and 496 with both (then 517 in all).
 #include "expert_ops.cuh"
