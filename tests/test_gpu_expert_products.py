@@ -318,3 +318,25 @@ def test_offsets_past_32_bits():
     dw = torch.empty(3, N, K, dtype=torch.float32, device="cuda")
     ep.ep_expert_matmul_grad_weights(out, a, base, dw)
     within(dw[2], d.t() @ a[-300:].double(), 302 * U * (d.abs().t() @ a[-300:].double().abs()), "gradient of the last matrix")
+
+
+def test_added_gradients_of_many_tiles():
+    c = make([150, 0, 64, 333, 1, 96, 40, 31], 600, 1032, seed=4)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    check_grad_weights(c, torch.float32, torch.randn(8, 600, 1032, device="cuda", generator=g))
+
+
+@pytest.mark.parametrize("dtype,accumulate", [(torch.bfloat16, False), (torch.float32, False), (torch.float32, True)])
+def test_weight_gradients_at_odd_addresses(dtype, accumulate):
+    """A gradient that lies on four bytes only has the values of one that lies on sixteen."""
+    c = make([150, 0, 64], 264, 96, seed=5)
+    before = torch.randn(3, 264, 96, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2)) if accumulate else None
+    ref = grad_weights(c, dtype, before)
+    step = 4 // ref.element_size()
+    for shift in (step, 2 * step, 3 * step):
+        flat = torch.full((ref.numel() + 4 * step,), 7.0, dtype=dtype, device="cuda")
+        out = flat[shift:shift + ref.numel()].view(ref.shape)
+        if accumulate:
+            out.copy_(before)
+        ep.ep_expert_matmul_grad_weights(c["dc"], c["a"], c["expert_base"], out, accumulate=accumulate)
+        assert torch.equal(out, ref) and (flat[:shift] == 7).all() and (flat[shift + ref.numel():] == 7).all()
