@@ -17,8 +17,8 @@
 // and one that brings the products of scales to shared memory (read where they are used, four bytes of 32 rows at a
 // time, they cost more than the FMAs).  Every wait is bounded (EP_ERR_TIMEOUT).
 //
-// Measured: 8192^3 461 us, 2380 TFLOP/s (without scales a library product takes 283); 128 experts of 1024 rows, 4096 x 2
-// x 1024 with SwiGLU 1143 us (at 1970 MHz and the power limit, as the library's product is at 1460 MHz); thin segments read
+// Measured: 8192^3 455 us, 2410 TFLOP/s (without scales a library product takes 283); 128 experts of 1024 rows, 4096 x 2
+// x 1024 with SwiGLU 1140 us (at 1970 MHz and the power limit, as the library's product is at 1460 MHz); thin segments read
 // weights: 8 rows for each of 512 experts, 4096 x 1024, 316 us, 6.8 TB/s.  What bounds the large tile is a warp's way through a
 // block, some 1020 clocks: wait, four reads of tensor memory with their FMAs, the word that the accumulator is free.  With
 // everything else as it is, 8192^3 took 320 us without the epilogue's waits, reads and FMAs, as much with the reads alone,
@@ -338,7 +338,7 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
         else arrive_one_cluster(lane, acc_empty0 + 8 * at);
     };
     Ring<kChunks> scales;
-    uint32_t use = 0;   // of the accumulators
+    Ring<C::accs> acc;
     int expert = 0;
     bool ok = true;
     for (int item = w.first; ok && item < w.items; item += w.step) {
@@ -352,11 +352,11 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
         for (int k = 0; ok && k < blocks; k += kChunk, scales.next()) {
             if (!wait_block(smem_addr(&w.sh.scale_full[scales.stage]), scales.parity)) { ok = false; break; }
             const int n = min(kChunk, blocks - k);
-            const uint32_t of = smem_addr(&w.sh.scales[scales.stage].of[cb][0][mine_row]);
-            float s = lds_f32(of), u = GLU ? lds_f32(of + kUps) : 0.0f;
-            for (int b = 0; b < n; ++b, ++use) {
-                const uint32_t at = use % C::accs;
-                if (!wait_block(acc_full + 8 * at, use / C::accs & 1)) { ok = false; break; }
+            uint32_t of = smem_addr(&w.sh.scales[scales.stage].of[cb][0][mine_row]);
+            for (const uint32_t end = of + n * 512; of != end; of += 512, acc.next()) {
+                const float s = lds_f32(of), u = GLU ? lds_f32(of + kUps) : 0.0f;
+                const uint32_t at = acc.stage;
+                if (!wait_block(acc_full + 8 * at, acc.parity)) { ok = false; break; }
                 tmem_fence_after();
                 if (some) {
                     const uint32_t d = columns + at * C::n;
@@ -373,10 +373,6 @@ __device__ __forceinline__ bool epilogue(const Work<C>& w, int warp) {
                 } else {
                     release(at);
                 }
-                // the next block's products of scales (behind the chunk's last one its own again, and not used)
-                const uint32_t after = of + min(b + 1, kChunk - 1) * 512;
-                s = lds_f32(after);
-                if (GLU) u = lds_f32(after + kUps);
             }
             __syncwarp();
             arrive_one(lane, smem_addr(&w.sh.scale_empty[scales.stage]));
