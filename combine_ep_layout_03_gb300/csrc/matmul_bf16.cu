@@ -482,6 +482,7 @@ matmul_bf16_kernel(const Bf16Args a, const __grid_constant__ CUtensorMap map_c, 
     cluster_sync();
     tmem_fence_after();
     wait_for_previous();   // (what is above runs while the kernel before ends: one tile 4.0 us, 4.2 with the clusters' wait below)
+    let_next_start();
     const bool fits = load_segments<kThreads>(sh.seg, a, C::tile);   // the same answer in both CTAs
 
     const int per_pair = F == GLU ? kRows : 2 * kRows;

@@ -387,6 +387,7 @@ matmul_tiles_kernel(const MatmulArgs a, const Divisor ctiles, const __grid_const
     cluster_sync();
     tmem_fence_after();
     wait_for_previous();   // (what is above runs while the kernel before ends: one tile 5.4 us in a graph, 6.4 where nothing did)
+    let_next_start();
     const bool fits = load_segments<kThreads>(sh.seg, a, C::tile);   // the same answer in both CTAs
 
     const int outs = GLU ? a.N / 2 : a.N;
