@@ -23,6 +23,8 @@
 // block, some 1020 clocks: wait, four reads of tensor memory with their FMAs, the word that the accumulator is free.  With
 // everything else as it is, 8192^3 took 320 us without the epilogue's waits, reads and FMAs, as much with the reads alone,
 // 392 with the FMAs alone, and 496 with both (then 517 in all).
+// The tile of 128 by 128 is bound by its loads, 64 bytes a clock of an SM: half the sums a thread, or twice the accumulators, left it
+// as it is (8.9 us for 1000 rows x 2048 x 2048).
 #include "expert_ops.cuh"
 #include "expert_tiles.cuh"
 #include "tcgen05.cuh"
