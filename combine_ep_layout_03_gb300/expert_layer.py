@@ -173,12 +173,16 @@ class TrainableExperts:
     """The experts of a layer in training, on one GPU that holds all R ranks: bf16 weights w13 [E, 2I, H] (gate rows, then
     up rows) and w2 [E, H, I], gradients grad_w13 and grad_w2 of their shapes in float32, to which each backward() adds.
     H a multiple of 8, I of 128.  What backward() needs of the forward pass is kept in this object's buffers: rows in bf16,
-    gates and ups in 8 bits.  Calls of one object are issued on one stream, or ordered across streams by the caller."""
+    gates and ups in 8 bits.  Calls of one object, its making among them, are issued on one stream, or ordered across streams by the
+    caller."""
 
     def __init__(self, R: int, T: int, w13: torch.Tensor, w2: torch.Tensor, topk: int, alpha: int = 1):
+        # (the products check these again, but by then a forward() is on its way)
+        if w13.dim() != 3 or w13.dtype is not torch.bfloat16 or not w13.is_contiguous() or w13.shape[1] % 256 or w13.shape[2] % 8:
+            raise ep.EPError(ep.EP_ERR_INVALID_ARG, "w13: contiguous bf16 [E, 2I, H], I a multiple of 128, H of 8")
         self.E, self.I, self.H = w13.shape[0], w13.shape[1] // 2, w13.shape[2]
-        if w13.dtype is not torch.bfloat16 or w2.dtype is not torch.bfloat16 or w2.shape != (self.E, self.H, self.I) or self.I % 128:
-            raise ep.EPError(ep.EP_ERR_INVALID_ARG, "w13: bf16 [E, 2I, H], w2: bf16 [E, H, I], I a multiple of 128")
+        if w2.dtype is not torch.bfloat16 or not w2.is_contiguous() or w2.shape != (self.E, self.H, self.I):
+            raise ep.EPError(ep.EP_ERR_INVALID_ARG, "w2: contiguous bf16 [E, H, I]")
         if R * T < 1:
             raise ep.EPError(ep.EP_ERR_INVALID_ARG, "R * T: at least one token")
         self.R, self.T, self.N, self.K, self.w13, self.w2 = R, T, R * T, topk, w13, w2
@@ -186,6 +190,10 @@ class TrainableExperts:
         self.layout = ep.EPLayout(R, T, self.H, self.E, topk, alpha, device=dev)
         cap = self.layout.worst_rows
         self._dst = self.layout.views()["dst_row"]
+        # a layout without entries, until one has run (a captured forward() runs when its graph is replayed)
+        self.layout.ws.zero_()
+        self._dst.fill_(-1)
+        self._ran = False   # whether the buffers are those of a whole forward()
         self.rows = torch.empty((cap, self.H), dtype=bf, device=dev)
         self.inner = torch.empty((cap, self.I), dtype=bf, device=dev)
         self.c = torch.empty((cap, 2 * self.I), dtype=bf, device=dev)       # and its gradient
@@ -217,7 +225,7 @@ class TrainableExperts:
                                   (topk_weights, torch.float32, self.N * self.K, "topk_weights: contiguous float32 [N, K]")):
             if t.dtype is not dtype or not t.is_contiguous() or t.numel() != n:
                 raise ep.EPError(ep.EP_ERR_INVALID_ARG, what)
-        lay = self.layout
+        lay, self._ran = self.layout, False
         lay.layout(topk_idx, stream)
         lay.dispatch(x, ep.EP_QUANT_NONE, self.rows.view(torch.uint8), None, stream)
         lay.expert_matmul_bf16(self.rows, self.w13, self.c, stream=stream)
@@ -227,11 +235,16 @@ class TrainableExperts:
             out = torch.empty((self.N, self.H), dtype=torch.bfloat16, device=x.device)
         ep.ep_swiglu_keep(self.c, self.inner, self.codes, self.scales, self.row_weights[:-1], lay.rows_used, stream)
         lay.expert_matmul_bf16(self.inner, self.w2, self.expert_out, stream=stream)
-        return lay.combine(self.expert_out, self.ones, out, None, stream)
+        lay.combine(self.expert_out, self.ones, out, None, stream)
+        self._ran = True
+        return out
 
     def backward(self, grad_out: torch.Tensor, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
         """(grad_x bf16 [R*T, H], grad_topk_weights float32 [R*T, K]) of the last forward(), of grad_out bf16 [R*T, H]; an
-        entry without an expert has gradient 0.  The weights' gradients are added to grad_w13 and grad_w2."""
+        entry without an expert has gradient 0.  The weights' gradients are added to grad_w13 and grad_w2.  Refused before the
+        first forward(), and after one that raised on its way."""
+        if not self._ran:
+            raise ep.EPError(ep.EP_ERR_INVALID_ARG, "backward() needs a forward() before it")
         if grad_out.dtype is not torch.bfloat16 or not grad_out.is_contiguous() or grad_out.numel() != self.N * self.H:
             raise ep.EPError(ep.EP_ERR_INVALID_ARG, "grad_out: contiguous bf16 [N, H]")
         lay = self.layout
