@@ -171,18 +171,23 @@ __device__ __forceinline__ bool load_tiles(const Work<C>& w, const CUtensorMap* 
 }
 
 // The waits and words of the loop over blocks, which is one chain of latencies: without branches on the lane (50 to 100
-// clocks each).  A wait is bounded by its polls, each of which may park the thread.  Its answer is the warp's: lanes need
-// not leave the loop together, and what follows (loads of tensor memory, elections) asks for a converged warp.
+// clocks each).  Polls and limit are mbar_wait_parked()'s: every 64 polls the clock is read.  The answer is the warp's: lanes
+// need not leave the loop together, and what follows (loads of tensor memory, elections) asks for a converged warp.
 __device__ __forceinline__ bool wait_block(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
-                 "POLL%=:\n\t"
-                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .u32 n, r;\n\t.reg .u64 start, now;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
                  "@p bra OVER%=;\n\t"
-                 "add.u32 n, n, 1;\n\tsetp.lt.u32 p, n, %3;\n\t@p bra POLL%=;\n\t"
+                 "mov.u32 n, 0;\n\tmov.u64 start, 0;\n"
+                 "POLL%=:\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                 "@p bra OVER%=;\n\t"
+                 "add.u32 n, n, 1;\n\tand.b32 r, n, 63;\n\tsetp.ne.u32 p, r, 0;\n\t@p bra POLL%=;\n\t"
+                 "mov.u64 now, %%globaltimer;\n\tsetp.eq.u32 p, n, 64;\n\t@p mov.u64 start, now;\n\t"
+                 "sub.u64 now, now, start;\n\tsetp.le.u64 p, now, %4;\n\t@p bra POLL%=;\n\t"
                  "setp.ne.u32 p, 0, 0;\n"
                  "OVER%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(bar), "r"(parity), "r"(kMaxPolls) : "memory");
+                 : "=r"(ok) : "r"(bar), "r"(parity), "r"(kParkNs), "l"(kWaitNs) : "memory");
     return __all_sync(0xffffffffu, ok != 0);
 }
 

@@ -43,7 +43,9 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
 
 // Bounded wait of a kernel whose warps share an SM's issue slots with the ones they wait for:
 // each poll may park the thread for up to 20 us, since short polls of a dozen warps took a third
-// of the slots.  Gives up after about four seconds.
+// of the slots.  Gives up after kWaitNs.
+constexpr uint32_t kParkNs = 20000;
+constexpr uint64_t kWaitNs = 4000000000ull;
 __device__ __forceinline__ bool mbar_wait_parked(uint64_t* bar, uint32_t parity) {
     uint64_t start = 0;
     for (uint32_t i = 0; i < kMaxPolls; ++i) {
@@ -51,13 +53,13 @@ __device__ __forceinline__ bool mbar_wait_parked(uint64_t* bar, uint32_t parity)
         asm volatile("{\n\t.reg .pred p;\n\t"
                      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
                      "selp.u32 %0, 1, 0, p;\n\t}"
-                     : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity), "r"(20000u) : "memory");
+                     : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity), "r"(kParkNs) : "memory");
         if (ok) return true;
         if ((i & 63u) == 63u) {
             uint64_t now;
             asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
             if (start == 0) start = now;
-            else if (now - start > 4000000000ull) return false;
+            else if (now - start > kWaitNs) return false;
         }
     }
     return false;
