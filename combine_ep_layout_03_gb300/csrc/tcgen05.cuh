@@ -41,6 +41,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
 }
 
+// 16 bytes of this CTA's shared memory to `dst` of another CTA of the cluster, whose barrier `bar` gets them as bytes that
+// have arrived (both as cluster addresses).  It is a release to the cluster that waits for nothing of this thread's: the copy
+// reads what this CTA's threads wrote before fence_proxy_async_smem(), and its completion is the release.
+__device__ __forceinline__ void copy16_to_cluster(uint32_t dst, uint32_t src, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(dst), "r"(src), "r"(16u), "r"(bar) : "memory");
+}
+
 // Bounded wait of a kernel whose warps share an SM's issue slots with the ones they wait for:
 // each poll may park the thread for up to 20 us, since short polls of a dozen warps took a third
 // of the slots.  Gives up after kWaitNs.
