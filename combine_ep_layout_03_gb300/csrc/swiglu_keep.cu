@@ -189,7 +189,9 @@ cudaError_t launch_grad(const KeepArgs& a, cudaStream_t st) {
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
 
 bool sizes_ok(int64_t rows, int32_t inner) {
-    return rows >= 0 && inner >= 128 && inner <= 65536 && inner % 128 == 0 && rows <= INT32_MAX / (inner / 128) - 64;
+    // (units of 128 gates: a grid covers them in 32s, so that the last one's number stays below 2^31 too)
+    static_assert(kUnits * kEach == 32, "2^31 is a multiple of a CTA's units");
+    return rows >= 0 && inner >= 128 && inner <= 65536 && inner % 128 == 0 && rows <= INT32_MAX / (inner / 128);
 }
 
 }  // namespace
