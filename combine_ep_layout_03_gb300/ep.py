@@ -467,6 +467,8 @@ def ep_expert_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w
 
 # Small calls are as long as their checks here, so these stand in line, and each attribute is asked for once.
 _BF16, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+# what rows in e4m3 and their scales may come as: themselves, or the bytes of a receive buffer
+_E4M3_OR_BYTES, _F32_OR_BYTES = (_E4M3, torch.uint8), (_F32, torch.uint8)
 
 
 def _base_ptr(expert_base, E: int):
@@ -482,7 +484,7 @@ def _base_ptr(expert_base, E: int):
 def ep_expert_matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, expert_base,
                          out: torch.Tensor, swiglu: bool = False, status=None, stream=None) -> None:
     """e4m3 rows times e4m3 expert matrices with a float32 scale for each block of 128: a [rows, K] with a_scales [rows,
-    K / 128] (both also as the bytes of a receive buffer), w [E, N, K] with w_scales [E, ceil(N / 128), K / 128], or [E,
+    K / 128] (both also as the bytes of a receive buffer, uint8), w [E, N, K] with w_scales [E, ceil(N / 128), K / 128], or [E,
     2 * ceil(N / 2 / 128), K / 128] with swiglu; expert_base int32 [E + 1] on the device (None: one matrix), out bf16
     [rows, N], or [rows, N / 2] = silu(gates) * ups with swiglu."""
     shape, wshape = a.shape, w.shape
@@ -492,11 +494,11 @@ def ep_expert_matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
     E, N, wk = wshape
     outs = N // 2 if swiglu else N
     blocks, bad = (outs + 127) // 128 * (2 if swiglu else 1), None
-    if a.element_size() != 1 or not a.is_contiguous():
+    if a.dtype not in _E4M3_OR_BYTES or not a.is_contiguous():
         bad = "a: e4m3 [rows, K]"
     elif w.dtype is not _E4M3 or not w.is_contiguous() or wk != K or K % 128 != 0:
         bad = "w: e4m3 [E, N, K], K a multiple of 128"
-    elif not a_scales.is_contiguous() or a_scales.nbytes != rows * (K // 32):
+    elif a_scales.dtype not in _F32_OR_BYTES or not a_scales.is_contiguous() or a_scales.nbytes != rows * (K // 32):
         bad = "a_scales: float32 [rows, K / 128]"
     elif w_scales.dtype is not _F32 or not w_scales.is_contiguous() or w_scales.numel() != E * blocks * (K // 128):
         bad = "w_scales: float32 [E, N / 128, K / 128]"
@@ -587,9 +589,9 @@ def _keep_rows(shape, codes, scales, row_weights, rows_used):
     rows, width = shape
     if width % 256 != 0:
         return "I: a multiple of 128"
-    if codes.element_size() != 1 or not codes.is_contiguous() or codes.shape != shape:
+    if codes.dtype not in _E4M3_OR_BYTES or not codes.is_contiguous() or codes.shape != shape:
         return "codes: e4m3 [rows, 2I]"
-    if not scales.is_contiguous() or scales.nbytes != rows * width // 32:
+    if scales.dtype not in _F32_OR_BYTES or not scales.is_contiguous() or scales.nbytes != rows * width // 32:
         return "scales: float32 [rows, 2I / 128]"
     if row_weights is not None and (row_weights.dtype is not _F32 or not row_weights.is_contiguous() or row_weights.numel() != rows):
         return "row_weights: float32 [rows]"
@@ -601,7 +603,7 @@ def _keep_rows(shape, codes, scales, row_weights, rows_used):
 def ep_swiglu_keep(c: torch.Tensor, inner: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, row_weights=None,
                    rows_used=None, stream=None) -> None:
     """inner = row_weights * silu(g) * u of bf16 rows c [rows, 2I] = [g, u], and c in 8 bits for the backward pass:
-    codes [rows, 2I] (e4m3, or bytes) and scales [rows, 2I / 128] float32 (or bytes).  rows_used: int32 [1] on the
+    codes [rows, 2I] (e4m3, or uint8) and scales [rows, 2I / 128] float32 (or their bytes, uint8).  rows_used: int32 [1] on the
     device, how many of the rows hold anything (None: all)."""
     shape = c.shape
     if len(shape) != 2 or c.dtype is not _BF16 or not c.is_contiguous():
