@@ -17,7 +17,7 @@ SOURCES = ["ep_api.cu", "layout.cu", "dispatch.cu", "dispatch_scaled.cu", "combi
            "noalloc.cu", "rows.cu", "few_tokens.cu", "matmul_skinny.cu", "matmul_tiles.cu",
            "swiglu_keep.cu", "matmul_bf16.cu", "matmul_fp8.cu"]
 HEADERS = ["ep_internal.cuh", "tma.cuh", "quant.cuh", "expert_ops.cuh", "skinny.cuh", "tcgen05.cuh",
-           "tensor_maps.cuh", "ring_places.cuh", "expert_tiles.cuh", "row_codes.cuh"]
+           "tensor_maps.cuh", "ring_places.cuh", "expert_tiles.cuh", "tile_places.cuh", "row_codes.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-Xptxas", "-v"]

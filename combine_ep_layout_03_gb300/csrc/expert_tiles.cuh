@@ -1,42 +1,12 @@
-// expert_tiles.cuh -- what the tensor-core kernels over expert segments share: where a tile lies, ring
-// positions, a warp's wait, and SwiGLU of float32 accumulators.
+// expert_tiles.cuh -- what the tensor-core kernels over expert segments share: looking up a tile (where it lies and ring
+// positions: tile_places.cuh), a warp's wait, and SwiGLU of float32 accumulators.
 #pragma once
 
 #include "expert_ops.cuh"
 #include "tcgen05.cuh"
+#include "tile_places.cuh"
 
 namespace {
-
-struct Tile { int64_t row0; int expert, m, n, channel; };   // n: MMA columns, channel: tile of output channels
-
-// A number that many are divided by, with a reciprocal: floor((2^32 - 1) / of).  A quotient by it is at most one too small.
-struct Divisor { uint32_t of, reciprocal; };
-inline Divisor divisor(uint32_t d) { return {d, 0xffffffffu / d}; }
-__device__ __forceinline__ uint32_t operator/(uint32_t n, const Divisor& d) {
-    const uint32_t q = __umulhi(n, d.reciprocal);
-    return q + (n - q * d.of >= d.of);
-}
-
-// n / d, n - d * (n / d) where the quotient is small (below 2^20): by an approximate reciprocal, one off at most.
-struct Quotient { uint32_t whole, rest; };
-__device__ __forceinline__ Quotient divide(uint32_t n, uint32_t d) {
-    uint32_t q = __float2uint_rz(__fdividef((float)n, (float)d));
-    int32_t rest = (int32_t)(n - q * d);
-    if (rest < 0) q -= 1, rest += d;
-    else if (rest >= (int32_t)d) q += 1, rest -= d;
-    return {q, (uint32_t)rest};
-}
-
-// In which order the tiles of a matrix are taken: token tiles in groups of eight, all channels of a group before the next
-// one, its token tiles fastest.  What runs at a time then covers about as many token tiles as channel tiles, and reads
-// few of either.  local: of the matrix's tiles (of token tiles and channel tiles), at: local / ctiles.
-struct Place { int tile, channel; };
-__device__ __forceinline__ Place place_of(uint32_t local, uint32_t at, uint32_t tiles, uint32_t ctiles) {
-    constexpr uint32_t kGroup = 8;
-    const uint32_t before = at / kGroup * kGroup;
-    const Quotient q = divide(local - before * ctiles, min(kGroup, tiles - before));
-    return {(int)(before + q.rest), (int)q.whole};
-}
 
 // Tiles of one expert are neighbours: concurrent pairs share weights and tokens in L2.
 // The roles look tiles up between one tile's work and the next, so it has to be quick: a whole warp goes on from
@@ -52,33 +22,8 @@ __device__ __forceinline__ Tile tile_of(const Segments& s, int E, const Divisor&
     } else {
         e = expert_of_tile(s, E, at);
     }
-    const uint32_t first_tile = s.tile[e], tiles = s.tile[e + 1] - first_tile;
-    // the segment's groups of 32 rows dealt out evenly: no tile is much shorter, and none pays for a row more
-    const Place p = place_of(item - first_tile * ctiles.of, at - first_tile, tiles, ctiles.of);
-    const Quotient q = divide((uint32_t)(s.rows[e] + 31) / 32, tiles);
-    const int j = p.tile, each = (int)q.whole, more = (int)q.rest;
-    const int first = 32 * (j * each + min(j, more));
-    Tile t;
-    t.expert = e;
-    t.row0 = (int64_t)s.base[e] + first;
-    t.m = min(32 * (each + (j < more)), s.rows[e] - first);
-    t.n = (t.m + 31) / 32 * 32;
-    t.channel = p.channel;
-    return t;
+    return tile_in_segment(item, at, ctiles, e, s.tile[e], s.tile[e + 1] - s.tile[e], s.base[e], s.rows[e]);
 }
-
-// A ring position: stage and parity of use i.
-template <int STAGES>
-struct Ring {
-    int stage = 0;
-    uint32_t parity = 0;
-    __device__ __forceinline__ void next() {
-        if (++stage == STAGES) { stage = 0; parity ^= 1; }
-    }
-    __device__ __forceinline__ void back() {
-        if (stage-- == 0) { stage = STAGES - 1; parity ^= 1; }
-    }
-};
 
 __device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");

@@ -67,12 +67,7 @@ struct Config {
     static constexpr uint32_t columns = ACCS * N;
     static_assert(columns <= 512 && (columns & (columns - 1)) == 0 && columns >= 32, "tensor memory");
     static_assert(bytes_a % 1024 == 0 && bytes % 1024 == 0 && width % 32 == 0 && N % width == 0, "swizzled rows; registers");
-    // Each of the two issuing warps looks at the stages of every other block only, and a parity tells two neighbouring
-    // phases apart, no more: with an odd number of stages it meets a stage at every second of its loads.  When it asks for
-    // block b there, block b - STAGES must be over.  It has issued b - 2, for which the accumulator of b - 2 - ACCS was
-    // read, and that is done in order.  (With five stages and four accumulators a warp could take a load that came late
-    // for the next one, and free its stage twice.)
-    static_assert(STAGES % 2 == 0 || STAGES >= ACCS + 2, "stages that no warp can lap");
+    static_assert(no_warp_laps(STAGES, ACCS), "stages that no warp can lap");
     static_assert(ACCS % 2 == 0, "an accumulator is one warp's");
     // an MMA reads 128 token rows, also where a stage has room for fewer: what follows is read for them, inside shared memory
     static_assert(bytes - bytes_a + staged >= (128 - ROWS) * 128, "rows past a stage's");
