@@ -593,8 +593,8 @@ cudaError_t launch(const Bf16Args& a, const void* c, const void* r, int split, i
                                       map_c, map_r, map_half);
 }
 
-// What few rows take in matmul_skinny.cu, in us: its items are 16 channels by 32 rows, so much for each round of items and for
-// each eight 128-byte pieces of a row.
+// What few rows take in matmul_skinny.cu, in us: 3.0 for its start, and its items are 16 channels by 32 rows, so much for each
+// round of items and for each eight 128-byte pieces of a row.  (Plan's estimates are of tiles alone: kStartUs before them.)
 // Measured, us in a graph (that kernel, Thin): one matrix: 8 rows x 4096 x 4096 7.1, 17.8; 32 rows 11.3, 17.8; 32 rows x 7168 x
 // 512 10.1, 27.2; experts of 2048 x 1024: 8 of 32 rows with SwiGLU 13.3, 14.4; 16 of 8 rows 14.4, 12.5; 32 of 8 rows 33.6,
 // 27.6; 64 of 4 rows, 4096 x 1024: 95.8, 87.9.
@@ -636,6 +636,10 @@ struct Plan {
     }
 };
 
+// Clusters, barriers, tensor memory and the first loads: a tile of 8 rows, 8 channels and 8 of the sum takes 3.7 to 4.0 us in
+// a graph.
+constexpr double kStartUs = 4.0;
+
 template <Form F>
 cudaError_t choose(const Bf16Args& a, const void* c, const void* r, int sms, cudaStream_t st) {
     const int64_t per_pair = F == GLU ? kRows : 2 * kRows, ctiles = (a.outs + per_pair - 1) / per_pair;
@@ -658,7 +662,7 @@ cudaError_t choose(const Bf16Args& a, const void* c, const void* r, int sms, cud
     plan.consider<Mid, F>(0.24, per_row, rtiles(Mid::tile) * ctiles, steps, sms);
     if (each > Mid::tile) plan.consider<Thick, F>(0.30, per_row, rtiles(Thick::tile) * ctiles, steps, sms);
     if constexpr (F == FORWARD || F == GLU) {
-        if (few_rows_us(a, F == GLU, sms) <= 4.0 + plan.us) {
+        if (few_rows_us(a, F == GLU, sms) <= kStartUs + plan.us) {
             MatmulArgs m{};
             m.a = (const uint8_t*)r;
             m.w = (const uint8_t*)c;

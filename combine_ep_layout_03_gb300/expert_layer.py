@@ -26,7 +26,22 @@ the second is the faster one where the tokens choose many experts (few, more; us
 
 ``TrainableExperts`` runs layout, dispatch, the products, SwiGLU with its gates and ups kept in 8 bits, and combine, and their
 gradients.  The routing weight of a row is multiplied in with SwiGLU, so that combine is a plain sum: its gradient is a
-dispatch of the output's gradient, and that of dispatch a combine.
+dispatch of the output's gradient, and that of dispatch a combine.  The two calls stand outside of autograd: ``forward`` returns
+a tensor without a graph, whatever x and the weights require.  A model whose other layers are autograd's puts them into a
+function of its own:
+
+    class Experts(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, topk_weights, topk_idx, experts):
+            ctx.experts = experts
+            return experts.forward(x, topk_idx, topk_weights)
+
+        @staticmethod
+        def backward(ctx, grad_out):
+            grad_x, grad_topk_weights = ctx.experts.backward(grad_out.contiguous())
+            return grad_x, grad_topk_weights, None, None
+
+    out = Experts.apply(x, topk_weights, topk_idx, experts)      # topk_weights [N, K]; one backward pass before the next forward
 """
 from __future__ import annotations
 
@@ -218,8 +233,8 @@ class TrainableExperts:
         return torch.where(self._dst < 0, self.row_weights.numel() - 1, self._dst).view(-1).long()
 
     def forward(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor, stream=None) -> torch.Tensor:
-        """The weighted sum of the chosen experts' outputs of x [R*T, H] bf16: a new bf16 [R*T, H].  topk_idx int64 and
-        topk_weights float32, contiguous, hold K entries for each token (-1: no expert)."""
+        """The weighted sum of the chosen experts' outputs of x [R*T, H] bf16: a new bf16 [R*T, H], without an autograd graph.
+        topk_idx int64 and topk_weights float32, contiguous, hold K entries for each token (-1: no expert)."""
         for t, dtype, n, what in ((x, torch.bfloat16, self.N * self.H, "x: contiguous bf16 [N, H]"),
                                   (topk_idx, torch.int64, self.N * self.K, "topk_idx: contiguous int64 [N, K]"),
                                   (topk_weights, torch.float32, self.N * self.K, "topk_weights: contiguous float32 [N, K]")):
