@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 5) swiglu_keep_grad_kernel(const Kee
     const bool in = row < rows_of(a);
     if (LANES >= 32 && !in) return;   // (halves of a warp stay together for their sums)
     const int inner = a.groups * 128;
-    const float weight = in && a.weights ? a.weights[row] : 1.0f, quarter = 0.25f * weight;
+    const float weight = in && a.weights ? a.weights[row] : 1.0f;
     const uint8_t* codes = a.codes + row * inner * 2;
     const float* scales = a.scales + row * a.groups * 2;
     float sum = 0.0f;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 5) swiglu_keep_grad_kernel(const Kee
                 asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(0.25f + e));
                 const float s = 0.25f * r, silu = g[h] * s, wd = weight * d[h];
                 sum = __fmaf_rn(d[h], silu * u[h], sum);
-                ny[h] = g[h] * (r * (u[h] * quarter));   // as the forward pass has it: silu * u alone may pass the range
+                ny[h] = silu * (weight * u[h]);   // silu * u alone may pass the range
                 nu[h] = wd * silu;
                 ng[h] = wd * (u[h] * __fmaf_rn(silu, 1.0f - s, s));
             }
