@@ -18,7 +18,7 @@
 //
 // dw reduces over token rows, and a segment ends anywhere: the rows of its last 16 that belong to others (to the next
 // expert, or to nobody, with any contents) are set to zero in shared memory, in both operands, between their arrival
-// and their product.  That the second CTA has done so the first one learns by a copy of 16 bytes, whose completion is a
+// and their product.  Its sums are taken 1024 rows at a time (sum_steps()).  That the second CTA has done so the first one learns by a copy of 16 bytes, whose completion is a
 // release to the cluster (16 experts of 166 rows, 1024 x 1408 in float32: 21.6 us in a graph; by an arrival that releases to the
 // cluster, which waits for the epilogue's stores, 32.1; with the rows loaded one by one and nothing cleared 25.6).
 //
@@ -61,6 +61,7 @@ constexpr int kBoxTokens = 32;            // rows of a small token box
 constexpr int kBlock = 64 * 128;          // MN-major: 64 channels or rows by 64 of the sum
 constexpr uint32_t kColumns = 512;        // of tensor memory
 constexpr int kMostParts = 4;             // of a tile's sum
+constexpr int kSteps = 16;                // WEIGHTS: of a sum that the tensor cores take in one go
 
 // TILE: rows of a tile, both CTAs.
 template <int TILE, int STAGES>
@@ -100,6 +101,8 @@ struct Work {
 
     // The first of the steps of a sum that part p takes.
     __device__ __forceinline__ int begin(int steps, int p) const { return steps * p / a.split; }
+    // Up to which step those from `first` on go to one accumulator.
+    __device__ __forceinline__ int until(int first, int end) const { return F == WEIGHTS ? min(first + kSteps, end) : end; }
 
     // The tile, and its stages of the sum.
     template <bool WARP>
@@ -242,38 +245,92 @@ __device__ __forceinline__ bool issue_mma(const Work<C, F>& w) {
     for (int item = w.first; ok && item < w.items; item += w.step) {
         int steps;
         const Tile t = w.template tile<true>(item, expert, steps);
-        const int begin = w.begin(steps, w.part), end = w.begin(steps, w.part + 1);
-        if (begin == end) continue;
         const uint32_t idesc = mma_desc_bf16(2 * kRows, t.n, a_mn, b_mn);
-        if (!warp_wait(&w.sh.acc_empty[acc.stage], acc.parity ^ 1)) { ok = false; break; }
-        tmem_fence_after();
-        const uint32_t d = w.tmem + acc.stage * C::tile;
-        for (int k = begin; k < end; ++k) {
-            if (!ready && !warp_wait(&w.sh.full[r.stage], r.parity)) { ok = false; break; }
+        for (int first = w.begin(steps, w.part), end = w.begin(steps, w.part + 1); ok && first < end; first = w.until(first, end)) {
+            if (!warp_wait(&w.sh.acc_empty[acc.stage], acc.parity ^ 1)) { ok = false; break; }
             tmem_fence_after();
-            const uint32_t at = smem0 + r.stage * C::bytes;
-            const uint64_t a = a_mn ? smem_desc_mn128(at, kBlock) : smem_desc_k128(at);
-            const uint64_t b = b_mn ? smem_desc_mn128(at + kBytesA, kBlock) : smem_desc_k128(at + kBytesA);
-            const int pieces = (w.left(t, k) + 15) / 16;
-            uint64_t* const empty = &w.sh.empty[r.stage];
-            r.next();
-            ready = __all_sync(0xffffffffu, mbar_test(&w.sh.full[r.stage], r.parity));
-            if (elect_one()) {
+            const uint32_t d = w.tmem + acc.stage * C::tile;
+            for (int k = first; k < w.until(first, end); ++k) {
+                if (!ready && !warp_wait(&w.sh.full[r.stage], r.parity)) { ok = false; break; }
+                tmem_fence_after();
+                const uint32_t at = smem0 + r.stage * C::bytes;
+                const uint64_t a = a_mn ? smem_desc_mn128(at, kBlock) : smem_desc_k128(at);
+                const uint64_t b = b_mn ? smem_desc_mn128(at + kBytesA, kBlock) : smem_desc_k128(at + kBytesA);
+                const int pieces = (w.left(t, k) + 15) / 16;
+                uint64_t* const empty = &w.sh.empty[r.stage];
+                r.next();
+                ready = __all_sync(0xffffffffu, mbar_test(&w.sh.full[r.stage], r.parity));
+                if (elect_one()) {
 #pragma unroll
-                for (int j = 0; j < kStep / 16; ++j)   // 16 of the sum: 32 bytes further on, or 16 rows of 128
-                    if (j < pieces) mma_pair_f16_ss(d, a + j * (a_mn ? 128 : 2), b + j * (b_mn ? 128 : 2), idesc, k > begin || j > 0);
-                commit_pair_of(empty, w.lead);
+                    for (int j = 0; j < kStep / 16; ++j)   // 16 of the sum: 32 bytes further on, or 16 rows of 128
+                        if (j < pieces) mma_pair_f16_ss(d, a + j * (a_mn ? 128 : 2), b + j * (b_mn ? 128 : 2), idesc, k > first || j > 0);
+                    commit_pair_of(empty, w.lead);
+                }
+                __syncwarp();
             }
+            if (ok && elect_one()) commit_pair_of(&w.sh.acc_full[acc.stage], w.lead);
             __syncwarp();
+            acc.next();
         }
-        if (ok && elect_one()) commit_pair_of(&w.sh.acc_full[acc.stage], w.lead);
-        __syncwarp();
-        acc.next();
     }
     // no MMA is left when the CTAs part, also when a wait gave up
     if (elect_one()) commit_leader(&w.sh.drained);
     __syncwarp();
     return warp_wait(&w.sh.drained, 0) && ok;
+}
+
+// Eight sums += what the accumulators hold.  Volatile, as what reads tmem_start8()'s registers has to be.
+__device__ __forceinline__ void add_columns(float* sum, uint32_t addr) {
+    uint32_t v[8];
+    tmem_start8(addr, v);
+    tmem_wait_loads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm volatile("add.rn.f32 %0, %0, %1;" : "+f"(sum[i]) : "f"(__uint_as_float(v[i])));
+}
+
+// WEIGHTS: a sum of more than kSteps steps, [begin, end).  The tensor cores cut what passes float32 wherever they add, always
+// towards zero, so they take kSteps at a time, and each thread adds up its columns of these in registers, rounding to nearest; the
+// last accumulator then gets the sums, as if it were the only one.  (A gradient of 16384 rows was off by 1.9e-5 of its norm,
+// 8.2e-5 where all terms have one sign; it is by 1.0e-6 and 2.2e-6.)
+template <class C, Form F>
+__device__ __forceinline__ bool sum_steps(const Work<C, F>& w, const Tile& t, int begin, int end, int warp, int group, Ring<2>& acc) {
+    if (w.until(begin, end) == end) return true;
+    constexpr int kTurns = C::tile / (32 * kGroups);
+    const uint32_t acc_empty0 = cluster_addr(smem_addr(&w.sh.acc_empty[0]), w.lead);
+    float sum[kTurns][32];
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sum[i][j] = 0.0f;
+    uint32_t d;
+#pragma unroll 1
+    while (true) {
+        if (!warp_wait(&w.sh.acc_full[acc.stage], acc.parity)) return false;
+        tmem_fence_after();
+        d = w.tmem + ((uint32_t)(warp * 32) << 16) + acc.stage * C::tile + 32 * group;
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+            if (32 * (group + kGroups * i) >= t.m) break;
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) add_columns(sum[i] + j, d + 32 * kGroups * i + j);
+        }
+        begin = w.until(begin, end);
+        if (begin == end) break;
+        tmem_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive_cluster(acc_empty0 + acc.stage * 8);
+        acc.next();
+    }
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        if (32 * (group + kGroups * i) >= t.m) break;
+        uint32_t v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(sum[i][j]);
+        tmem_store32(d + 32 * kGroups * i, v);
+    }
+    tmem_wait_stores();
+    return true;
 }
 
 // A part of a tile's sum: its accumulators go to shared memory, whose stages have been used by then, a column of 128
@@ -283,13 +340,16 @@ __device__ __forceinline__ bool leave_part(const Work<C, F>& w, int warp, int gr
     if (w.first >= w.items) return true;
     int steps, expert = 0;
     const Tile t = w.template tile<true>(w.first, expert, steps);
-    if (w.begin(steps, w.part) == w.begin(steps, w.part + 1)) return true;
-    if (!warp_wait(&w.sh.acc_full[0], 0)) return false;
+    const int begin = w.begin(steps, w.part), end = w.begin(steps, w.part + 1);
+    if (begin == end) return true;
+    Ring<2> acc;
+    if (!sum_steps(w, t, begin, end, warp, group, acc)) return false;
+    if (!warp_wait(&w.sh.acc_full[acc.stage], acc.parity)) return false;
     tmem_fence_after();
     const uint32_t to = smem_addr(w.smem) + (warp * 32 + (threadIdx.x & 31)) * 4;
     for (int c0 = 32 * group; c0 < t.m; c0 += 32 * kGroups) {
         uint32_t v[32];
-        tmem_load32(w.tmem + ((uint32_t)(warp * 32) << 16) + c0, v);
+        tmem_load32(w.tmem + ((uint32_t)(warp * 32) << 16) + acc.stage * C::tile + c0, v);
 #pragma unroll
         for (int i = 0; i < 32; ++i) asm volatile("st.shared.u32 [%0], %1;" :: "r"(to + (c0 + i) * 512), "r"(v[i]) : "memory");
     }
@@ -432,6 +492,7 @@ __device__ __forceinline__ bool epilogue(const Work<C, F>& w, int warp, int grou
                 asm volatile("prefetch.global.L2 [%0];" :: "l"(to + c0 * outs));
         }
         if (some && w.a.split == 1) {   // (parts have been waited for)
+            if (!sum_steps(w, t, 0, steps, warp, group, acc)) return false;
             if (!warp_wait(&w.sh.acc_full[acc.stage], acc.parity)) return false;
             tmem_fence_after();
         }

@@ -578,11 +578,11 @@ ep_status ep_expert_matmul_bf16(const void* a, int64_t rows, int32_t k, const vo
  * is ep_swiglu_keep_grad), for the rows r of expert e's segment
  *   grad_a[r,k] = sum_n grad_c[r,n] * w[e,n,k]                        (bf16 [rows, k]),
  *   grad_w[e,n,k] = sum over the segment's r of grad_c[r,n] * a[r,k]  (bf16 or float32 [E, n, k]),
- * sums in float32.  (The tensor cores add 16 products at a time and cut what passes float32, so that long sums come out a
- * little small: a float32 grad_w of 1024 rows by about 1e-6 of itself, of 16384 by 4e-6, and by 1.4e-5 where all terms have
- * one sign.)  grad_w of an expert without rows is zeros.  float32_out = 1 writes float32; accumulate = 1, which
- * needs float32_out, adds to what grad_w holds (an expert without rows is left as it is).  Rows outside the
- * segments take no part, whatever they hold.
+ * sums in float32.  (The tensor cores cut what passes float32 where they add; for grad_w they take 1024 rows at a time,
+ * whose sums are then added rounding to nearest: a float32 grad_w is off by about 1e-6 of its norm however many rows it
+ * sums, and by 2.2e-6 where all terms have one sign.)  grad_w of an expert without rows is zeros.  float32_out = 1
+ * writes float32; accumulate = 1, which needs float32_out, adds to what grad_w holds (an expert without rows is left as
+ * it is).  Rows outside the segments take no part, whatever they hold.
  * n and k multiples of 8, in [8, 65536]; grad_c, a, w 16-byte aligned, grad_a and grad_w 4-byte aligned;
  * segments and errors as for ep_expert_matmul.  With rows = 0, grad_w is written all the same. */
 ep_status ep_expert_matmul_grad_rows(const void* grad_c, int64_t rows, int32_t n, const void* w, int32_t k,
