@@ -18,16 +18,21 @@ def test_loads_that_wait_are_one_piece():
     body = text[text.index("void tmem_load32("):]
     body = body[:body.index("\n}\n")]
     assert body.count("asm volatile") == 1 and "tcgen05.ld." in body and "tcgen05.wait::ld" in body
-    # the only other load is the one whose readers are volatile
-    assert sum(t.count('"tcgen05.ld.') for _, t in sources()) == 2
+    # the only other loads are those whose readers are volatile
+    assert sum(t.count('"tcgen05.ld.') for _, t in sources()) == 1 + len(re.findall(r"void tmem_start\d+\(", text))
 
 
-def test_readers_of_the_other_load_are_volatile():
-    text = dict(sources())["matmul_fp8.cu"]
-    assert all("tmem_start16" not in t for name, t in sources() if name not in ("matmul_fp8.cu", "tcgen05.cuh"))
-    uses = re.findall(r"tmem_start16\(([^;]*), v\);(.*?)\n\s*}\n", text, re.S)
-    assert len(uses) == 1
-    readers = re.findall(r"(\w+)\([^;]*\bv\[i\]", uses[0][1])
-    assert readers == ["add_scaled"]
-    add = text[text.index("void add_scaled("):]
+def test_readers_of_the_other_loads_are_volatile():
+    """Behind each such load, up to the end of its block: the wait, then nothing but assembly or add_scaled() reads v."""
+    found = 0
+    for name, text in sources():
+        for use in re.finditer(r"tmem_start\d+\([^;{]*, v\);(.*?)\n\s*}\n", text, re.S):
+            found += 1
+            head, *readers = [x for x in use.group(1).split(";") if x.strip()]
+            assert head.strip() == "tmem_wait_loads()", name
+            for x in readers:
+                assert not re.search(r"\bv\[", x) or "asm volatile(" in x or "add_scaled(" in x, (name, x)
+    assert found == 2
+    fp8 = dict(sources())["matmul_fp8.cu"]
+    add = fp8[fp8.index("void add_scaled("):]
     assert "asm volatile" in add[:add.index("\n}\n")]
