@@ -28,7 +28,7 @@ def test_readers_of_the_other_loads_are_volatile():
     for name, text in sources():
         for use in re.finditer(r"tmem_start\d+\([^;{]*, v\);(.*?)\n\s*}\n", text, re.S):
             found += 1
-            head, *readers = [x for x in use.group(1).split(";") if x.strip()]
+            head, *readers = [x for x in re.sub(r'"[^"]*"', "", use.group(1)).split(";") if x.strip()]
             assert head.strip() == "tmem_wait_loads()", name
             for x in readers:
                 assert not re.search(r"\bv\[", x) or "asm volatile(" in x or "add_scaled(" in x, (name, x)
