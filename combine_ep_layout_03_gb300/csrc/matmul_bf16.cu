@@ -19,7 +19,7 @@
 // dw reduces over token rows, and a segment ends anywhere: the rows of its last 16 that belong to others (to the next
 // expert, or to nobody, with any contents) are set to zero in shared memory, in both operands, between their arrival
 // and their product.  Its sums are taken 1024 rows at a time (sum_steps()).  That the second CTA has done so the first one learns by a copy of 16 bytes, whose completion is a
-// release to the cluster (16 experts of 166 rows, 1024 x 1408 in float32: 21.6 us in a graph; by an arrival that releases to the
+// release to the cluster (16 experts of 166 rows, 1024 x 1408 in float32: 21.6 us in a graph at that; by an arrival that releases to the
 // cluster, which waits for the epilogue's stores, 32.1; with the rows loaded one by one and nothing cleared 25.6).
 //
 // Measured: 8192^3 578 us, 1902 TFLOP/s (0.99 of the measured rate); 128 experts of 1088 rows, 4096 x 2048: 1520 us one after
@@ -291,7 +291,9 @@ __device__ __forceinline__ void add_columns(float* sum, uint32_t addr) {
 // WEIGHTS: a sum of more than kSteps steps, [begin, end).  The tensor cores cut what passes float32 wherever they add, always
 // towards zero, so they take kSteps at a time, and each thread adds up its columns of these in registers, rounding to nearest; the
 // last accumulator then gets the sums, as if it were the only one.  (A gradient of 16384 rows was off by 1.9e-5 of its norm,
-// 8.2e-5 where all terms have one sign; it is by 1.0e-6 and 2.2e-6.)
+// 8.2e-5 where all terms have one sign; it is by 1.0e-6 and 2.2e-6.  Us in a graph, before and now: 2 experts of 16384 rows, 4096 x
+// 2048: 375, 375; 32 of 1088 rows, added: 500, 525, and 600 with eight steps at a time, which are half as far off; 4 of 2000 rows, 512 x
+// 2048: 17.0, 17.9; 16 of 166 rows, which has no long sums: 23.3, 24.0.)
 template <class C, Form F>
 __device__ __forceinline__ bool sum_steps(const Work<C, F>& w, const Tile& t, int begin, int end, int warp, int group, Ring<2>& acc) {
     if (w.until(begin, end) == end) return true;
@@ -486,7 +488,7 @@ __device__ __forceinline__ bool epilogue(const Work<C, F>& w, int warp, int grou
         const bool some = F != WEIGHTS || steps > 0;   // an expert without rows: zeros
         if (ADD && ch - lane < outs) {
             // what the tile is added to, on its way to L2 under the products, a row a lane: 128 experts of 64 rows, 2048 x 1024:
-            // 339 us in a graph, 461 without (its bytes take 324); of 500 rows 455, 465 (of the next tile instead 397, 546)
+            // 335 us in a graph, 461 without (its bytes take 324); of 500 rows 420 to 428, 465 (of the next tile instead 397, 546)
             const float* to = (const float*)w.a.out + row0 * outs + ch - lane;
             for (int c0 = 32 * (group + kGroups * w.part) + lane; c0 < t.m; c0 += 32 * kGroups * w.a.split)
                 asm volatile("prefetch.global.L2 [%0];" :: "l"(to + c0 * outs));

@@ -17,11 +17,11 @@
 // and one that brings the products of scales to shared memory (read where they are used, four bytes of 32 rows at a
 // time, they cost more than the FMAs).  Every wait is bounded (EP_ERR_TIMEOUT).
 //
-// Measured: 8192^3 455 us, 2410 TFLOP/s (without scales a library product takes 283); 128 experts of 1024 rows, 4096 x 2
-// x 1024 with SwiGLU 1140 us (at 1970 MHz and the power limit, as the library's product is at 1460 MHz); thin segments read
+// Measured: 8192^3 440 us, 2500 TFLOP/s (without scales a library product takes 283); 128 experts of 1024 rows, 4096 x 2
+// x 1024 with SwiGLU 1100 to 1150 us (at 1970 MHz and the power limit, as the library's product is at 1460 MHz); thin segments read
 // weights: 8 rows for each of 512 experts, 4096 x 1024, 316 us, 6.8 TB/s.  What bounds the large tile is a warp's way through a
 // block, some 1020 clocks: wait, four reads of tensor memory with their FMAs, the word that the accumulator is free.  With
-// everything else as it is, 8192^3 took 320 us without the epilogue's waits, reads and FMAs, as much with the reads alone,
+// everything else as it was then, 8192^3 took 320 us without the epilogue's waits, reads and FMAs, as much with the reads alone,
 // 392 with the FMAs alone, and 496 with both (then 517 in all).
 // The tile of 128 by 128 is bound by its loads, 64 bytes a clock of an SM: half the sums a thread, or twice the accumulators, left it
 // as it is (8.9 us for 1000 rows x 2048 x 2048).
