@@ -18,9 +18,10 @@
 //
 // dw reduces over token rows, and a segment ends anywhere: the rows of its last 16 that belong to others (to the next
 // expert, or to nobody, with any contents) are set to zero in shared memory, in both operands, between their arrival
-// and their product.  Its sums are taken 1024 rows at a time (sum_steps()).  That the second CTA has done so the first one learns by a copy of 16 bytes, whose completion is a
-// release to the cluster (16 experts of 166 rows, 1024 x 1408 in float32: 21.6 us in a graph at that; by an arrival that releases to the
-// cluster, which waits for the epilogue's stores, 32.1; with the rows loaded one by one and nothing cleared 25.6).
+// and their product.  That the second CTA has done so the first one learns by a copy of 16 bytes, whose completion is a
+// release to the cluster (16 experts of 166 rows, 1024 x 1408 in float32: 21.6 us in a graph at that; by an arrival that
+// releases to the cluster, which waits for the epilogue's stores, 32.1; with the rows loaded one by one and nothing cleared
+// 25.6).  Its sums are taken 1024 rows at a time: sum_steps().
 //
 // Measured: 8192^3 578 us, 1902 TFLOP/s (0.99 of the measured rate); 128 experts of 1088 rows, 4096 x 2048: 1520 us one after
 // the other (at 1390 MHz and the power limit; 1310 after a rest), dw of the same 1410 to 1630; 6 rows for each of 128 experts,
